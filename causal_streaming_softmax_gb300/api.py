@@ -27,6 +27,7 @@ ATTN_ERR_CUDA = -5
 ATTN_ERR_DEVICE_TIMEOUT = -6
 ATTN_ERR_DEVICE = -7
 ATTN_ERR_SCRATCH_LIMIT = -8
+ATTN_ERR_DEVICE_INDEX = -9
 ATTN_STEP_STORED = 0
 ATTN_STEP_FUSED = 1
 
@@ -54,6 +55,24 @@ class AttnDeviceBuffers(ctypes.Structure):
 
 class AttnProjection(ctypes.Structure):
     _fields_ = [("f32", ctypes.c_void_p), ("bf16", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class AttnPackedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "batch", "heads", "kv_heads", "head_dim",
+                                              "causal", "dtype")] + \
+        [("scale", ctypes.c_float)] + \
+        [(n, ctypes.c_int64) for n in ("q_token", "q_head", "k_token", "k_head", "v_token",
+                                       "v_head", "o_token", "o_head")]
+
+
+class AttnPagedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "tokens", "heads", "kv_heads", "head_dim",
+                                              "page_size", "num_pages", "table_width", "max_new",
+                                              "dtype")] + \
+        [("scale", ctypes.c_float)] + \
+        [(n, ctypes.c_int64) for n in ("q_token", "q_head", "o_token", "o_head", "k_token",
+                                       "k_head", "v_token", "v_head", "kc_page", "kc_head",
+                                       "kc_row", "vc_page", "vc_head", "vc_row")]
 
 
 class AttnError(RuntimeError):
@@ -113,8 +132,16 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                          ctypes.POINTER(AttnDeviceBuffers)]
     lib.attn_step_host_order.restype = ctypes.c_int
     lib.attn_selftest_arith.restype = ctypes.c_int
+    lib.attn_packed_fwd.argtypes = [ctypes.POINTER(AttnPackedShape)] + [vp] * 7
+    gp = ctypes.POINTER(AttnPagedShape)
+    lib.attn_paged_plan.argtypes = [gp] + [vp] * 10
+    lib.attn_paged_store.argtypes = [gp] + [vp] * 6
+    lib.attn_paged_workspace_bytes.argtypes = [gp]
+    lib.attn_paged_workspace_bytes.restype = sz
+    lib.attn_paged_fwd.argtypes = [gp] + [vp] * 7 + [sz, vp, vp, vp]
     for name in ("attn_fwd", "attn_row_terms", "attn_bwd_keys", "attn_bwd_queries",
-                 "attn_last_device_error", "attn_selftest_wait_timeout"):
+                 "attn_last_device_error", "attn_selftest_wait_timeout", "attn_packed_fwd",
+                 "attn_paged_plan", "attn_paged_store", "attn_paged_fwd"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -466,3 +493,265 @@ def attn_step_host(s: Shape, host: HostProblem, dev_in: DeviceInputs, bufs: Buff
 
 
 forward_backward_host = attn_step_host
+
+
+# ---------------------------------------------------------------------------
+# Answering with a model: packed prompts and the paged cache
+# ---------------------------------------------------------------------------
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+# attn_paged_plan's status bits
+PLAN_PAGES = 1
+PLAN_WIDTH = 2
+PLAN_TOKENS = 4
+PLAN_STATE = 8
+
+
+@dataclass
+class PackedShape:
+    """Sequences packed one behind the other: ``tokens`` rows of q, k, v, o in
+    all, ``batch`` sequences whose offsets a device array gives."""
+    tokens: int
+    batch: int
+    heads: int
+    kv_heads: int
+    causal: bool = True
+    scale: float = 0.125
+    dtype: torch.dtype = torch.float16
+
+
+@dataclass
+class PagedShape:
+    """A step over a paged cache: ``batch`` requests (rows of the table),
+    ``tokens`` rows of q, k, v, o, slots, pools of ``num_pages`` pages of
+    ``page_size`` tokens, a table of ``table_width`` pages a request, and
+    ``max_new``, the most new tokens a request has in the step."""
+    batch: int
+    tokens: int
+    heads: int
+    kv_heads: int
+    page_size: int
+    num_pages: int
+    table_width: int
+    max_new: int = 1
+    scale: float = 0.125
+    dtype: torch.dtype = torch.float16
+
+    def c_struct(self) -> AttnPagedShape:
+        return AttnPagedShape(self.batch, self.tokens, self.heads, self.kv_heads, HEAD_DIM,
+                              self.page_size, self.num_pages, self.table_width, self.max_new,
+                              _dtype_code(self.dtype), self.scale)
+
+
+def _dtype_code(dt) -> int:
+    if dt not in _DTYPES:
+        raise TypeError("dtype must be torch.float16 or torch.bfloat16, got %s" % (dt,))
+    return _DTYPES[dt]
+
+
+def _strided(t, name, dtype, shape, device):
+    """Pointer and strides of a tensor whose last dimension is dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device or device.type != "cuda":
+        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError("%s must be dense in its last dimension" % name)
+    return t.data_ptr(), st
+
+
+def _dense(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device or device.type != "cuda":
+        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    return t.device
+
+
+def _run(name, device, stream, *args):
+    """Calls an entry point on the tensors' device and the stream given, or
+    that device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != ATTN_OK:
+        raise AttnError(name, rc)
+
+
+def attn_packed_fwd(s: PackedShape, q, k, v, cu, o, lse=None, stream=None) -> None:
+    """Attention over packed sequences: q [tokens][heads][64], k, v
+    [tokens][kv_heads][64] and o as q, any strides over tokens and heads; cu
+    int32 [batch + 1] on the device; lse float32 [heads][tokens] or None."""
+    n, H, Hkv = s.tokens, s.heads, s.kv_heads
+    dev = _device_of(q, "q")
+    code = _dtype_code(s.dtype)
+    qp, qs = _strided(q, "q", s.dtype, (n, H, 64), dev)
+    kp, ks = _strided(k, "k", s.dtype, (n, Hkv, 64), dev)
+    vp, vs = _strided(v, "v", s.dtype, (n, Hkv, 64), dev)
+    op, os_ = _strided(o, "o", s.dtype, (n, H, 64), dev)
+    cup = _dense(cu, "cu", torch.int32, (s.batch + 1,), dev)
+    lp = None if lse is None else _dense(lse, "lse", torch.float32, (H, n), dev)
+    shape = AttnPackedShape(n, s.batch, H, Hkv, HEAD_DIM, 1 if s.causal else 0, code, s.scale,
+                            qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
+    _run("attn_packed_fwd", dev, stream, ctypes.byref(shape), qp, kp, vp, cup, op, lp)
+
+
+def attn_paged_plan(s: PagedShape, cached, fresh, ring, state, table, cu, lens, slots, next,
+                    stream=None) -> None:
+    """Hands out and takes back pages and writes table, cu, lens, slots, next
+    (int32 CUDA tensors; see attn.h).  ``fresh`` < 0 marks a finished request."""
+    B, i32 = s.batch, torch.int32
+    dev = _device_of(cached, "cached")
+    args = (_dense(cached, "cached", i32, (B,), dev), _dense(fresh, "fresh", i32, (B,), dev),
+            _dense(ring, "ring", i32, (s.num_pages,), dev), _dense(state, "state", i32, (4,), dev),
+            _dense(table, "table", i32, (B, s.table_width), dev),
+            _dense(cu, "cu", i32, (B + 1,), dev), _dense(lens, "lens", i32, (B,), dev),
+            _dense(slots, "slots", i32, (s.tokens,), dev), _dense(next, "next", i32, (4,), dev))
+    shape = s.c_struct()
+    _run("attn_paged_plan", dev, stream, ctypes.byref(shape), *args)
+
+
+def _pool_strides(s, shape, k_cache, v_cache, dev):
+    dims = (s.num_pages, s.kv_heads, s.page_size, 64)
+    kp, ks = _strided(k_cache, "k_cache", s.dtype, dims, dev)
+    vp, vs = _strided(v_cache, "v_cache", s.dtype, dims, dev)
+    shape.kc_page, shape.kc_head, shape.kc_row = ks[0], ks[1], ks[2]
+    shape.vc_page, shape.vc_head, shape.vc_row = vs[0], vs[1], vs[2]
+    return kp, vp
+
+
+def attn_paged_store(s: PagedShape, k, v, slots, k_cache, v_cache, stream=None) -> None:
+    """Rows of k, v [tokens][kv_heads][64] into the caches
+    [num_pages][kv_heads][page_size][64] (any strides) at slots int32 [tokens]."""
+    dev = _device_of(k, "k")
+    shape = s.c_struct()
+    kp, ks = _strided(k, "k", s.dtype, (s.tokens, s.kv_heads, 64), dev)
+    vp, vs = _strided(v, "v", s.dtype, (s.tokens, s.kv_heads, 64), dev)
+    sp = _dense(slots, "slots", torch.int32, (s.tokens,), dev)
+    kc, vc = _pool_strides(s, shape, k_cache, v_cache, dev)
+    shape.k_token, shape.k_head, shape.v_token, shape.v_head = ks[0], ks[1], vs[0], vs[1]
+    _run("attn_paged_store", dev, stream, ctypes.byref(shape), kp, vp, sp, kc, vc)
+
+
+def paged_workspace_bytes(s: PagedShape) -> int:
+    shape = s.c_struct()
+    n = load_library().attn_paged_workspace_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise AttnError("attn_paged_workspace_bytes", ATTN_ERR_SHAPE)
+    return n
+
+
+def alloc_paged_workspace(s: PagedShape, device=None) -> torch.Tensor:
+    """A uint8 CUDA tensor large enough for attn_paged_fwd's workspace."""
+    return torch.empty(paged_workspace_bytes(s), dtype=torch.uint8,
+                       device=device or torch.device("cuda"))
+
+
+def attn_paged_fwd(s: PagedShape, q, k_cache, v_cache, table, cu, lens, ws, o, lse=None,
+                   stream=None) -> None:
+    """Attention of the new rows q [tokens][heads][64] over the cache; o as q,
+    lse float32 [heads][tokens] or None; ws from alloc_paged_workspace."""
+    n, H = s.tokens, s.heads
+    dev = _device_of(q, "q")
+    shape = s.c_struct()
+    qp, qs = _strided(q, "q", s.dtype, (n, H, 64), dev)
+    op, os_ = _strided(o, "o", s.dtype, (n, H, 64), dev)
+    kc, vc = _pool_strides(s, shape, k_cache, v_cache, dev)
+    shape.q_token, shape.q_head, shape.o_token, shape.o_head = qs[0], qs[1], os_[0], os_[1]
+    tp = _dense(table, "table", torch.int32, (s.batch, s.table_width), dev)
+    cup = _dense(cu, "cu", torch.int32, (s.batch + 1,), dev)
+    lenp = _dense(lens, "lens", torch.int32, (s.batch,), dev)
+    lp = None if lse is None else _dense(lse, "lse", torch.float32, (H, n), dev)
+    if not (isinstance(ws, torch.Tensor) and ws.dtype == torch.uint8 and ws.is_contiguous()
+            and ws.device == dev):
+        raise TypeError("ws must be a contiguous uint8 CUDA tensor on the device of the others")
+    _run("attn_paged_fwd", dev, stream, ctypes.byref(shape), qp, kc, vc, tp, cup, lenp,
+         ws.data_ptr(), ws.numel(), op, lp)
+
+
+class PagedCache:
+    """The device state of a server's cache: pools of K and V pages, the block
+    table, the requests' lengths and the ring of free pages."""
+
+    def __init__(self, batch: int, heads: int, kv_heads: int, num_pages: int, page_size: int = 16,
+                 table_width: Optional[int] = None, dtype=torch.float16, scale: float = 0.125,
+                 device=None):
+        dev = torch.device(device or "cuda")
+        self.batch, self.heads, self.kv_heads = batch, heads, kv_heads
+        self.num_pages, self.page_size, self.scale, self.dtype = num_pages, page_size, scale, dtype
+        self.table_width = table_width or num_pages
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.k = torch.zeros((num_pages, kv_heads, page_size, 64), dtype=dtype, device=dev)
+        self.v = torch.zeros_like(self.k)
+        self.table = torch.full((batch, self.table_width), -1, **i32)
+        self.ring = torch.arange(num_pages, **i32)
+        self.cu = torch.zeros(batch + 1, **i32)
+        # lengths and ring state, each read by a step and written for the next
+        self.lens, self._lens = torch.zeros(batch, **i32), torch.zeros(batch, **i32)
+        self.state = torch.tensor([0, num_pages, 0, 0], **i32)
+        self._state = torch.zeros(4, **i32)
+        self.ws = None
+
+    def shape(self, tokens: int, max_new: int) -> PagedShape:
+        return PagedShape(self.batch, tokens, self.heads, self.kv_heads, self.page_size,
+                          self.num_pages, self.table_width, max_new, self.scale, self.dtype)
+
+    def step(self, fresh, q, k, v, o, lse=None, max_new: Optional[int] = None,
+             stream=None) -> None:
+        """One step of every request: ``fresh`` int32 [batch] new tokens each
+        (negative: finished, its pages go back), whose rows stand in q, k, v
+        one behind the other; plans, stores K and V and writes o (and lse).
+        ``max_new``: the most new tokens of a request (default: all of them).
+        Steps are ordered by their streams alone.  The lengths and the ring
+        state swap between two buffers from step to step, so a graph that is
+        replayed holds an even number of steps."""
+        if stream is not None:  # the step's own buffers belong to its stream
+            with torch.cuda.stream(stream):
+                return self.step(fresh, q, k, v, o, lse, max_new)
+        n = q.shape[0]
+        s = self.shape(n, max_new or max(n, 1))
+        need = paged_workspace_bytes(s)
+        if self.ws is None or self.ws.numel() < need:
+            self.ws = torch.empty(need, dtype=torch.uint8, device=self.k.device)
+        slots = torch.empty(n, dtype=torch.int32, device=self.k.device)
+        attn_paged_plan(s, self.lens, fresh, self.ring, self.state, self.table, self.cu,
+                        self._lens, slots, self._state)
+        self.lens, self._lens = self._lens, self.lens
+        self.state, self._state = self._state, self.state
+        if n:
+            attn_paged_store(s, k, v, slots, self.k, self.v)
+            self.ws.record_stream(torch.cuda.current_stream(self.k.device))
+            attn_paged_fwd(s, q, self.k, self.v, self.table, self.cu, self.lens, self.ws, o, lse)
+
+    def status(self) -> int:
+        """The last step's status (0, or a sum of PLAN_ bits: the step handed
+        out nothing, stored nothing and left o as it was).  Synchronises."""
+        return int(self.state[3])
+
+    def free_pages(self) -> int:
+        """Pages that are free after the last step.  Synchronises."""
+        return int(self.state[1])

@@ -167,6 +167,8 @@ const char* attn_error_string(int code) {
     case ATTN_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out";
     case ATTN_ERR_DEVICE: return "the current device is not sm_103";
     case ATTN_ERR_SCRATCH_LIMIT: return "problem exceeds the static scratch of attn_bwd_noalloc";
+    case ATTN_ERR_DEVICE_INDEX:
+      return "a kernel met an offset, length, slot or page id outside its range";
     default: return "unknown error";
   }
 }
@@ -340,7 +342,7 @@ int attn_last_device_error(void* stream) {
   if (v == 0) return ATTN_OK;
   const uint32_t zero = 0;
   if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)) != cudaSuccess) return ATTN_ERR_CUDA;
-  return ATTN_ERR_DEVICE_TIMEOUT;
+  return (v & kErrWaitTimeout) ? ATTN_ERR_DEVICE_TIMEOUT : ATTN_ERR_DEVICE_INDEX;
 }
 
 int attn_selftest_arith(const float* x, uint32_t* packed, float* e2, int n, void* stream) {

@@ -89,9 +89,10 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 // ---------------------------------------------------------------------------
 // bounded waits
 // ---------------------------------------------------------------------------
-// Device-side error word bits (the host maps any nonzero value to
-// ATTN_ERR_DEVICE_TIMEOUT).
+// Device-side error word bits (the host maps the first to
+// ATTN_ERR_DEVICE_TIMEOUT, the second alone to ATTN_ERR_DEVICE_INDEX).
 constexpr uint32_t kErrWaitTimeout = 1u;
+constexpr uint32_t kErrIndex = 2u;
 
 struct WaitCtl {
   uint32_t* err;        // device error word (global), may be null

@@ -67,8 +67,11 @@ enum {
   ATTN_ERR_CUDA = -5,           /* a CUDA runtime/driver call failed         */
   ATTN_ERR_DEVICE_TIMEOUT = -6, /* a kernel's bounded wait ran out           */
   ATTN_ERR_DEVICE = -7,         /* the current device is not sm_103          */
-  ATTN_ERR_SCRATCH_LIMIT = -8   /* attn_bwd_noalloc: problem exceeds its
+  ATTN_ERR_SCRATCH_LIMIT = -8,  /* attn_bwd_noalloc: problem exceeds its
                                    static scratch                            */
+  ATTN_ERR_DEVICE_INDEX = -9    /* a kernel met an offset, length, slot or page
+                                   id outside its range (device arrays of the
+                                   packed and paged calls)                   */
 };
 
 /* Size of the static device scratch that attn_bwd_noalloc works in. */
@@ -353,14 +356,166 @@ ATTN_API int attn_bwd_noalloc(const attn_shape* shape, const uint16_t* q,
                               const float* delta, float* dq, float* dk,
                               float* dvt, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Answering with a model: packed prompts and a paged cache.
+ *
+ * The calls below are the library's own; the method's pages have no
+ * counterpart beyond the arithmetic, which is the forward pass's (base-2
+ * streaming softmax, P rounded to the operands' type before its product with
+ * V, sums in binary32).  q, k, v and o are token-major: element
+ * (token, head, c) lies at token * <t>_token + head * <t>_head + c, strides in
+ * elements, so that q, k and v can be column blocks of one fused projection.
+ * Strides are multiples of 8 (16 bytes) and at least 64 in a dimension longer
+ * than one (ATTN_ERR_SHAPE otherwise; the stride of a dimension of one is not
+ * read); o's rows must not overlap.  Base pointers are 16-byte aligned.
+ *
+ * Arrays of offsets, lengths, slots and page ids live on the device and are
+ * read there.  A value outside its range never leads to an access outside the
+ * tensors: the kernel leaves the row or key out and sets the device error
+ * word (attn_last_device_error then returns ATTN_ERR_DEVICE_INDEX); the
+ * outputs of that sequence are then undefined.
+ *
+ * An output row depends on the keys that its row sees and on nothing else:
+ * infinities and NaN in masked keys, in pages past a length or in other
+ * sequences do not reach it.  A row that sees no key gives O = 0, L = -inf.
+ */
+enum { ATTN_F16 = 0, ATTN_BF16 = 1 };
+
+/*
+ * Packed sequences.  tokens: rows of q, k, v, o (>= 0); batch: sequences,
+ * 1..65535; heads a multiple of kv_heads, at most 128 query heads per K/V
+ * head; head_dim 64; causal 0 or 1; dtype ATTN_F16 or ATTN_BF16 (q, k, v, o).
+ */
+typedef struct attn_packed_shape {
+  int32_t tokens;
+  int32_t batch;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t causal;
+  int32_t dtype;
+  float scale;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+} attn_packed_shape;
+
+/*
+ * Attention over whole prompts packed one behind the other.  cu: device int32
+ * [batch + 1], ascending; sequence i has rows cu[i] .. cu[i+1] - 1 (possibly
+ * none).  Row r of a sequence sees its keys 0..r (causal) or all of them.
+ * Writes o and, if lse is not NULL, lse [heads][tokens] (base 2, binary32).
+ * Rows outside every sequence (before cu[0], from cu[batch] on) are left as
+ * they were in o and lse.  tokens = 0 launches nothing.
+ */
+ATTN_API int attn_packed_fwd(const attn_packed_shape* shape, const void* q, const void* k,
+                             const void* v, const int32_t* cu, void* o, float* lse,
+                             void* stream);
+
+/*
+ * The paged cache.  K and V each live in a pool of num_pages pages of
+ * page_size tokens (a power of two, 8..1024; num_pages * page_size < 2^31):
+ * element (page, kv head, row, c) at page * <c>_page + head * <c>_head +
+ * row * <c>_row + c, any order of strides under the rule above.  Slot
+ * s = page * page_size + row names one token's place in both pools.
+ * Request i (row i of batch, 1..4096) holds kv tokens; token p of it lies in
+ * page table[i * table_width + p / page_size], row p % page_size.
+ * tokens: rows of q, o (k, v, slots in the store), all requests' new tokens
+ * one behind the other and perhaps padding.  max_new: the most new tokens any
+ * request has in this call (the host's bound; 1 for a token step).
+ */
+typedef struct attn_paged_shape {
+  int32_t batch;
+  int32_t tokens;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t table_width;
+  int32_t max_new;
+  int32_t dtype;
+  float scale;
+  int64_t q_token, q_head, o_token, o_head;              /* attn_paged_fwd   */
+  int64_t k_token, k_head, v_token, v_head;              /* attn_paged_store */
+  int64_t kc_page, kc_head, kc_row, vc_page, vc_head, vc_row;
+} attn_paged_shape;
+
+/*
+ * Plans a step on the device: hands out pages, builds the slot map and the
+ * offsets, and takes back the pages of finished requests, in one launch.
+ *   cached [batch]  tokens that request i has in the cache (>= 0)
+ *   fresh [batch]   new tokens of request i; negative: it is finished
+ *   ring [num_pages], state {head, free, -, -}: the free pages are
+ *                   ring[(head + x) % num_pages], 0 <= x < free
+ *   table           a request's first ceil(cached / page_size) entries name
+ *                   its pages
+ * Writes: cu [batch + 1], the offsets of the new tokens (a finished request
+ * has none); lens [batch], cached + fresh (0 for a finished one); slots
+ * [tokens], each new token's slot, -1 behind the last; the table's entries
+ * for the pages handed out (in order of requests, then positions, from the
+ * ring's head; other entries stay); the pages of finished requests behind the
+ * ring's tail; and next = {head', free', pages handed out, status}.
+ * status 0, or a sum of ATTN_PLAN_ bits, in which case nothing is handed out
+ * or taken back: the table and the ring stay, every offset is 0, every slot
+ * -1, lens = cached and next = {head, free, 0, status}.
+ * All arrays int32.  The outputs may overlap neither each other nor an input
+ * (ATTN_ERR_SHAPE where a pointer is given twice), so that the next step
+ * passes lens as cached and next as state.  Only batch, tokens, page_size,
+ * num_pages and table_width of the shape are read.
+ */
+enum {
+  ATTN_PLAN_PAGES = 1,  /* fewer free pages than the step needs             */
+  ATTN_PLAN_WIDTH = 2,  /* a request outgrows table_width pages             */
+  ATTN_PLAN_TOKENS = 4, /* more new tokens than `tokens`                    */
+  ATTN_PLAN_STATE = 8   /* a negative cached length, or a ring state that
+                           cannot be (head, free, or more pages than exist) */
+};
+ATTN_API int attn_paged_plan(const attn_paged_shape* shape, const int32_t* cached,
+                             const int32_t* fresh, int32_t* ring, const int32_t* state,
+                             int32_t* table, int32_t* cu, int32_t* lens, int32_t* slots,
+                             int32_t* next, void* stream);
+
+/*
+ * Stores new K and V rows into the cache: row t of k and v (all K/V heads)
+ * goes to slot slots[t]; a negative slot is skipped.  Slots of one call are
+ * distinct (attn_paged_plan's are): where one is given twice, which row it
+ * ends with is not determined.  Uses batch, tokens, kv_heads, page_size,
+ * num_pages, dtype and the k, v, kc and vc strides.
+ */
+ATTN_API int attn_paged_store(const attn_paged_shape* shape, const void* k, const void* v,
+                              const int32_t* slots, void* k_cache, void* v_cache, void* stream);
+
+/*
+ * Bytes of the workspace of attn_paged_fwd (0 if the shape is invalid).  It
+ * holds the parts of rows whose keys were split over several blocks; its
+ * contents need not be initialised and mean nothing after the call.  Calls
+ * that overlap on the GPU need workspaces of their own.
+ */
+ATTN_API size_t attn_paged_workspace_bytes(const attn_paged_shape* shape);
+
+/*
+ * Attention of the new tokens over the cache.  Request i's new tokens are
+ * rows cu[i] .. cu[i+1] - 1 of q and o; lens[i] counts its tokens in the
+ * cache, the new ones (already stored) the last among them: its row r of n
+ * sees keys 0 .. lens[i] - n + r (none where that is negative).  Writes o
+ * and, if lse is not NULL, lse [heads][tokens] (base 2, binary32); rows
+ * outside every request are left as they were.
+ */
+ATTN_API int attn_paged_fwd(const attn_paged_shape* shape, const void* q, const void* k_cache,
+                            const void* v_cache, const int32_t* table, const int32_t* cu,
+                            const int32_t* lens, void* ws, size_t ws_bytes, void* o, float* lse,
+                            void* stream);
+
 /* A static, human-readable message for an ATTN_ code. */
 ATTN_API const char* attn_error_string(int code);
 
 /*
  * Synchronises the stream, then reports and clears the current device's
- * device-side error word: ATTN_OK, or ATTN_ERR_DEVICE_TIMEOUT when a kernel
- * gave up a bounded wait (its outputs are then undefined).  ATTN_ERR_CUDA if
- * the synchronisation itself failed.
+ * device-side error word: ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT when a kernel
+ * gave up a bounded wait (its outputs are then undefined), or
+ * ATTN_ERR_DEVICE_INDEX when one met a bad offset, length, slot or page id
+ * and none gave up a wait.  ATTN_ERR_CUDA if the synchronisation itself
+ * failed.
  */
 ATTN_API int attn_last_device_error(void* stream);
 

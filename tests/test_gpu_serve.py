@@ -1,0 +1,644 @@
+"""The packed and paged calls on the GPU against plain 64-bit forms."""
+import math
+import random
+
+import pytest
+
+from serve_util import attend64, check, gather, packed64, paged64, plan_host
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def torch(cuda_device):
+    import torch
+    from causal_streaming_softmax_gb300 import build
+    build.build()
+    return torch
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(cuda_device):
+    from causal_streaming_softmax_gb300 import api
+    yield
+    assert api.last_device_error() == 0
+
+
+def scan(xs):
+    out = [0]
+    for x in xs:
+        out.append(out[-1] + x)
+    return out
+
+
+def i32(torch, xs):
+    return torch.tensor(xs, dtype=torch.int32, device="cuda")
+
+
+def rnd(torch, shape, dtype, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def packed_inputs(torch, t, H, Hkv, dtype, seed, layout="fused"):
+    if layout == "fused":  # column blocks of one projection
+        x = rnd(torch, (t, H + 2 * Hkv, 64), dtype, seed)
+        x[:, :H] *= 2
+        return x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:]
+    if layout == "planes":  # [heads][tokens][64]
+        return tuple(rnd(torch, (h, t, 64), dtype, seed + i, s).permute(1, 0, 2)
+                     for i, (h, s) in enumerate(((H, 2.0), (Hkv, 1.0), (Hkv, 1.0))))
+    return (rnd(torch, (t, H, 64), dtype, seed, 2.0), rnd(torch, (t, Hkv, 64), dtype, seed + 1),
+            rnd(torch, (t, Hkv, 64), dtype, seed + 2))
+
+
+SENTINEL = 7.0
+
+
+def run_packed(torch, q, k, v, cu, causal=True, scale=0.125, lse=True, o_layout="dense",
+               stream=None):
+    from causal_streaming_softmax_gb300 import api
+    t, H, _ = q.shape
+    dt = q.dtype
+    if o_layout == "planes":
+        o = torch.full((H, t, 64), SENTINEL, dtype=dt, device="cuda").permute(1, 0, 2)
+    elif o_layout == "wide":
+        o = torch.full((t, H + 3, 72), SENTINEL, dtype=dt, device="cuda")[:, 1:H + 1, :64]
+    else:
+        o = torch.full((t, H, 64), SENTINEL, dtype=dt, device="cuda")
+    L = torch.full((H, t), SENTINEL, device="cuda") if lse else None
+    s = api.PackedShape(t, len(cu) - 1, H, k.shape[1], causal=causal, scale=scale, dtype=dt)
+    api.attn_packed_fwd(s, q, k, v, i32(torch, cu), o, L, stream=stream)
+    return o, L
+
+
+def check_packed(torch, q, k, v, cu, causal, o, L, scale=0.125):
+    inside = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
+    for rows, eo, el, to, tl in packed64(q, k, v, cu, causal, scale):
+        check(o[rows], eo, to, "O of rows %s" % rows)
+        if L is not None:
+            check(L[:, rows], el, tl, "L of rows %s" % rows)
+        inside[rows] = True
+    assert (o[~inside] == SENTINEL).all(), "a row outside the sequences was written"
+    if L is not None:
+        assert (L[:, ~inside] == SENTINEL).all()
+
+
+PACKS = [[1], [0], [2], [0, 3, 0, 0, 5, 0], [63, 64, 65], [127, 128, 129], [1] * 300,
+         [300, 1, 517, 32, 33, 31], [1025], [5, 900, 4, 3], list(range(0, 60, 3))]
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("heads", [(2, 1), (4, 4), (8, 2), (15, 5), (8, 1), (7, 1)])
+@pytest.mark.parametrize("pack", range(len(PACKS)))
+def test_packed(torch, dtype, heads, pack):
+    H, Hkv = heads
+    lens = PACKS[pack]
+    cu = scan(lens)
+    if pack % 2:  # rows before the first sequence and behind the last
+        cu = [c + 3 for c in cu]
+    t = cu[-1] + (5 if pack % 2 else 0)
+    if t == 0:
+        t = 2
+    dt = getattr(torch, dtype)
+    q, k, v = packed_inputs(torch, t, H, Hkv, dt, 10 * pack + H,
+                            ["fused", "planes", "dense"][(pack + H) % 3])
+    for causal in (True, False):
+        o, L = run_packed(torch, q, k, v, cu, causal,
+                          o_layout=["dense", "wide", "planes"][pack % 3], lse=pack % 4 != 3)
+        check_packed(torch, q, k, v, cu, causal, o, L)
+
+
+@pytest.mark.parametrize("heads", [(128, 1), (100, 1), (65, 1), (34, 2), (33, 1)])
+def test_packed_wide_groups(torch, heads):
+    H, Hkv = heads
+    cu = scan([3, 130, 1, 40])
+    q, k, v = packed_inputs(torch, cu[-1], H, Hkv, torch.bfloat16, 5)
+    o, L = run_packed(torch, q, k, v, cu)
+    check_packed(torch, q, k, v, cu, True, o, L)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.01, 3.0])
+def test_packed_scales_and_large_scores(torch, scale):
+    cu = scan([200, 77])
+    q, k, v = packed_inputs(torch, cu[-1], 4, 2, torch.float16, 8)
+    q, k = q * 4, k * 4
+    o, L = run_packed(torch, q, k, v, cu, scale=scale)
+    check_packed(torch, q, k, v, cu, True, o, L, scale)
+
+
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (8, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_packed_bad_values_stay_where_they_are_seen(torch, H, Hkv, causal):
+    """NaN and infinities in one sequence's keys reach the rows that see them
+    and no other: not earlier rows, not the neighbours, not the padding."""
+    lens = [40, 200, 3, 129, 260]
+    cu = [c + 2 for c in scan(lens)]
+    t = cu[-1] + 9
+    q, k, v = (x.clone() for x in packed_inputs(torch, t, H, Hkv, torch.float16, 4, "dense"))
+    for x in (q, k, v):
+        x[:2] = NAN
+        x[cu[-1]:] = math.inf
+    v[cu[1] + 150, 0, 5] = NAN
+    v[cu[1] + 170, 1, 9] = math.inf
+    v[cu[3] + 128] = -math.inf
+    k[cu[4] + 100, 0] = NAN
+    v[cu[4] + 131, 1, 3] = math.inf
+    q[cu[2] + 1, 0] = NAN
+    o, L = run_packed(torch, q, k, v, cu, causal)
+    check_packed(torch, q, k, v, cu, causal, o, L)
+
+
+def test_packed_long_prompt(torch):
+    """Sampled rows of a long prompt."""
+    n, H, Hkv = 9001, 4, 2
+    q, k, v = packed_inputs(torch, n, H, Hkv, torch.bfloat16, 6)
+    o, L = run_packed(torch, q, k, v, [0, n])
+    rows = torch.tensor([0, 1, 127, 128, 255, 256, 4095, 4096, 8999, 9000], device="cuda")
+    eo, el, to, tl = attend64(q[rows], k, v, rows + 1)
+    check(o[rows], eo, to, "O")
+    check(L[:, rows], el, tl, "L")
+
+
+def test_packed_many_units_are_deterministic(torch):
+    cu = scan([random.Random(1).randint(1, 700) for _ in range(40)])
+    q, k, v = packed_inputs(torch, cu[-1], 8, 2, torch.float16, 7)
+    o, L = run_packed(torch, q, k, v, cu)
+    for _ in range(3):
+        o2, L2 = run_packed(torch, q, k, v, cu)
+        assert torch.equal(o, o2) and torch.equal(L, L2)
+
+
+def test_packed_agrees_with_the_padded_forward(torch):
+    """The same rows as attn_fwd computes from padded planes."""
+    from causal_streaming_softmax_gb300 import api
+    lens, T, H, Hkv = [256, 192, 64], 256, 4, 2
+    cu = scan(lens)
+    q, k, v = packed_inputs(torch, cu[-1], H, Hkv, torch.float16, 9)
+    o, L = run_packed(torch, q, k, v, cu)
+    pad = lambda x: torch.stack([torch.nn.functional.pad(
+        x[a:b], (0, 0, 0, 0, 0, T - (b - a))).permute(1, 0, 2) for a, b in zip(cu, cu[1:])])
+    s = api.Shape(3, T, H, Hkv, seq_lens=i32(torch, lens), v_rows=True)
+    bufs = api.Buffers(s, workspace=False)
+    api.attn_fwd(s, pad(q).contiguous(), pad(k).contiguous(), pad(v).contiguous(), bufs.o, bufs.lse)
+    for i, (a, b) in enumerate(zip(cu, cu[1:])):
+        _, _, to, tl = attend64(q[a:b], k[a:b], v[a:b],
+                                torch.arange(1, b - a + 1, device="cuda"))
+        check(bufs.o[i, :b - a].view(b - a, H, 64), o[a:b].double(), 2 * to, "padded O")
+        check(bufs.lse[i, :, :b - a], L[:, a:b].double(), 2 * tl, "padded L")
+
+
+# ---------------------------------------------------------------- paged cache
+def paged_problem(torch, reqs, H, Hkv, page, dtype, seed, layout="pages", stale=NAN, pad=0):
+    """reqs: (keys in the cache, new tokens).  Places that no request holds are
+    ``stale``; unused table entries name pages that do not exist."""
+    r = random.Random(seed)
+    up = [-(-max(n, 0) // page) for n, _ in reqs]
+    width, pages = max(1, max(up)) + 1, sum(up) + 3
+    order = list(range(pages))
+    r.shuffle(order)
+    table, used = [], torch.zeros((pages, page), dtype=torch.bool)
+    for (n, _), u in zip(reqs, up):
+        ids = [order.pop() for _ in range(u)]
+        for x in range(max(n, 0)):
+            used[ids[x // page], x % page] = True
+        table.append(ids + [r.choice([-1, pages, 2 ** 31 - 1, -2 ** 31])] * (width - u))
+    used = used.cuda()
+    pools = []
+    for i in range(2):
+        x = rnd(torch, (pages, Hkv, page, 64), dtype, seed + 50 + i)
+        x.masked_fill_(~used[:, None, :, None], stale)
+        if layout == "rows":  # [page][row][head]
+            x = x.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+        elif layout == "both":  # K and V of a page side by side
+            x = torch.stack([x, x], 1)[:, i]
+        pools.append(x)
+    new = [n for _, n in reqs]
+    cu = scan(new)
+    q = rnd(torch, (cu[-1] + pad, H, 64), dtype, seed + 60, 2.0)
+    return q, pools[0], pools[1], table, cu, [n for n, _ in reqs], width
+
+
+def run_paged(torch, q, kc, vc, table, cu, lens, max_new=None, lse=True, o=None, stream=None):
+    from causal_streaming_softmax_gb300 import api
+    t, H, _ = q.shape
+    B = len(lens)
+    s = api.PagedShape(B, t, H, kc.shape[1], kc.shape[2], kc.shape[0], len(table[0]),
+                       max_new=max_new or max(1, max(b - a for a, b in zip(cu, cu[1:]))),
+                       dtype=q.dtype)
+    ws = api.alloc_paged_workspace(s)
+    ws.fill_(255)  # its contents mean nothing
+    if o is None:
+        o = torch.full((t, H, 64), SENTINEL, dtype=q.dtype, device="cuda")
+    L = torch.full((H, t), SENTINEL, device="cuda") if lse else None
+    api.attn_paged_fwd(s, q, kc, vc, i32(torch, table), i32(torch, cu), i32(torch, lens), ws, o, L,
+                       stream=stream)
+    return o, L
+
+
+def check_paged(torch, q, kc, vc, table, cu, lens, o, L):
+    inside = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
+    tt = torch.tensor(table, dtype=torch.int64, device="cuda")
+    for rows, eo, el, to, tl in paged64(q, kc, vc, tt, cu, lens):
+        check(o[rows], eo, to, "O of rows %s" % rows)
+        if L is not None:
+            check(L[:, rows], el, tl, "L of rows %s" % rows)
+        inside[rows] = True
+    assert (o[~inside] == SENTINEL).all(), "a row outside the requests was written"
+    if L is not None:
+        assert (L[:, ~inside] == SENTINEL).all()
+
+
+REQS = [
+    [(1, 1)],
+    [(0, 0)],
+    [(777, 1)],
+    [(16, 1), (17, 1), (15, 1), (1, 1), (0, 0), (64, 1), (65, 1), (2000, 1)],
+    [(5000, 1), (3, 1)],
+    [(100, 2), (7, 2), (2, 2), (129, 1), (1, 2)],           # a few new tokens each
+    [(50, 50), (1, 1), (300, 33), (128, 128)],              # prompts and tokens
+    [(0, 1), (1, 3), (2, 5), (700, 1)],                     # rows that see nothing
+    [(3000, 700), (64, 64), (9, 1), (4097, 129)],
+    [(1 + 37 * i % 400, 1) for i in range(150)],
+    [(40 + i, 1 + i % 5) for i in range(90)],
+    [(20000, 3), (11, 2)],
+]
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("heads", [(2, 1), (4, 4), (8, 2), (15, 5), (16, 1)])
+@pytest.mark.parametrize("reqs", range(len(REQS)))
+def test_paged(torch, dtype, heads, reqs):
+    H, Hkv = heads
+    page = [16, 8, 64, 256, 32, 128, 1024][(reqs + H) % 7]
+    p = paged_problem(torch, REQS[reqs], H, Hkv, page, getattr(torch, dtype), 100 * reqs + H,
+                      ["pages", "rows", "both"][(reqs + H) % 3], pad=(reqs % 3) * 2)
+    q, kc, vc, table, cu, lens, _ = p
+    if q.shape[0] == 0:
+        q = rnd(torch, (3, H, 64), q.dtype, 1)
+    o, L = run_paged(torch, q, kc, vc, table, cu, lens, lse=reqs % 2 == 0)
+    check_paged(torch, q, kc, vc, table, cu, lens, o, L)
+
+
+@pytest.mark.parametrize("heads", [(128, 1), (100, 1), (40, 2), (17, 1), (33, 1)])
+@pytest.mark.parametrize("new", [1, 2, 9])
+def test_paged_wide_groups(torch, heads, new):
+    p = paged_problem(torch, [(500, new), (13, new), (1, 1)], heads[0], heads[1], 16,
+                      torch.float16, 3)
+    q, kc, vc, table, cu, lens, _ = p
+    o, L = run_paged(torch, q, kc, vc, table, cu, lens)
+    check_paged(torch, q, kc, vc, table, cu, lens, o, L)
+
+
+@pytest.mark.parametrize("bound", [1, 4, 40, 1000])
+def test_paged_whatever_the_bound_on_new_tokens(torch, bound):
+    """max_new is a bound: any value at or above the truth gives the answer."""
+    p = paged_problem(torch, [(900, 1), (33, 1), (1, 1)], 8, 2, 32, torch.bfloat16, 4)
+    q, kc, vc, table, cu, lens, _ = p
+    o, L = run_paged(torch, q, kc, vc, table, cu, lens, max_new=bound)
+    check_paged(torch, q, kc, vc, table, cu, lens, o, L)
+
+
+@pytest.mark.parametrize("new", [2, 5, 64, 150])
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (8, 2)])
+def test_paged_bad_values_stay_where_they_are_seen(torch, new, H, Hkv):
+    """A NaN among the new tokens' keys does not reach the rows before it."""
+    p = paged_problem(torch, [(300, new), (new, new), (260, 1)], H, Hkv, 16, torch.float16, 5,
+                      stale=math.inf)
+    q, kc, vc, table, cu, lens, _ = p
+    for req, back in ((0, 1), (1, new // 2)):
+        pos = lens[req] - max(1, back)
+        pg = table[req][pos // 16]
+        vc[pg, 0, pos % 16, 7] = NAN
+        vc[pg, 1, pos % 16, 9] = math.inf
+    pos = lens[0] - new // 2 - 1
+    kc[table[0][pos // 16], 1, pos % 16, 3] = NAN
+    o, L = run_paged(torch, q, kc, vc, table, cu, lens)
+    check_paged(torch, q, kc, vc, table, cu, lens, o, L)
+
+
+def test_paged_is_deterministic(torch):
+    reqs = [(random.Random(i).randint(1, 3000), 1 + (i % 7 == 0) * 40) for i in range(60)]
+    q, kc, vc, table, cu, lens, _ = paged_problem(torch, reqs, 8, 2, 16, torch.float16, 6)
+    o, L = run_paged(torch, q, kc, vc, table, cu, lens)
+    for _ in range(3):
+        o2, L2 = run_paged(torch, q, kc, vc, table, cu, lens)
+        assert torch.equal(o, o2) and torch.equal(L, L2)
+
+
+def test_paged_strided_output_and_queries(torch):
+    q, kc, vc, table, cu, lens, _ = paged_problem(torch, [(90, 3), (700, 20), (5, 1)], 8, 2, 16,
+                                                  torch.bfloat16, 7)
+    t = q.shape[0]
+    wide = torch.zeros((t, 12, 64), dtype=q.dtype, device="cuda")
+    wide[:, 2:10] = q
+    o = torch.full((8, t, 64), SENTINEL, dtype=q.dtype, device="cuda").permute(1, 0, 2)
+    o, L = run_paged(torch, wide[:, 2:10], kc, vc, table, cu, lens, o=o)
+    check_paged(torch, q, kc, vc, table, cu, lens, o, L)
+
+
+# ------------------------------------------------------------- plan and store
+def run_plan(torch, cached, fresh, ring, state, table, tokens, page, width):
+    from causal_streaming_softmax_gb300 import api
+    B, N = len(cached), len(ring)
+    s = api.PagedShape(B, tokens, 1, 1, page, N, width)
+    out = {n: torch.full((k,), -99, dtype=torch.int32, device="cuda")
+           for n, k in (("cu", B + 1), ("lens", B), ("slots", tokens), ("next", 4))}
+    ring, table = i32(torch, ring), i32(torch, table)
+    api.attn_paged_plan(s, i32(torch, cached), i32(torch, fresh), ring, i32(torch, state), table,
+                        out["cu"], out["lens"], out["slots"], out["next"])
+    return [out["cu"].tolist(), out["lens"].tolist(), out["slots"].tolist(), ring.tolist(),
+            table.tolist(), out["next"].tolist()]
+
+
+@pytest.mark.parametrize("B,page,hi,new", [(1, 16, 100, 1), (1, 8, 0, 5000), (7, 16, 300, 90),
+                                           (64, 16, 900, 1), (513, 32, 200, 30),
+                                           (4096, 8, 40, 9), (33, 1024, 3000, 2000)])
+@pytest.mark.parametrize("trouble", ["", "pages", "width", "tokens", "state", "negative", "full"])
+def test_plan(torch, B, page, hi, new, trouble):
+    r = random.Random(B + page)
+    cached = [r.randint(0, hi) for _ in range(B)]
+    fresh = [r.choice([-1, 0, 1, r.randint(0, new)]) for _ in range(B)]
+    up = lambda x: -(-x // page)
+    width = max(1, max(up(c + max(0, f)) for c, f in zip(cached, fresh)))
+    held = sum(up(c) for c in cached)
+    need = sum(up(c + f) - up(c) for c, f in zip(cached, fresh) if f > 0)
+    total = sum(max(0, f) for f in fresh)
+    if trouble in ("", "pages", "full"):
+        spare = {"": 3, "pages": -1, "full": 0}[trouble]
+    else:
+        spare = 3
+    if trouble == "pages" and need == 0:
+        pytest.skip("needs no page")
+    N = max(1, held + need + max(0, spare) if trouble != "pages" else held + need)
+    order = list(range(N))
+    r.shuffle(order)
+    table = []
+    for c in cached:
+        table.append([order.pop() for _ in range(up(c))] + [-1] * (width - up(c)))
+    free = need - 1 if trouble == "pages" else len(order)
+    head = r.randrange(N)
+    ring = [-5] * N
+    for x, p in enumerate(order[:free]):
+        ring[(head + x) % N] = p
+    tokens = total + r.choice([0, 5])
+    if trouble == "width":
+        cached[B // 2], fresh[B // 2] = width * page, 1
+    if trouble == "tokens":
+        fresh[-1], tokens = max(1, fresh[-1]), 0
+    if trouble == "state":
+        head = N
+    if trouble == "negative":
+        cached[0] = -3
+    want = plan_host(cached, fresh, ring, [head, free], table, tokens, page, width)
+    assert (want[5][3] != 0) == (trouble not in ("", "full"))
+    got = run_plan(torch, cached, fresh, ring, [head, free, 0, 0], table, tokens, page, width)
+    for name, g, w in zip(("cu", "lens", "slots", "ring", "table", "next"), got, want):
+        assert g == list(w), name
+
+
+def test_plan_reports_a_page_that_does_not_exist(torch):
+    from causal_streaming_softmax_gb300 import api
+    got = run_plan(torch, [0, 3], [5, 1], [99, -4, 2, 3], [0, 4, 0, 0], [[-1] * 4, [7, 0, 0, 0]],
+                   6, 8, 4)
+    assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX
+    assert got[2] == [-1] * 6
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("Hkv,page,n", [(1, 16, 1), (8, 16, 64), (5, 32, 999), (3, 8, 5000),
+                                        (16, 256, 300)])
+@pytest.mark.parametrize("layout", ["pages", "rows"])
+def test_store(torch, dtype, Hkv, page, n, layout):
+    from causal_streaming_softmax_gb300 import api
+    dt = getattr(torch, dtype)
+    pages = -(-n // page) + 4
+    g = torch.Generator().manual_seed(n)
+    slots = torch.randperm(pages * page, generator=g)[:n].to(torch.int32)
+    slots[::7] = -1
+    slots = slots.cuda()
+    kv = rnd(torch, (n, 2 * Hkv, 64), dt, n)
+    kv[0] = NAN
+    k, v = kv[:, :Hkv], kv[:, Hkv:]
+    pools = []
+    for i in range(2):
+        x = rnd(torch, (pages, Hkv, page, 64), dt, 70 + i)
+        if layout == "rows":
+            x = x.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+        pools.append(x)
+    want = [x.clone() for x in pools]
+    live = slots >= 0
+    at = slots[live].long()
+    for w, x in zip(want, (k, v)):
+        w[at // page, :, at % page] = x[live]
+    s = api.PagedShape(1, n, Hkv, Hkv, page, pages, 1, dtype=dt)
+    api.attn_paged_store(s, k, v, slots, *pools)
+    for w, x in zip(want, pools):
+        assert torch.equal(w.view(torch.int16), x.contiguous().view(torch.int16).view(w.shape))
+
+
+def test_store_skips_and_reports_a_slot_past_the_pool(torch):
+    from causal_streaming_softmax_gb300 import api
+    k = rnd(torch, (3, 1, 64), torch.float16, 1)
+    kc = torch.zeros((2, 1, 8, 64), dtype=torch.float16, device="cuda")
+    vc = torch.zeros_like(kc)
+    s = api.PagedShape(1, 3, 1, 1, 8, 2, 1)
+    api.attn_paged_store(s, k, k, i32(torch, [16, 2 ** 31 - 1, 9]), kc, vc)
+    assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX
+    assert torch.equal(kc[1, 0, 1], k[2, 0]) and int((kc != 0).any(-1).sum()) == 1
+
+
+# --------------------------------------------------- device arrays that lie
+def test_bad_offsets_are_reported(torch):
+    from causal_streaming_softmax_gb300 import api
+    q, k, v = packed_inputs(torch, 50, 4, 2, torch.float16, 1)
+    for cu in ([0, 60], [0, 2 ** 31 - 1], [-5, 50], [0, 30, 20, 50]):
+        run_packed(torch, q, k, v, cu)
+        assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX, cu
+
+
+def test_bad_pages_are_reported(torch):
+    """A page id outside the pool, a length past the table, offsets past the
+    rows: reported, the other requests right."""
+    from causal_streaming_softmax_gb300 import api
+    for new in (1, 40):
+        q, kc, vc, table, cu, lens, width = paged_problem(
+            torch, [(200, new), (500, new), (100, new)], 8, 2, 16, torch.float16, 2)
+        for bad in (-1, kc.shape[0], 2 ** 31 - 1, -2 ** 31):
+            tab = [list(r) for r in table]
+            tab[1][3] = bad
+            o, L = run_paged(torch, q, kc, vc, tab, cu, lens)
+            assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX
+            tt = torch.tensor(table, device="cuda")
+            for i in (0, 2):
+                r = paged64(q, kc, vc, tt, cu, lens)[i]
+                check(o[r[0]], r[1], r[3], "request %d" % i)
+        for bad in (16 * width + 1, 2 ** 31 - 1, -1):
+            run_paged(torch, q, kc, vc, [[0] * width] * 3, cu, [200, bad, 100])
+            assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX
+        run_paged(torch, q, kc, vc, table, [0, new, 2 * new, 3 * new + 1], lens, max_new=new + 1)
+        assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX
+
+
+def test_more_new_tokens_than_the_bound_are_reported(torch):
+    from causal_streaming_softmax_gb300 import api
+    q, kc, vc, table, cu, lens, _ = paged_problem(torch, [(200, 40), (500, 1)], 8, 2, 16,
+                                                  torch.float16, 2)
+    run_paged(torch, q, kc, vc, table, cu, lens, max_new=1)
+    assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX
+
+
+# ------------------------------------------------------------------- together
+def serve(torch, steps, graph=None):
+    """A small server: requests come, grow by chunks and tokens, and finish.
+    Returns every row's output beside the row's request and position."""
+    from causal_streaming_softmax_gb300 import api
+    H, Hkv, B, page = 8, 2, 5, 16
+    cache = api.PagedCache(B, H, Hkv, num_pages=90, page_size=page, table_width=40)
+    r = random.Random(11)
+    hist = [[] for _ in range(B)]
+    for step in range(steps):
+        fresh = [r.choice([1, 1, 1, r.randint(0, 70), -1 if len(hist[i]) > 150 else 1])
+                 for i in range(B)]
+        n = sum(max(0, f) for f in fresh)
+        q, k, v = packed_inputs(torch, n, H, Hkv, torch.float16, 1000 + step)
+        o = torch.empty((n, H, 64), dtype=torch.float16, device="cuda")
+        L = torch.empty((H, n), device="cuda")
+        cache.step(i32(torch, fresh), q, k, v, o, L, max_new=max(max(fresh), 1))
+        at = 0
+        for i, f in enumerate(fresh):
+            if f < 0:
+                hist[i] = []
+                continue
+            hist[i] += [(k[at + x], v[at + x]) for x in range(f)]
+            m = len(hist[i])
+            if f:
+                ks = torch.stack([x[0] for x in hist[i]])
+                vs = torch.stack([x[1] for x in hist[i]])
+                seen = torch.arange(m - f + 1, m + 1, device="cuda")
+                eo, el, to, tl = attend64(q[at:at + f], ks, vs, seen)
+                check(o[at:at + f], eo, to, "step %d request %d" % (step, i))
+                check(L[:, at:at + f], el, tl, "L of step %d request %d" % (step, i))
+            at += f
+        assert cache.status() == 0
+        assert cache.lens.tolist() == [len(h) for h in hist]
+        assert cache.free_pages() == 90 - sum(-(-len(h) // page) for h in hist)
+
+
+def test_a_server_of_several_steps(torch):
+    serve(torch, 25)
+
+
+def test_prompt_through_the_cache_equals_the_packed_prompt(torch):
+    """A prompt in chunks over the cache gives what attn_packed_fwd gives."""
+    from causal_streaming_softmax_gb300 import api
+    H, Hkv, n = 8, 2, 700
+    q, k, v = packed_inputs(torch, n, H, Hkv, torch.bfloat16, 12)
+    o, L = run_packed(torch, q, k, v, [0, n])
+    _, _, to, tl = attend64(q, k, v, torch.arange(1, n + 1, device="cuda"))
+    cache = api.PagedCache(1, H, Hkv, num_pages=50, dtype=torch.bfloat16)
+    at = 0
+    for c in (1, 3, 200, 1, 129, 366):
+        o2 = torch.empty((c, H, 64), dtype=q.dtype, device="cuda")
+        L2 = torch.empty((H, c), device="cuda")
+        cache.step(i32(torch, [c]), q[at:at + c], k[at:at + c], v[at:at + c], o2, L2, max_new=c)
+        check(o2, o[at:at + c].double(), 2 * to[at:at + c], "chunk at %d" % at)
+        check(L2, L[:, at:at + c].double(), 2 * tl[:, at:at + c], "L of chunk at %d" % at)
+        at += c
+
+
+def test_a_refused_step_leaves_everything(torch):
+    from causal_streaming_softmax_gb300 import api
+    cache = api.PagedCache(2, 4, 2, num_pages=4)
+    q, k, v = packed_inputs(torch, 70, 4, 2, torch.float16, 1)
+    o = torch.full((70, 4, 64), SENTINEL, dtype=torch.float16, device="cuda")
+    cache.step(i32(torch, [60, 10]), q, k, v, o)
+    assert cache.status() == api.PLAN_PAGES and cache.free_pages() == 4
+    assert (o == SENTINEL).all() and (cache.k == 0).all() and cache.lens.tolist() == [0, 0]
+    cache.step(i32(torch, [40, 10]), q[:50], k[:50], v[:50], o[:50])
+    assert cache.status() == 0 and cache.free_pages() == 0
+
+
+def test_captured_steps_replay(torch):
+    """Two token steps captured into a graph and replayed, on a stream of
+    their own: the tokens go on, the plan, store and attention follow."""
+    from causal_streaming_softmax_gb300 import api
+    H, Hkv, B = 8, 2, 3
+    cache = api.PagedCache(B, H, Hkv, num_pages=60)
+    plen = [37, 5, 130]
+    q, k, v = packed_inputs(torch, sum(plen), H, Hkv, torch.float16, 20)
+    o = torch.empty((sum(plen), H, 64), dtype=torch.float16, device="cuda")
+    cache.step(i32(torch, plen), q, k, v, o, max_new=130)
+    cu = scan(plen)
+    hist = [[(k[j], v[j]) for j in range(a, b)] for a, b in zip(cu, cu[1:])]
+    one = i32(torch, [1] * B)
+    buf = [[x.clone() for x in packed_inputs(torch, B, H, Hkv, torch.float16, 21)]
+           + [torch.empty((B, H, 64), dtype=torch.float16, device="cuda")] for _ in range(2)]
+    # a warm-up pair of steps outside the graph
+    for qs, ks, vs, out in buf:
+        cache.step(one, qs, ks, vs, out, max_new=1)
+        for i in range(B):
+            hist[i].append((ks[i].clone(), vs[i].clone()))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        for qs, ks, vs, out in buf:
+            cache.step(one, qs, ks, vs, out, max_new=1)
+    for rep in range(40):
+        for s, b in enumerate(buf):
+            for x, y in zip(b, packed_inputs(torch, B, H, Hkv, torch.float16, 100 + 2 * rep + s)):
+                x.copy_(y)
+        g.replay()
+        torch.cuda.synchronize()
+        for qs, ks, vs, out in buf:
+            for i in range(B):
+                hist[i].append((ks[i].clone(), vs[i].clone()))
+        if rep % 13 == 0:
+            qs, ks, vs, out = buf[1]
+            for i in range(B):
+                kk, vv = (torch.stack([h[j] for h in hist[i]]) for j in (0, 1))
+                seen = torch.tensor([len(hist[i])], device="cuda")
+                eo, _, to, _ = attend64(qs[i:i + 1], kk, vv, seen)
+                check(out[i:i + 1], eo, to, "replay %d request %d" % (rep, i))
+    assert cache.lens.tolist() == [len(h) for h in hist] and cache.status() == 0
+
+
+def test_calls_on_two_streams(torch):
+    """The same problem on two streams at once, each with its own workspace."""
+    q, kc, vc, table, cu, lens, _ = paged_problem(torch, [(3000, 1), (40, 1)] * 8, 8, 2, 16,
+                                                  torch.float16, 9)
+    o, L = run_paged(torch, q, kc, vc, table, cu, lens)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append([run_paged(torch, q, kc, vc, table, cu, lens) for _ in range(5)])
+    torch.cuda.synchronize()
+    for per in got:
+        for o2, L2 in per:
+            assert torch.equal(o, o2) and torch.equal(L, L2)
+
+
+def test_pool_beyond_32_bits(torch):
+    """Element offsets past 2^32 in the pools."""
+    from causal_streaming_softmax_gb300 import api
+    H, Hkv, page = 8, 4, 1024
+    pages = (1 << 32) // (Hkv * page * 64) + 3  # 8.6 GB a pool
+    kc = torch.zeros((pages, Hkv, page, 64), dtype=torch.float16, device="cuda")
+    vc = torch.zeros_like(kc)
+    table = [[pages - 1, 0, pages - 2]]
+    n = 2500
+    k, v = (rnd(torch, (n, Hkv, 64), torch.float16, i) for i in (1, 2))
+    slots = torch.tensor([table[0][p // page] * page + p % page for p in range(n)],
+                         dtype=torch.int32, device="cuda")
+    s = api.PagedShape(1, n, H, Hkv, page, pages, 3)
+    api.attn_paged_store(s, k, v, slots, kc, vc)
+    assert torch.equal(gather(kc, torch.tensor(table[0], device="cuda"), n), k)
+    for new in (1, 100):
+        q = rnd(torch, (new, H, 64), torch.float16, 3, 2.0)
+        o, L = run_paged(torch, q, kc, vc, table, [0, new], [n])
+        check_paged(torch, q, kc, vc, table, [0, new], [n], o, L)

@@ -1,0 +1,320 @@
+"""The packed and paged calls without a GPU: refusals on the host before any
+launch, and the index arithmetic that keeps device accesses inside the tensors
+whatever the device arrays hold."""
+import ctypes
+import itertools
+import os
+import random
+import subprocess
+
+import pytest
+import torch
+
+import serve_util
+from causal_streaming_softmax_gb300 import api, build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return api.load_library()
+
+
+def packed(**kw):
+    base = dict(tokens=100, batch=3, heads=4, kv_heads=2, head_dim=64, causal=1, dtype=0,
+                scale=0.125, q_token=256, q_head=64, k_token=128, k_head=64, v_token=128,
+                v_head=64, o_token=256, o_head=64)
+    base.update(kw)
+    return api.AttnPackedShape(**base)
+
+
+def paged(**kw):
+    base = dict(batch=3, tokens=10, heads=4, kv_heads=2, head_dim=64, page_size=16, num_pages=50,
+                table_width=8, max_new=4, dtype=1, scale=0.125, q_token=256, q_head=64,
+                o_token=256, o_head=64, k_token=128, k_head=64, v_token=128, v_head=64,
+                kc_page=2048, kc_head=1024, kc_row=64, vc_page=2048, vc_head=1024, vc_row=64)
+    base.update(kw)
+    return api.AttnPagedShape(**base)
+
+
+def fwd(lib, s, q=P, k=P, v=P, cu=P, o=P, lse=None):
+    return lib.attn_packed_fwd(None if s is None else ctypes.byref(s), q, k, v, cu, o, lse, None)
+
+
+def pfwd(lib, s, q=P, k=P, v=P, table=P, cu=P, lens=P, ws=P, n=1 << 40, o=P, lse=None):
+    return lib.attn_paged_fwd(None if s is None else ctypes.byref(s), q, k, v, table, cu, lens,
+                              ws, n, o, lse, None)
+
+
+BAD_PACKED = [
+    dict(tokens=-1), dict(tokens=(1 << 30) + 1), dict(batch=0), dict(batch=65536), dict(heads=3),
+    dict(heads=0), dict(kv_heads=0), dict(heads=258, kv_heads=2), dict(head_dim=128),
+    dict(causal=2), dict(dtype=2), dict(dtype=-1), dict(scale=0.0), dict(scale=float("nan")),
+    dict(scale=float("inf")), dict(scale=-1.0), dict(q_token=0), dict(k_head=0), dict(v_token=60),
+    dict(q_head=68), dict(k_token=-256), dict(o_head=1 << 38),
+    dict(o_token=64), dict(o_token=192), dict(o_token=64, o_head=99 * 64),
+]
+
+
+@pytest.mark.parametrize("kw", BAD_PACKED)
+def test_packed_shape_refused(lib, kw):
+    assert fwd(lib, packed(**kw)) == api.ATTN_ERR_SHAPE
+
+
+def test_packed_pointers_refused(lib):
+    assert fwd(lib, None) == api.ATTN_ERR_NULL
+    s = packed()
+    for name in ("q", "k", "v", "cu", "o"):
+        assert fwd(lib, s, **{name: None}) == api.ATTN_ERR_NULL, name
+        assert fwd(lib, s, **{name: P + 2}) == api.ATTN_ERR_ALIGN, name
+    assert fwd(lib, s, lse=P + 4) == api.ATTN_ERR_ALIGN
+    # nothing to do: no pointer is looked at
+    assert fwd(lib, packed(tokens=0), None, None, None, None, None) == api.ATTN_OK
+    # the stride of a dimension of one is not read
+    assert fwd(lib, packed(tokens=1, q_token=3, o_token=0), cu=None) == api.ATTN_ERR_NULL
+
+
+BAD_PAGED = [
+    dict(batch=0), dict(batch=4097), dict(tokens=-1), dict(page_size=4), dict(page_size=2048),
+    dict(page_size=24), dict(page_size=0), dict(num_pages=0), dict(num_pages=1 << 27),
+    dict(table_width=0), dict(table_width=1 << 27),
+]
+BAD_ATTEND = BAD_PAGED + [
+    dict(heads=5), dict(kv_heads=0), dict(head_dim=32), dict(dtype=7), dict(scale=0.0),
+    dict(max_new=0), dict(heads=129, kv_heads=1), dict(q_token=8), dict(o_token=64),
+    dict(kc_page=0), dict(kc_row=65), dict(vc_head=-1024), dict(vc_row=32),
+]
+
+
+@pytest.mark.parametrize("kw", BAD_ATTEND)
+def test_paged_shape_refused(lib, kw):
+    assert pfwd(lib, paged(**kw)) == api.ATTN_ERR_SHAPE
+    if not set(kw) & {"q_token", "o_token", "kc_page", "kc_row", "vc_head", "vc_row"}:
+        s = paged(**kw)
+        assert lib.attn_paged_workspace_bytes(ctypes.byref(s)) == 0
+
+
+def test_paged_pointers_refused(lib):
+    assert pfwd(lib, None) == api.ATTN_ERR_NULL
+    s = paged()
+    for name in ("q", "k", "v", "table", "cu", "lens", "ws", "o"):
+        assert pfwd(lib, s, **{name: None}) == api.ATTN_ERR_NULL, name
+        assert pfwd(lib, s, **{name: P + 2}) == api.ATTN_ERR_ALIGN, name
+    need = lib.attn_paged_workspace_bytes(ctypes.byref(s))
+    assert need > 0
+    assert pfwd(lib, s, n=need - 1) == api.ATTN_ERR_WORKSPACE
+    assert pfwd(lib, paged(tokens=0), *[None] * 7, 0, None) == api.ATTN_OK
+
+
+def plan_args():
+    return [P + 4096 * i for i in range(9)]
+
+
+def plan(lib, s, args):
+    return lib.attn_paged_plan(None if s is None else ctypes.byref(s), *args, None)
+
+
+@pytest.mark.parametrize("kw", BAD_PAGED)
+def test_plan_shape_refused(lib, kw):
+    assert plan(lib, paged(**kw), plan_args()) == api.ATTN_ERR_SHAPE
+
+
+def test_plan_pointers_refused(lib):
+    assert plan(lib, None, plan_args()) == api.ATTN_ERR_NULL
+    for i in range(9):
+        a = plan_args()
+        a[i] = None
+        assert plan(lib, paged(), a) == api.ATTN_ERR_NULL, i
+        a[i] = P + 1 + 4096 * i
+        assert plan(lib, paged(), a) == api.ATTN_ERR_ALIGN, i
+    # cached, fresh, ring, state, table, cu, lens, slots, next: an output given twice
+    read_only = {0, 1, 3}
+    for i, j in itertools.combinations(range(9), 2):
+        if i in read_only and j in read_only:
+            continue
+        a = plan_args()
+        a[j] = a[i]
+        assert plan(lib, paged(), a) == api.ATTN_ERR_SHAPE, (i, j)
+
+
+def test_store_refused(lib):
+    def store(s, k=P, v=P, slots=P, kc=P, vc=P):
+        return lib.attn_paged_store(None if s is None else ctypes.byref(s), k, v, slots, kc, vc,
+                                    None)
+    assert store(None) == api.ATTN_ERR_NULL
+    for kw in BAD_PAGED + [dict(kv_heads=0), dict(dtype=3), dict(head_dim=32), dict(k_token=8),
+                           dict(v_head=0), dict(kc_row=0), dict(vc_page=100)]:
+        assert store(paged(**kw)) == api.ATTN_ERR_SHAPE, kw
+    for name in ("k", "v", "slots", "kc", "vc"):
+        assert store(paged(), **{name: None}) == api.ATTN_ERR_NULL, name
+        assert store(paged(), **{name: P + 2}) == api.ATTN_ERR_ALIGN, name
+    assert store(paged(tokens=0), None, None, None, None, None) == api.ATTN_OK
+
+
+def test_error_string(lib):
+    assert "outside its range" in api.error_string(api.ATTN_ERR_DEVICE_INDEX)
+
+
+def test_python_binding_refuses_cpu_tensors_and_types():
+    h = lambda *s: torch.zeros(*s, dtype=torch.float16)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    s = api.PackedShape(4, 1, 2, 1)
+    with pytest.raises(ValueError):
+        api.attn_packed_fwd(s, h(4, 2, 64), h(4, 1, 64), h(4, 1, 64), i(2), h(4, 2, 64))
+    with pytest.raises(TypeError):
+        api.attn_packed_fwd(s, h(4, 2, 64).float(), h(4, 1, 64), h(4, 1, 64), i(2), h(4, 2, 64))
+    with pytest.raises(TypeError):
+        api.attn_packed_fwd(s, None, h(4, 1, 64), h(4, 1, 64), i(2), h(4, 2, 64))
+    with pytest.raises(TypeError):
+        api.PagedShape(1, 1, 1, 1, 16, 4, 4, dtype=torch.float32).c_struct()
+    with pytest.raises(api.AttnError):
+        api.paged_workspace_bytes(api.PagedShape(1, 1, 3, 2, 16, 4, 4))
+    p = api.PagedShape(2, 4, 2, 1, 16, 4, 4)
+    with pytest.raises(ValueError):
+        api.attn_paged_plan(p, i(2), i(2), i(4), i(4), i(2, 4), i(3), i(2), i(4), i(4))
+
+
+# ------------------------------------------------------------ index arithmetic
+HARNESS = r"""
+#include <stdio.h>
+#include "serve_index.h"
+using namespace css;
+int main() {
+  int what;
+  while (scanf("%d", &what) == 1) {
+    if (what == 0) {
+      int a, b, t; scanf("%d %d %d", &a, &b, &t);
+      RowRange r = row_range(a, b, t);
+      printf("%d %d %d\n", r.begin, r.end, (int)r.bad);
+    } else if (what == 1) {
+      int n, x; static int32_t cu[1000]; scanf("%d %d", &n, &x);
+      for (int i = 0; i < n; ++i) scanf("%d", &cu[i]);
+      printf("%d\n", last_at_or_below(cu, n, x));
+    } else if (what == 2) {
+      int len, w, s; bool bad; scanf("%d %d %d", &len, &w, &s);
+      int k = key_count(len, w, s, &bad);
+      printf("%d %d\n", k, (int)bad);
+    } else if (what == 3) {
+      int h, n; long long x; scanf("%d %lld %d", &h, &x, &n);
+      printf("%d\n", ring_at(h, x, n));
+    } else if (what == 4) {
+      int c, f, w, s; scanf("%d %d %d %d", &c, &f, &w, &s);
+      PlanRow r = plan_row(c, f, w, s);
+      printf("%lld %lld %lld %lld %d\n", r.add, r.have, r.need, r.back, r.status);
+    } else {
+      int rows, head, fr, np, tok; long long add, need, back;
+      scanf("%d %lld %lld %lld %d %d %d %d", &rows, &add, &need, &back, &head, &fr, &np, &tok);
+      printf("%d\n", plan_status(rows, add, need, back, head, fr, np, tok));
+    }
+  }
+  return 0;
+}
+"""
+
+EXTREMES = [-2 ** 31, -2 ** 31 + 1, -7, -1, 0, 1, 5, 99, 100, 101, 2 ** 30, 2 ** 31 - 1]
+
+
+@pytest.fixture(scope="module")
+def harness(tmp_path_factory):
+    d = tmp_path_factory.mktemp("serve_index")
+    (d / "h.cpp").write_text(HARNESS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined",
+                    "-fno-sanitize-recover=undefined", "-I", build.CSRC, "-o", str(d / "h"),
+                    str(d / "h.cpp")], check=True)
+
+    def ask(lines):
+        r = subprocess.run([str(d / "h")], input="\n".join(lines), capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
+        return [[int(x) for x in ln.split()] for ln in r.stdout.splitlines()]
+    return ask
+
+
+def test_row_range_stays_inside(harness):
+    asks = [(a, b, t) for a in EXTREMES for b in EXTREMES for t in (0, 1, 100)]
+    for (a, b, t), (begin, end, bad) in zip(asks, harness("0 %d %d %d" % x for x in asks)):
+        assert 0 <= begin <= end <= t
+        assert bad == (not 0 <= a <= b <= t)
+        if not bad:
+            assert (begin, end) == (a, b)
+
+
+def test_bisection(harness):
+    r = random.Random(1)
+    asks = []
+    for _ in range(300):
+        n = r.randint(1, 40)
+        cu = sorted(r.randint(0, 50) for _ in range(n))
+        asks.append((cu, r.randint(-1, 60)))
+    for _ in range(200):  # any contents: the answer stays in range
+        asks.append(([r.choice(EXTREMES) for _ in range(r.randint(1, 40))], r.choice(EXTREMES)))
+    got = harness("1 %d %d %s" % (len(c), x, " ".join(map(str, c))) for c, x in asks)
+    for k, ((cu, x), (i,)) in enumerate(zip(asks, got)):
+        assert -1 <= i < len(cu)
+        if k < 300:
+            assert i == max((j for j, c in enumerate(cu) if c <= x), default=-1)
+
+
+def test_key_count_stays_in_the_table(harness):
+    asks = [(n, w, s) for n in EXTREMES for w, s in ((1, 3), (7, 4), ((1 << 27) - 1, 4),
+                                                     ((1 << 21) - 1, 10))]
+    for (n, w, s), (k, bad) in zip(asks, harness("2 %d %d %d" % x for x in asks)):
+        assert 0 <= k <= w << s
+        assert bad == (not 0 <= n <= w << s)
+        if not bad:
+            assert k == n
+
+
+def test_ring_positions(harness):
+    asks = [(h, x, n) for n in (1, 2, 7) for h in range(n) for x in range(n + 1)]
+    asks += [(2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31 - 1)]
+    for (h, x, n), (p,) in zip(asks, harness("3 %d %d %d" % a for a in asks)):
+        assert p == (h + x) % n
+
+
+def test_plan_rows_and_status(harness):
+    asks = [(c, f, w, s) for c in EXTREMES for f in EXTREMES for w, s in ((1, 3), (50, 4),
+                                                                          ((1 << 27) - 1, 4))]
+    up = lambda x, s: (x + (1 << s) - 1) >> s
+    for (c, f, w, s), (add, have, need, back, st) in zip(
+            asks, harness("4 %d %d %d %d" % a for a in asks)):
+        cc = max(c, 0)
+        assert add == max(f, 0) and have == up(cc, s)
+        assert need == (up(cc + f, s) - have if f >= 0 else 0) and need >= 0
+        assert back == (have if f < 0 else 0)
+        assert st == (8 if c < 0 else 0) + (2 if up(cc + max(f, 0), s) > w else 0)
+    big = 4096 * (2 ** 31 - 1)
+    cases = [((0, 5, 2, 0, 0, 2, 10, 5), 0), ((0, 5, 3, 0, 0, 2, 10, 5), 1),
+             ((0, 6, 2, 0, 0, 2, 10, 5), 4), ((2, 5, 2, 0, 0, 2, 10, 5), 2),
+             ((0, 5, 2, 0, -1, 2, 10, 5), 8), ((0, 5, 2, 0, 10, 2, 10, 5), 8),
+             ((0, 5, 2, 0, 0, 11, 10, 5), 8), ((0, 5, 0, 9, 0, 2, 10, 5), 8),
+             ((0, 5, 2, 8, 0, 2, 10, 5), 0), ((8, big, big, big, 5, 2, 10, 5), 13)]
+    got = harness("5 %s" % " ".join(map(str, a)) for a, _ in cases)
+    assert [g[0] for g in got] == [w for _, w in cases]
+
+
+def test_host_form_of_the_plan():
+    """The plan's plain form: pages are handed out once, come back, and every
+    slot is the place its table names."""
+    r = random.Random(3)
+    page, width, N, B = 8, 6, 40, 7
+    ring, state = list(range(N)), [0, N, 0, 0]
+    table, lens = [[-1] * width for _ in range(B)], [0] * B
+    for _ in range(200):
+        fresh = [r.choice([-1, 0, 1, 1, 1, r.randint(0, 12)]) for _ in range(B)]
+        cu, new, slots, ring, table, nxt = serve_util.plan_host(lens, fresh, ring, state, table,
+                                                                60, page, width)
+        if nxt[3]:
+            assert new == lens and set(slots) == {-1}
+            fresh = [-1] * B
+            cu, new, slots, ring, table, nxt = serve_util.plan_host(lens, fresh, ring, state,
+                                                                    table, 60, page, width)
+            assert nxt[3] == 0
+        lens, state = new, nxt
+        held = [table[i][x] for i in range(B) for x in range(-(-lens[i] // page))]
+        free = [ring[(state[0] + x) % N] for x in range(state[1])]
+        assert sorted(held + free) == list(range(N))
+        live = [s for s in slots if s >= 0]
+        assert len(set(live)) == len(live) == cu[-1]
