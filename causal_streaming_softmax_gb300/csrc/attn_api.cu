@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "attn_internal.h"
+#include "serve_internal.h"
 #include "sm103.cuh"
 
 namespace css {
@@ -142,6 +143,22 @@ bool encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1
   cuuint32_t estride[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides,
                   box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_4d(CUtensorMap* map, bool bf16, const void* base, uint64_t d1, uint64_t d2,
+                    uint64_t d3, uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b1, uint32_t b2,
+                    uint32_t b3) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {64, d1, d2, d3};
+  cuuint64_t strides[3] = {s1 * 2, s2 * 2, s3 * 2};
+  cuuint32_t box[4] = {64, b1, b2, b3};
+  cuuint32_t estride[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, estride,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

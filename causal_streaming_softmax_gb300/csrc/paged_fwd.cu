@@ -1,0 +1,103 @@
+// paged_fwd.cu - attn_paged_fwd: which kernels a call runs, its workspace, and
+// the kernel that joins the parts of split rows.
+#include <mutex>
+
+#include "serve_internal.h"
+#include "serve_parts.cuh"
+#include "sm103.cuh"
+
+namespace css {
+namespace {
+
+constexpr int kJoinThreads = 128;
+
+// One block a tail part: O = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m).
+template <bool BF16>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_kernel(const PartArgs p, const RowsArg o, float* lse, int tokens, int G) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = blockIdx.x;
+  const PartDesc d = p.desc[c];
+  const int c0 = (threadIdx.x & 7) * 8;
+  for (int row = threadIdx.x >> 3; row < d.rows; row += kJoinThreads / 8) {
+    float m = -INFINITY;
+    for (int b = c; b <= d.last; ++b) m = fmaxf(m, p.ml[part_row(p, b, b == c, row)].x);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
+#pragma unroll 4
+    for (int b = c; b <= d.last; ++b) {
+      const long long at = part_row(p, b, b == c, row);
+      const float2 ml = p.ml[at];
+      const float4* const s = reinterpret_cast<const float4*>(p.o + at * 64 + c0);
+      const float4 x = s[0], y = s[1];
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // no key of this part is seen
+      const float f = ex2_approx(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      acc[0] = fmaf(x.x, f, acc[0]);
+      acc[1] = fmaf(x.y, f, acc[1]);
+      acc[2] = fmaf(x.z, f, acc[2]);
+      acc[3] = fmaf(x.w, f, acc[3]);
+      acc[4] = fmaf(y.x, f, acc[4]);
+      acc[5] = fmaf(y.y, f, acc[5]);
+      acc[6] = fmaf(y.z, f, acc[6]);
+      acc[7] = fmaf(y.w, f, acc[7]);
+    }
+    write_row<BF16>(o, lse, tokens, d.q0 + row / G, d.kv * G + row % G, c0, acc, m, l);
+  }
+}
+
+int launch_join(const PagedDims& d, const PartArgs& part, int blocks, const RowsArg& o, float* lse,
+                cudaStream_t stream) {
+  return cuda_status(launch_dependent(d.bf16 ? join_kernel<true> : join_kernel<false>,
+                                      dim3(blocks), dim3(kJoinThreads), 0, stream, part, o, lse,
+                                      d.tokens, d.G));
+}
+
+// The largest grid of the split kernels on any device this library runs on:
+// the workspace's size must not depend on the current device.
+constexpr int kMaxSm = 160;
+
+}  // namespace
+
+int allow_smem(int which, const void* kernel, size_t bytes) {
+  static std::once_flag once[kSmemKernels][64];
+  static cudaError_t status[kSmemKernels][64];
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e);
+  std::call_once(once[which][dev & 63], [&] {
+    status[which][dev & 63] = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  });
+  return cuda_status(status[which][dev & 63]);
+}
+
+size_t paged_workspace_bytes(const PagedDims& d) {
+  (void)d;
+  const size_t blocks = 2 * kMaxSm;
+  return blocks * sizeof(PartDesc) + blocks * 2 * kDecodeRows * (64 * 4 + 8);
+}
+
+int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
+                     const PoolArg& vc, const int32_t* table, const int32_t* cu,
+                     const int32_t* lens, void* ws, const RowsArg& o, float* lse,
+                     cudaStream_t stream) {
+  const int ntok = decode_tokens(d.G);
+  int rc;
+  if (ntok > 0) {
+    const int blocks = 2 * (ctx.sm_count < kMaxSm ? ctx.sm_count : kMaxSm);
+    PartArgs part;
+    part.desc = static_cast<PartDesc*>(ws);
+    part.ml = reinterpret_cast<float2*>(part.desc + blocks);
+    part.o = reinterpret_cast<float*>(part.ml + (size_t)blocks * 2 * kDecodeRows);
+    part.rows = kDecodeRows;
+    part.min_tiles = 2;
+    rc = launch_paged_decode(d, ctx, q, kc, vc, table, cu, lens, part, blocks, o, lse, stream);
+    if (rc != ATTN_OK) return rc;
+    if ((rc = launch_join(d, part, blocks, o, lse, stream)) != ATTN_OK) return rc;
+  }
+  if (d.max_new > ntok) return launch_paged_rows(d, ctx, q, kc, vc, table, cu, lens, o, lse, ntok, stream);
+  return ATTN_OK;
+}
+
+}  // namespace css

@@ -23,6 +23,7 @@ struct AttendArgs {
   const int32_t *cu, *lens, *table;
   float* lse;
   uint32_t* err;
+  int skip;
 };
 
 template <bool BF16>
@@ -51,6 +52,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
   int n = 0;  // visible keys
   if (t >= rr.begin && t < rr.end) {
     if (a.paged) {
+      if (rr.end - rr.begin <= a.skip) return;
       bool b;
       const int len = key_count(a.lens[i], a.width, a.shift, &b);
       bad |= b;
@@ -158,19 +160,16 @@ int launch_packed_fwd(const PackedDims& d, const DevCtx& ctx, const RowsArg& q, 
                       cudaStream_t stream) {
   const AttendArgs a{d.tokens, d.batch, d.H, d.G, d.causal, 0, d.tokens, 1, 0, 0, d.c, q, o,
                      PoolArg{k.p, 0, k.h, k.t}, PoolArg{v.p, 0, v.h, v.t}, cu, nullptr, nullptr,
-                     lse, ctx.err};
+                     lse, ctx.err, 0};
   return launch(a, d.bf16, stream);
 }
 
-size_t paged_workspace_bytes(const PagedDims& d) { return 16; }
-
-int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
+int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
                      const PoolArg& vc, const int32_t* table, const int32_t* cu,
-                     const int32_t* lens, void* ws, const RowsArg& o, float* lse,
+                     const int32_t* lens, const RowsArg& o, float* lse, int skip,
                      cudaStream_t stream) {
-  (void)ws;
   const AttendArgs a{d.tokens, d.batch, d.H, d.G, 1, 1, d.max_new, d.pages, d.width, d.shift, d.c, q, o, kc,
-                     vc, cu, lens, table, lse, ctx.err};
+                     vc, cu, lens, table, lse, ctx.err, skip};
   return launch(a, d.bf16, stream);
 }
 

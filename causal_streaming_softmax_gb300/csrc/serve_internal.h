@@ -29,6 +29,42 @@ struct PagedDims {
   float c;
 };
 
+// The parts of rows whose keys were split over blocks (serve_parts.cuh).
+struct PartDesc {  // of a block's tail part: what it is and the block that ends it
+  int q0, kv, rows, last;
+};
+struct PartArgs {
+  float* o;    // [block][head, tail][rows][64]
+  float2* ml;  // [block][head, tail][rows]
+  PartDesc* desc;
+  int rows;       // rows a part has room for
+  int min_tiles;  // a block takes at least so many tiles
+};
+
+// Rows (new tokens x heads of a group) of a request that paged_decode takes,
+// and the new tokens that makes for a group of G heads (0: none).
+constexpr int kDecodeRows = 16;
+int decode_tokens(int G);
+int launch_paged_decode(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
+                        const PoolArg& kc, const PoolArg& vc, const int32_t* table,
+                        const int32_t* cu, const int32_t* lens, const PartArgs& part, int blocks,
+                        const RowsArg& o, float* lse, cudaStream_t stream);
+int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
+                     const PoolArg& vc, const int32_t* table, const int32_t* cu,
+                     const int32_t* lens, const RowsArg& o, float* lse, int skip,
+                     cudaStream_t stream);
+
+// Lets `kernel` (known by an index of its own) use `bytes` of dynamic shared
+// memory on the current device; set once a device.
+enum { kSmemDecodeF16, kSmemDecodeBf16, kSmemKernels };
+int allow_smem(int which, const void* kernel, size_t bytes);
+
+// A rank-4 tiled tensor map of 64-wide 16-bit rows with the 128-byte swizzle:
+// dimensions 64, d1, d2, d3, strides in elements, boxes 64 x b1 x b2 x b3.
+bool encode_tmap_4d(CUtensorMap* map, bool bf16, const void* base, uint64_t d1, uint64_t d2,
+                    uint64_t d3, uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b1, uint32_t b2,
+                    uint32_t b3);
+
 int launch_packed_fwd(const PackedDims& d, const DevCtx& ctx, const RowsArg& q, const RowsArg& k,
                       const RowsArg& v, const int32_t* cu, const RowsArg& o, float* lse,
                       cudaStream_t stream);
