@@ -72,10 +72,29 @@ int allow_smem(int which, const void* kernel, size_t bytes) {
   return cuda_status(status[which][dev & 63]);
 }
 
+namespace {
+
+// A workspace of parts for `blocks` blocks of `rows` rows; 16-byte aligned.
+constexpr size_t parts_bytes(size_t blocks, size_t rows) {
+  return blocks * sizeof(PartDesc) + blocks * 2 * rows * (64 * 4 + 8);
+}
+
+PartArgs parts_at(void* ws, size_t blocks, int rows, int min_tiles) {
+  PartArgs p;
+  p.desc = static_cast<PartDesc*>(ws);
+  p.o = reinterpret_cast<float*>(p.desc + blocks);
+  p.ml = reinterpret_cast<float2*>(p.o + blocks * 2 * rows * 64);
+  p.rows = rows;
+  p.min_tiles = min_tiles;
+  return p;
+}
+
+}  // namespace
+
 size_t paged_workspace_bytes(const PagedDims& d) {
-  (void)d;
-  const size_t blocks = 2 * kMaxSm;
-  return blocks * sizeof(PartDesc) + blocks * 2 * kDecodeRows * (64 * 4 + 8);
+  const int ntok = decode_tokens(d.G);
+  return (ntok > 0 ? parts_bytes(2 * kMaxSm, kDecodeRows) : 0) +
+         (d.max_new > ntok ? parts_bytes(kMaxSm, kItemRows) : 0);
 }
 
 int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
@@ -83,20 +102,23 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
                      const int32_t* lens, void* ws, const RowsArg& o, float* lse,
                      cudaStream_t stream) {
   const int ntok = decode_tokens(d.G);
+  const int sms = ctx.sm_count < kMaxSm ? ctx.sm_count : kMaxSm;
+  uint8_t* at = static_cast<uint8_t*>(ws);
   int rc;
   if (ntok > 0) {
-    const int blocks = 2 * (ctx.sm_count < kMaxSm ? ctx.sm_count : kMaxSm);
-    PartArgs part;
-    part.desc = static_cast<PartDesc*>(ws);
-    part.ml = reinterpret_cast<float2*>(part.desc + blocks);
-    part.o = reinterpret_cast<float*>(part.ml + (size_t)blocks * 2 * kDecodeRows);
-    part.rows = kDecodeRows;
-    part.min_tiles = 2;
+    const int blocks = 2 * sms;
+    const PartArgs part = parts_at(at, 2 * kMaxSm, kDecodeRows, 2);
+    at += parts_bytes(2 * kMaxSm, kDecodeRows);
     rc = launch_paged_decode(d, ctx, q, kc, vc, table, cu, lens, part, blocks, o, lse, stream);
     if (rc != ATTN_OK) return rc;
     if ((rc = launch_join(d, part, blocks, o, lse, stream)) != ATTN_OK) return rc;
   }
-  if (d.max_new > ntok) return launch_paged_rows(d, ctx, q, kc, vc, table, cu, lens, o, lse, ntok, stream);
+  if (d.max_new > ntok) {
+    const PartArgs part = parts_at(at, kMaxSm, kItemRows, 2);
+    rc = launch_paged_rows(d, ctx, q, kc, vc, table, cu, lens, part, sms, ntok, o, lse, stream);
+    if (rc != ATTN_OK) return rc;
+    if ((rc = launch_join(d, part, sms, o, lse, stream)) != ATTN_OK) return rc;
+  }
   return ATTN_OK;
 }
 

@@ -44,19 +44,29 @@ struct PartArgs {
 // Rows (new tokens x heads of a group) of a request that paged_decode takes,
 // and the new tokens that makes for a group of G heads (0: none).
 constexpr int kDecodeRows = 16;
+// Rows of a work item of the tile kernel: two tiles.
+constexpr int kItemRows = 256;
 int decode_tokens(int G);
 int launch_paged_decode(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
                         const PoolArg& kc, const PoolArg& vc, const int32_t* table,
                         const int32_t* cu, const int32_t* lens, const PartArgs& part, int blocks,
                         const RowsArg& o, float* lse, cudaStream_t stream);
 int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
-                     const PoolArg& vc, const int32_t* table, const int32_t* cu,
-                     const int32_t* lens, const RowsArg& o, float* lse, int skip,
-                     cudaStream_t stream);
+                      const PoolArg& vc, const int32_t* table, const int32_t* cu,
+                      const int32_t* lens, const PartArgs& part, int blocks, int skip,
+                      const RowsArg& o, float* lse, cudaStream_t stream);
 
 // Lets `kernel` (known by an index of its own) use `bytes` of dynamic shared
 // memory on the current device; set once a device.
-enum { kSmemDecodeF16, kSmemDecodeBf16, kSmemKernels };
+enum {
+  kSmemDecodeF16,
+  kSmemDecodeBf16,
+  kSmemPackedF16,
+  kSmemPackedBf16,
+  kSmemRowsF16,
+  kSmemRowsBf16,
+  kSmemKernels
+};
 int allow_smem(int which, const void* kernel, size_t bytes);
 
 // A rank-4 tiled tensor map of 64-wide 16-bit rows with the 128-byte swizzle:
