@@ -44,8 +44,8 @@ struct PartArgs {
 // Rows (new tokens x heads of a group) of a request that paged_decode takes,
 // and the new tokens that makes for a group of G heads (0: none).
 constexpr int kDecodeRows = 16;
-// Rows of a work item of the tile kernel: two tiles.
-constexpr int kItemRows = 256;
+// Rows of a work item of the tile kernel: three tiles.
+constexpr int kItemRows = 384;
 int decode_tokens(int G);
 int launch_paged_decode(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
                         const PoolArg& kc, const PoolArg& vc, const int32_t* table,

@@ -12,26 +12,30 @@
 // Rows: a row tile of 128 holds tpt = 128 / G tokens times the G query heads
 // of one K/V head (row = token * G + head), so that a group's heads share
 // every K and V tile and a short chunk still fills the rows.  A work item is
-// two such tiles, A and B, one behind the other, that share K/V tiles of 128
-// keys.  Packed prompts cut the token axis into windows of 2 tpt tokens
-// whatever sequences lie in them, each row with its own interval of keys
-// [lo, hi): many short sequences share a tile, and no table of blocks is
-// needed.  Paged chunks cut each request's new tokens, and the list of their
-// key tiles is shared out over the blocks in equal runs (serve_parts.cuh).
+// three such tiles, one behind the other, that share K/V tiles of 64 keys.
+// Packed prompts cut the token axis into windows of 3 tpt tokens whatever
+// sequences lie in them, each row with its own interval of keys [lo, hi): many
+// short sequences share a tile, and no table of blocks is needed.  Paged
+// chunks cut each request's new tokens, and the list of their key tiles is
+// shared out over the blocks in equal runs (serve_parts.cuh).
 //
-// Warps (12, 168 registers a thread):
-//   0-3 softmax of tile A, one thread per row (= tensor-memory lane); 4-7 of B
-//   8   finds the work items and issues the TMA loads (Q, K, V rows; a copy
-//       per page, lanes in parallel)
-//   9, 10 products of tile A and of tile B: S of the next key tile, then
-//       O += P V of this one, in the order in which their inputs get ready
-//   11  only allocates
-// Tensor memory: S_A, S_B 128 columns each, P_A, P_B 64, O_A, O_B 64.  S is
-// computed in halves of 64 keys with barriers of their own: a row's thread
-// keeps the first half in registers from the maximum to the exponential, so
-// that the next tile's first half is computed during the exponentials of this
-// one, and the second half while the last of them finish; the round trip
-// softmax -> product -> softmax no longer sits in every tile's path.
+// Warps (16, 128 registers a thread):
+//   0-3, 4-7, 8-11  softmax of row tile 0, 1, 2: one thread per row (= tensor-
+//       memory lane)
+//   12-14  products of a row tile each: S of the next key tile as soon as the
+//       softmax has read this one's, then O += P V
+//   15  allocates, finds the work items and issues the TMA loads (Q, K, V
+//       rows; a copy per page, lanes in parallel)
+// Tensor memory (480 of 512 columns): S 64 columns a row tile, P 32, O 64.
+// A row's thread holds a tile's whole S (64 values) in registers, so S is free
+// for the next product at once; P waits in registers for the product before.
+//
+// Why three tiles of 64 keys: one tile step of a softmax warp is a chain of
+// waits and tensor-memory round trips that its arithmetic does not fill, so
+// the work in flight sets the rate.  With two row tiles of 128 keys (two
+// softmax warps a scheduler) a pair of steps took 2650 clocks where the
+// exponential, conversion and add pipes need 1311, however the two were
+// phased and however many warps issued the products.
 //
 // What a mask excludes cannot reach a row, infinities and NaN included: S is
 // replaced by -inf, and on tiles where some row misses a key the rows of V
@@ -49,40 +53,43 @@
 namespace css {
 namespace {
 
-constexpr int kBN = 128;  // keys a tile
-constexpr int kStages = 4;
-constexpr int kThreads = 384;
+constexpr int kNT = 3;   // row tiles of a work item
+constexpr int kBN = 64;  // keys a tile
+constexpr int kStages = 6;
+constexpr int kThreads = 512;
 constexpr float kSlack = 8.f;
 constexpr uint32_t kTileBytes = 128 * 128;
-constexpr uint32_t kStageBytes = 2 * kTileBytes;  // K tile, V tile
-constexpr uint32_t kSmemStage0 = 4 * kTileBytes;  // behind two Q buffers of two tiles
+constexpr uint32_t kHalfBytes = kBN * 128;         // K (or V) of a stage
+constexpr uint32_t kStageBytes = 2 * kHalfBytes;
+constexpr uint32_t kSmemStage0 = 2 * kNT * kTileBytes;  // behind two Q buffers
 constexpr uint32_t kSmemBar = kSmemStage0 + kStages * kStageBytes;
 constexpr uint32_t kSmemPre = kSmemBar + 512;  // paged: prefix of tiles
 
-constexpr uint32_t kColS = 0;    // + 128 t
-constexpr uint32_t kColP = 256;  // + 64 t
-constexpr uint32_t kColO = 384;  // + 64 t
+constexpr uint32_t kColS = 0;                // + 64 t
+constexpr uint32_t kColP = kColS + 64 * kNT;  // + 32 t
+constexpr uint32_t kColO = kColP + 32 * kNT;  // + 64 t
 constexpr uint32_t kTmemCols = 512;
+static_assert(kColO + 64 * kNT <= kTmemCols, "tensor memory");
 
 enum {
   BAR_Q = 0,                             // [Q buffer] the item's Q tiles landed
-  BAR_Q_FREE = BAR_Q + 2,                // [Q buffer] both chains are done with it
+  BAR_Q_FREE = BAR_Q + 2,                // [Q buffer] every tile's products done
   BAR_KV_FULL = BAR_Q_FREE + 2,          // [stage]
-  BAR_KV_EMPTY = BAR_KV_FULL + kStages,  // [stage] both chains are done with it
-  BAR_S_FULL = BAR_KV_EMPTY + kStages,   // [2 t + half]
-  BAR_S_FREE = BAR_S_FULL + 4,           // [2 t + half] read by the softmax (128 threads)
-  BAR_P_FULL = BAR_S_FREE + 4,           // [t] P stored, O rescaled (128 threads)
-  BAR_P_FREE = BAR_P_FULL + 2,           // [t] O += P V done
-  BAR_O_FREE = BAR_P_FREE + 2,           // [t] the epilogue has read O (128 threads)
-  BAR_V_OK = BAR_O_FREE + 2,             // [t] rows of V looked at (128 threads)
-  BAR_UNIT = BAR_V_OK + 2,               // [item buffer] description written
-  BAR_UNIT_FREE = BAR_UNIT + 2,          // [item buffer] read by 8 + 2 warps
-  BAR_MMA_DONE = BAR_UNIT_FREE + 2,      // every product of the block done (2 commits)
+  BAR_KV_EMPTY = BAR_KV_FULL + kStages,  // [stage] every tile's products done
+  BAR_S_FULL = BAR_KV_EMPTY + kStages,   // [t]
+  BAR_S_FREE = BAR_S_FULL + kNT,         // [t] read by the softmax (128 threads)
+  BAR_P_FULL = BAR_S_FREE + kNT,         // [t] P stored, O rescaled (128 threads)
+  BAR_P_FREE = BAR_P_FULL + kNT,         // [t] O += P V done
+  BAR_O_FREE = BAR_P_FREE + kNT,         // [t] the epilogue has read O (128 threads)
+  BAR_V_OK = BAR_O_FREE + kNT,           // [t] rows of V looked at (128 threads)
+  BAR_UNIT = BAR_V_OK + kNT,             // [item buffer] description written
+  BAR_UNIT_FREE = BAR_UNIT + 2,          // [item buffer] read by 5 kNT warps
+  BAR_MMA_DONE = BAR_UNIT_FREE + 2,      // every product of the block done (kNT commits)
   BAR_COUNT
 };
 static_assert(BAR_COUNT * 8 <= 512, "barrier area");
 
-// A work item as warp 8 describes it.  Keys count from the item's first key.
+// A work item as warp 15 describes it.  Keys count from the item's first key.
 struct Unit {
   int more;      // 0: no further item
   int q0;        // token row of tile A's first row
@@ -90,8 +97,8 @@ struct Unit {
   int kv;
   int kbeg;      // packed: row of key 0
   int j0, nj;    // key tiles j0 .. j0 + nj - 1
-  int t0[2], t1[2];          // those of row tile t: [t0, t1), counted from j0
-  int lo_max[2], hi_min[2];  // keys that every row of tile t sees: [lo_max, hi_min)
+  int t0[kNT], t1[kNT];          // those of row tile t: [t0, t1), counted from j0
+  int lo_max[kNT], hi_min[kNT];  // keys that every row of tile t sees: [lo_max, hi_min)
   int kend;      // no row sees a key from here on
   int s0, s1;    // packed: first and last sequence in the window
   int lim;       // paged: keys that the first token of the item sees
@@ -173,9 +180,15 @@ __device__ __forceinline__ int tiles_of_block(const PagedReq& r, int w, int b) {
   return end <= 0 ? 1 : (int)((end + kBN - 1) / kBN);
 }
 
-__device__ __forceinline__ void paged_unit(const TileArgs& a, const long long* pre, long long pos,
-                                           long long end, Unit* u, int* req, int* n_keys,
-                                           int* steps) {
+// A place in the list of tiles: tile t0 of a row block of a request and head.
+struct Place {
+  PagedReq r;
+  int req, kv, blk, t0;
+};
+
+// The place at position pos of the list; pre[i] counts the tiles of one head
+// of the requests before i.
+__device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pre, long long pos) {
   int lo = 0, hi = a.batch;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -184,41 +197,57 @@ __device__ __forceinline__ void paged_unit(const TileArgs& a, const long long* p
     else
       hi = mid;
   }
-  const int i = lo - 1;
+  Place p;
+  p.req = lo - 1;
   bool b;
-  const PagedReq r = paged_req(a, i, &b);
-  const int w = 2 * a.tpt;
-  const int nblk = (r.n_new + w - 1) / w;
-  const long long per = pre[i + 1] - pre[i], off = pos - pre[i] * a.Hkv;
-  const int kv = (int)(off / per);
-  const long long at = off - (long long)kv * per;
-  int x = 0, y = nblk;  // the last block with tiles_before <= at
+  p.r = paged_req(a, p.req, &b);
+  const int w = kNT * a.tpt;
+  const long long per = pre[lo] - pre[p.req], off = pos - pre[p.req] * a.Hkv;
+  p.kv = (int)(off / per);
+  const long long at = off - (long long)p.kv * per;
+  int x = 0, y = (p.r.n_new + w - 1) / w;  // the last block with tiles_before <= at
   while (x < y) {
     const int mid = (x + y) >> 1;
-    if (tiles_before(r, w, mid) <= at)
+    if (tiles_before(p.r, w, mid) <= at)
       x = mid + 1;
     else
       y = mid;
   }
-  const int blk = x - 1;
-  const int nt = tiles_of_block(r, w, blk);
-  const int t0 = (int)(at - tiles_before(r, w, blk));
-  const long long left = end - pos;
-  const int t1 = left < nt - t0 ? t0 + (int)left : nt;
-  *req = i;
-  *n_keys = r.n_keys;
-  *steps = t1 - t0;
+  p.blk = x - 1;
+  p.t0 = (int)(at - tiles_before(p.r, w, p.blk));
+  return p;
+}
+
+// The place behind a block: the next block, head or request with rows.  Called
+// only where the list goes on.
+__device__ __forceinline__ void next_block(const TileArgs& a, Place* p) {
+  p->t0 = 0;
+  if (++p->blk * kNT * a.tpt < p->r.n_new) return;
+  p->blk = 0;
+  if (++p->kv < a.Hkv) return;
+  p->kv = 0;
+  do {
+    bool b;
+    p->r = paged_req(a, ++p->req, &b);
+  } while (p->r.n_new == 0 && p->req + 1 < a.batch);
+}
+
+// Describes the item at a place, tiles [t0, t1) of nt.
+__device__ __forceinline__ void paged_unit(const TileArgs& a, const Place& p, int t1, int nt,
+                                           Unit* u) {
+  const PagedReq r = p.r;
+  const int w = kNT * a.tpt, blk = p.blk, t0 = p.t0;
   u->more = 1;
   u->q0 = r.q0 + blk * w;
   u->q_end = min(r.q0 + r.n_new, u->q0 + w);
-  u->kv = kv;
+  u->kv = p.kv;
   u->kbeg = 0;
   u->j0 = t0;
   u->lim = r.n_keys - r.n_new + 1 + blk * w;
   u->nj = 0;
   u->kend = 0;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < kNT; ++t) {
     const int first = u->q0 + t * a.tpt, past = min(u->q_end, first + a.tpt);
     u->t0[t] = u->t1[t] = 0;
     u->lo_max[t] = u->hi_min[t] = 0;
@@ -238,12 +267,12 @@ __device__ __forceinline__ void paged_unit(const TileArgs& a, const long long* p
 
 // --------------------------------------------------------------- packed items
 __device__ __forceinline__ void packed_unit(const TileArgs& a, int block, Unit* u) {
-  const int nwin = (a.tokens + 2 * a.tpt - 1) / (2 * a.tpt);
+  const int w = kNT * a.tpt, nwin = (a.tokens + w - 1) / w;
   const int kv = block % a.Hkv, win = nwin - 1 - block / a.Hkv;
   u->more = 1;
   u->kv = kv;
-  u->q0 = win * 2 * a.tpt;
-  u->q_end = min(a.tokens, u->q0 + 2 * a.tpt);
+  u->q0 = win * w;
+  u->q_end = min(a.tokens, u->q0 + w);
   u->j0 = u->nj = 0;
   u->lim = 0;
   u->whole = 1;
@@ -252,23 +281,24 @@ __device__ __forceinline__ void packed_unit(const TileArgs& a, int block, Unit* 
   u->kbeg = 0;
   u->s0 = 0;
   u->s1 = -1;
-  // first and last row that belong to a sequence, of both tiles; lane l of the
-  // first four searches one of them
+  // first and last row that belong to a sequence, of every tile; lanes 2 t and
+  // 2 t + 1 search them
   const int front = a.cu[0], back = a.cu[a.batch];
   const int lane = threadIdx.x & 31;
-  int f[2], e[2];
+  int f[kNT], e[kNT], want = 0;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < kNT; ++t) {
     f[t] = max(u->q0 + t * a.tpt, front);
     e[t] = min(min(u->q_end, u->q0 + (t + 1) * a.tpt), back) - 1;
+    if (lane == 2 * t) want = f[t];
+    if (lane == 2 * t + 1) want = e[t];
   }
-  const int want = lane == 0 ? f[0] : lane == 1 ? e[0] : lane == 2 ? f[1] : e[1];
   int s = last_at_or_below(a.cu, a.batch, want);
   s = s < 0 ? 0 : s;
   const RowRange r = row_range(a.cu[s], a.cu[s + 1], a.tokens);
   bool seen = false;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < kNT; ++t) {
     const int sf = __shfl_sync(0xffffffffu, s, 2 * t), se = __shfl_sync(0xffffffffu, s, 2 * t + 1);
     const int bf = __shfl_sync(0xffffffffu, r.begin, 2 * t);
     const int ef = __shfl_sync(0xffffffffu, r.end, 2 * t);
@@ -328,6 +358,22 @@ __device__ __forceinline__ void exp32(const uint32_t (&v)[32], float c, float ne
   }
 }
 
+// O *= alpha for the rows of a warp.
+__device__ __forceinline__ void rescale(uint32_t t_o, float alpha) {
+  const float2 al = make_float2(alpha, alpha);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t o[32];
+    tmem_ld32_wait(t_o + 32 * h, o);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float2 x = __fmul2_rn(make_float2(as_f(o[e]), as_f(o[e + 1])), al);
+      o[e] = __float_as_uint(x.x), o[e + 1] = __float_as_uint(x.y);
+    }
+    tmem_st32(t_o + 32 * h, o);
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ bool any_nonfinite(const uint4& w) {
   constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
@@ -342,16 +388,16 @@ __device__ __forceinline__ bool any_nonfinite(const uint4& w) {
 // thread: P from its tensor-memory columns, V from the stage.  Rare.
 template <bool BF16>
 __device__ __forceinline__ void row_product(uint32_t t_p, uint32_t t_o, const uint8_t* v, int lo,
-                                            int hi, float alpha, bool first) {
+                                            int hi, bool first) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {  // 16 columns at a time
     uint32_t o[16];
     float acc[16];
     tmem_ld16_wait(t_o + 16 * c, o);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = first ? 0.f : as_f(o[e]) * alpha;
+    for (int e = 0; e < 16; ++e) acc[e] = first ? 0.f : as_f(o[e]);
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {  // 32 keys at a time
+    for (int i = 0; i < kBN / 32; ++i) {  // 32 keys at a time
       uint32_t p[16];
       __syncwarp();
       tmem_ld16_wait(t_p + 16 * i, p);
@@ -392,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ Unit s_unit[2];
-  __shared__ int s_odd[2][2];  // [t][use & 1]: number of the use whose V is not all finite
+  __shared__ int s_odd[kNT][2];  // [t][use & 1]: number of the use whose V is not all finite
+  __shared__ volatile int s_turn[kNT];  // [t] key tiles whose product is issued
   __shared__ long long s_scan[kThreads / 32];
   griddep_launch_dependents();
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -405,31 +452,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     s_abort = 0;
-    s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(BAR_Q + i), 1);
-      mbar_init(BAR(BAR_Q_FREE + i), 2);
+      mbar_init(BAR(BAR_Q_FREE + i), kNT);
+      mbar_init(BAR(BAR_UNIT + i), 1);
+      mbar_init(BAR(BAR_UNIT_FREE + i), 5 * kNT);
+    }
+    for (int i = 0; i < kNT; ++i) {
+      s_turn[i] = 0;
+      s_odd[i][0] = s_odd[i][1] = 0;
+      mbar_init(BAR(BAR_S_FULL + i), 1);
+      mbar_init(BAR(BAR_S_FREE + i), 128);
       mbar_init(BAR(BAR_P_FULL + i), 128);
       mbar_init(BAR(BAR_P_FREE + i), 1);
       mbar_init(BAR(BAR_O_FREE + i), 128);
       mbar_init(BAR(BAR_V_OK + i), 128);
-      mbar_init(BAR(BAR_UNIT + i), 1);
-      mbar_init(BAR(BAR_UNIT_FREE + i), 10);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(BAR(BAR_S_FULL + i), 1);
-      mbar_init(BAR(BAR_S_FREE + i), 128);
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(BAR(BAR_KV_FULL + s), 1);
-      mbar_init(BAR(BAR_KV_EMPTY + s), 2);
+      mbar_init(BAR(BAR_KV_EMPTY + s), kNT);
     }
-    mbar_init(BAR(BAR_MMA_DONE), 2);
+    mbar_init(BAR(BAR_MMA_DONE), kNT);
     fence_mbarrier_init();
   }
-  if (warp == 11) tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+  if (warp == 15) tmem_alloc(smem_u32(&s_tmem), kTmemCols);
   if (a.tpt * a.G < 128) {  // rows that no copy fills read as zero
-    for (int i = tid; i < (int)(4 * kTileBytes / 16); i += kThreads)
+    for (int i = tid; i < (int)(2 * kNT * kTileBytes / 16); i += kThreads)
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_shared();
   }
@@ -444,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tiles of one head before each request, every block for itself
     const int per = (a.batch + kThreads - 1) / kThreads;
     const int i0 = min(a.batch, tid * per), i1 = min(a.batch, i0 + per);
-    const int w = 2 * a.tpt;
+    const int w = kNT * a.tpt;
     long long sum = 0;
     bool bad = false;
     for (int i = i0; i < i1; ++i) {
@@ -476,271 +524,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (bad) atomicOr(a.err, kErrIndex);
   }
 
-  if (warp == 8) {
-    // ---------------- work items and loads ----------------
-    int kt = 0, nu = 0, nq = 0;
-    bool ok = true, bad = false, tail = false;
-    const int q_rows = a.tpt * a.G;
-    long long pos = share.begin;
-    for (bool more = true; more; ++nu) {
-      Unit u;
-      int req = 0, n_keys = 0, steps = 0;
-      u.more = 0;
-      if (PAGED) {
-        if (pos < share.end) paged_unit(a, s_pre, pos, share.end, &u, &req, &n_keys, &steps);
-      } else {
-        if (nu == 0) packed_unit(a, blockIdx.x, &u);
-      }
-      more = u.more != 0;
-      const int ub = nu & 1;
-      if (nu >= 2 && !mbar_wait_warp(BAR(BAR_UNIT_FREE + ub), ((nu >> 1) - 1) & 1, wc)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        s_unit[ub] = u;
-        mbar_arrive(BAR(BAR_UNIT + ub));
-      }
-      if (!more) break;
-      if (PAGED) {
-        if (!u.whole && u.tail) {
-          tail = true;
-          if (lane == 0) {
-            const int left = tiles_of_block(PagedReq{0, u.q_end - u.q0, u.lim - 1 + (u.q_end - u.q0)},
-                                            2 * a.tpt, 0);
-            a.part.desc[blockIdx.x] = PartDesc{u.q0, u.kv, (u.q_end - u.q0) * a.G,
-                                               last_block(share, pos + left - 1)};
-          }
-        }
-        pos += steps;
-      }
-      if (u.nj == 0) continue;
-      const int qbuf = nq & 1;
-      if (nq >= 2 && !mbar_wait_warp(BAR(BAR_Q_FREE + qbuf), ((nq >> 1) - 1) & 1, wc)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        const uint32_t q_s = sbase + qbuf * 2 * kTileBytes;
-        const int na = u.t1[0] > u.t0[0], nb = u.t1[1] > u.t0[1];
-        mbar_arrive_expect_tx(BAR(BAR_Q + qbuf), (na + nb) * q_rows * 128);
-        if (na) tma_load_4d(q_s, &tm_q, BAR(BAR_Q + qbuf), 0, 0, u.kv, u.q0);
-        if (nb) tma_load_4d(q_s + kTileBytes, &tm_q, BAR(BAR_Q + qbuf), 0, 0, u.kv, u.q0 + a.tpt);
-      }
-      __syncwarp();
-      ++nq;
-      // paged: page ids 32 at a time, one group ahead
-      const int32_t* const row = PAGED ? a.table + (long long)req * a.width : nullptr;
-      const int n_pages = PAGED ? (int)pages_for(n_keys, a.shift) : 0;
-      const int box = PAGED ? min(1 << a.shift, kBN) : kBN;
-      const int boxes = kBN / box;
-      int base = PAGED ? (int)(((long long)u.j0 * kBN) >> a.shift) : 0;
-      int ids = 0, next = 0;
-      if (PAGED) {
-        ids = base + lane < n_pages ? row[base + lane] : a.pages;
-        next = base + 32 + lane < n_pages ? row[base + 32 + lane] : a.pages;
-      }
-      for (int j = 0; j < u.nj; ++j, ++kt) {
-        const int s = kt % kStages;
-        if (kt >= kStages && !mbar_wait_warp(BAR(BAR_KV_EMPTY + s), (kt / kStages - 1) & 1, wc)) {
-          ok = false;
-          break;
-        }
-        const uint32_t st = sbase + kSmemStage0 + s * kStageBytes;
-        const int k0 = (u.j0 + j) * kBN;
-        if (PAGED) {
-          const int page = k0 >> a.shift;
-          if (page - base >= 32) {
-            base += 32;
-            ids = next;
-            next = base + 32 + lane < n_pages ? row[base + 32 + lane] : a.pages;
-          }
-          const int live = n_keys <= k0 ? 0 : min(boxes, (n_keys - k0 + box - 1) / box);
-          const int bx = lane & 15;
-          const int id = __shfl_sync(0xffffffffu, ids, (page - base + (boxes > 1 ? bx : 0)) & 31);
-          const bool fine = page_ok(id, a.pages);
-          if (lane == 0) mbar_arrive_expect_tx(BAR(BAR_KV_FULL + s), 2 * live * box * 128);
-          __syncwarp();
-          if (bx < live) {
-            bad |= !fine;
-            tma_load_4d(st + (lane >> 4) * kTileBytes + bx * box * 128, lane < 16 ? &tm_k : &tm_v,
-                        BAR(BAR_KV_FULL + s), 0, boxes > 1 ? 0 : k0 & ((1 << a.shift) - 1), u.kv,
-                        fine ? id : a.pages);  // past the pool: reads as zero
-          }
-        } else if (lane == 0) {
-          mbar_arrive_expect_tx(BAR(BAR_KV_FULL + s), kStageBytes);
-          tma_load_4d(st, &tm_k, BAR(BAR_KV_FULL + s), 0, u.kbeg + k0, u.kv, 0);
-          tma_load_4d(st + kTileBytes, &tm_v, BAR(BAR_KV_FULL + s), 0, u.kbeg + k0, u.kv, 0);
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-    }
-    if (PAGED) {
-      if (bad) atomicOr(a.err, kErrIndex);
-      if (!tail && lane == 0) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
-    }
-    // no copy may still be landing when the block exits (matters only when a
-    // wait gave up)
-    if (lane == 0) {
-      for (int q = 0; q < 2 && q < nq; ++q) drain_wait(BAR(BAR_Q + q), ((nq - q + 1) / 2 - 1) & 1);
-      for (int k = kt > kStages ? kt - kStages : 0; k < kt; ++k)
-        drain_wait(BAR(BAR_KV_FULL + k % kStages), (k / kStages) & 1);
-    }
-  } else if (warp == 9 || warp == 10) {
-    // ---------------- products of row tile t ----------------
-    const int t = warp - 9;
-    const uint32_t d_s = tmem + kColS + 128 * t, d_p = tmem + kColP + 64 * t,
-                   d_o = tmem + kColO + 64 * t;
-    int kt = 0, nq = 0, ns = 0, np = 0, no = 0;
-    bool ok = true;
-    for (int nu = 0; ok; ++nu) {
-      if (!mbar_wait_warp(BAR(BAR_UNIT + (nu & 1)), (nu >> 1) & 1, wc)) break;
-      const Unit& su = s_unit[nu & 1];
-      const int more = su.more, nj = su.nj, j0 = su.t0[t], j1 = su.t1[t];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(BAR_UNIT_FREE + (nu & 1)));
-      if (!more) break;
-      if (nj == 0) continue;
-      const int qbuf = nq & 1;
-      if (!mbar_wait_warp(BAR(BAR_Q + qbuf), (nq >> 1) & 1, wc)) break;
-      const uint32_t q_s = sbase + (qbuf * 2 + t) * kTileBytes;
-      // step j forms S of key tile j, then O += P V of tile j - 1
-      for (int j = 0; ok && j <= nj; ++j) {
-        if (j < nj) {
-          const int s = (kt + j) % kStages;
-          ok = mbar_wait_warp(BAR(BAR_KV_FULL + s), ((kt + j) / kStages) & 1, wc);
-          if (!ok) break;
-          if (j >= j0 && j < j1) {
-            const uint32_t k_s = sbase + kSmemStage0 + s * kStageBytes;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              if (ns > 0 && !mbar_wait_warp(BAR(BAR_S_FREE + 2 * t + h), (ns - 1) & 1, wc)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_ss(d_s + 64 * h, sdesc_sw128(q_s + kk * 32, 16, 1024),
-                         sdesc_sw128(k_s + h * 8192 + kk * 32, 16, 1024), idesc<BF16>(64, 0),
-                         kk > 0);
-                mma_commit(BAR(BAR_S_FULL + 2 * t + h));
-              }
-              __syncwarp();
-            }
-            if (!ok) break;
-            ++ns;
-          }
-        }
-        if (j > 0) {
-          const int i = j - 1, s = (kt + i) % kStages;
-          if (i >= j0 && i < j1) {
-            if (!mbar_wait_warp(BAR(BAR_P_FULL + t), np & 1, wc)) {
-              ok = false;
-              break;
-            }
-            // the item's first product overwrites O: the epilogue before must
-            // have read it
-            if (i == j0 && no > 0 && !mbar_wait_warp(BAR(BAR_O_FREE + t), (no - 1) & 1, wc)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t v_s = sbase + kSmemStage0 + s * kStageBytes + kTileBytes;
-            const bool by_rows = s_odd[t][np & 1] == np + 1;  // the rows' threads did it
-            if (elect_one()) {
-              if (!by_rows) {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  mma_ts(d_o, d_p + kk * 8, sdesc_sw128(v_s + kk * 2048, 8192, 1024),
-                         idesc<BF16>(64, 1), (i > j0 || kk > 0) ? 1u : 0u);
-              }
-              mma_commit(BAR(BAR_P_FREE + t));
-            }
-            __syncwarp();
-            ++np;
-          }
-          if (elect_one()) mma_commit(BAR(BAR_KV_EMPTY + s));
-          __syncwarp();
-        }
-      }
-      if (!ok) break;
-      if (elect_one()) mma_commit(BAR(BAR_Q_FREE + qbuf));
-      __syncwarp();
-      kt += nj;
-      ++nq;
-      if (j1 > j0) ++no;
-    }
-    if (elect_one()) mma_commit(BAR(BAR_MMA_DONE));
-    __syncwarp();
-  } else if (warp < 8) {
+  Place place{};
+  if (PAGED && warp == 15 && share.begin < share.end) place = place_at(a, s_pre, share.begin);
+
+  if (warp < 4 * kNT) {
     // ---------------- softmax: thread = row of tile t ----------------
     const int t = warp >> 2, row = tid & 127;
     const int rt = row / a.G, rh = row - rt * a.G;  // token and head of the row
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + kColS + 128 * t;
-    const uint32_t t_p = tmem + lane_base + kColP + 64 * t;
+    const uint32_t t_s = tmem + lane_base + kColS + 64 * t;
+    const uint32_t t_p = tmem + lane_base + kColP + 32 * t;
     const uint32_t t_o = tmem + lane_base + kColO + 64 * t;
     const float c = a.c;
     int kt = 0, ns = 0, nv = 0;  // tiles walked, S tiles read, V tiles looked at
     bool ok = true;
     for (int nu = 0; ok; ++nu) {
-      if (!mbar_wait_warp(BAR(BAR_UNIT + (nu & 1)), (nu >> 1) & 1, wc)) break;
+      if (!mbar_wait_inline(BAR(BAR_UNIT + (nu & 1)), (nu >> 1) & 1, wc)) break;
       const Unit& su = s_unit[nu & 1];
-      const int more = su.more, nj = su.nj, j0 = su.t0[t], j1 = su.t1[t], kbase = su.j0 * kBN;
-      const int lo_max = su.lo_max[t], hi_min = su.hi_min[t], kend = su.kend;
-      const int tok = su.q0 + t * a.tpt + rt, kv = su.kv;
-      const int whole = su.whole, tail = su.tail, lrow = t * a.tpt * a.G + row;
-      const int kbeg = su.kbeg, s0 = su.s0, s1 = su.s1, lim = su.lim + (tok - su.q0);
-      bool valid = more && rt < a.tpt && tok < su.q_end;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(BAR_UNIT_FREE + (nu & 1)));
-      if (!more) break;
+      if (!su.more) break;
+      const int j0 = su.t0[t], j1 = su.t1[t];
       // keys that this row sees: [lo, hi) from the item's first key
       int lo = 0, hi = 0;
-      if (PAGED) {
-        if (valid) hi = lim;
-      } else if (valid) {
-        int s = s0;
-        if (s1 > s0) s += last_at_or_below(a.cu + s0, s1 - s0 + 1, tok);
-        const RowRange r = row_range(a.cu[s], a.cu[s + 1], a.tokens);
-        valid = s >= s0 && s <= s1 && tok >= r.begin && tok < r.end;
-        lo = r.begin - kbeg;
-        hi = valid ? (a.causal ? tok + 1 : r.end) - kbeg : 0;
+      bool valid;
+      {
+        const int tok = su.q0 + t * a.tpt + rt;
+        valid = rt < a.tpt && tok < su.q_end;
+        if (PAGED) {
+          if (valid) hi = su.lim + (tok - su.q0);
+        } else if (valid) {
+          int s = su.s0;
+          if (su.s1 > s) s += last_at_or_below(a.cu + s, su.s1 - s + 1, tok);
+          const RowRange r = row_range(a.cu[max(s, 0)], a.cu[max(s, 0) + 1], a.tokens);
+          valid = s >= su.s0 && s <= su.s1 && tok >= r.begin && tok < r.end;
+          lo = r.begin - su.kbeg;
+          hi = valid ? (a.causal ? tok + 1 : r.end) - su.kbeg : 0;
+        }
+        lo -= su.j0 * kBN;  // from here on, keys count from the first tile walked
+        hi -= su.j0 * kBN;
       }
+      const int lo_max = su.lo_max[t] - su.j0 * kBN, hi_min = su.hi_min[t] - su.j0 * kBN;
       float m = -INFINITY, l = 0.f;
       for (int j = j0; j < j1; ++j) {
-        const int k0 = kbase + j * kBN;
+        const int k0 = j * kBN;
         const bool edge = k0 < lo_max || k0 + kBN > hi_min;  // the same for the whole tile
         const int lo_l = lo - k0, hi_l = hi - k0;
-        if (!mbar_wait_warp(BAR(BAR_S_FULL + 2 * t), ns & 1, wc)) {
+        if (!mbar_wait_inline(BAR(BAR_S_FULL + t), ns & 1, wc)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t x0[32], x1[32];  // the first half, kept until the exponentials
+        uint32_t x0[32], x1[32];
         tmem_ld32x2_wait(t_s, t_s + 32, x0, x1);
         tc_fence_before();
-        mbar_arrive(BAR(BAR_S_FREE + 2 * t));
+        mbar_arrive(BAR(BAR_S_FREE + t));
         if (edge) {
           mask32(x0, lo_l, hi_l);
           mask32(x1, lo_l - 32, hi_l - 32);
         }
-        float mx = max32(x1, max32(x0, -INFINITY));
-        if (!mbar_wait_warp(BAR(BAR_S_FULL + 2 * t + 1), ns & 1, wc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        uint32_t y[32];
-        tmem_ld32_wait(t_s + 64, y);
-        if (edge) mask32(y, lo_l - 64, hi_l - 64);
-        mx = max32(y, mx);
-        tmem_ld32_wait(t_s + 96, y);
-        if (edge) mask32(y, lo_l - 96, hi_l - 96);
-        mx = max32(y, mx);
+        const float mx = max32(x1, max32(x0, -INFINITY));
         // c > 0, so max(S) c is the maximum of the scaled scores
         const float top = mx * c;
         float alpha = 1.f;
@@ -750,78 +591,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = m_new;
         }
         const float neg_m = m == -INFINITY ? 0.f : -m;
-        uint32_t pk[64];
+        uint32_t pk[32];
         float2 a0 = make_float2(0.f, 0.f), a1 = a0;
         exp32<BF16>(x0, c, neg_m, pk, a0, a1);
         exp32<BF16>(x1, c, neg_m, pk + 16, a0, a1);
-        exp32<BF16>(y, c, neg_m, pk + 48, a0, a1);
-        tmem_ld32_wait(t_s + 64, y);
-        tc_fence_before();
-        mbar_arrive(BAR(BAR_S_FREE + 2 * t + 1));
-        if (edge) mask32(y, lo_l - 64, hi_l - 64);
-        exp32<BF16>(y, c, neg_m, pk + 32, a0, a1);
         const float2 s01 = __fadd2_rn(a0, a1);
         l = l * alpha + (s01.x + s01.y);
-
+        // P of the previous tile has been read by its product, and O is final
+        // for a rescale
+        if (ns > 0 && !mbar_wait_inline(BAR(BAR_P_FREE + t), (ns - 1) & 1, wc)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
         bool by_rows = false;
-        const uint8_t* v_s = smem;
         if (edge) {
           // look at row `row` of the V tile
           const int s = (kt + j) % kStages;
-          if (!mbar_wait_warp(BAR(BAR_KV_FULL + s), ((kt + j) / kStages) & 1, wc)) {
+          if (!mbar_wait_inline(BAR(BAR_KV_FULL + s), ((kt + j) / kStages) & 1, wc)) {
             ok = false;
             break;
           }
-          uint8_t* const v = smem + kSmemStage0 + s * kStageBytes + kTileBytes;
-          v_s = v;
-          uint4* const vr = reinterpret_cast<uint4*>(v + row * 128);
-          if (k0 + row >= kend) {
+          if (row < kBN) {
+            uint4* const vr = reinterpret_cast<uint4*>(smem + kSmemStage0 + s * kStageBytes +
+                                                       kHalfBytes + row * 128);
+            if (k0 + row >= su.kend - su.j0 * kBN) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) vr[i] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_shared();
-          } else {
-            bool odd = false;
+              for (int i = 0; i < 8; ++i) vr[i] = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_shared();
+            } else {
+              bool odd = false;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) odd |= any_nonfinite<BF16>(vr[i]);
-            if (odd) *(volatile int*)&s_odd[t][ns & 1] = ns + 1;
+              for (int i = 0; i < 8; ++i) odd |= any_nonfinite<BF16>(vr[i]);
+              if (odd) *(volatile int*)&s_odd[t][ns & 1] = ns + 1;
+            }
           }
           mbar_arrive(BAR(BAR_V_OK + t));
-          if (!mbar_wait_warp(BAR(BAR_V_OK + t), nv & 1, wc)) {
+          if (!mbar_wait_inline(BAR(BAR_V_OK + t), nv & 1, wc)) {
             ok = false;
             break;
           }
           ++nv;
           by_rows = *(volatile int*)&s_odd[t][ns & 1] == ns + 1;
         }
-        // P of the previous tile has been read by its product, and O is final
-        // for a rescale
-        if (ns > 0 && !mbar_wait_warp(BAR(BAR_P_FREE + t), (ns - 1) & 1, wc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        {
-          const uint32_t(&w0)[32] = *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]);
-          const uint32_t(&w1)[32] = *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]);
-          tmem_st32(t_p, w0);
-          tmem_st32(t_p + 32, w1);
-        }
+        if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale(t_o, alpha);
+        tmem_st32(t_p, pk);
         if (by_rows) {
           tmem_st_wait();
-          row_product<BF16>(t_p, t_o, v_s, max(lo_l, 0), min(hi_l, kBN), alpha, j == j0);
-        } else if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          uint32_t o0[32], o1[32];
-          tmem_ld32x2_wait(t_o, t_o + 32, o0, o1);
-          const float2 al = make_float2(alpha, alpha);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 x = __fmul2_rn(make_float2(as_f(o0[e]), as_f(o0[e + 1])), al);
-            const float2 z = __fmul2_rn(make_float2(as_f(o1[e]), as_f(o1[e + 1])), al);
-            o0[e] = __float_as_uint(x.x), o0[e + 1] = __float_as_uint(x.y);
-            o1[e] = __float_as_uint(z.x), o1[e + 1] = __float_as_uint(z.y);
-          }
-          tmem_st32(t_o, o0);
-          tmem_st32(t_o + 32, o1);
+          row_product<BF16>(
+              t_p, t_o, smem + kSmemStage0 + ((kt + j) % kStages) * kStageBytes + kHalfBytes,
+              max(lo_l, 0), min(hi_l, kBN), j == j0);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -829,13 +648,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
       }
       if (!ok) break;
-      kt += nj;
+      kt += su.nj;
 
       // ---------------- epilogue ----------------
       uint32_t o0[32], o1[32];
       if (j1 > j0) {
         // the last product of the item is the one that frees its P
-        if (!mbar_wait_warp(BAR(BAR_P_FREE + t), (ns - 1) & 1, wc)) {
+        if (!mbar_wait_inline(BAR(BAR_P_FREE + t), (ns - 1) & 1, wc)) {
           ok = false;
           break;
         }
@@ -848,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 32; ++e) o0[e] = o1[e] = 0;
       }
       if (valid) {
-        const int h = kv * a.G + rh;
-        if (!PAGED || whole) {
+        const int tok = su.q0 + t * a.tpt + rt, h = su.kv * a.G + rh;
+        if (!PAGED || su.whole) {
           const bool some = l > 0.f || l != l;
           const float inv = some ? 1.0f / l : 0.f;
           uint4* const dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o.p) +
@@ -867,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (a.lse) a.lse[(long long)h * a.tokens + tok] = some ? m + lg2_approx(l) : -INFINITY;
         } else {
-          const long long at = part_row(a.part, blockIdx.x, tail, lrow);
+          const long long at = part_row(a.part, blockIdx.x, su.tail, t * a.tpt * a.G + row);
           // rows without a key so far have no sums: O may hold anything then
           const bool some = l > 0.f || l != l;
           float4* const d = reinterpret_cast<float4*>(a.part.o + at * 64);
@@ -883,12 +702,223 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.part.ml[at] = make_float2(some ? m : -INFINITY, l);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(BAR_UNIT_FREE + (nu & 1)));
+    }
+  } else {
+    if (warp == 15) {
+      // ---------------- work items and loads ----------------
+      int kt = 0, nu = 0, nq = 0;
+      bool ok = true, bad = false, tail = false;
+      const int q_rows = a.tpt * a.G;
+      long long pos = share.begin;
+      for (;; ++nu) {
+        const int ub = nu & 1;
+        if (nu >= 2 && !mbar_wait_warp(BAR(BAR_UNIT_FREE + ub), ((nu >> 1) - 1) & 1, wc)) {
+          ok = false;
+          break;
+        }
+        Unit u;
+        u.more = PAGED ? pos < share.end : nu == 0;
+        int steps = 0, nt = 0;
+        if (u.more && PAGED) {
+          nt = tiles_of_block(place.r, kNT * a.tpt, place.blk);
+          steps = (int)min((long long)(nt - place.t0), share.end - pos);
+          paged_unit(a, place, place.t0 + steps, nt, &u);
+        } else if (u.more) {
+          packed_unit(a, blockIdx.x, &u);
+        }
+        if (lane == 0) {
+          s_unit[ub] = u;
+          mbar_arrive(BAR(BAR_UNIT + ub));
+        }
+        __syncwarp();
+        if (!u.more) break;
+        const int req = place.req, n_keys = place.r.n_keys;
+        if (PAGED) {
+          if (!u.whole && u.tail) {
+            tail = true;
+            if (lane == 0)
+              a.part.desc[blockIdx.x] = PartDesc{u.q0, u.kv, (u.q_end - u.q0) * a.G,
+                                                 last_block(share, pos + nt - 1)};
+          }
+          pos += steps;
+          if (pos < share.end) next_block(a, &place);
+        }
+        if (u.nj == 0) continue;
+        const int qbuf = nq & 1;
+        if (nq >= 2 && !mbar_wait_warp(BAR(BAR_Q_FREE + qbuf), ((nq >> 1) - 1) & 1, wc)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t q_s = sbase + qbuf * kNT * kTileBytes;
+          int n = 0;
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) n += u.t1[t] > u.t0[t];
+          mbar_arrive_expect_tx(BAR(BAR_Q + qbuf), n * q_rows * 128);
+#pragma unroll
+          for (int t = 0; t < kNT; ++t)
+            if (u.t1[t] > u.t0[t])
+              tma_load_4d(q_s + t * kTileBytes, &tm_q, BAR(BAR_Q + qbuf), 0, 0, u.kv,
+                          u.q0 + t * a.tpt);
+        }
+        __syncwarp();
+        ++nq;
+        // paged: page ids 32 at a time, one group ahead
+        const int32_t* const row = PAGED ? a.table + (long long)req * a.width : nullptr;
+        const int n_pages = PAGED ? (int)pages_for(n_keys, a.shift) : 0;
+        const int box = PAGED ? min(1 << a.shift, kBN) : kBN;
+        const int boxes = kBN / box;
+        int base = PAGED ? (int)(((long long)u.j0 * kBN) >> a.shift) : 0;
+        int ids = 0, next = 0;
+        if (PAGED) {
+          ids = base + lane < n_pages ? row[base + lane] : a.pages;
+          next = base + 32 + lane < n_pages ? row[base + 32 + lane] : a.pages;
+        }
+        for (int j = 0; j < u.nj; ++j, ++kt) {
+          const int s = kt % kStages;
+          if (kt >= kStages && !mbar_wait_warp(BAR(BAR_KV_EMPTY + s), (kt / kStages - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = sbase + kSmemStage0 + s * kStageBytes;
+          const int k0 = (u.j0 + j) * kBN;
+          if (PAGED) {
+            const int page = k0 >> a.shift;
+            if (page - base >= 32) {
+              base += 32;
+              ids = next;
+              next = base + 32 + lane < n_pages ? row[base + 32 + lane] : a.pages;
+            }
+            const int live = n_keys <= k0 ? 0 : min(boxes, (n_keys - k0 + box - 1) / box);
+            const int bx = lane & 15;
+            const int id = __shfl_sync(0xffffffffu, ids, (page - base + (boxes > 1 ? bx : 0)) & 31);
+            const bool fine = page_ok(id, a.pages);
+            if (lane == 0) mbar_arrive_expect_tx(BAR(BAR_KV_FULL + s), 2 * live * box * 128);
+            __syncwarp();
+            if (bx < live) {
+              bad |= !fine;
+              tma_load_4d(st + (lane >> 4) * kHalfBytes + bx * box * 128, lane < 16 ? &tm_k : &tm_v,
+                          BAR(BAR_KV_FULL + s), 0, boxes > 1 ? 0 : k0 & ((1 << a.shift) - 1), u.kv,
+                          fine ? id : a.pages);  // past the pool: reads as zero
+            }
+          } else if (lane == 0) {
+            mbar_arrive_expect_tx(BAR(BAR_KV_FULL + s), kStageBytes);
+            tma_load_4d(st, &tm_k, BAR(BAR_KV_FULL + s), 0, u.kbeg + k0, u.kv, 0);
+            tma_load_4d(st + kHalfBytes, &tm_v, BAR(BAR_KV_FULL + s), 0, u.kbeg + k0, u.kv, 0);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      if (PAGED) {
+        if (bad) atomicOr(a.err, kErrIndex);
+        if (!tail && lane == 0) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
+      }
+      // no copy may still be landing when the block exits (matters only when a
+      // wait gave up)
+      if (lane == 0) {
+        for (int q = 0; q < 2 && q < nq; ++q) drain_wait(BAR(BAR_Q + q), ((nq - q + 1) / 2 - 1) & 1);
+        for (int k = kt > kStages ? kt - kStages : 0; k < kt; ++k)
+          drain_wait(BAR(BAR_KV_FULL + k % kStages), (k / kStages) & 1);
+      }
+    } else {
+      // ---------------- products of row tile t ----------------
+      const int t = warp - 4 * kNT;
+      const uint32_t d_s = tmem + kColS + 64 * t, d_p = tmem + kColP + 32 * t,
+                     d_o = tmem + kColO + 64 * t;
+      int kt = 0, nq = 0, ns = 0, np = 0, no = 0;
+      bool ok = true;
+      for (int nu = 0; ok; ++nu) {
+        if (!mbar_wait_warp(BAR(BAR_UNIT + (nu & 1)), (nu >> 1) & 1, wc)) break;
+        const Unit& su = s_unit[nu & 1];
+        const int more = su.more, nj = su.nj, j0 = su.t0[t], j1 = su.t1[t];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(BAR_UNIT_FREE + (nu & 1)));
+        if (!more) break;
+        if (nj == 0) continue;
+        const int qbuf = nq & 1;
+        if (!mbar_wait_warp(BAR(BAR_Q + qbuf), (nq >> 1) & 1, wc)) break;
+        const uint32_t q_lo = sdesc_lo(sbase + (qbuf * kNT + t) * kTileBytes, 16);
+        // step j forms S of key tile j, then O += P V of tile j - 1.  Every
+        // stage is waited for and released, whether the row tile uses it or
+        // not: a barrier's parity tells two uses of a stage apart, not three
+        for (int j = 0; ok && j <= nj; ++j) {
+          if (j < nj) {
+            const int s = (kt + j) % kStages;
+            ok = mbar_wait_warp(BAR(BAR_KV_FULL + s), ((kt + j) / kStages) & 1, wc);
+            if (ok && j >= j0 && j < j1) {
+              ok = ns == 0 || mbar_wait_warp(BAR(BAR_S_FREE + t), (ns - 1) & 1, wc);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t k_lo = sdesc_lo(sbase + kSmemStage0 + s * kStageBytes, 16);
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_ss(d_s, sdesc_of(q_lo + 2 * kk), sdesc_of(k_lo + 2 * kk), idesc<BF16>(64, 0),
+                         kk > 0);
+                mma_commit(BAR(BAR_S_FULL + t));
+              }
+              __syncwarp();
+              ++ns;
+            }
+            if (!ok) break;
+          }
+          if (j > 0) {
+            const int i = j - 1, s = (kt + i) % kStages;
+            if (i >= j0 && i < j1) {
+              ok = mbar_wait_warp(BAR(BAR_P_FULL + t), np & 1, wc);
+              // the item's first product overwrites O: the epilogue before must
+              // have read it
+              if (ok && i == j0 && no > 0)
+                ok = mbar_wait_warp(BAR(BAR_O_FREE + t), (no - 1) & 1, wc);
+              if (!ok) break;
+              // A hint, bounded and without consequence for results: the row
+              // tiles' products go one behind the other.  Issued together they
+              // interleave on the pipe, end together and pull the three
+              // softmaxes into step, where they queue for the same units
+              // (prompt of 16384 tokens, 32 / 4 heads: 1108 -> 1074 us).
+              if (t > 0)
+                for (int spin = 0; spin < 32 && s_turn[t - 1] <= kt + i; ++spin) {}
+              __syncwarp();
+              tc_fence_after();
+              const uint32_t v_lo =
+                  sdesc_lo(sbase + kSmemStage0 + s * kStageBytes + kHalfBytes, 8192);
+              const bool by_rows = s_odd[t][np & 1] == np + 1;  // the rows' threads did it
+              if (elect_one()) {
+                if (!by_rows) {
+#pragma unroll
+                  for (int kk = 0; kk < kBN / 16; ++kk)
+                    mma_ts(d_o, d_p + kk * 8, sdesc_of(v_lo + 128 * kk), idesc<BF16>(64, 1),
+                           (i > j0 || kk > 0) ? 1u : 0u);
+                }
+                mma_commit(BAR(BAR_P_FREE + t));
+                mma_commit(BAR(BAR_KV_EMPTY + s));
+              }
+              __syncwarp();
+              ++np;
+            } else if (lane == 0) {
+              mbar_arrive(BAR(BAR_KV_EMPTY + s));
+            }
+            s_turn[t] = kt + i + 1;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit(BAR(BAR_Q_FREE + qbuf));
+        __syncwarp();
+        kt += nj;
+        ++nq;
+        if (j1 > j0) ++no;
+      }
+      if (elect_one()) mma_commit(BAR(BAR_MMA_DONE));
+      __syncwarp();
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 11) {
+  if (warp == 15) {
     tc_fence_after();
     // every product of this block has completed before its tensor memory goes
     drain_wait(BAR(BAR_MMA_DONE), 0);
@@ -922,7 +952,7 @@ int launch_packed_fwd(const PackedDims& d, const DevCtx& ctx, const RowsArg& q, 
       !encode_tmap_4d(&tk, d.bf16, k.p, d.tokens, d.Hkv, 1, k.t, k.h, 64, kBN, 1, 1) ||
       !encode_tmap_4d(&tv, d.bf16, v.p, d.tokens, d.Hkv, 1, v.t, v.h, 64, kBN, 1, 1))
     return ATTN_ERR_CUDA;
-  const long long units = (long long)d.Hkv * ((d.tokens + 2 * a.tpt - 1) / (2 * a.tpt));
+  const long long units = (long long)d.Hkv * ((d.tokens + kNT * a.tpt - 1) / (kNT * a.tpt));
   if (units > 0x7fffffffLL) return ATTN_ERR_SHAPE;
   auto* kernel = d.bf16 ? tiles_kernel<false, true> : tiles_kernel<false, false>;
   const size_t smem = kSmemPre + 1024;

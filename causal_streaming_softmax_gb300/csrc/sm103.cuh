@@ -129,6 +129,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Waits for the phase with the given parity to complete.  Returns false (and
 // records the failure) once the limit has passed or another thread of the
 // block has already given up; the caller must then stop its role.
@@ -174,6 +187,43 @@ static __device__ __noinline__ bool drain_wait(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const WaitCtl& w) {
   const bool ok = mbar_wait(bar, parity, w);
   return __all_sync(0xffffffffu, ok);
+}
+
+// A bound on a warp's polling of several barriers: reset by progress, it says
+// when to give up.
+struct PollBound {
+  uint64_t t0;
+  uint32_t idle;
+  __device__ __forceinline__ void reset() { idle = 0; }
+  __device__ __forceinline__ bool give_up(const WaitCtl& w) {
+    if ((++idle & 31u) != 0) return false;
+    const uint64_t now = global_timer_ns();
+    if (idle == 32u) t0 = now;
+    const bool late = now - t0 > w.limit_ns;
+    if (!__any_sync(0xffffffffu, late || *w.abort != 0)) return false;
+    *w.abort = 1;
+    if (late && w.err) atomicOr(w.err, kErrWaitTimeout);
+    return true;
+  }
+};
+
+// mbar_wait_warp without a call: for code that holds more registers than a
+// call preserves (a call there moves them through local memory).
+__device__ __forceinline__ bool mbar_wait_inline(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  uint32_t spins = 0;
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if ((++spins & 15u) == 0) {
+      const bool late = global_timer_ns() - t0 > w.limit_ns;
+      if (__any_sync(0xffffffffu, late || *w.abort != 0)) {
+        *w.abort = 1;
+        if (late && w.err) atomicOr(w.err, kErrWaitTimeout);
+        return false;
+      }
+    }
+  }
+  return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -308,6 +358,15 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   d |= static_cast<uint64_t>(1) << 46;  // descriptor version for this family
   d |= static_cast<uint64_t>(2) << 61;  // 128-byte swizzle
   return d;
+}
+
+// The same in two steps, for loops that walk a tile: the low word holds the
+// address and lbo (advance it by bytes / 16), the high word is sbo = 1024's.
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+__device__ __forceinline__ uint64_t sdesc_of(uint32_t lo) {
+  return (static_cast<uint64_t>((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
 }
 
 // Instruction descriptor of kind::f16: binary16 A and B, binary32 D, dense.
