@@ -25,7 +25,9 @@
 //   12-14  products of a row tile each: S of the next key tile as soon as the
 //       softmax has read this one's, then O += P V
 //   15  allocates, finds the work items and issues the TMA loads (Q, K, V
-//       rows; a copy per page, lanes in parallel)
+//       rows; a copy per page, lanes in parallel).  Packed: a block takes over
+//       the next window that no block has started (cluster launch control),
+//       whose description and first loads then overlap the window before
 // Tensor memory (480 of 512 columns): S 64 columns a row tile, P 32, O 64.
 // A row's thread holds a tile's whole S (64 values) in registers, so S is free
 // for the next product at once; P waits in registers for the product before.
@@ -85,6 +87,7 @@ enum {
   BAR_UNIT = BAR_V_OK + kNT,             // [item buffer] description written
   BAR_UNIT_FREE = BAR_UNIT + 2,          // [item buffer] read by 5 kNT warps
   BAR_MMA_DONE = BAR_UNIT_FREE + 2,      // every product of the block done (kNT commits)
+  BAR_TAKE = BAR_MMA_DONE + 1,           // an answer of take_block
   BAR_COUNT
 };
 static_assert(BAR_COUNT * 8 <= 512, "barrier area");
@@ -438,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ Unit s_unit[2];
+  __shared__ __align__(16) uint4 s_answer;
   __shared__ int s_odd[kNT][2];  // [t][use & 1]: number of the use whose V is not all finite
   __shared__ volatile int s_turn[kNT];  // [t] key tiles whose product is issued
   __shared__ long long s_scan[kThreads / 32];
@@ -473,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(BAR_KV_EMPTY + s), kNT);
     }
     mbar_init(BAR(BAR_MMA_DONE), kNT);
+    mbar_init(BAR(BAR_TAKE), 1);
     fence_mbarrier_init();
   }
   if (warp == 15) tmem_alloc(smem_u32(&s_tmem), kTmemCols);
@@ -516,12 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) s_pre[0] = 0;
     __syncthreads();
     share = share_of(s_pre[a.batch] * a.Hkv, a.part.min_tiles, gridDim.x, blockIdx.x);
-  } else if (blockIdx.x == 0) {
-    // every pair of offsets is looked at once, whichever rows it spans
-    bool bad = false;
-    for (int i = tid; i < a.batch; i += kThreads)
-      bad |= row_range(a.cu[i], a.cu[i + 1], a.tokens).bad;
-    if (bad) atomicOr(a.err, kErrIndex);
   }
 
   Place place{};
@@ -712,21 +711,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, bad = false, tail = false;
       const int q_rows = a.tpt * a.G;
       long long pos = share.begin;
+      int block = blockIdx.x, taken = 0;  // packed: the window and head of this round
       for (;; ++nu) {
         const int ub = nu & 1;
+        if (!PAGED && nu > 0) {
+          // asked for once this window's loads are under way: no earlier, so
+          // that the last windows go to the blocks that get there first
+          if (lane == 0) {
+            fence_proxy_async_shared();
+            mbar_arrive_expect_tx(BAR(BAR_TAKE), 16);
+            take_block(smem_u32(&s_answer), BAR(BAR_TAKE));
+          }
+          __syncwarp();
+          ++taken;
+          if (!mbar_wait_warp(BAR(BAR_TAKE), (nu - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          block = taken_block(smem_u32(&s_answer));
+          __syncwarp();
+        }
         if (nu >= 2 && !mbar_wait_warp(BAR(BAR_UNIT_FREE + ub), ((nu >> 1) - 1) & 1, wc)) {
           ok = false;
           break;
         }
         Unit u;
-        u.more = PAGED ? pos < share.end : nu == 0;
+        u.more = PAGED ? pos < share.end : block >= 0;
         int steps = 0, nt = 0;
         if (u.more && PAGED) {
           nt = tiles_of_block(place.r, kNT * a.tpt, place.blk);
           steps = (int)min((long long)(nt - place.t0), share.end - pos);
           paged_unit(a, place, place.t0 + steps, nt, &u);
         } else if (u.more) {
-          packed_unit(a, blockIdx.x, &u);
+          packed_unit(a, block, &u);
+          if (block == 0) {
+            // every pair of offsets is looked at once, whichever rows it spans
+            for (int i = lane; i < a.batch; i += 32)
+              bad |= row_range(a.cu[i], a.cu[i + 1], a.tokens).bad;
+          }
         }
         if (lane == 0) {
           s_unit[ub] = u;
@@ -812,13 +834,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
+      if (bad) atomicOr(a.err, kErrIndex);
       if (PAGED) {
-        if (bad) atomicOr(a.err, kErrIndex);
         if (!tail && lane == 0) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
       }
       // no copy may still be landing when the block exits (matters only when a
       // wait gave up)
       if (lane == 0) {
+        if (taken > 0) drain_wait(BAR(BAR_TAKE), (taken - 1) & 1);
         for (int q = 0; q < 2 && q < nq; ++q) drain_wait(BAR(BAR_Q + q), ((nq - q + 1) / 2 - 1) & 1);
         for (int k = kt > kStages ? kt - kStages : 0; k < kt; ++k)
           drain_wait(BAR(BAR_KV_FULL + k % kStages), (k / kStages) & 1);
@@ -831,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kt = 0, nq = 0, ns = 0, np = 0, no = 0;
       bool ok = true;
       for (int nu = 0; ok; ++nu) {
-        if (!mbar_wait_warp(BAR(BAR_UNIT + (nu & 1)), (nu >> 1) & 1, wc)) break;
+        if (!mbar_wait_inline(BAR(BAR_UNIT + (nu & 1)), (nu >> 1) & 1, wc)) break;
         const Unit& su = s_unit[nu & 1];
         const int more = su.more, nj = su.nj, j0 = su.t0[t], j1 = su.t1[t];
         __syncwarp();
@@ -839,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!more) break;
         if (nj == 0) continue;
         const int qbuf = nq & 1;
-        if (!mbar_wait_warp(BAR(BAR_Q + qbuf), (nq >> 1) & 1, wc)) break;
+        if (!mbar_wait_inline(BAR(BAR_Q + qbuf), (nq >> 1) & 1, wc)) break;
         const uint32_t q_lo = sdesc_lo(sbase + (qbuf * kNT + t) * kTileBytes, 16);
         // step j forms S of key tile j, then O += P V of tile j - 1.  Every
         // stage is waited for and released, whether the row tile uses it or
@@ -847,9 +870,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; ok && j <= nj; ++j) {
           if (j < nj) {
             const int s = (kt + j) % kStages;
-            ok = mbar_wait_warp(BAR(BAR_KV_FULL + s), ((kt + j) / kStages) & 1, wc);
+            ok = mbar_wait_inline(BAR(BAR_KV_FULL + s), ((kt + j) / kStages) & 1, wc);
             if (ok && j >= j0 && j < j1) {
-              ok = ns == 0 || mbar_wait_warp(BAR(BAR_S_FREE + t), (ns - 1) & 1, wc);
+              ok = ns == 0 || mbar_wait_inline(BAR(BAR_S_FREE + t), (ns - 1) & 1, wc);
               if (!ok) break;
               tc_fence_after();
               const uint32_t k_lo = sdesc_lo(sbase + kSmemStage0 + s * kStageBytes, 16);
@@ -868,11 +891,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j > 0) {
             const int i = j - 1, s = (kt + i) % kStages;
             if (i >= j0 && i < j1) {
-              ok = mbar_wait_warp(BAR(BAR_P_FULL + t), np & 1, wc);
+              ok = mbar_wait_inline(BAR(BAR_P_FULL + t), np & 1, wc);
               // the item's first product overwrites O: the epilogue before must
               // have read it
               if (ok && i == j0 && no > 0)
-                ok = mbar_wait_warp(BAR(BAR_O_FREE + t), (no - 1) & 1, wc);
+                ok = mbar_wait_inline(BAR(BAR_O_FREE + t), (no - 1) & 1, wc);
               if (!ok) break;
               // A hint, bounded and without consequence for results: the row
               // tiles' products go one behind the other.  Issued together they
@@ -880,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // softmaxes into step, where they queue for the same units
               // (prompt of 16384 tokens, 32 / 4 heads: 1108 -> 1074 us).
               if (t > 0)
-                for (int spin = 0; spin < 32 && s_turn[t - 1] <= kt + i; ++spin) {}
+                for (int spin = 0; spin < 8 && s_turn[t - 1] <= kt + i; ++spin) {}
               __syncwarp();
               tc_fence_after();
               const uint32_t v_lo =

@@ -226,6 +226,32 @@ __device__ __forceinline__ bool mbar_wait_inline(uint32_t bar, uint32_t parity, 
   return true;
 }
 
+// Takes over a block of this grid that has not started (cluster launch
+// control): the 16-byte answer lands in shared memory and completes on `bar`
+// (16 bytes expected).  After an answer without a block none may be asked for.
+__device__ __forceinline__ void take_block(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" ::"r"(answer),
+      "r"(bar)
+      : "memory");
+}
+
+// The x index of the block an answer hands over, or -1.
+__device__ __forceinline__ int taken_block(uint32_t answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n\t}"
+      : "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
+}
+
 // ---------------------------------------------------------------------------
 // TMA and bulk copies
 // ---------------------------------------------------------------------------
