@@ -9,6 +9,7 @@ if the library is missing or a call fails, an exception is raised.
 """
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -132,8 +133,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                          ctypes.POINTER(AttnDeviceBuffers)]
     lib.attn_step_host_order.restype = ctypes.c_int
     lib.attn_selftest_arith.restype = ctypes.c_int
-    lib.attn_packed_fwd.argtypes = [ctypes.POINTER(AttnPackedShape)] + [vp] * 7
-    gp = ctypes.POINTER(AttnPagedShape)
+    # shapes go in as a struct or as the bytes of one (pointers: void*)
+    lib.attn_packed_fwd.argtypes = [vp] * 8
+    gp = vp
     lib.attn_paged_plan.argtypes = [gp] + [vp] * 10
     lib.attn_paged_store.argtypes = [gp] + [vp] * 6
     lib.attn_paged_workspace_bytes.argtypes = [gp]
@@ -500,6 +502,14 @@ forward_backward_host = attn_step_host
 # ---------------------------------------------------------------------------
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
+# attn_packed_shape and attn_paged_shape as bytes (a call's struct is packed in
+# one step: a token step's calls are as long as their marshalling)
+_PACKED = struct.Struct("@7if8q")
+_PAGED = struct.Struct("@10if14q")
+assert _PACKED.size == ctypes.sizeof(AttnPackedShape)
+assert _PAGED.size == ctypes.sizeof(AttnPagedShape)
+_NO_STRIDES = (0,) * 14
+
 # attn_paged_plan's status bits
 PLAN_PAGES = 1
 PLAN_WIDTH = 2
@@ -537,67 +547,74 @@ class PagedShape:
     scale: float = 0.125
     dtype: torch.dtype = torch.float16
 
-    def c_struct(self) -> AttnPagedShape:
-        return AttnPagedShape(self.batch, self.tokens, self.heads, self.kv_heads, HEAD_DIM,
-                              self.page_size, self.num_pages, self.table_width, self.max_new,
-                              _dtype_code(self.dtype), self.scale)
+    def c_bytes(self, strides=_NO_STRIDES) -> bytes:
+        """attn_paged_shape with the strides of q, o, k, v and the pools."""
+        try:
+            return _PAGED.pack(self.batch, self.tokens, self.heads, self.kv_heads, HEAD_DIM,
+                               self.page_size, self.num_pages, self.table_width, self.max_new,
+                               _dtype_code(self.dtype), self.scale, *strides)
+        except struct.error as e:
+            raise ValueError("a size does not fit the C struct: %s" % e) from None
 
 
 def _dtype_code(dt) -> int:
-    if dt not in _DTYPES:
+    code = _DTYPES.get(dt)
+    if code is None:
         raise TypeError("dtype must be torch.float16 or torch.bfloat16, got %s" % (dt,))
-    return _DTYPES[dt]
+    return code
 
 
-def _strided(t, name, dtype, shape, device):
+def _refuse(t, name, dtype, shape, dev, what):
+    """Raises for an argument that a check turned away."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != dev or dev < 0:
+        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    raise ValueError("%s must be %s" % (name, what))
+
+
+def _strided(t, name, dtype, shape, dev):
     """Pointer and strides of a tensor whose last dimension is dense."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 \
+            and t.shape == shape:
+        st = t.stride()
+        if st[-1] == 1:
+            return t.data_ptr(), st
+    _refuse(t, name, dtype, shape, dev, "dense in its last dimension")
+
+
+def _dense(t, name, dtype, shape, dev):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 \
+            and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev, "contiguous")
+
+
+def _device_of(t, name) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device or device.type != "cuda":
-        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError("%s must be dense in its last dimension" % name)
-    return t.data_ptr(), st
+    return t.get_device()
 
 
-def _dense(t, name, dtype, shape, device):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device or device.type != "cuda":
-        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
-
-
-def _device_of(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch tensor" % name)
-    return t.device
-
-
-def _run(name, device, stream, *args):
+def _run(name, dev, stream, *args):
     """Calls an entry point on the tensors' device and the stream given, or
     that device's current stream."""
+    fn = getattr(_lib or load_library(), name)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
         raise ValueError("the stream belongs to another device than the tensors")
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
     if rc != ATTN_OK:
         raise AttnError(name, rc)
 
@@ -606,18 +623,17 @@ def attn_packed_fwd(s: PackedShape, q, k, v, cu, o, lse=None, stream=None) -> No
     """Attention over packed sequences: q [tokens][heads][64], k, v
     [tokens][kv_heads][64] and o as q, any strides over tokens and heads; cu
     int32 [batch + 1] on the device; lse float32 [heads][tokens] or None."""
-    n, H, Hkv = s.tokens, s.heads, s.kv_heads
+    n, H, Hkv, dt = s.tokens, s.heads, s.kv_heads, s.dtype
     dev = _device_of(q, "q")
-    code = _dtype_code(s.dtype)
-    qp, qs = _strided(q, "q", s.dtype, (n, H, 64), dev)
-    kp, ks = _strided(k, "k", s.dtype, (n, Hkv, 64), dev)
-    vp, vs = _strided(v, "v", s.dtype, (n, Hkv, 64), dev)
-    op, os_ = _strided(o, "o", s.dtype, (n, H, 64), dev)
+    qp, qs = _strided(q, "q", dt, (n, H, 64), dev)
+    kp, ks = _strided(k, "k", dt, (n, Hkv, 64), dev)
+    vp, vs = _strided(v, "v", dt, (n, Hkv, 64), dev)
+    op, os_ = _strided(o, "o", dt, (n, H, 64), dev)
     cup = _dense(cu, "cu", torch.int32, (s.batch + 1,), dev)
     lp = None if lse is None else _dense(lse, "lse", torch.float32, (H, n), dev)
-    shape = AttnPackedShape(n, s.batch, H, Hkv, HEAD_DIM, 1 if s.causal else 0, code, s.scale,
-                            qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
-    _run("attn_packed_fwd", dev, stream, ctypes.byref(shape), qp, kp, vp, cup, op, lp)
+    shape = _PACKED.pack(n, s.batch, H, Hkv, HEAD_DIM, 1 if s.causal else 0, _dtype_code(dt),
+                         s.scale, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
+    _run("attn_packed_fwd", dev, stream, shape, qp, kp, vp, cup, op, lp)
 
 
 def attn_paged_plan(s: PagedShape, cached, fresh, ring, state, table, cu, lens, slots, next,
@@ -626,40 +642,31 @@ def attn_paged_plan(s: PagedShape, cached, fresh, ring, state, table, cu, lens, 
     (int32 CUDA tensors; see attn.h).  ``fresh`` < 0 marks a finished request."""
     B, i32 = s.batch, torch.int32
     dev = _device_of(cached, "cached")
-    args = (_dense(cached, "cached", i32, (B,), dev), _dense(fresh, "fresh", i32, (B,), dev),
-            _dense(ring, "ring", i32, (s.num_pages,), dev), _dense(state, "state", i32, (4,), dev),
-            _dense(table, "table", i32, (B, s.table_width), dev),
-            _dense(cu, "cu", i32, (B + 1,), dev), _dense(lens, "lens", i32, (B,), dev),
-            _dense(slots, "slots", i32, (s.tokens,), dev), _dense(next, "next", i32, (4,), dev))
-    shape = s.c_struct()
-    _run("attn_paged_plan", dev, stream, ctypes.byref(shape), *args)
-
-
-def _pool_strides(s, shape, k_cache, v_cache, dev):
-    dims = (s.num_pages, s.kv_heads, s.page_size, 64)
-    kp, ks = _strided(k_cache, "k_cache", s.dtype, dims, dev)
-    vp, vs = _strided(v_cache, "v_cache", s.dtype, dims, dev)
-    shape.kc_page, shape.kc_head, shape.kc_row = ks[0], ks[1], ks[2]
-    shape.vc_page, shape.vc_head, shape.vc_row = vs[0], vs[1], vs[2]
-    return kp, vp
+    _run("attn_paged_plan", dev, stream, s.c_bytes(),
+         _dense(cached, "cached", i32, (B,), dev), _dense(fresh, "fresh", i32, (B,), dev),
+         _dense(ring, "ring", i32, (s.num_pages,), dev), _dense(state, "state", i32, (4,), dev),
+         _dense(table, "table", i32, (B, s.table_width), dev),
+         _dense(cu, "cu", i32, (B + 1,), dev), _dense(lens, "lens", i32, (B,), dev),
+         _dense(slots, "slots", i32, (s.tokens,), dev), _dense(next, "next", i32, (4,), dev))
 
 
 def attn_paged_store(s: PagedShape, k, v, slots, k_cache, v_cache, stream=None) -> None:
     """Rows of k, v [tokens][kv_heads][64] into the caches
     [num_pages][kv_heads][page_size][64] (any strides) at slots int32 [tokens]."""
-    dev = _device_of(k, "k")
-    shape = s.c_struct()
-    kp, ks = _strided(k, "k", s.dtype, (s.tokens, s.kv_heads, 64), dev)
-    vp, vs = _strided(v, "v", s.dtype, (s.tokens, s.kv_heads, 64), dev)
+    dev, dt = _device_of(k, "k"), s.dtype
+    rows, dims = (s.tokens, s.kv_heads, 64), (s.num_pages, s.kv_heads, s.page_size, 64)
+    kp, ks = _strided(k, "k", dt, rows, dev)
+    vp, vs = _strided(v, "v", dt, rows, dev)
     sp = _dense(slots, "slots", torch.int32, (s.tokens,), dev)
-    kc, vc = _pool_strides(s, shape, k_cache, v_cache, dev)
-    shape.k_token, shape.k_head, shape.v_token, shape.v_head = ks[0], ks[1], vs[0], vs[1]
-    _run("attn_paged_store", dev, stream, ctypes.byref(shape), kp, vp, sp, kc, vc)
+    kc, kcs = _strided(k_cache, "k_cache", dt, dims, dev)
+    vc, vcs = _strided(v_cache, "v_cache", dt, dims, dev)
+    _run("attn_paged_store", dev, stream,
+         s.c_bytes((0, 0, 0, 0, ks[0], ks[1], vs[0], vs[1]) + kcs[:3] + vcs[:3]), kp, vp, sp, kc,
+         vc)
 
 
 def paged_workspace_bytes(s: PagedShape) -> int:
-    shape = s.c_struct()
-    n = load_library().attn_paged_workspace_bytes(ctypes.byref(shape))
+    n = load_library().attn_paged_workspace_bytes(s.c_bytes())
     if n == 0:
         raise AttnError("attn_paged_workspace_bytes", ATTN_ERR_SHAPE)
     return n
@@ -675,22 +682,23 @@ def attn_paged_fwd(s: PagedShape, q, k_cache, v_cache, table, cu, lens, ws, o, l
                    stream=None) -> None:
     """Attention of the new rows q [tokens][heads][64] over the cache; o as q,
     lse float32 [heads][tokens] or None; ws from alloc_paged_workspace."""
-    n, H = s.tokens, s.heads
+    n, H, B, dt = s.tokens, s.heads, s.batch, s.dtype
     dev = _device_of(q, "q")
-    shape = s.c_struct()
-    qp, qs = _strided(q, "q", s.dtype, (n, H, 64), dev)
-    op, os_ = _strided(o, "o", s.dtype, (n, H, 64), dev)
-    kc, vc = _pool_strides(s, shape, k_cache, v_cache, dev)
-    shape.q_token, shape.q_head, shape.o_token, shape.o_head = qs[0], qs[1], os_[0], os_[1]
-    tp = _dense(table, "table", torch.int32, (s.batch, s.table_width), dev)
-    cup = _dense(cu, "cu", torch.int32, (s.batch + 1,), dev)
-    lenp = _dense(lens, "lens", torch.int32, (s.batch,), dev)
+    dims = (s.num_pages, s.kv_heads, s.page_size, 64)
+    qp, qs = _strided(q, "q", dt, (n, H, 64), dev)
+    op, os_ = _strided(o, "o", dt, (n, H, 64), dev)
+    kc, kcs = _strided(k_cache, "k_cache", dt, dims, dev)
+    vc, vcs = _strided(v_cache, "v_cache", dt, dims, dev)
+    tp = _dense(table, "table", torch.int32, (B, s.table_width), dev)
+    cup = _dense(cu, "cu", torch.int32, (B + 1,), dev)
+    lenp = _dense(lens, "lens", torch.int32, (B,), dev)
     lp = None if lse is None else _dense(lse, "lse", torch.float32, (H, n), dev)
-    if not (isinstance(ws, torch.Tensor) and ws.dtype == torch.uint8 and ws.is_contiguous()
-            and ws.device == dev):
+    if not (isinstance(ws, torch.Tensor) and ws.dtype is torch.uint8 and ws.is_contiguous()
+            and ws.get_device() == dev):
         raise TypeError("ws must be a contiguous uint8 CUDA tensor on the device of the others")
-    _run("attn_paged_fwd", dev, stream, ctypes.byref(shape), qp, kc, vc, tp, cup, lenp,
-         ws.data_ptr(), ws.numel(), op, lp)
+    _run("attn_paged_fwd", dev, stream,
+         s.c_bytes((qs[0], qs[1], os_[0], os_[1], 0, 0, 0, 0) + kcs[:3] + vcs[:3]), qp, kc, vc, tp,
+         cup, lenp, ws.data_ptr(), ws.numel(), op, lp)
 
 
 class PagedCache:

@@ -10,47 +10,62 @@ namespace css {
 namespace {
 
 constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = kJoinThreads / 8;  // rows of a block: eight threads a row
 
-// One block a tail part: O = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m).
+// O = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m), in the order of the keys.
+// Block (x, y) joins rows [16 y, 16 y + 16) of the item whose tail part block
+// x of the first kernel (x < n1) or of the second wrote.  Latency bound: the
+// parts lie in L2, and every block's loads of one row's m and l go out
+// together before they are used.
 template <bool BF16>
 __global__ void __launch_bounds__(kJoinThreads)
-    join_kernel(const PartArgs p, const RowsArg o, float* lse, int tokens, int G) {
+    join_kernel(const PartArgs p1, int n1, const PartArgs p2, const RowsArg o, float* lse,
+                int tokens, int G) {
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x;
+  const bool one = (int)blockIdx.x < n1;
+  const PartArgs& p = one ? p1 : p2;
+  const int c = one ? blockIdx.x : blockIdx.x - n1;
   const PartDesc d = p.desc[c];
-  const int c0 = (threadIdx.x & 7) * 8;
-  for (int row = threadIdx.x >> 3; row < d.rows; row += kJoinThreads / 8) {
-    float m = -INFINITY;
-    for (int b = c; b <= d.last; ++b) m = fmaxf(m, p.ml[part_row(p, b, b == c, row)].x);
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 3), lane = threadIdx.x & 7;
+  if (row >= d.rows) return;  // the eight threads of a row together
+  const unsigned mask = 0xffu << (threadIdx.x & 24);
+  const int c0 = lane * 8;
+  // part i of n: the tail part of block c, then head parts
+  const int n = d.last - c + 1;
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 8) m = fmaxf(m, p.ml[part_row(p, c + i, i == 0, row)].x);
+#pragma unroll
+  for (int by = 1; by < 8; by <<= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, by));
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
 #pragma unroll 4
-    for (int b = c; b <= d.last; ++b) {
-      const long long at = part_row(p, b, b == c, row);
-      const float2 ml = p.ml[at];
-      const float4* const s = reinterpret_cast<const float4*>(p.o + at * 64 + c0);
-      const float4 x = s[0], y = s[1];
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // no key of this part is seen
-      const float f = ex2_approx(ml.x - m);
-      l = fmaf(ml.y, f, l);
-      acc[0] = fmaf(x.x, f, acc[0]);
-      acc[1] = fmaf(x.y, f, acc[1]);
-      acc[2] = fmaf(x.z, f, acc[2]);
-      acc[3] = fmaf(x.w, f, acc[3]);
-      acc[4] = fmaf(y.x, f, acc[4]);
-      acc[5] = fmaf(y.y, f, acc[5]);
-      acc[6] = fmaf(y.z, f, acc[6]);
-      acc[7] = fmaf(y.w, f, acc[7]);
-    }
-    write_row<BF16>(o, lse, tokens, d.q0 + row / G, d.kv * G + row % G, c0, acc, m, l);
+  for (int i = 0; i < n; ++i) {
+    const long long at = part_row(p, c + i, i == 0, row);
+    const float2 ml = p.ml[at];
+    const float4* const s = reinterpret_cast<const float4*>(p.o + at * 64 + c0);
+    const float4 x = s[0], y = s[1];
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // no key of this part is seen
+    const float f = ex2_approx(ml.x - m);
+    l = fmaf(ml.y, f, l);
+    acc[0] = fmaf(x.x, f, acc[0]);
+    acc[1] = fmaf(x.y, f, acc[1]);
+    acc[2] = fmaf(x.z, f, acc[2]);
+    acc[3] = fmaf(x.w, f, acc[3]);
+    acc[4] = fmaf(y.x, f, acc[4]);
+    acc[5] = fmaf(y.y, f, acc[5]);
+    acc[6] = fmaf(y.z, f, acc[6]);
+    acc[7] = fmaf(y.w, f, acc[7]);
   }
+  write_row<BF16>(o, lse, tokens, d.q0 + row / G, d.kv * G + row % G, c0, acc, m, l);
 }
 
-int launch_join(const PagedDims& d, const PartArgs& part, int blocks, const RowsArg& o, float* lse,
-                cudaStream_t stream) {
+int launch_join(const PagedDims& d, const PartArgs& p1, int n1, const PartArgs& p2, int n2,
+                const RowsArg& o, float* lse, cudaStream_t stream) {
+  const int rows = n2 > 0 ? p2.rows : p1.rows;
   return cuda_status(launch_dependent(d.bf16 ? join_kernel<true> : join_kernel<false>,
-                                      dim3(blocks), dim3(kJoinThreads), 0, stream, part, o, lse,
-                                      d.tokens, d.G));
+                                      dim3(n1 + n2, (rows + kJoinRows - 1) / kJoinRows),
+                                      dim3(kJoinThreads), 0, stream, p1, n1, p2, o, lse, d.tokens,
+                                      d.G));
 }
 
 // The largest grid of the split kernels on any device this library runs on:
@@ -104,22 +119,22 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
   const int ntok = decode_tokens(d.G);
   const int sms = ctx.sm_count < kMaxSm ? ctx.sm_count : kMaxSm;
   uint8_t* at = static_cast<uint8_t*>(ws);
-  int rc;
+  PartArgs few{}, rows{};
+  int n_few = 0, n_rows = 0, rc;
   if (ntok > 0) {
-    const int blocks = 2 * sms;
-    const PartArgs part = parts_at(at, 2 * kMaxSm, kDecodeRows, 2);
+    few = parts_at(at, 2 * kMaxSm, kDecodeRows, 2);
     at += parts_bytes(2 * kMaxSm, kDecodeRows);
-    rc = launch_paged_decode(d, ctx, q, kc, vc, table, cu, lens, part, blocks, o, lse, stream);
+    n_few = 2 * sms;
+    rc = launch_paged_decode(d, ctx, q, kc, vc, table, cu, lens, few, n_few, o, lse, stream);
     if (rc != ATTN_OK) return rc;
-    if ((rc = launch_join(d, part, blocks, o, lse, stream)) != ATTN_OK) return rc;
   }
   if (d.max_new > ntok) {
-    const PartArgs part = parts_at(at, kMaxSm, kItemRows, 2);
-    rc = launch_paged_rows(d, ctx, q, kc, vc, table, cu, lens, part, sms, ntok, o, lse, stream);
+    rows = parts_at(at, kMaxSm, kItemRows, 2);
+    n_rows = sms;
+    rc = launch_paged_rows(d, ctx, q, kc, vc, table, cu, lens, rows, n_rows, ntok, o, lse, stream);
     if (rc != ATTN_OK) return rc;
-    if ((rc = launch_join(d, part, sms, o, lse, stream)) != ATTN_OK) return rc;
   }
-  return ATTN_OK;
+  return launch_join(d, few, n_few, rows, n_rows, o, lse, stream);
 }
 
 }  // namespace css

@@ -79,8 +79,9 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs a) 
   }
   __syncthreads();
   Sums before{0, 0, 0}, total{0, 0, 0};
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  const int used = (a.batch + 32 * kPer - 1) / (32 * kPer);  // warps that hold requests
+#pragma unroll 4
+  for (int w = 0; w < used; ++w) {
     if (w == warp) before = total;
     total = total + s_warp[w];
     status |= s_status[w];

@@ -169,7 +169,7 @@ def test_python_binding_refuses_cpu_tensors_and_types():
     with pytest.raises(TypeError):
         api.attn_packed_fwd(s, None, h(4, 1, 64), h(4, 1, 64), i(2), h(4, 2, 64))
     with pytest.raises(TypeError):
-        api.PagedShape(1, 1, 1, 1, 16, 4, 4, dtype=torch.float32).c_struct()
+        api.PagedShape(1, 1, 1, 1, 16, 4, 4, dtype=torch.float32).c_bytes()
     with pytest.raises(api.AttnError):
         api.paged_workspace_bytes(api.PagedShape(1, 1, 3, 2, 16, 4, 4))
     p = api.PagedShape(2, 4, 2, 1, 16, 4, 4)
