@@ -85,32 +85,47 @@ __device__ __forceinline__ int tiles_of(int n_keys) {
   return n_keys <= 0 ? 1 : (n_keys - 1) / kTileKeys + 1;
 }
 
-// A run of tiles [t0, t1) of one request and K/V head.
-struct Segment {
-  int req, kv, t0, t1, nt;
+// A place in the tile list: tile t0 of nt of a request and K/V head.
+struct Place {
+  Request r;
+  int req, kv, t0, nt;
 };
 
-// The segment at position pos of the tile list, cut at `end`.  pre[i] counts
-// the tiles of one head of the requests before i.
-__device__ __forceinline__ Segment segment_at(const long long* pre, int batch, int Hkv,
-                                              long long pos, long long end) {
-  int lo = 0, hi = batch;  // the last i with pre[i] * Hkv <= pos: never an empty request
+// The place at position pos.  pre[i] counts the tiles of one head of the
+// requests before i.
+__device__ __forceinline__ Place place_at(const DecodeArgs& a, const long long* pre,
+                                          long long pos) {
+  int lo = 0, hi = a.batch;  // the last i with pre[i] * Hkv <= pos: never an empty request
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (pre[mid] * Hkv <= pos)
+    if (pre[mid] * a.Hkv <= pos)
       lo = mid + 1;
     else
       hi = mid;
   }
-  Segment s;
-  s.req = lo - 1;
-  s.nt = (int)(pre[s.req + 1] - pre[s.req]);
-  const long long off = pos - pre[s.req] * Hkv;
-  s.kv = (int)(off / s.nt);
-  s.t0 = (int)(off - (long long)s.kv * s.nt);
-  const long long left = end - pos;
-  s.t1 = left < s.nt - s.t0 ? s.t0 + (int)left : s.nt;
-  return s;
+  Place p;
+  p.req = lo - 1;
+  p.nt = (int)(pre[lo] - pre[p.req]);
+  const long long off = pos - pre[p.req] * a.Hkv;
+  p.kv = (int)quot(off, p.nt);
+  p.t0 = (int)(off - (long long)p.kv * p.nt);
+  bool b;
+  p.r = request_at(a, p.req, &b);
+  return p;
+}
+
+// The place behind an item: the next head or the next request with tiles.
+// Called only where the list goes on.
+__device__ __forceinline__ void next_place(const DecodeArgs& a, const long long* pre, Place* p) {
+  p->t0 = 0;
+  if (++p->kv < a.Hkv) return;
+  p->kv = 0;
+  do {
+    ++p->req;
+    p->nt = (int)(pre[p->req + 1] - pre[p->req]);
+  } while (p->nt == 0 && p->req + 1 < a.batch);
+  bool b;
+  p->r = request_at(a, p->req, &b);
 }
 
 template <bool BF16>
@@ -186,13 +201,34 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int per_tile = (1 << a.shift) >= kTileKeys ? 0 : boxes;
     int it = 0, nq = 0;
     bool ok = true, bad = false;
+    // page ids go 32 at a time: lane l of group g has page first + 32 g + l.
+    // The first two groups of the next item are read while this one runs.
+    Place nx{};
+    int nx_ids = 0, nx_next = 0;
+    const auto read_ids = [&] {
+      const int32_t* const row = a.table + (long long)nx.req * a.width;
+      const int at = (int)(((long long)nx.t0 * kTileKeys) >> a.shift) + lane;
+      const int n = (int)pages_for(nx.r.n_keys, a.shift);
+      nx_ids = at < n ? row[at] : a.pages;
+      nx_next = at + 32 < n ? row[at + 32] : a.pages;
+    };
+    if (share.begin < share.end) {
+      nx = place_at(a, s_pre, share.begin);
+      read_ids();
+    }
     for (long long pos = share.begin; ok && pos < share.end;) {
-      const Segment sg = segment_at(s_pre, a.batch, a.Hkv, pos, share.end);
-      pos += sg.t1 - sg.t0;
-      bool b;
-      const Request r = request_at(a, sg.req, &b);
+      const Place sg = nx;
+      const Request r = sg.r;
+      const int t1 = (int)min((long long)sg.nt, sg.t0 + (share.end - pos));
       const int32_t* const row = a.table + (long long)sg.req * a.width;
       const int n_pages = (int)pages_for(r.n_keys, a.shift);
+      int base = (int)(((long long)sg.t0 * kTileKeys) >> a.shift);
+      int ids = nx_ids, next = nx_next;
+      pos += t1 - sg.t0;
+      if (pos < share.end) {
+        next_place(a, s_pre, &nx);
+        read_ids();
+      }
       const int qbuf = nq & 1;
       ok = !(nq >= 2) || mbar_wait_warp(BAR(BAR_Q_FREE + qbuf), ((nq >> 1) - 1) & 1, wc);
       if (!ok) break;
@@ -201,13 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tma_load_4d(sbase + kSmemQ + qbuf * kQ, &tm_q, BAR(BAR_Q + qbuf), 0, 0, sg.kv, r.q0);
       }
       ++nq;
-      // page ids, 32 at a time and one group ahead: lane l of group g has page
-      // first + 32 g + l
-      const int first = (int)(((long long)sg.t0 * kTileKeys) >> a.shift);
-      int base = first;
-      int ids = base + lane < n_pages ? row[base + lane] : a.pages;
-      int next = base + 32 + lane < n_pages ? row[base + 32 + lane] : a.pages;
-      for (int t = sg.t0; t < sg.t1; ++t, ++it) {
+      for (int t = sg.t0; t < t1; ++t, ++it) {
         const int s = it % kStages;
         if (it >= kStages && !mbar_wait_warp(BAR(BAR_EMPTY + s), (it / kStages - 1) & 1, wc)) {
           ok = false;
@@ -250,11 +280,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int mi = lane >> 3, mr = lane & 7;
     int it = 0, nq = 0;
     bool ok = true, tail = false;
+    Place sg{};
+    if (share.begin < share.end) sg = place_at(a, s_pre, share.begin);
     for (long long pos = share.begin; pos < share.end;) {
-      const Segment sg = segment_at(s_pre, a.batch, a.Hkv, pos, share.end);
-      pos += sg.t1 - sg.t0;
-      bool b;
-      const Request r = request_at(a, sg.req, &b);
+      const Request r = sg.r;
+      const int t1 = (int)min((long long)sg.nt, sg.t0 + (share.end - pos));
+      pos += t1 - sg.t0;
       const int rows = r.n_new * a.G;
       const int qbuf = nq & 1;
       uint32_t q[4][4];
@@ -277,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-      for (int t = sg.t0; t < sg.t1; ++t, ++it) {
+      for (int t = sg.t0; t < t1; ++t, ++it) {
         const int s = it % kStages;
         ok = ok && mbar_wait_warp(BAR(BAR_FULL + s), (it / kStages) & 1, wc);
         if (!ok) continue;
@@ -412,17 +443,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int e = 0; e < 8; ++e) acc[e] = fmaf(d[e], f, acc[e]);
         }
         const int tok = r.q0 + row / a.G, h = sg.kv * a.G + row % a.G;
-        if (sg.t0 == 0 && sg.t1 == sg.nt)
+        if (sg.t0 == 0 && t1 == sg.nt)
           write_row<BF16>(a.o, a.lse, a.tokens, tok, h, c0, acc, m, l);
         else
           store_part(a.part, blockIdx.x, sg.t0 == 0, row, c0, acc, m, l);
       }
-      if (sg.t0 == 0 && sg.t1 < sg.nt) {
+      if (sg.t0 == 0 && t1 < sg.nt) {
         tail = true;
         if (tid == 0)
           a.part.desc[blockIdx.x] =
-              PartDesc{r.q0, sg.kv, rows, last_block(share, pos - sg.t1 + sg.nt - 1)};
+              PartDesc{r.q0, sg.kv, rows, last_block(share, pos - t1 + sg.nt - 1)};
       }
+      if (pos < share.end) next_place(a, s_pre, &sg);
       named_barrier_sync(1, kConsumers * 32);
     }
     if (tid == 0 && !tail) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};

@@ -12,51 +12,72 @@ namespace {
 constexpr int kJoinThreads = 128;
 constexpr int kJoinRows = kJoinThreads / 8;  // rows of a block: eight threads a row
 
-// O = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m), in the order of the keys.
-// Block (x, y) joins rows [16 y, 16 y + 16) of the item whose tail part block
-// x of the first kernel (x < n1) or of the second wrote.  Latency bound: the
-// parts lie in L2, and every block's loads of one row's m and l go out
-// together before they are used.
+// O = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m).  Block (x, y) joins rows
+// [16 y, 16 y + 16) of the item whose tail part block x of the first kernel
+// (x < n1) or of the second wrote.  Latency bound, the parts lie in L2: with
+// fewer than 16 rows the threads that are left take every g-th part of a row,
+// and the g sums are added in order, so the result does not depend on timing.
 template <bool BF16>
 __global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const PartArgs p1, int n1, const PartArgs p2, const RowsArg o, float* lse,
                 int tokens, int G) {
+  __shared__ float s_sum[kJoinRows][8][9];
   griddep_launch_dependents();
   griddep_wait();
   const bool one = (int)blockIdx.x < n1;
   const PartArgs& p = one ? p1 : p2;
   const int c = one ? blockIdx.x : blockIdx.x - n1;
   const PartDesc d = p.desc[c];
-  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 3), lane = threadIdx.x & 7;
-  if (row >= d.rows) return;  // the eight threads of a row together
-  const unsigned mask = 0xffu << (threadIdx.x & 24);
-  const int c0 = lane * 8;
-  // part i of n: the tail part of block c, then head parts
-  const int n = d.last - c + 1;
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 8) m = fmaxf(m, p.ml[part_row(p, c + i, i == 0, row)].x);
+  const int row0 = blockIdx.y * kJoinRows, rows = min(d.rows - row0, kJoinRows);
+  if (rows <= 0) return;  // the whole block
+  int span = 1;           // rows rounded up to a power of two
+  while (span < rows) span <<= 1;
+  const int slot = threadIdx.x >> 3, lane = threadIdx.x & 7, c0 = lane * 8;
+  const int at_row = slot & (span - 1), group = slot / span, groups = kJoinRows / span;
+  const int row = row0 + at_row;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f, m = -INFINITY;
+  if (at_row < rows) {
+    // part i of n: the tail part of block c, then head parts
+    const unsigned mask = 0xffu << (threadIdx.x & 24);
+    const int n = d.last - c + 1;
+    for (int i = lane; i < n; i += 8) m = fmaxf(m, p.ml[part_row(p, c + i, i == 0, row)].x);
 #pragma unroll
-  for (int by = 1; by < 8; by <<= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, by));
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
+    for (int by = 1; by < 8; by <<= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, by));
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const long long at = part_row(p, c + i, i == 0, row);
-    const float2 ml = p.ml[at];
-    const float4* const s = reinterpret_cast<const float4*>(p.o + at * 64 + c0);
-    const float4 x = s[0], y = s[1];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // no key of this part is seen
-    const float f = ex2_approx(ml.x - m);
-    l = fmaf(ml.y, f, l);
-    acc[0] = fmaf(x.x, f, acc[0]);
-    acc[1] = fmaf(x.y, f, acc[1]);
-    acc[2] = fmaf(x.z, f, acc[2]);
-    acc[3] = fmaf(x.w, f, acc[3]);
-    acc[4] = fmaf(y.x, f, acc[4]);
-    acc[5] = fmaf(y.y, f, acc[5]);
-    acc[6] = fmaf(y.z, f, acc[6]);
-    acc[7] = fmaf(y.w, f, acc[7]);
+    for (int i = group; i < n; i += groups) {
+      const long long at = part_row(p, c + i, i == 0, row);
+      const float2 ml = p.ml[at];
+      const float4* const s = reinterpret_cast<const float4*>(p.o + at * 64 + c0);
+      const float4 x = s[0], y = s[1];
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // no key of this part is seen
+      const float f = ex2_approx(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      acc[0] = fmaf(x.x, f, acc[0]);
+      acc[1] = fmaf(x.y, f, acc[1]);
+      acc[2] = fmaf(x.z, f, acc[2]);
+      acc[3] = fmaf(x.w, f, acc[3]);
+      acc[4] = fmaf(y.x, f, acc[4]);
+      acc[5] = fmaf(y.y, f, acc[5]);
+      acc[6] = fmaf(y.z, f, acc[6]);
+      acc[7] = fmaf(y.w, f, acc[7]);
+    }
   }
-  write_row<BF16>(o, lse, tokens, d.q0 + row / G, d.kv * G + row % G, c0, acc, m, l);
+  if (groups > 1) {
+    float* const mine = s_sum[slot][lane];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mine[e] = acc[e];
+    mine[8] = l;
+    __syncthreads();
+    if (group != 0) return;
+    for (int g = 1; g < groups; ++g) {
+      const float* const other = s_sum[g * span + at_row][lane];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += other[e];
+      l += other[8];
+    }
+  }
+  if (at_row < rows)
+    write_row<BF16>(o, lse, tokens, d.q0 + row / G, d.kv * G + row % G, c0, acc, m, l);
 }
 
 int launch_join(const PagedDims& d, const PartArgs& p1, int n1, const PartArgs& p2, int n2,
@@ -122,7 +143,7 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
   PartArgs few{}, rows{};
   int n_few = 0, n_rows = 0, rc;
   if (ntok > 0) {
-    few = parts_at(at, 2 * kMaxSm, kDecodeRows, 2);
+    few = parts_at(at, 2 * kMaxSm, kDecodeRows, 4);
     at += parts_bytes(2 * kMaxSm, kDecodeRows);
     n_few = 2 * sms;
     rc = launch_paged_decode(d, ctx, q, kc, vc, table, cu, lens, few, n_few, o, lse, stream);

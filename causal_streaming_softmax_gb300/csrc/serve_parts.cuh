@@ -2,8 +2,8 @@
 // of rows whose keys were split between blocks.
 //
 // The list holds the tiles of every work item (a request's block of rows and a
-// K/V head) one item behind the other.  Block c of n takes the positions
-// [c W / n, (c + 1) W / n), so that at most its first and its last item are
+// K/V head) one item behind the other.  The n blocks take equal runs of it (to one
+// position), so that at most its first and its last item are
 // shared with other blocks.  Of a shared item each block writes the running
 // maximum m, the sum l and the unscaled O in binary32: the block that starts
 // the item into its tail part, the later ones into their head parts.  The
@@ -20,28 +20,39 @@
 
 namespace css {
 
+// a / b of non-negative numbers: the 32-bit division where both fit (a 64-bit
+// one is some four hundred clocks, and several stand before a block's first
+// load).
+__host__ __device__ inline long long quot(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 struct Share {
-  long long begin, end, total;
-  int blocks;
+  long long begin, end;
+  long long each;  // positions of a block; the first `more` blocks take one more
+  int more, blocks;
 };
 
 __host__ __device__ inline Share share_of(long long total, int min_tiles, int grid, int block) {
   Share s;
-  s.total = total;
-  const long long most = total / min_tiles;
+  const long long most = quot(total, min_tiles);
   s.blocks = most < 1 ? 1 : (most < grid ? (int)most : grid);
+  s.each = quot(total, s.blocks);
+  s.more = (int)(total - s.each * s.blocks);
   if (block >= s.blocks) {
     s.begin = s.end = total;
   } else {
-    s.begin = (long long)block * total / s.blocks;
-    s.end = (long long)(block + 1) * total / s.blocks;
+    s.begin = block * s.each + (block < s.more ? block : s.more);
+    s.end = s.begin + s.each + (block < s.more ? 1 : 0);
   }
   return s;
 }
 
 // The block whose share holds position x.
 __host__ __device__ inline int last_block(const Share& s, long long x) {
-  return (int)(((x + 1) * s.blocks - 1) / s.total);
+  const long long big = s.more * (s.each + 1);  // positions of the longer shares
+  return x < big ? (int)quot(x, s.each + 1) : s.more + (int)quot(x - big, s.each);
 }
 
 __device__ __forceinline__ long long part_row(const PartArgs& p, int block, bool tail, int row) {

@@ -132,13 +132,14 @@ constexpr uint32_t idesc(int N, int b_mn) {
 __host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
   long long s = 0;
   while (n > 0) {
-    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
+    const long long qa = quot(a, m), qb = quot(b, m);
+    s += n * (n - 1) / 2 * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
     const long long y = a * n + b;
     if (y < m) break;
-    n = y / m;
-    b = y % m;
+    n = quot(y, m);
+    b = y - n * m;
     const long long x = a;
     a = m;
     m = x;
@@ -173,7 +174,7 @@ __device__ __forceinline__ long long tiles_before(const PagedReq& r, int w, int 
   }
   // blocks that end at or before key 0 count one tile
   long long lead = 0;
-  if (base < 0) lead = min(full, (-base) / w);
+  if (base < 0) lead = min(full, quot(-base, w));
   const long long b0 = base + lead * w;  // > -w
   return s + lead + floor_sum(full - lead, kBN, w, b0 + w + kBN - 1);
 }
@@ -206,7 +207,7 @@ __device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pr
   p.r = paged_req(a, p.req, &b);
   const int w = kNT * a.tpt;
   const long long per = pre[lo] - pre[p.req], off = pos - pre[p.req] * a.Hkv;
-  p.kv = (int)(off / per);
+  p.kv = (int)quot(off, per);
   const long long at = off - (long long)p.kv * per;
   int x = 0, y = (p.r.n_new + w - 1) / w;  // the last block with tiles_before <= at
   while (x < y) {
