@@ -570,7 +570,7 @@ def _refuse(t, name, dtype, shape, dev, what):
         raise TypeError("%s must be a torch tensor" % name)
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.get_device() != dev or dev < 0:
+    if t.get_device() != dev:
         raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
@@ -579,22 +579,28 @@ def _refuse(t, name, dtype, shape, dev, what):
 
 def _strided(t, name, dtype, shape, dev):
     """Pointer and strides of a tensor whose last dimension is dense."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 \
-            and t.shape == shape:
-        st = t.stride()
-        if st[-1] == 1:
-            return t.data_ptr(), st
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+            st = t.stride()
+            if st[-1] == 1:
+                return t.data_ptr(), st
+    except AttributeError:  # not a tensor
+        pass
     _refuse(t, name, dtype, shape, dev, "dense in its last dimension")
 
 
 def _dense(t, name, dtype, shape, dev):
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 \
-            and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _refuse(t, name, dtype, shape, dev, "contiguous")
 
 
 def _device_of(t, name) -> int:
+    """The tensor's device, on which all others have to be (_run refuses -1,
+    host memory)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     return t.get_device()
@@ -603,6 +609,8 @@ def _device_of(t, name) -> int:
 def _run(name, dev, stream, *args):
     """Calls an entry point on the tensors' device and the stream given, or
     that device's current stream."""
+    if dev < 0:
+        raise ValueError("%s takes CUDA tensors" % name)
     fn = getattr(_lib or load_library(), name)
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(dev)

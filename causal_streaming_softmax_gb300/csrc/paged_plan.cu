@@ -21,9 +21,7 @@
 namespace css {
 namespace {
 
-constexpr int kThreads = 1024;
 constexpr int kPer = 4;  // requests a thread scans
-constexpr int kMaxBatch = kThreads * kPer;
 
 struct PlanArgs {
   int batch, tokens, pages, width, shift;
@@ -45,7 +43,9 @@ __device__ __forceinline__ Sums shfl_up(const Sums& a, int by) {
               __shfl_up_sync(0xffffffffu, a.back, by)};
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs a) {
+  constexpr int kMaxBatch = kThreads * kPer;
   __shared__ int s_cu[kMaxBatch + 1], s_need[kMaxBatch + 1], s_back[kMaxBatch + 1];
   __shared__ Sums s_warp[kThreads / 32];
   __shared__ int s_status[kThreads / 32];
@@ -164,13 +164,22 @@ int launch_paged_plan(const PagedDims& d, const DevCtx& ctx, const int32_t* cach
                       const int32_t* fresh, int32_t* ring, const int32_t* state, int32_t* table,
                       int32_t* cu, int32_t* lens, int32_t* slots, int32_t* next,
                       cudaStream_t stream) {
-  static_assert(kMaxBatch >= 4096, "admitted batch");
-  const int blocks = (d.tokens + 2 * kThreads - 1) / (2 * kThreads);
   const PlanArgs args{d.batch, d.tokens, d.pages, d.width, d.shift, cached, fresh, state,
                       ring,    table,    cu,      lens,    slots,   next,   ctx.err};
-  return cuda_status(launch_dependent(
-      paged_plan_kernel, dim3(blocks < 1 ? 1 : (blocks > ctx.sm_count ? ctx.sm_count : blocks)),
-      dim3(kThreads), 0, stream, args));
+  // 256 threads scan up to 1024 requests, 1024 threads 4096: the smaller block
+  // starts and meets faster (64 requests 3.7 us against 4.2, 512 requests with
+  // 110,000 slots 5.8 against 6.7; 128 threads measured the same as 256).
+  const auto blocks = [&](int threads) {
+    const int n = (d.tokens + 2 * threads - 1) / (2 * threads);
+    const int most = ctx.sm_count * (1024 / threads);
+    return dim3(n < 1 ? 1 : (n > most ? most : n));
+  };
+  if (d.batch <= 256 * kPer)
+    return cuda_status(
+        launch_dependent(paged_plan_kernel<256>, blocks(256), dim3(256), 0, stream, args));
+  static_assert(1024 * kPer >= 4096, "admitted batch");
+  return cuda_status(
+      launch_dependent(paged_plan_kernel<1024>, blocks(1024), dim3(1024), 0, stream, args));
 }
 
 }  // namespace css
