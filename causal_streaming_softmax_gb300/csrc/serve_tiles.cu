@@ -344,6 +344,18 @@ __device__ __forceinline__ float max32(const uint32_t (&v)[32], float m) {
   return fmaxf(a, b);
 }
 
+__device__ __forceinline__ float max64(const uint32_t (&v)[32], const uint32_t (&w)[32]) {
+  float a = -INFINITY, b = a, c = a, d = a;
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    a = fmax3(a, as_f(v[e]), as_f(v[e + 1]));
+    b = fmax3(b, as_f(v[e + 2]), as_f(v[e + 3]));
+    c = fmax3(c, as_f(w[e]), as_f(w[e + 1]));
+    d = fmax3(d, as_f(w[e + 2]), as_f(w[e + 3]));
+  }
+  return fmaxf(fmax3(a, b, c), d);
+}
+
 // P = 2^(S c - m) of 32 columns as 16 packed words, and the sum of the
 // unrounded values.
 template <bool BF16>
@@ -581,14 +593,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           mask32(x0, lo_l, hi_l);
           mask32(x1, lo_l - 32, hi_l - 32);
         }
-        const float mx = max32(x1, max32(x0, -INFINITY));
+        const float mx = max64(x0, x1);
         // c > 0, so max(S) c is the maximum of the scaled scores
         const float top = mx * c;
         float alpha = 1.f;
-        if (top > m + kSlack || m == -INFINITY) {
-          const float m_new = fmaxf(m, top);
-          alpha = ex2_approx(m - (m_new == -INFINITY ? 0.f : m_new));
-          m = m_new;
+        const bool moved = __any_sync(0xffffffffu, top > m + kSlack);
+        if (moved) {
+          if (top > m + kSlack) {  // m = -inf: any key that is seen
+            const float m_new = fmaxf(m, top);
+            alpha = ex2_approx(m - m_new);
+            m = m_new;
+          }
+          __syncwarp();
         }
         const float neg_m = m == -INFINITY ? 0.f : -m;
         uint32_t pk[32];
@@ -634,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nv;
           by_rows = *(volatile int*)&s_odd[t][ns & 1] == ns + 1;
         }
-        if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale(t_o, alpha);
+        if (j > j0 && moved && __any_sync(0xffffffffu, alpha != 1.f)) rescale(t_o, alpha);
         tmem_st32(t_p, pk);
         if (by_rows) {
           tmem_st_wait();
@@ -858,6 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_inline(BAR(BAR_UNIT + (nu & 1)), (nu >> 1) & 1, wc)) break;
         const Unit& su = s_unit[nu & 1];
         const int more = su.more, nj = su.nj, j0 = su.t0[t], j1 = su.t1[t];
+        // keys that every row of the tile sees, from the first tile walked
+        const int lo_max = su.lo_max[t] - su.j0 * kBN, hi_min = su.hi_min[t] - su.j0 * kBN;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(BAR_UNIT_FREE + (nu & 1)));
         if (!more) break;
@@ -903,13 +921,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               // interleave on the pipe, end together and pull the three
               // softmaxes into step, where they queue for the same units
               // (prompt of 16384 tokens, 32 / 4 heads: 1108 -> 1074 us).
-              if (t > 0)
+              if (t > 0 && s_turn[t - 1] <= kt + i)
                 for (int spin = 0; spin < 8 && s_turn[t - 1] <= kt + i; ++spin) {}
-              __syncwarp();
               tc_fence_after();
               const uint32_t v_lo =
                   sdesc_lo(sbase + kSmemStage0 + s * kStageBytes + kHalfBytes, 8192);
-              const bool by_rows = s_odd[t][np & 1] == np + 1;  // the rows' threads did it
+              // on a masked tile the rows' threads may have formed the product
+              const bool by_rows = (i * kBN < lo_max || (i + 1) * kBN > hi_min) &&
+                                   s_odd[t][np & 1] == np + 1;
               if (elect_one()) {
                 if (!by_rows) {
 #pragma unroll
