@@ -639,8 +639,11 @@ def attn_packed_fwd(s: PackedShape, q, k, v, cu, o, lse=None, stream=None) -> No
     op, os_ = _strided(o, "o", dt, (n, H, 64), dev)
     cup = _dense(cu, "cu", torch.int32, (s.batch + 1,), dev)
     lp = None if lse is None else _dense(lse, "lse", torch.float32, (H, n), dev)
-    shape = _PACKED.pack(n, s.batch, H, Hkv, HEAD_DIM, 1 if s.causal else 0, _dtype_code(dt),
-                         s.scale, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
+    try:
+        shape = _PACKED.pack(n, s.batch, H, Hkv, HEAD_DIM, 1 if s.causal else 0, _dtype_code(dt),
+                             s.scale, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
+    except struct.error as e:
+        raise ValueError("a size does not fit the C struct: %s" % e) from None
     _run("attn_packed_fwd", dev, stream, shape, qp, kp, vp, cup, op, lp)
 
 
@@ -730,7 +733,8 @@ class PagedCache:
         self.lens, self._lens = torch.zeros(batch, **i32), torch.zeros(batch, **i32)
         self.state = torch.tensor([0, num_pages, 0, 0], **i32)
         self._state = torch.zeros(4, **i32)
-        self.ws = None
+        # as large as any step needs: a captured step keeps reading it
+        self.ws = alloc_paged_workspace(self.shape(1, 1 << 30), dev)
 
     def shape(self, tokens: int, max_new: int) -> PagedShape:
         return PagedShape(self.batch, tokens, self.heads, self.kv_heads, self.page_size,
@@ -750,9 +754,14 @@ class PagedCache:
                 return self.step(fresh, q, k, v, o, lse, max_new)
         n = q.shape[0]
         s = self.shape(n, max_new or max(n, 1))
-        need = paged_workspace_bytes(s)
-        if self.ws is None or self.ws.numel() < need:
-            self.ws = torch.empty(need, dtype=torch.uint8, device=self.k.device)
+        # everything is looked at before the plan moves the cache on
+        dev, dt, rows = _device_of(q, "q"), self.dtype, (n, self.heads, 64)
+        _strided(q, "q", dt, rows, dev)
+        _strided(k, "k", dt, (n, self.kv_heads, 64), dev)
+        _strided(v, "v", dt, (n, self.kv_heads, 64), dev)
+        _strided(o, "o", dt, rows, dev)
+        if lse is not None:
+            _dense(lse, "lse", torch.float32, (self.heads, n), dev)
         slots = torch.empty(n, dtype=torch.int32, device=self.k.device)
         attn_paged_plan(s, self.lens, fresh, self.ring, self.state, self.table, self.cu,
                         self._lens, slots, self._state)
@@ -760,7 +769,6 @@ class PagedCache:
         self.state, self._state = self._state, self.state
         if n:
             attn_paged_store(s, k, v, slots, self.k, self.v)
-            self.ws.record_stream(torch.cuda.current_stream(self.k.device))
             attn_paged_fwd(s, q, self.k, self.v, self.table, self.cu, self.lens, self.ws, o, lse)
 
     def status(self) -> int:

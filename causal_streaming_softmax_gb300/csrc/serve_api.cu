@@ -70,6 +70,25 @@ int validate_attend(const attn_paged_shape* s, PagedDims* d) {
   return softmax_scale(s->scale, &d->c);
 }
 
+// No two rows of a pool share an element: each stride, in rising order, is past
+// the extent of the dimensions before it.
+bool pool_apart(const PoolArg& p, int64_t pages, int64_t heads, int64_t rows) {
+  int64_t st[3] = {p.r, p.h, p.pg}, n[3] = {rows, heads, pages};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if ((n[i] <= 1 && n[j] > 1) || (n[j] > 1 && st[j] < st[i])) {
+        const int64_t a = st[i], b = n[i];
+        st[i] = st[j], n[i] = n[j];
+        st[j] = a, n[j] = b;
+      }
+  int64_t extent = 64;
+  for (int i = 0; i < 3 && n[i] > 1; ++i) {
+    if (st[i] < extent) return false;
+    extent += (n[i] - 1) * st[i];
+  }
+  return true;
+}
+
 int pools(const attn_paged_shape* s, const void* kc, const void* vc, PoolArg* k, PoolArg* v) {
   *k = PoolArg{const_cast<void*>(kc), s->kc_page, s->kc_head, s->kc_row};
   *v = PoolArg{const_cast<void*>(vc), s->vc_page, s->vc_head, s->vc_row};
@@ -129,12 +148,23 @@ int attn_paged_plan(const attn_paged_shape* s, const int32_t* cached, const int3
   if (!cached || !fresh || !ring || !state || !table || !cu || !lens || !next ||
       (!slots && s->tokens > 0))
     return ATTN_ERR_NULL;
-  const void* p[9] = {cached, fresh, ring, state, table, cu, lens, next, slots};
+  const int64_t B = d.batch;
+  const struct {
+    const int32_t* p;
+    int64_t n;
+    bool out;
+  } arr[9] = {{cached, B, false},     {fresh, B, false},       {ring, d.pages, true},
+              {state, 4, false},      {table, B * d.width, true}, {cu, B + 1, true},
+              {lens, B, true},        {slots, d.tokens, true}, {next, 4, true}};
   for (int i = 0; i < 9; ++i) {
-    if (reinterpret_cast<uintptr_t>(p[i]) & 3) return ATTN_ERR_ALIGN;
-    // two inputs may be one array; an output may be none of the others
-    for (int j = 0; j < i; ++j)
-      if (p[i] == p[j] && p[i] && (i == 2 || i >= 4 || j == 2)) return ATTN_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(arr[i].p) & 3) return ATTN_ERR_ALIGN;
+    // inputs may overlap one another; an output overlaps nothing
+    for (int j = 0; j < i; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(arr[i].p),
+                      y = reinterpret_cast<uintptr_t>(arr[j].p);
+      if ((arr[i].out || arr[j].out) && x < y + 4 * arr[j].n && y < x + 4 * arr[i].n)
+        return ATTN_ERR_SHAPE;
+    }
   }
   DevCtx ctx;
   if ((rc = device_context(&ctx)) != ATTN_OK) return rc;
@@ -155,6 +185,9 @@ int attn_paged_store(const attn_paged_shape* s, const void* k, const void* v,
     if (!fix_stride(&st[i], (i & 1) ? s->kv_heads : s->tokens)) return ATTN_ERR_SHAPE;
   PoolArg kc, vc;
   if ((rc = pools(s, k_cache, v_cache, &kc, &vc)) != ATTN_OK) return rc;
+  if (!pool_apart(kc, d.pages, d.Hkv, 1 << d.shift) ||
+      !pool_apart(vc, d.pages, d.Hkv, 1 << d.shift))
+    return ATTN_ERR_SHAPE;
   if (s->tokens == 0) return ATTN_OK;
   if (!k || !v || !slots || !k_cache || !v_cache) return ATTN_ERR_NULL;
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||

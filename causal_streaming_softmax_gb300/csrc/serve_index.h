@@ -104,4 +104,85 @@ CSS_HD int plan_status(int rows, long long add, long long need, long long back, 
   return st;
 }
 
+// a / b of non-negative numbers: the 32-bit division where both fit (a 64-bit
+// one is some four hundred clocks, and several stand before a block's first
+// load).
+CSS_HD long long quot(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+struct Share {
+  long long begin, end;
+  long long each;  // positions of a block; the first `more` blocks take one more
+  int more, blocks;
+};
+
+CSS_HD Share share_of(long long total, int min_tiles, int grid, int block) {
+  Share s;
+  const long long most = quot(total, min_tiles);
+  s.blocks = most < 1 ? 1 : (most < grid ? (int)most : grid);
+  s.each = quot(total, s.blocks);
+  s.more = (int)(total - s.each * s.blocks);
+  if (block >= s.blocks) {
+    s.begin = s.end = total;
+  } else {
+    s.begin = block * s.each + (block < s.more ? block : s.more);
+    s.end = s.begin + s.each + (block < s.more ? 1 : 0);
+  }
+  return s;
+}
+
+// The block whose share holds position x.
+CSS_HD int last_block(const Share& s, long long x) {
+  const long long big = s.more * (s.each + 1);  // positions of the longer shares
+  return x < big ? (int)quot(x, s.each + 1) : s.more + (int)quot(x - big, s.each);
+}
+
+// sum over i < n of floor((a i + b) / m), all non-negative, m > 0
+CSS_HD long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    const long long qa = quot(a, m), qb = quot(b, m);
+    s += n * (n - 1) / 2 * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = quot(y, m);
+    b = y - n * m;
+    const long long x = a;
+    a = m;
+    m = x;
+  }
+  return s;
+}
+
+// Key tiles (bn keys) of the first nb row blocks (w tokens each) of a request
+// with n_keys keys, its n_new new tokens the last of them.  Block b's last row
+// sees n_keys - n_new + min(n_new, (b + 1) w) keys; a block has at least one
+// tile.  nb is at most the request's blocks.
+CSS_HD long long tiles_before(int n_keys, int n_new, int w, int bn, int nb) {
+  const long long base = (long long)n_keys - n_new;
+  long long full = nb;  // blocks whose last row is a full block's
+  long long s = 0;
+  if ((long long)nb * w > n_new) {
+    full = nb - 1;
+    s = n_keys <= 0 ? 1 : (n_keys - 1) / bn + 1;
+  }
+  // blocks that end at or before key 0 count one tile
+  long long lead = 0;
+  if (base < 0) {
+    lead = quot(-base, w);
+    if (lead > full) lead = full;
+  }
+  return s + lead + (full > lead ? floor_sum(full - lead, bn, w, base + (lead + 1) * w + bn - 1) : 0);
+}
+
+CSS_HD int tiles_of_block(int n_keys, int n_new, int w, int bn, int b) {
+  const long long past = (b + 1ll) * w;
+  const long long end = (long long)n_keys - n_new + (past < n_new ? past : n_new);
+  return end <= 0 ? 1 : (int)((end - 1) / bn) + 1;
+}
+
 }  // namespace css

@@ -14,46 +14,12 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "serve_index.h"
 #include "serve_internal.h"
 #include "sm103.cuh"
 #include "warp_mma.cuh"
 
 namespace css {
-
-// a / b of non-negative numbers: the 32-bit division where both fit (a 64-bit
-// one is some four hundred clocks, and several stand before a block's first
-// load).
-__host__ __device__ inline long long quot(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
-
-struct Share {
-  long long begin, end;
-  long long each;  // positions of a block; the first `more` blocks take one more
-  int more, blocks;
-};
-
-__host__ __device__ inline Share share_of(long long total, int min_tiles, int grid, int block) {
-  Share s;
-  const long long most = quot(total, min_tiles);
-  s.blocks = most < 1 ? 1 : (most < grid ? (int)most : grid);
-  s.each = quot(total, s.blocks);
-  s.more = (int)(total - s.each * s.blocks);
-  if (block >= s.blocks) {
-    s.begin = s.end = total;
-  } else {
-    s.begin = block * s.each + (block < s.more ? block : s.more);
-    s.end = s.begin + s.each + (block < s.more ? 1 : 0);
-  }
-  return s;
-}
-
-// The block whose share holds position x.
-__host__ __device__ inline int last_block(const Share& s, long long x) {
-  const long long big = s.more * (s.each + 1);  // positions of the longer shares
-  return x < big ? (int)quot(x, s.each + 1) : s.more + (int)quot(x - big, s.each);
-}
 
 __device__ __forceinline__ long long part_row(const PartArgs& p, int block, bool tail, int row) {
   return ((long long)block * 2 + (tail ? 1 : 0)) * p.rows + row;

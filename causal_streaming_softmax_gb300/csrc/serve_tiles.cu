@@ -128,25 +128,6 @@ constexpr uint32_t idesc(int N, int b_mn) {
   return idesc_f16_f32(128, N, 0, b_mn) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// sum over i < n of floor((a i + b) / m), all non-negative, m > 0
-__host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long s = 0;
-  while (n > 0) {
-    const long long qa = quot(a, m), qb = quot(b, m);
-    s += n * (n - 1) / 2 * qa + n * qb;
-    a -= qa * m;
-    b -= qb * m;
-    const long long y = a * n + b;
-    if (y < m) break;
-    n = quot(y, m);
-    b = y - n * m;
-    const long long x = a;
-    a = m;
-    m = x;
-  }
-  return s;
-}
-
 // ---------------------------------------------------------------- paged items
 struct PagedReq {
   int q0, n_new, n_keys;  // n_new 0: not for this kernel
@@ -159,29 +140,6 @@ __device__ __forceinline__ PagedReq paged_req(const TileArgs& a, int i, bool* ba
   *bad = r.bad || b || q.n_new > a.max_new;
   if (q.n_new <= a.skip) q.n_new = 0;
   return q;
-}
-
-// Key tiles of the first nb row blocks (w tokens each) of a request, one head.
-// Block b's last row sees base + min(n_new, (b + 1) w) keys, base = n_keys -
-// n_new; a block has at least one tile.
-__device__ __forceinline__ long long tiles_before(const PagedReq& r, int w, int nb) {
-  const long long base = (long long)r.n_keys - r.n_new;
-  long long full = nb;  // blocks whose last row is a full block's
-  long long s = 0;
-  if ((long long)nb * w > r.n_new) {
-    full = nb - 1;
-    s += max(1ll, ((long long)r.n_keys + kBN - 1) / kBN);
-  }
-  // blocks that end at or before key 0 count one tile
-  long long lead = 0;
-  if (base < 0) lead = min(full, quot(-base, w));
-  const long long b0 = base + lead * w;  // > -w
-  return s + lead + floor_sum(full - lead, kBN, w, b0 + w + kBN - 1);
-}
-
-__device__ __forceinline__ int tiles_of_block(const PagedReq& r, int w, int b) {
-  const long long end = (long long)r.n_keys - r.n_new + min((long long)r.n_new, (b + 1ll) * w);
-  return end <= 0 ? 1 : (int)((end + kBN - 1) / kBN);
 }
 
 // A place in the list of tiles: tile t0 of a row block of a request and head.
@@ -212,13 +170,13 @@ __device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pr
   int x = 0, y = (p.r.n_new + w - 1) / w;  // the last block with tiles_before <= at
   while (x < y) {
     const int mid = (x + y) >> 1;
-    if (tiles_before(p.r, w, mid) <= at)
+    if (tiles_before(p.r.n_keys, p.r.n_new, w, kBN, mid) <= at)
       x = mid + 1;
     else
       y = mid;
   }
   p.blk = x - 1;
-  p.t0 = (int)(at - tiles_before(p.r, w, p.blk));
+  p.t0 = (int)(at - tiles_before(p.r.n_keys, p.r.n_new, w, kBN, p.blk));
   return p;
 }
 
@@ -517,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool b;
       const PagedReq r = paged_req(a, i, &b);
       bad |= b;
-      s_pre[i + 1] = sum += r.n_new > 0 ? tiles_before(r, w, (r.n_new + w - 1) / w) : 0;
+      s_pre[i + 1] = sum += r.n_new > 0 ? tiles_before(r.n_keys, r.n_new, w, kBN, (r.n_new + w - 1) / w) : 0;
     }
     if (bad && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
     long long upto = sum;
@@ -756,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         u.more = PAGED ? pos < share.end : block >= 0;
         int steps = 0, nt = 0;
         if (u.more && PAGED) {
-          nt = tiles_of_block(place.r, kNT * a.tpt, place.blk);
+          nt = tiles_of_block(place.r.n_keys, place.r.n_new, kNT * a.tpt, kBN, place.blk);
           steps = (int)min((long long)(nt - place.t0), share.end - pos);
           paged_unit(a, place, place.t0 + steps, nt, &u);
         } else if (u.more) {

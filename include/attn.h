@@ -368,7 +368,8 @@ ATTN_API int attn_bwd_noalloc(const attn_shape* shape, const uint16_t* q,
  * elements, so that q, k and v can be column blocks of one fused projection.
  * Strides are multiples of 8 (16 bytes) and at least 64 in a dimension longer
  * than one (ATTN_ERR_SHAPE otherwise; the stride of a dimension of one is not
- * read); o's rows must not overlap.  Base pointers are 16-byte aligned.
+ * read); o's rows overlap neither one another nor an input.  Base pointers are
+ * 16-byte aligned.
  *
  * Arrays of offsets, lengths, slots and page ids live on the device and are
  * read there.  A value outside its range never leads to an access outside the
@@ -458,9 +459,10 @@ typedef struct attn_paged_shape {
  * status 0, or a sum of ATTN_PLAN_ bits, in which case nothing is handed out
  * or taken back: the table and the ring stay, every offset is 0, every slot
  * -1, lens = cached and next = {head, free, 0, status}.
- * All arrays int32.  The outputs may overlap neither each other nor an input
- * (ATTN_ERR_SHAPE where a pointer is given twice), so that the next step
- * passes lens as cached and next as state.  Only batch, tokens, page_size,
+ * All arrays int32.  The arrays written (ring, table, cu, lens, slots, next)
+ * overlap neither each other nor another (ATTN_ERR_SHAPE): a step reads cached
+ * and state and writes lens and next, and the next step takes those as its
+ * cached and state.  Only batch, tokens, page_size,
  * num_pages and table_width of the shape are read.
  */
 enum {
@@ -479,7 +481,8 @@ ATTN_API int attn_paged_plan(const attn_paged_shape* shape, const int32_t* cache
  * Stores new K and V rows into the cache: row t of k and v (all K/V heads)
  * goes to slot slots[t]; a negative slot is skipped.  Slots of one call are
  * distinct (attn_paged_plan's are): where one is given twice, which row it
- * ends with is not determined.  Uses batch, tokens, kv_heads, page_size,
+ * ends with is not determined.  The pools' rows must not overlap one another
+ * within a pool (ATTN_ERR_SHAPE).  Uses batch, tokens, kv_heads, page_size,
  * num_pages, dtype and the k, v, kc and vc strides.
  */
 ATTN_API int attn_paged_store(const attn_paged_shape* shape, const void* k, const void* v,

@@ -642,3 +642,142 @@ def test_pool_beyond_32_bits(torch):
         q = rnd(torch, (new, H, 64), torch.float16, 3, 2.0)
         o, L = run_paged(torch, q, kc, vc, table, [0, new], [n])
         check_paged(torch, q, kc, vc, table, [0, new], [n], o, L)
+
+
+def test_requests_that_share_pages(torch):
+    """Two requests over the same pages (a prompt's common beginning) read
+    them alike, each to its own length."""
+    for new in (1, 30):
+        q, kc, vc, table, cu, lens, _ = paged_problem(torch, [(400, new), (400, new), (90, new)],
+                                                      8, 2, 16, torch.float16, 13)
+        table[1], lens = list(table[0]), [400, 333, 90]
+        o, L = run_paged(torch, q, kc, vc, table, cu, lens)
+        check_paged(torch, q, kc, vc, table, cu, lens, o, L)
+
+
+@pytest.mark.parametrize("heads", [(2, 1), (17, 1)])
+def test_the_largest_batch(torch, heads):
+    reqs = [(i % 50, min(1, i % 50)) for i in range(4096)]
+    q, kc, vc, table, cu, lens, _ = paged_problem(torch, reqs, heads[0], heads[1], 8,
+                                                  torch.bfloat16, 14)
+    o, L = run_paged(torch, q, kc, vc, table, cu, lens)
+    pick = [0, 1, 2, 49, 50, 99, 2047, 4001, 4095]
+    tt = torch.tensor([table[i] for i in pick], device="cuda")
+    for i, row in zip(pick, tt):
+        a, b, m = cu[i], cu[i + 1], lens[i]
+        seen = torch.full((b - a,), m, device="cuda")
+        eo, el, to, tl = attend64(q[a:b], gather(kc, row, m), gather(vc, row, m), seen)
+        check(o[a:b], eo, to, "request %d" % i)
+        check(L[:, a:b], el, tl, "L of request %d" % i)
+    assert torch.isfinite(o).all()
+
+
+def test_many_empty_sequences(torch):
+    r = random.Random(2)
+    lens = [0] * 65535
+    for i in r.sample(range(65535), 700):
+        lens[i] = r.randint(1, 3)
+    cu = scan(lens)
+    q, k, v = packed_inputs(torch, cu[-1], 4, 2, torch.float16, 15)
+    o, L = run_packed(torch, q, k, v, cu)
+    live = [0] + [c for c, n in zip(cu[1:], lens) if n]  # the same without the empty ones
+    check_packed(torch, q, k, v, live, True, o, L)
+
+
+def test_step_on_a_stream_of_its_own(torch):
+    from causal_streaming_softmax_gb300 import api
+    n = 90
+    q, k, v = packed_inputs(torch, n, 8, 2, torch.float16, 16)
+    cache = api.PagedCache(1, 8, 2, num_pages=20)
+    o = torch.empty((n, 8, 64), dtype=torch.float16, device="cuda")
+    fresh = [i32(torch, [50]), i32(torch, [40])]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    cache.step(fresh[0], q[:50], k[:50], v[:50], o[:50], stream=s)
+    cache.step(fresh[1], q[50:], k[50:], v[50:], o[50:], stream=s)
+    s.synchronize()
+    check_packed(torch, q, k, v, [0, n], True, o, None)
+
+
+def test_step_refuses_before_it_plans(torch):
+    from causal_streaming_softmax_gb300 import api
+    q, k, v = packed_inputs(torch, 10, 4, 2, torch.float16, 17)
+    cache = api.PagedCache(1, 4, 2, num_pages=5)
+    o = torch.empty((10, 4, 64), dtype=torch.float16, device="cuda")
+    for bad in (dict(k=k[:9]), dict(o=o[:, :3]), dict(v=v.float()), dict(q=q.cpu()),
+                dict(lse=torch.empty((4, 9), device="cuda"))):
+        args = dict(dict(q=q, k=k, v=v, o=o, lse=None), **bad)
+        with pytest.raises((ValueError, TypeError)):
+            cache.step(i32(torch, [10]), **args)
+    assert cache.lens.tolist() == [0] and cache.free_pages() == 5
+    cache.step(i32(torch, [10]), q, k, v, o)
+    assert cache.lens.tolist() == [10]
+
+
+FIRST_CALL = """
+import torch
+from causal_streaming_softmax_gb300 import api
+g = torch.cuda.CUDAGraph()
+cache = api.PagedCache(2, 8, 2, num_pages=40)
+x = torch.randn(60, 12, 64, device="cuda", dtype=torch.float16)
+q, k, v = x[:, :8], x[:, 8:10], x[:, 10:]
+o = torch.zeros(60, 8, 64, device="cuda", dtype=torch.float16)
+p = torch.zeros_like(o)
+fresh = torch.tensor([60, 0], dtype=torch.int32, device="cuda")
+done = torch.tensor([-1, -1], dtype=torch.int32, device="cuda")
+cu = torch.tensor([0, 60, 60], dtype=torch.int32, device="cuda")
+none = torch.empty(0, 12, 64, device="cuda", dtype=torch.float16)
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    cache.step(fresh, q, k, v, o, max_new=60)
+    cache.step(done, none[:, :8], none[:, 8:10], none[:, 10:], none[:, :8])
+    api.attn_packed_fwd(api.PackedShape(60, 2, 8, 2), q, k, v, cu, p)
+for _ in range(3):
+    o.zero_(), p.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert api.last_device_error() == 0
+    assert cache.status() == 0 and cache.free_pages() == 40
+    assert (o.float() - p.float()).abs().max() < 4e-3 and o.abs().max() > 0
+print("fine")
+"""
+
+
+def test_first_calls_inside_a_capture(torch):
+    """A process whose first calls are captured: nothing has been loaded or
+    set up before."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
+def test_a_captured_step_outlives_larger_steps(torch):
+    """A captured token step replays after steps that need more workspace."""
+    from causal_streaming_softmax_gb300 import api
+    cache = api.PagedCache(1, 8, 2, num_pages=300)
+    q, k, v = packed_inputs(torch, 3000, 8, 2, torch.float16, 18)
+    o = torch.empty((3000, 8, 64), dtype=torch.float16, device="cuda")
+    one, two = i32(torch, [1]), torch.empty((2, 1, 8, 64), dtype=torch.float16, device="cuda")
+    cache.step(i32(torch, [500]), q[:500], k[:500], v[:500], o[:500], max_new=500)
+    qs, ks, vs = q[500:501].clone(), k[500:501].clone(), v[500:501].clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for x in two:
+            cache.step(one, qs, ks, vs, x, max_new=1)
+    g.replay()
+    cache.step(i32(torch, [2000]), q[502:2502], k[502:2502], v[502:2502], o[502:2502])
+    cache.step(i32(torch, [498]), q[2502:], k[2502:], v[2502:], o[2502:])
+    junk = [torch.full((1 << 20,), -1, dtype=torch.int32, device="cuda") for _ in range(20)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert all((j == -1).all() for j in junk)
+    kk = torch.cat([k[:500], ks, ks, k[502:], ks, ks])
+    vv = torch.cat([v[:500], vs, vs, v[502:], vs, vs])
+    eo, _, to, _ = attend64(qs, kk, vv, torch.tensor([kk.shape[0]], device="cuda"))
+    check(two[1], eo, to, "replayed step")
+    assert cache.lens.tolist() == [kk.shape[0]] and cache.status() == 0

@@ -130,6 +130,10 @@ def test_plan_pointers_refused(lib):
         assert plan(lib, paged(), a) == api.ATTN_ERR_NULL, i
         a[i] = P + 1 + 4096 * i
         assert plan(lib, paged(), a) == api.ATTN_ERR_ALIGN, i
+    # partly on top of one another: the last entry of cached, the first of lens
+    a = plan_args()
+    a[6] = a[0] + 8
+    assert plan(lib, paged(), a) == api.ATTN_ERR_SHAPE
     # cached, fresh, ring, state, table, cu, lens, slots, next: an output given twice
     read_only = {0, 1, 3}
     for i, j in itertools.combinations(range(9), 2):
@@ -152,6 +156,14 @@ def test_store_refused(lib):
         assert store(paged(), **{name: None}) == api.ATTN_ERR_NULL, name
         assert store(paged(), **{name: P + 2}) == api.ATTN_ERR_ALIGN, name
     assert store(paged(tokens=0), None, None, None, None, None) == api.ATTN_OK
+    # rows of a pool on top of one another
+    for kw in (dict(kc_row=64, kc_head=64), dict(vc_head=512), dict(vc_page=1024),
+               dict(kc_row=128, kc_head=1024, kc_page=2048)):
+        assert store(paged(**kw)) == api.ATTN_ERR_SHAPE, kw
+    # any order of strides that keeps them apart
+    for kw in (dict(kc_row=128, kc_head=64, kc_page=2048), dict(kc_page=64, kc_head=3200, kc_row=6400),
+               dict(vc_row=72, vc_head=1160, vc_page=2400)):
+        assert store(paged(**kw), slots=None) == api.ATTN_ERR_NULL, kw
 
 
 def test_error_string(lib):
@@ -204,6 +216,17 @@ int main() {
       int c, f, w, s; scanf("%d %d %d %d", &c, &f, &w, &s);
       PlanRow r = plan_row(c, f, w, s);
       printf("%lld %lld %lld %lld %d\n", r.add, r.have, r.need, r.back, r.status);
+    } else if (what == 6) {
+      long long t; int m, g, b; scanf("%lld %d %d %d", &t, &m, &g, &b);
+      Share s = share_of(t, m, g, b);
+      printf("%lld %lld %d\n", s.begin, s.end, s.blocks);
+    } else if (what == 7) {
+      long long t, x; int m, g; scanf("%lld %d %d %lld", &t, &m, &g, &x);
+      Share s = share_of(t, m, g, 0);
+      printf("%d\n", last_block(s, x));
+    } else if (what == 8) {
+      int k, n, w, bn, nb; scanf("%d %d %d %d %d", &k, &n, &w, &bn, &nb);
+      printf("%lld %d\n", tiles_before(k, n, w, bn, nb), tiles_of_block(k, n, w, bn, nb));
     } else {
       int rows, head, fr, np, tok; long long add, need, back;
       scanf("%d %lld %lld %lld %d %d %d %d", &rows, &add, &need, &back, &head, &fr, &np, &tok);
@@ -293,6 +316,50 @@ def test_plan_rows_and_status(harness):
              ((0, 5, 2, 8, 0, 2, 10, 5), 0), ((8, big, big, big, 5, 2, 10, 5), 13)]
     got = harness("5 %s" % " ".join(map(str, a)) for a, _ in cases)
     assert [g[0] for g in got] == [w for _, w in cases]
+
+
+def test_shares_partition_the_list(harness):
+    r = random.Random(5)
+    for total in (0, 1, 3, 4, 5, 1000, 12345, 2 ** 31 - 1, 2 ** 33 + 7, 2 ** 52 + 12345):
+        for least, grid in ((1, 1), (4, 304), (2, 152), (8, 3)):
+            got = harness("6 %d %d %d %d" % (total, least, grid, b) for b in range(grid))
+            at = 0
+            for b, (begin, end, blocks) in enumerate(got):
+                assert 1 <= blocks <= grid and (blocks == 1 or blocks * least <= total)
+                if b < blocks:
+                    assert begin == at and end >= begin
+                    assert end - begin - total // blocks in (0, 1)
+                    at = end
+                else:
+                    assert begin == end == total
+            assert at == total
+            if total:
+                xs = [0, total - 1] + [r.randrange(total) for _ in range(20)]
+                xs += [g[0] for g in got if g[0] < total] + [g[1] - 1 for g in got if g[1] > g[0]]
+                ans = harness("7 %d %d %d %d" % (total, least, grid, x) for x in xs)
+                for x, (b,) in zip(xs, ans):
+                    assert got[b][0] <= x < got[b][1], (total, least, grid, x, b)
+
+
+def test_tiles_of_row_blocks(harness):
+    r = random.Random(6)
+    asks, want = [], []
+    for _ in range(3000):
+        n = r.randint(1, 900)
+        k = r.choice([r.randint(0, 3000), r.randint(0, n), n, 0, 2 ** 31 - 1])
+        w, bn = 3 * (128 // r.randint(1, 128)), r.choice([64, 128])
+        blocks = -(-n // w)
+        ends = [k - n + min(n, (b + 1) * w) for b in range(blocks)]
+        tiles = [1 if e <= 0 else -(-e // bn) for e in ends]
+        nb = r.choice([0, 1, blocks // 2, blocks - 1])
+        if nb >= blocks:
+            continue
+        asks.append("8 %d %d %d %d %d" % (k, n, w, bn, nb))
+        want.append([sum(tiles[:nb]), tiles[nb]])
+        asks.append("8 %d %d %d %d %d" % (k, n, w, bn, blocks))
+        want.append([sum(tiles), None])
+    for a, g, x in zip(asks, harness(asks), want):
+        assert g[0] == x[0] and x[1] in (None, g[1]), a
 
 
 def test_host_form_of_the_plan():
