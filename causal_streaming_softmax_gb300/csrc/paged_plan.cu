@@ -14,6 +14,8 @@
 // bisection of the scanned offsets in shared memory.  The pages read are at
 // the ring's head and the table's old entries, those written behind its tail
 // and in the table's new entries, so no block reads what another writes.
+// Measured (GB300): 64 requests of one token 3.6 us, 512 requests with 110,000
+// slots 5.8 us, of which about 2 are the launch.
 #include "serve_index.h"
 #include "serve_internal.h"
 #include "sm103.cuh"

@@ -37,7 +37,18 @@
 // the work in flight sets the rate.  With two row tiles of 128 keys (two
 // softmax warps a scheduler) a pair of steps took 2650 clocks where the
 // exponential, conversion and add pipes need 1311, however the two were
-// phased and however many warps issued the products.
+// phased and however many warps issued the products (1.25 ms for a prompt of
+// 16384 tokens, 32 / 4 heads); three tiles of 64 keys take 0.95 ms.
+//
+// Measured (GB300): that prompt 952 us = 1155 TFLOP/s, 62% of the measured
+// dense rate; 16 prompts of 256..4096 tokens, 32 / 8 heads, 504 us = 861
+// TFLOP/s.  The matrix pipe is busy 45% of the time and the issue slots 58%:
+// what bounds is the latency of a tile step (wait for S, load, maximum,
+// exponentials, store of P, wait of the products) times the three in flight.
+// Slower were: a warp for S and one for O += P V (1.38 ms, the second's own
+// latency), six issuing warps of 20 with registers moved between the warps
+// (1.13 ms, the waiting warps' polls), P tested against the last maximum
+// first and the maximum taken only where it grew (1.06 ms).
 //
 // What a mask excludes cannot reach a row, infinities and NaN included: S is
 // replaced by -inf, and on tiles where some row misses a key the rows of V
@@ -333,7 +344,7 @@ __device__ __forceinline__ void exp32(const uint32_t (&v)[32], float c, float ne
 }
 
 // O *= alpha for the rows of a warp.
-__device__ __forceinline__ void rescale(uint32_t t_o, float alpha) {
+__device__ __noinline__ void rescale(uint32_t t_o, float alpha) {
   const float2 al = make_float2(alpha, alpha);
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
@@ -361,7 +372,7 @@ __device__ __forceinline__ bool any_nonfinite(const uint4& w) {
 // O += P V of one row over the keys [lo, hi) of the tile, by the row's own
 // thread: P from its tensor-memory columns, V from the stage.  Rare.
 template <bool BF16>
-__device__ __forceinline__ void row_product(uint32_t t_p, uint32_t t_o, const uint8_t* v, int lo,
+__device__ __noinline__ void row_product(uint32_t t_p, uint32_t t_o, const uint8_t* v, int lo,
                                             int hi, bool first) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {  // 16 columns at a time
@@ -375,7 +386,7 @@ __device__ __forceinline__ void row_product(uint32_t t_p, uint32_t t_o, const ui
       uint32_t p[16];
       __syncwarp();
       tmem_ld16_wait(t_p + 16 * i, p);
-#pragma unroll
+#pragma unroll 2
       for (int k = 0; k < 32; ++k) {
         const int key = 32 * i + k;
         if (key >= lo && key < hi) {
@@ -547,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32x2_wait(t_s, t_s + 32, x0, x1);
         tc_fence_before();
         mbar_arrive(BAR(BAR_S_FREE + t));
-        if (edge) {
+        if (__builtin_expect(edge, 0)) {
           mask32(x0, lo_l, hi_l);
           mask32(x1, lo_l - 32, hi_l - 32);
         }
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = mx * c;
         float alpha = 1.f;
         const bool moved = __any_sync(0xffffffffu, top > m + kSlack);
-        if (moved) {
+        if (__builtin_expect(moved, 0)) {
           if (top > m + kSlack) {  // m = -inf: any key that is seen
             const float m_new = fmaxf(m, top);
             alpha = ex2_approx(m - m_new);
@@ -579,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         bool by_rows = false;
-        if (edge) {
+        if (__builtin_expect(edge, 0)) {
           // look at row `row` of the V tile
           const int s = (kt + j) % kStages;
           if (!mbar_wait_inline(BAR(BAR_KV_FULL + s), ((kt + j) / kStages) & 1, wc)) {
@@ -610,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (j > j0 && moved && __any_sync(0xffffffffu, alpha != 1.f)) rescale(t_o, alpha);
         tmem_st32(t_p, pk);
-        if (by_rows) {
+        if (__builtin_expect(by_rows, 0)) {
           tmem_st_wait();
           row_product<BF16>(
               t_p, t_o, smem + kSmemStage0 + ((kt + j) % kStages) * kStageBytes + kHalfBytes,
