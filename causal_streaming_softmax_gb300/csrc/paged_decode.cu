@@ -27,9 +27,7 @@
 // heads 309 us = 6.84 TB/s, 101% of the measured copy rate; 64 over 17..8192,
 // 32 / 8 heads 92 us = 6.02 TB/s; 2 over 50000..65536, 16 / 16 heads 75 us =
 // 6.26 TB/s; one over 777 keys 9 us, of which about 8 are two launches and the
-// chain of loads lengths -> page ids -> pages -> parts.  Blocks take at least
-// four tiles (one request of 4000 keys: 17.0, 14.2 and 13.9 us with at least
-// 2, 4 and 8 tiles before the join was spread over idle threads).
+// chain of loads lengths -> page ids -> pages -> parts.
 #include <math.h>
 
 #include <mutex>

@@ -9,31 +9,33 @@
 namespace css {
 namespace {
 
-constexpr int kJoinThreads = 128;
-constexpr int kJoinRows = kJoinThreads / 8;  // rows of a block: eight threads a row
+constexpr int kJoinThreads = 256;
+constexpr int kJoinSlots = kJoinThreads / 8;  // eight threads a row
+constexpr int kJoinRows = 16;                 // rows of a block
 
-// O = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m).  Block (x, y) joins rows
-// [16 y, 16 y + 16) of the item whose tail part block x of the first kernel
-// (x < n1) or of the second wrote.  Latency bound, the parts lie in L2: with
-// fewer than 16 rows the threads that are left take every g-th part of a row,
-// and the g sums are added in order, so the result does not depend on timing.
+// O = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m).  The first n1 blocks join
+// the items whose tail parts the blocks of the first kernel wrote, the others
+// 16 rows each of those of the second (`chunks` blocks an item).  Latency
+// bound, the parts lie in L2: the slots that rows leave free take every g-th
+// part of a row; the g sums are added in order, so the result does not depend
+// on timing.
 template <bool BF16>
 __global__ void __launch_bounds__(kJoinThreads)
-    join_kernel(const PartArgs p1, int n1, const PartArgs p2, const RowsArg o, float* lse,
-                int tokens, int G) {
-  __shared__ float s_sum[kJoinRows][8][9];
+    join_kernel(const PartArgs p1, int n1, const PartArgs p2, int chunks, const RowsArg o,
+                float* lse, int tokens, int G) {
+  __shared__ float s_sum[kJoinSlots][8][9];
   griddep_launch_dependents();
   griddep_wait();
   const bool one = (int)blockIdx.x < n1;
   const PartArgs& p = one ? p1 : p2;
-  const int c = one ? blockIdx.x : blockIdx.x - n1;
+  const int at_2 = blockIdx.x - n1, c = one ? blockIdx.x : at_2 / chunks;
   const PartDesc d = p.desc[c];
-  const int row0 = blockIdx.y * kJoinRows, rows = min(d.rows - row0, kJoinRows);
+  const int row0 = one ? 0 : at_2 % chunks * kJoinRows, rows = min(d.rows - row0, kJoinRows);
   if (rows <= 0) return;  // the whole block
   int span = 1;           // rows rounded up to a power of two
   while (span < rows) span <<= 1;
   const int slot = threadIdx.x >> 3, lane = threadIdx.x & 7, c0 = lane * 8;
-  const int at_row = slot & (span - 1), group = slot / span, groups = kJoinRows / span;
+  const int at_row = slot & (span - 1), group = slot / span, groups = kJoinSlots / span;
   const int row = row0 + at_row;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f, m = -INFINITY;
   if (at_row < rows) {
@@ -62,31 +64,31 @@ __global__ void __launch_bounds__(kJoinThreads)
       acc[7] = fmaf(y.w, f, acc[7]);
     }
   }
-  if (groups > 1) {
-    float* const mine = s_sum[slot][lane];
+  float* const mine = s_sum[slot][lane];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mine[e] = acc[e];
-    mine[8] = l;
-    __syncthreads();
-    if (group != 0) return;
-    for (int g = 1; g < groups; ++g) {
-      const float* const other = s_sum[g * span + at_row][lane];
+  for (int e = 0; e < 8; ++e) mine[e] = acc[e];
+  mine[8] = l;
+  __syncthreads();
+  if (group != 0 || at_row >= rows) return;
+  for (int g = 1; g < groups; ++g) {
+    const float* const other = s_sum[g * span + at_row][lane];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += other[e];
-      l += other[8];
-    }
+    for (int e = 0; e < 8; ++e) acc[e] += other[e];
+    l += other[8];
   }
-  if (at_row < rows)
-    write_row<BF16>(o, lse, tokens, d.q0 + row / G, d.kv * G + row % G, c0, acc, m, l);
+  write_row<BF16>(o, lse, tokens, d.q0 + row / G, d.kv * G + row % G, c0, acc, m, l);
 }
 
 int launch_join(const PagedDims& d, const PartArgs& p1, int n1, const PartArgs& p2, int n2,
                 const RowsArg& o, float* lse, cudaStream_t stream) {
-  const int rows = n2 > 0 ? p2.rows : p1.rows;
+  static_assert(kDecodeRows <= kJoinRows && kItemRows % kJoinRows == 0, "rows of a block");
+  // no item has more rows than the largest request, nor than its tiles hold
+  const long long most = (long long)d.max_new * d.G;
+  const int rows = most < kItemRows ? (int)most : kItemRows;
+  const int chunks = (rows + kJoinRows - 1) / kJoinRows;
   return cuda_status(launch_dependent(d.bf16 ? join_kernel<true> : join_kernel<false>,
-                                      dim3(n1 + n2, (rows + kJoinRows - 1) / kJoinRows),
-                                      dim3(kJoinThreads), 0, stream, p1, n1, p2, o, lse, d.tokens,
-                                      d.G));
+                                      dim3(n1 + n2 * chunks), dim3(kJoinThreads), 0, stream, p1,
+                                      n1, p2, chunks, o, lse, d.tokens, d.G));
 }
 
 // The largest grid of the split kernels on any device this library runs on:
@@ -125,6 +127,12 @@ PartArgs parts_at(void* ws, size_t blocks, int rows, int min_tiles) {
   return p;
 }
 
+// A block takes at least so many tiles: below, starting it and joining its
+// parts costs more than its tiles.  Few rows (64-key tiles), us with at least
+// 1 / 2 / 4: one request of 100 keys 7.0 / 6.1 / 8.1, of 777 8.3 / 8.7 / 9.4, of
+// 4000 12.8 / 10.6 / 10.8, eight of 256 7.9 / 8.3 / 7.2.
+constexpr int kLeastFew = 2, kLeastRows = 2;
+
 }  // namespace
 
 size_t paged_workspace_bytes(const PagedDims& d) {
@@ -143,14 +151,14 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
   PartArgs few{}, rows{};
   int n_few = 0, n_rows = 0, rc;
   if (ntok > 0) {
-    few = parts_at(at, 2 * kMaxSm, kDecodeRows, 4);
+    few = parts_at(at, 2 * kMaxSm, kDecodeRows, kLeastFew);
     at += parts_bytes(2 * kMaxSm, kDecodeRows);
     n_few = 2 * sms;
     rc = launch_paged_decode(d, ctx, q, kc, vc, table, cu, lens, few, n_few, o, lse, stream);
     if (rc != ATTN_OK) return rc;
   }
   if (d.max_new > ntok) {
-    rows = parts_at(at, kMaxSm, kItemRows, 2);
+    rows = parts_at(at, kMaxSm, kItemRows, kLeastRows);
     n_rows = sms;
     rc = launch_paged_rows(d, ctx, q, kc, vc, table, cu, lens, rows, n_rows, ntok, o, lse, stream);
     if (rc != ATTN_OK) return rc;

@@ -176,7 +176,13 @@ CSS_HD long long tiles_before(int n_keys, int n_new, int w, int bn, int nb) {
     lead = quot(-base, w);
     if (lead > full) lead = full;
   }
-  return s + lead + (full > lead ? floor_sum(full - lead, bn, w, base + (lead + 1) * w + bn - 1) : 0);
+  s += lead;
+  const long long n = full - lead, first = base + (lead + 1) * w + bn - 1;  // first > 0 where n > 0
+  if (n > 32 || first + n * w > 0x7fffffffLL) return n > 0 ? s + floor_sum(n, bn, w, first) : s;
+  // a few blocks: the sum itself is faster than the divisions
+  uint32_t sum = 0, at = (uint32_t)first;
+  for (int b = 0; b < (int)n; ++b, at += (uint32_t)w) sum += at / (uint32_t)bn;
+  return s + sum;
 }
 
 CSS_HD int tiles_of_block(int n_keys, int n_new, int w, int bn, int b) {

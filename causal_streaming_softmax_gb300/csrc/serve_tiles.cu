@@ -121,7 +121,7 @@ struct Unit {
 };
 
 struct TileArgs {
-  int tokens, batch, H, Hkv, G, tpt, causal;
+  int tokens, batch, H, Hkv, G, tpt, causal, windows;
   float c;
   const int32_t *cu, *lens, *table;
   int pages, width, shift, skip, max_new;
@@ -160,7 +160,7 @@ struct Place {
 };
 
 // The place at position pos of the list; pre[i] counts the tiles of one head
-// of the requests before i.
+// of the requests before i.  Called by a whole warp.
 __device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pre, long long pos) {
   int lo = 0, hi = a.batch;
   while (lo < hi) {
@@ -178,16 +178,20 @@ __device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pr
   const long long per = pre[lo] - pre[p.req], off = pos - pre[p.req] * a.Hkv;
   p.kv = (int)quot(off, per);
   const long long at = off - (long long)p.kv * per;
-  int x = 0, y = (p.r.n_new + w - 1) / w;  // the last block with tiles_before <= at
-  while (x < y) {
-    const int mid = (x + y) >> 1;
-    if (tiles_before(p.r.n_keys, p.r.n_new, w, kBN, mid) <= at)
-      x = mid + 1;
-    else
-      y = mid;
+  // the last block with tiles_before <= at: the warp's lanes try 32 at a time
+  const int lane = threadIdx.x & 31;
+  int x = 0, n = (p.r.n_new + w - 1) / w;  // the block is in [x, x + n)
+  long long before = 0;
+  while (n > 1) {
+    const int step = (n + 31) / 32, mine = x + min(lane * step, n - 1);
+    const long long v = tiles_before(p.r.n_keys, p.r.n_new, w, kBN, mine);
+    const int hit = __popc(__ballot_sync(0xffffffffu, lane * step < n && v <= at)) - 1;
+    before = __shfl_sync(0xffffffffu, v, hit);
+    x += hit * step;
+    n = min(step, n - hit * step);
   }
-  p.blk = x - 1;
-  p.t0 = (int)(at - tiles_before(p.r.n_keys, p.r.n_new, w, kBN, p.blk));
+  p.blk = x;
+  p.t0 = (int)(at - before);
   return p;
 }
 
@@ -240,8 +244,8 @@ __device__ __forceinline__ void paged_unit(const TileArgs& a, const Place& p, in
 
 // --------------------------------------------------------------- packed items
 __device__ __forceinline__ void packed_unit(const TileArgs& a, int block, Unit* u) {
-  const int w = kNT * a.tpt, nwin = (a.tokens + w - 1) / w;
-  const int kv = block % a.Hkv, win = nwin - 1 - block / a.Hkv;
+  const int w = kNT * a.tpt, win_rev = block / a.Hkv;
+  const int kv = block - win_rev * a.Hkv, win = a.windows - 1 - win_rev;
   u->more = 1;
   u->kv = kv;
   u->q0 = win * w;
@@ -254,20 +258,41 @@ __device__ __forceinline__ void packed_unit(const TileArgs& a, int block, Unit* 
   u->kbeg = 0;
   u->s0 = 0;
   u->s1 = -1;
-  // first and last row that belong to a sequence, of every tile; lanes 2 t and
-  // 2 t + 1 search them
+  // first and last row that belong to a sequence, of every tile, and the
+  // sequences they belong to: the warp's lanes try 32 offsets at a time, all
+  // six rows in one round of loads (one round up to 32 sequences)
   const int front = a.cu[0], back = a.cu[a.batch];
   const int lane = threadIdx.x & 31;
-  int f[kNT], e[kNT], want = 0;
+  int f[kNT], e[kNT], at[2 * kNT], lo[2 * kNT], n[2 * kNT];
 #pragma unroll
   for (int t = 0; t < kNT; ++t) {
     f[t] = max(u->q0 + t * a.tpt, front);
     e[t] = min(min(u->q_end, u->q0 + (t + 1) * a.tpt), back) - 1;
-    if (lane == 2 * t) want = f[t];
-    if (lane == 2 * t + 1) want = e[t];
+    at[2 * t] = f[t];
+    at[2 * t + 1] = e[t];
+    lo[2 * t] = lo[2 * t + 1] = 0;
+    n[2 * t] = n[2 * t + 1] = a.batch;
   }
-  int s = last_at_or_below(a.cu, a.batch, want);
-  s = s < 0 ? 0 : s;
+  for (int left = a.batch, last = 0; !last; left = (left + 31) / 32) {
+    last = left <= 32;
+    int v[2 * kNT];
+#pragma unroll
+    for (int i = 0; i < 2 * kNT; ++i)
+      v[i] = a.cu[lo[i] + min(lane * ((n[i] + 31) / 32), n[i] - 1)];
+#pragma unroll
+    for (int i = 0; i < 2 * kNT; ++i) {
+      const int step = (n[i] + 31) / 32;
+      // offsets at or below the row, at least the first
+      const int hit =
+          max(__popc(__ballot_sync(0xffffffffu, lane * step < n[i] && v[i] <= at[i])), 1) - 1;
+      lo[i] += hit * step;
+      n[i] = min(step, n[i] - hit * step);
+    }
+  }
+  int s = 0;  // lane i of the first six holds the sequence of row i
+#pragma unroll
+  for (int i = 0; i < 2 * kNT; ++i)
+    if (lane == i) s = lo[i];
   const RowRange r = row_range(a.cu[s], a.cu[s + 1], a.tokens);
   bool seen = false;
 #pragma unroll
@@ -964,7 +989,8 @@ int launch_packed_fwd(const PackedDims& d, const DevCtx& ctx, const RowsArg& q, 
       !encode_tmap_4d(&tk, d.bf16, k.p, d.tokens, d.Hkv, 1, k.t, k.h, 64, kBN, 1, 1) ||
       !encode_tmap_4d(&tv, d.bf16, v.p, d.tokens, d.Hkv, 1, v.t, v.h, 64, kBN, 1, 1))
     return ATTN_ERR_CUDA;
-  const long long units = (long long)d.Hkv * ((d.tokens + kNT * a.tpt - 1) / (kNT * a.tpt));
+  a.windows = (d.tokens + kNT * a.tpt - 1) / (kNT * a.tpt);
+  const long long units = (long long)d.Hkv * a.windows;
   if (units > 0x7fffffffLL) return ATTN_ERR_SHAPE;
   auto* kernel = d.bf16 ? tiles_kernel<false, true> : tiles_kernel<false, false>;
   const size_t smem = kSmemPre + 1024;
