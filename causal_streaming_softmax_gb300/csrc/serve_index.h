@@ -8,8 +8,10 @@
 
 #if defined(__CUDACC__)
 #define CSS_HD __host__ __device__ __forceinline__
+#define CSS_RARE static __host__ __device__ __noinline__
 #else
 #define CSS_HD inline
+#define CSS_RARE static inline
 #endif
 
 namespace css {
@@ -140,7 +142,7 @@ CSS_HD int last_block(const Share& s, long long x) {
 }
 
 // sum over i < n of floor((a i + b) / m), all non-negative, m > 0
-CSS_HD long long floor_sum(long long n, long long m, long long a, long long b) {
+CSS_RARE long long floor_sum(long long n, long long m, long long a, long long b) {
   long long s = 0;
   while (n > 0) {
     const long long qa = quot(a, m), qb = quot(b, m);

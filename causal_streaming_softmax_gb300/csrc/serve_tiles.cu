@@ -209,114 +209,111 @@ __device__ __forceinline__ void next_block(const TileArgs& a, Place* p) {
   } while (p->r.n_new == 0 && p->req + 1 < a.batch);
 }
 
-// Describes the item at a place, tiles [t0, t1) of nt.
+// Describes the item at a place, tiles [t0, t1) of nt; lane t looks after row
+// tile t.
 __device__ __forceinline__ void paged_unit(const TileArgs& a, const Place& p, int t1, int nt,
                                            Unit* u) {
-  const PagedReq r = p.r;
-  const int w = kNT * a.tpt, blk = p.blk, t0 = p.t0;
-  u->more = 1;
-  u->q0 = r.q0 + blk * w;
-  u->q_end = min(r.q0 + r.n_new, u->q0 + w);
-  u->kv = p.kv;
-  u->kbeg = 0;
-  u->j0 = t0;
-  u->lim = r.n_keys - r.n_new + 1 + blk * w;
-  u->nj = 0;
-  u->kend = 0;
-#pragma unroll
-  for (int t = 0; t < kNT; ++t) {
-    const int first = u->q0 + t * a.tpt, past = min(u->q_end, first + a.tpt);
-    u->t0[t] = u->t1[t] = 0;
-    u->lo_max[t] = u->hi_min[t] = 0;
-    if (first < past) {
-      const int keys = u->lim + (past - 1 - u->q0);  // the last row's
-      u->hi_min[t] = u->lim + (first - u->q0);
-      const int n = keys <= 0 ? 0 : (keys + kBN - 1) / kBN;
-      u->t1[t] = max(0, min(n, t1) - t0);
-      u->kend = max(u->kend, keys);
-    }
-    u->nj = max(u->nj, u->t1[t]);
+  const int w = kNT * a.tpt, lane = threadIdx.x & 31, t = lane;
+  const int q0 = p.r.q0 + p.blk * w, q_end = min(p.r.q0 + p.r.n_new, q0 + w);
+  const int lim = p.r.n_keys - p.r.n_new + 1 + p.blk * w;
+  const int first = q0 + t * a.tpt, past = min(q_end, first + a.tpt);
+  const bool some = t < kNT && first < past;
+  const int keys = some ? lim + (past - 1 - q0) : 0;  // the last row's
+  const int n = keys <= 0 ? 0 : (keys + kBN - 1) / kBN;
+  const int mine = some ? max(0, min(n, t1) - p.t0) : 0;
+  const int nj = __reduce_max_sync(0xffffffffu, mine);
+  const int kend = __reduce_max_sync(0xffffffffu, max(keys, 0));
+  if (t < kNT) {
+    u->t0[t] = 0;
+    u->t1[t] = mine;
+    u->lo_max[t] = 0;
+    u->hi_min[t] = some ? lim + (first - q0) : 0;
   }
-  u->whole = t0 == 0 && t1 == nt;
-  u->tail = t0 == 0;
-  u->s0 = u->s1 = 0;
+  if (lane == 0) {
+    u->more = 1;
+    u->q0 = q0;
+    u->q_end = q_end;
+    u->kv = p.kv;
+    u->kbeg = 0;
+    u->j0 = p.t0;
+    u->nj = nj;
+    u->kend = kend;
+    u->s0 = u->s1 = 0;
+    u->lim = lim;
+    u->whole = p.t0 == 0 && t1 == nt;
+    u->tail = p.t0 == 0;
+  }
 }
 
 // --------------------------------------------------------------- packed items
+// Lanes 2 t and 2 t + 1 look after the first and the last row of row tile t.
+// Kept short: a block runs it once or a few times, and code that has to be
+// fetched first takes some ten clocks an instruction.
 __device__ __forceinline__ void packed_unit(const TileArgs& a, int block, Unit* u) {
   const int w = kNT * a.tpt, win_rev = block / a.Hkv;
-  const int kv = block - win_rev * a.Hkv, win = a.windows - 1 - win_rev;
-  u->more = 1;
-  u->kv = kv;
-  u->q0 = win * w;
-  u->q_end = min(a.tokens, u->q0 + w);
-  u->j0 = u->nj = 0;
-  u->lim = 0;
-  u->whole = 1;
-  u->tail = 0;
-  u->kend = 0;
-  u->kbeg = 0;
-  u->s0 = 0;
-  u->s1 = -1;
-  // first and last row that belong to a sequence, of every tile, and the
-  // sequences they belong to: the warp's lanes try 32 offsets at a time, all
-  // six rows in one round of loads (one round up to 32 sequences)
-  const int front = a.cu[0], back = a.cu[a.batch];
-  const int lane = threadIdx.x & 31;
-  int f[kNT], e[kNT], at[2 * kNT], lo[2 * kNT], n[2 * kNT];
-#pragma unroll
-  for (int t = 0; t < kNT; ++t) {
-    f[t] = max(u->q0 + t * a.tpt, front);
-    e[t] = min(min(u->q_end, u->q0 + (t + 1) * a.tpt), back) - 1;
-    at[2 * t] = f[t];
-    at[2 * t + 1] = e[t];
-    lo[2 * t] = lo[2 * t + 1] = 0;
-    n[2 * t] = n[2 * t + 1] = a.batch;
+  const int lane = threadIdx.x & 31, t = lane >> 1;
+  const int q0 = (a.windows - 1 - win_rev) * w, q_end = min(a.tokens, q0 + w);
+  // the first and last row of the tile that lie in a sequence
+  const int first = max(q0 + t * a.tpt, a.cu[0]);
+  const int past = min(min(q_end, q0 + (t + 1) * a.tpt), a.cu[a.batch]);
+  const bool some = t < kNT && first < past;
+  // the last sequence that starts at or before this lane's row: the warp looks
+  // at 32 offsets at once, the lane bisects what lies between two of them
+  const int row = lane & 1 ? past - 1 : first;
+  const int step = (a.batch + 31) / 32;
+  const int v = a.cu[min(lane * step, a.batch - 1)];
+  int lo = 0;
+#pragma unroll 1
+  for (int i = 0; i < 2 * kNT; ++i) {
+    const int x = __shfl_sync(0xffffffffu, row, i);
+    const int c = __popc(__ballot_sync(0xffffffffu, lane * step < a.batch && v <= x));
+    if (lane == i) lo = max(c - 1, 0) * step;
   }
-  for (int left = a.batch, last = 0; !last; left = (left + 31) / 32) {
-    last = left <= 32;
-    int v[2 * kNT];
-#pragma unroll
-    for (int i = 0; i < 2 * kNT; ++i)
-      v[i] = a.cu[lo[i] + min(lane * ((n[i] + 31) / 32), n[i] - 1)];
-#pragma unroll
-    for (int i = 0; i < 2 * kNT; ++i) {
-      const int step = (n[i] + 31) / 32;
-      // offsets at or below the row, at least the first
-      const int hit =
-          max(__popc(__ballot_sync(0xffffffffu, lane * step < n[i] && v[i] <= at[i])), 1) - 1;
-      lo[i] += hit * step;
-      n[i] = min(step, n[i] - hit * step);
-    }
+  int hi = min(lo + step, a.batch);
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= row)
+      lo = mid;
+    else
+      hi = mid;
   }
-  int s = 0;  // lane i of the first six holds the sequence of row i
-#pragma unroll
-  for (int i = 0; i < 2 * kNT; ++i)
-    if (lane == i) s = lo[i];
-  const RowRange r = row_range(a.cu[s], a.cu[s + 1], a.tokens);
-  bool seen = false;
-#pragma unroll
-  for (int t = 0; t < kNT; ++t) {
-    const int sf = __shfl_sync(0xffffffffu, s, 2 * t), se = __shfl_sync(0xffffffffu, s, 2 * t + 1);
-    const int bf = __shfl_sync(0xffffffffu, r.begin, 2 * t);
-    const int ef = __shfl_sync(0xffffffffu, r.end, 2 * t);
-    const int be = __shfl_sync(0xffffffffu, r.begin, 2 * t + 1);
-    const int ee = __shfl_sync(0xffffffffu, r.end, 2 * t + 1);
-    u->t0[t] = u->t1[t] = u->lo_max[t] = u->hi_min[t] = 0;
-    if (f[t] > e[t]) continue;
-    if (!seen) {
-      seen = true;
-      u->kbeg = bf;
-      u->s0 = sf;
-    }
-    u->s1 = se;
-    u->hi_min[t] = (a.causal ? f[t] + 1 : ef) - u->kbeg;
-    u->lo_max[t] = be - u->kbeg;
-    const int keys = (a.causal ? e[t] + 1 : ee) - u->kbeg;
-    u->t0[t] = max(0, bf - u->kbeg) / kBN;
-    u->t1[t] = max(u->t0[t], (max(keys, 0) + kBN - 1) / kBN);
-    u->kend = max(u->kend, keys);
-    u->nj = max(u->nj, u->t1[t]);
+  __syncwarp();
+  const RowRange r = row_range(a.cu[lo], a.cu[lo + 1], a.tokens);
+  // key 0 of the window is the first key of its first row
+  const unsigned live = __ballot_sync(0xffffffffu, some);
+  const int lead = live ? __ffs(live) - 1 : 0, tail = live ? 31 - __clz(live) : 0;
+  const int kbeg = live ? __shfl_sync(0xffffffffu, r.begin, lead) : 0;
+  const int s0 = __shfl_sync(0xffffffffu, lo, lead), s1 = __shfl_sync(0xffffffffu, lo, tail);
+  const int begin = r.begin - kbeg, end = (a.causal ? row + 1 : r.end) - kbeg;
+  // even lanes hold the first row's, odd lanes the last row's
+  const int begin_last = __shfl_down_sync(0xffffffffu, begin, 1);
+  const int end_last = __shfl_down_sync(0xffffffffu, end, 1);
+  const int t0 = some ? max(begin, 0) / kBN : 0;
+  const int t1 = some ? max(t0, (max(end_last, 0) + kBN - 1) / kBN) : 0;
+  const bool mine = !(lane & 1) && t < kNT;
+  const int nj = __reduce_max_sync(0xffffffffu, mine ? t1 : 0);
+  const int kend = __reduce_max_sync(0xffffffffu, mine && some ? end_last : 0);
+  if (mine) {
+    u->t0[t] = t0;
+    u->t1[t] = t1;
+    u->lo_max[t] = some ? begin_last : 0;
+    u->hi_min[t] = some ? end : 0;
+  }
+  if (lane == 0) {
+    u->more = 1;
+    u->q0 = q0;
+    u->q_end = q_end;
+    u->kv = block - win_rev * a.Hkv;
+    u->kbeg = kbeg;
+    u->j0 = 0;
+    u->nj = nj;
+    u->kend = kend;
+    u->s0 = s0;
+    u->s1 = live ? s1 : -1;
+    u->lim = 0;
+    u->whole = 1;
+    u->tail = 0;
   }
 }
 
@@ -326,16 +323,6 @@ __device__ __forceinline__ void mask32(uint32_t (&v)[32], int lo, int hi) {
 #pragma unroll
   for (int e = 0; e < 32; ++e)
     if (e < lo || e >= hi) v[e] = 0xff800000u;
-}
-
-__device__ __forceinline__ float max32(const uint32_t (&v)[32], float m) {
-  float a = m, b = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < 32; e += 4) {
-    a = fmax3(a, as_f(v[e]), as_f(v[e + 1]));
-    b = fmax3(b, as_f(v[e + 2]), as_f(v[e + 3]));
-  }
-  return fmaxf(a, b);
 }
 
 __device__ __forceinline__ float max64(const uint32_t (&v)[32], const uint32_t (&w)[32]) {
@@ -746,14 +733,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        Unit u;
-        u.more = PAGED ? pos < share.end : block >= 0;
+        Unit& u = s_unit[ub];
+        const bool more = PAGED ? pos < share.end : block >= 0;
         int steps = 0, nt = 0;
-        if (u.more && PAGED) {
+        if (!more) {
+          if (lane == 0) u.more = 0;
+        } else if (PAGED) {
           nt = tiles_of_block(place.r.n_keys, place.r.n_new, kNT * a.tpt, kBN, place.blk);
           steps = (int)min((long long)(nt - place.t0), share.end - pos);
           paged_unit(a, place, place.t0 + steps, nt, &u);
-        } else if (u.more) {
+        } else {
           packed_unit(a, block, &u);
           if (block == 0) {
             // every pair of offsets is looked at once, whichever rows it spans
@@ -761,12 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               bad |= row_range(a.cu[i], a.cu[i + 1], a.tokens).bad;
           }
         }
-        if (lane == 0) {
-          s_unit[ub] = u;
-          mbar_arrive(BAR(BAR_UNIT + ub));
-        }
         __syncwarp();
-        if (!u.more) break;
+        if (lane == 0) mbar_arrive(BAR(BAR_UNIT + ub));
+        if (!more) break;
         const int req = place.req, n_keys = place.r.n_keys;
         if (PAGED) {
           if (!u.whole && u.tail) {
