@@ -146,8 +146,28 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "attn_paged_plan", "attn_paged_store", "attn_paged_fwd"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
+        _bind_native(lib)
         _lib = lib
     return lib
+
+
+# csrc/marshal.cpp, once the library is loaded: the serving calls' checks and
+# launch in one step for tensors of the current device on its current stream.
+# It returns the call's code, or None where the path below it has to go on.
+_native = None
+
+
+def _bind_native(lib) -> None:
+    global _native
+    try:
+        from . import _marshal
+    except ImportError as e:
+        raise ImportError("_marshal.so could not be loaded (%s): build it with "
+                          "causal_streaming_softmax_gb300.build.build()" % e) from e
+    _marshal.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                    for n in ("attn_packed_fwd", "attn_paged_plan", "attn_paged_store",
+                              "attn_paged_fwd")))
+    _native = _marshal
 
 
 def error_string(code: int) -> str:
@@ -553,7 +573,7 @@ class PagedShape:
             return _PAGED.pack(self.batch, self.tokens, self.heads, self.kv_heads, HEAD_DIM,
                                self.page_size, self.num_pages, self.table_width, self.max_new,
                                _dtype_code(self.dtype), self.scale, *strides)
-        except struct.error as e:
+        except (struct.error, OverflowError) as e:
             raise ValueError("a size does not fit the C struct: %s" % e) from None
 
 
@@ -631,6 +651,12 @@ def attn_packed_fwd(s: PackedShape, q, k, v, cu, o, lse=None, stream=None) -> No
     """Attention over packed sequences: q [tokens][heads][64], k, v
     [tokens][kv_heads][64] and o as q, any strides over tokens and heads; cu
     int32 [batch + 1] on the device; lse float32 [heads][tokens] or None."""
+    if stream is None and _native is not None:
+        rc = _native.packed_fwd(s, q, k, v, cu, o, lse)
+        if rc == ATTN_OK:
+            return
+        if rc is not None:
+            raise AttnError("attn_packed_fwd", rc)
     n, H, Hkv, dt = s.tokens, s.heads, s.kv_heads, s.dtype
     dev = _device_of(q, "q")
     qp, qs = _strided(q, "q", dt, (n, H, 64), dev)
@@ -642,7 +668,7 @@ def attn_packed_fwd(s: PackedShape, q, k, v, cu, o, lse=None, stream=None) -> No
     try:
         shape = _PACKED.pack(n, s.batch, H, Hkv, HEAD_DIM, 1 if s.causal else 0, _dtype_code(dt),
                              s.scale, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
-    except struct.error as e:
+    except (struct.error, OverflowError) as e:
         raise ValueError("a size does not fit the C struct: %s" % e) from None
     _run("attn_packed_fwd", dev, stream, shape, qp, kp, vp, cup, op, lp)
 
@@ -651,6 +677,12 @@ def attn_paged_plan(s: PagedShape, cached, fresh, ring, state, table, cu, lens, 
                     stream=None) -> None:
     """Hands out and takes back pages and writes table, cu, lens, slots, next
     (int32 CUDA tensors; see attn.h).  ``fresh`` < 0 marks a finished request."""
+    if stream is None and _native is not None:
+        rc = _native.paged_plan(s, cached, fresh, ring, state, table, cu, lens, slots, next)
+        if rc == ATTN_OK:
+            return
+        if rc is not None:
+            raise AttnError("attn_paged_plan", rc)
     B, i32 = s.batch, torch.int32
     dev = _device_of(cached, "cached")
     _run("attn_paged_plan", dev, stream, s.c_bytes(),
@@ -664,6 +696,12 @@ def attn_paged_plan(s: PagedShape, cached, fresh, ring, state, table, cu, lens, 
 def attn_paged_store(s: PagedShape, k, v, slots, k_cache, v_cache, stream=None) -> None:
     """Rows of k, v [tokens][kv_heads][64] into the caches
     [num_pages][kv_heads][page_size][64] (any strides) at slots int32 [tokens]."""
+    if stream is None and _native is not None:
+        rc = _native.paged_store(s, k, v, slots, k_cache, v_cache)
+        if rc == ATTN_OK:
+            return
+        if rc is not None:
+            raise AttnError("attn_paged_store", rc)
     dev, dt = _device_of(k, "k"), s.dtype
     rows, dims = (s.tokens, s.kv_heads, 64), (s.num_pages, s.kv_heads, s.page_size, 64)
     kp, ks = _strided(k, "k", dt, rows, dev)
@@ -693,6 +731,12 @@ def attn_paged_fwd(s: PagedShape, q, k_cache, v_cache, table, cu, lens, ws, o, l
                    stream=None) -> None:
     """Attention of the new rows q [tokens][heads][64] over the cache; o as q,
     lse float32 [heads][tokens] or None; ws from alloc_paged_workspace."""
+    if stream is None and _native is not None:
+        rc = _native.paged_fwd(s, q, k_cache, v_cache, table, cu, lens, ws, o, lse)
+        if rc == ATTN_OK:
+            return
+        if rc is not None:
+            raise AttnError("attn_paged_fwd", rc)
     n, H, B, dt = s.tokens, s.heads, s.batch, s.dtype
     dev = _device_of(q, "q")
     dims = (s.num_pages, s.kv_heads, s.page_size, 64)

@@ -4,13 +4,19 @@ Each translation unit is compiled by its own nvcc process (in parallel), then
 linked into ``causal_streaming_softmax_gb300/libattn.so``.  Objects go to
 ``causal_streaming_softmax_gb300/_build/``.  A rebuild happens only when a
 source or header is newer than the library.
+
+``_marshal.so`` beside it is a small Python extension (host code) that hands
+PyTorch tensors to the library's serving calls; it is compiled by g++ against
+the installed PyTorch's headers in the same way.
 """
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libattn.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -48,8 +56,45 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def marshal_up_to_date() -> bool:
+    if not os.path.exists(MARSHAL):
+        return False
+    t = os.path.getmtime(MARSHAL)
+    return all(os.path.getmtime(p) <= t for p in (MARSHAL_SRC, os.path.join(INCLUDE, "attn.h"),
+                                                  os.path.join(_torch(), "version.py"), __file__))
+
+
+def _torch() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("PyTorch not found: its headers are required to build _marshal.so")
+    return spec.submodule_search_locations[0]
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compile the Python extension that marshals the serving calls."""
+    if not force and marshal_up_to_date():
+        return MARSHAL
+    torch, cuda = _torch(), os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    lib = os.path.join(torch, "lib")
+    tmp = MARSHAL + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden"] + \
+        [x for p in inc for x in ("-isystem", p)] + [MARSHAL_SRC, "-o", tmp, "-L" + lib,
+         "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on %s:\n%s%s" % (MARSHAL_SRC, r.stdout, r.stderr))
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
+    if not force and up_to_date() and marshal_up_to_date():
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -67,8 +112,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
-        objs = list(ex.map(compile_one, srcs))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        marshal = ex.submit(build_marshal, force, verbose)
+        objs = [] if not force and up_to_date() else list(ex.map(compile_one, srcs))
+        marshal.result()
+    if not objs:
+        return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     if verbose:

@@ -781,3 +781,70 @@ def test_a_captured_step_outlives_larger_steps(torch):
     eo, _, to, _ = attend64(qs, kk, vv, torch.tensor([kk.shape[0]], device="cuda"))
     check(two[1], eo, to, "replayed step")
     assert cache.lens.tolist() == [kk.shape[0]] and cache.status() == 0
+
+
+def test_both_marshalling_paths(torch, monkeypatch):
+    """The calls through the native marshaller and through Python's checks
+    (another stream, or a case the marshaller leaves) do the same."""
+    from causal_streaming_softmax_gb300 import api
+    q, k, v = packed_inputs(torch, 300, 8, 2, torch.bfloat16, 19)
+    paged = paged_problem(torch, [(400, 1), (90, 30), (7, 1)], 8, 2, 16, torch.float16, 20, "rows")
+
+    def everything():
+        cache = api.PagedCache(2, 8, 2, num_pages=30, dtype=torch.bfloat16)
+        o = torch.zeros((300, 8, 64), dtype=torch.bfloat16, device="cuda")
+        cache.step(i32(torch, [200, 100]), q, k, v, o)
+        return run_packed(torch, q, k, v, [0, 120, 300], o_layout="wide") + \
+            run_packed(torch, q, k, v, [0, 120, 300], causal=False, lse=False)[:1] + \
+            run_paged(torch, *paged[:6]) + (o, cache.k, cache.v, cache.table, cache.lens)
+
+    api.load_library()
+    assert api._native is not None
+    native = everything()
+    with monkeypatch.context() as m:
+        m.setattr(api, "_native", None)
+        python = everything()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    o, L = run_packed(torch, q, k, v, [0, 120, 300], stream=side)
+    side.synchronize()
+    for a, b in zip(native + (native[0],), python + (o,)):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def test_python_names_what_is_wrong(torch):
+    from causal_streaming_softmax_gb300 import api
+    n, H, Hkv = 10, 4, 2
+    q, k, v = packed_inputs(torch, n, H, Hkv, torch.float16, 21)
+    cu, o = i32(torch, [0, n]), torch.empty((n, H, 64), dtype=torch.float16, device="cuda")
+    s = api.PackedShape(n, 1, H, Hkv)
+    call = lambda **kw: api.attn_packed_fwd(**dict(dict(s=s, q=q, k=k, v=v, cu=cu, o=o), **kw))
+    call()
+    for kw, err, word in [
+            (dict(q=q.bfloat16()), TypeError, "q must be torch.float16"),
+            (dict(k=k[:9]), ValueError, "k must have shape"),
+            (dict(v=v.cpu()), ValueError, "v must be a CUDA tensor"),
+            (dict(cu=cu.long()), TypeError, "cu must be torch.int32"),
+            (dict(cu=i32(torch, [0, 3, n])), ValueError, "cu must have shape"),
+            (dict(o=o.transpose(1, 2).contiguous().transpose(1, 2)), ValueError, "dense in its last"),
+            (dict(lse=torch.empty((n, H), device="cuda").t()), ValueError, "lse must be contiguous"),
+            (dict(q=None), TypeError, "q must be a torch tensor"),
+            (dict(s=api.PackedShape(n, 1, H, Hkv, dtype=torch.float32)), TypeError, "float32"),
+            (dict(s=api.PackedShape(1 << 40, 1, H, Hkv)), ValueError, "shape"),
+            (dict(s=api.PackedShape(n, 1, H, Hkv, scale=0.0)), api.AttnError, "admission"),
+            (dict(o=o[:1].expand(n, H, 64)), api.AttnError, "admission"),
+            (dict(q=torch.empty(n * H * 64 + 1, dtype=torch.float16, device="cuda")[1:]
+                  .view(n, H, 64)), api.AttnError, "16-byte aligned")]:
+        with pytest.raises(err, match=word):
+            call(**kw)
+    p = api.PagedShape(1, n, H, Hkv, 16, 4, 4, max_new=n)
+    with pytest.raises(TypeError, match="ws must be"):
+        api.attn_paged_fwd(p, q, torch.empty((4, Hkv, 16, 64), dtype=torch.float16, device="cuda"),
+                           torch.empty((4, Hkv, 16, 64), dtype=torch.float16, device="cuda"),
+                           i32(torch, [[0, 1, 2, 3]]), cu, i32(torch, [n]),
+                           torch.empty(1 << 26, device="cuda"), o)
+    with pytest.raises(api.AttnError, match="workspace"):
+        api.attn_paged_fwd(p, q, torch.empty((4, Hkv, 16, 64), dtype=torch.float16, device="cuda"),
+                           torch.empty((4, Hkv, 16, 64), dtype=torch.float16, device="cuda"),
+                           i32(torch, [[0, 1, 2, 3]]), cu, i32(torch, [n]),
+                           torch.empty(1 << 10, dtype=torch.uint8, device="cuda"), o)
