@@ -41,28 +41,33 @@
 namespace css {
 namespace {
 
-constexpr int kTileKeys = 64;
-constexpr int kStages = 5;
-constexpr int kConsumers = 4;
-constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr uint32_t kHalf = kTileKeys * 128;  // K (or V) of a stage
-constexpr uint32_t kStage = 2 * kHalf;
-constexpr uint32_t kQ = kDecodeRows * 128;
-constexpr int kLd = 68;  // floats a row of the joining buffer (bank spread)
-constexpr uint32_t kSmemQ = kStages * kStage;
-constexpr uint32_t kSmemJoin = kSmemQ + 2 * kQ;
-constexpr uint32_t kSmemMl = kSmemJoin + kConsumers * kDecodeRows * kLd * 4;
-constexpr uint32_t kSmemBar = kSmemMl + kConsumers * kDecodeRows * 8;
-constexpr uint32_t kSmemPre = kSmemBar + 128;  // + 8 (batch + 1), + alignment slack
-
-enum {
-  BAR_FULL = 0,
-  BAR_EMPTY = BAR_FULL + kStages,
-  BAR_Q = BAR_EMPTY + kStages,  // [2]
-  BAR_Q_FREE = BAR_Q + 2,       // [2]
-  BAR_COUNT = BAR_Q_FREE + 2
+// A block's shape: consumer warps of 16 keys each, stages, and its shared
+// memory.  kWhole: a block takes whole items, so that nothing is joined.
+template <int CONSUMERS, int STAGES, bool WHOLE>
+struct Config {
+  static constexpr bool kWhole = WHOLE;
+  static constexpr int kMaxBatch = WHOLE ? 1024 : kMaxPagedBatch;  // whole: <= the SMs
+  static constexpr int kConsumers = CONSUMERS, kStages = STAGES;
+  static constexpr int kThreads = 32 * (CONSUMERS + 1);
+  static constexpr int kTileKeys = 16 * CONSUMERS;
+  static constexpr uint32_t kHalf = kTileKeys * 128;  // K (or V) of a stage
+  static constexpr uint32_t kStage = 2 * kHalf;
+  static constexpr uint32_t kQ = kDecodeRows * 128;
+  static constexpr uint32_t kSmemQ = kStages * kStage;
+  static constexpr uint32_t kSmemJoin = kSmemQ + 2 * kQ;
+  static constexpr uint32_t kSmemMl = kSmemJoin + kConsumers * kDecodeRows * 68 * 4;
+  static constexpr uint32_t kSmemBar = kSmemMl + kConsumers * kDecodeRows * 8;
+  static constexpr uint32_t kSmemPre = kSmemBar + 128;  // + 8 (batch + 1), + alignment slack
+  // barriers
+  static constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQFree = kQFull + 2;
+  static_assert((kQFree + 2) * 8 <= 128, "barrier area");
 };
-static_assert(BAR_COUNT * 8 <= 128, "barrier area");
+using Split = Config<4, 5, false>;
+using Whole = Config<8, 4, true>;
+static_assert(Split::kSmemPre + 8 * (Split::kMaxBatch + 1) + 1024 <= 227 * 1024 - 2048 &&
+                  Whole::kSmemPre + 8 * (Whole::kMaxBatch + 1) + 1024 <= 227 * 1024 - 2048,
+              "shared memory of a block");
+constexpr int kLd = 68;  // floats a row of the joining buffer (bank spread)
 
 struct DecodeArgs {
   int batch, tokens, H, Hkv, G, ntok, max_new, pages, width, shift;
@@ -89,8 +94,9 @@ __device__ __forceinline__ Request request_at(const DecodeArgs& a, int i, bool* 
   return q;
 }
 
+template <class C>
 __device__ __forceinline__ int tiles_of(int n_keys) {
-  return n_keys <= 0 ? 1 : (n_keys - 1) / kTileKeys + 1;
+  return n_keys <= 0 ? 1 : (n_keys - 1) / C::kTileKeys + 1;
 }
 
 // A place in the tile list: tile t0 of nt of a request and K/V head.
@@ -99,8 +105,9 @@ struct Place {
   int req, kv, t0, nt;
 };
 
-// The place at position pos.  pre[i] counts the tiles of one head of the
-// requests before i.
+// The place at position pos.  pre[i] counts the tiles (whole: the items) of one
+// head of the requests before i.
+template <class C>
 __device__ __forceinline__ Place place_at(const DecodeArgs& a, const long long* pre,
                                           long long pos) {
   int lo = 0, hi = a.batch;  // the last i with pre[i] * Hkv <= pos: never an empty request
@@ -113,44 +120,50 @@ __device__ __forceinline__ Place place_at(const DecodeArgs& a, const long long* 
   }
   Place p;
   p.req = lo - 1;
-  p.nt = (int)(pre[lo] - pre[p.req]);
   const long long off = pos - pre[p.req] * a.Hkv;
-  p.kv = (int)quot(off, p.nt);
-  p.t0 = (int)(off - (long long)p.kv * p.nt);
   bool b;
   p.r = request_at(a, p.req, &b);
+  p.nt = tiles_of<C>(p.r.n_keys);
+  p.kv = C::kWhole ? (int)off : (int)quot(off, p.nt);
+  p.t0 = C::kWhole ? 0 : (int)(off - (long long)p.kv * p.nt);
   return p;
 }
 
-// The place behind an item: the next head or the next request with tiles.
+// The place behind an item: the next head or the next request with rows.
 // Called only where the list goes on.
+template <class C>
 __device__ __forceinline__ void next_place(const DecodeArgs& a, const long long* pre, Place* p) {
   p->t0 = 0;
   if (++p->kv < a.Hkv) return;
   p->kv = 0;
   do {
     ++p->req;
-    p->nt = (int)(pre[p->req + 1] - pre[p->req]);
-  } while (p->nt == 0 && p->req + 1 < a.batch);
+  } while (pre[p->req + 1] == pre[p->req] && p->req + 1 < a.batch);
   bool b;
   p->r = request_at(a, p->req, &b);
+  p->nt = tiles_of<C>(p->r.n_keys);
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 2)
+template <bool BF16, class C>
+__global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a) {
+  constexpr int kConsumers = C::kConsumers, kStages = C::kStages, kThreads = C::kThreads,
+                kTileKeys = C::kTileKeys;
+  constexpr uint32_t kHalf = C::kHalf, kStage = C::kStage, kQ = C::kQ, kSmemQ = C::kSmemQ;
+  constexpr int BAR_FULL = C::kFull, BAR_EMPTY = C::kEmpty, BAR_Q = C::kQFull,
+                BAR_Q_FREE = C::kQFree;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int s_abort;
   __shared__ long long s_scan[kThreads / 32];
   griddep_launch_dependents();
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (sbase - smem_u32(smem_raw));
-  float* const s_join = reinterpret_cast<float*>(smem + kSmemJoin);
-  float2* const s_ml = reinterpret_cast<float2*>(smem + kSmemMl);
-  long long* const s_pre = reinterpret_cast<long long*>(smem + kSmemPre);
-  const uint32_t bar0 = sbase + kSmemBar;
+  float* const s_join = reinterpret_cast<float*>(smem + C::kSmemJoin);
+  float2* const s_ml = reinterpret_cast<float2*>(smem + C::kSmemMl);
+  long long* const s_pre = reinterpret_cast<long long*>(smem + C::kSmemPre);
+  const uint32_t bar0 = sbase + C::kSmemBar;
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const WaitCtl wc{a.err, a.wait_ns, &s_abort};
@@ -183,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool b;
       const Request r = request_at(a, i, &b);
       bad |= b;
-      s_pre[i + 1] = sum += r.n_new > 0 ? tiles_of(r.n_keys) : 0;
+      s_pre[i + 1] = sum += r.n_new > 0 ? (C::kWhole ? 1 : tiles_of<C>(r.n_keys)) : 0;
     }
     if (bad && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
     long long upto = sum;
@@ -200,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 0) s_pre[0] = 0;
     __syncthreads();
   }
-  const Share share = share_of(s_pre[a.batch] * a.Hkv, a.part.min_tiles, gridDim.x, blockIdx.x);
+  const Share share = share_of(s_pre[a.batch] * a.Hkv, C::kWhole ? 1 : a.part.min_tiles, gridDim.x, blockIdx.x);
 
   if (warp == kConsumers) {
     // ---------------- producer ----------------
@@ -221,20 +234,20 @@ __global__ void __launch_bounds__(kThreads, 2)
       nx_next = at + 32 < n ? row[at + 32] : a.pages;
     };
     if (share.begin < share.end) {
-      nx = place_at(a, s_pre, share.begin);
+      nx = place_at<C>(a, s_pre, share.begin);
       read_ids();
     }
     for (long long pos = share.begin; ok && pos < share.end;) {
       const Place sg = nx;
       const Request r = sg.r;
-      const int t1 = (int)min((long long)sg.nt, sg.t0 + (share.end - pos));
+      const int t1 = C::kWhole ? sg.nt : (int)min((long long)sg.nt, sg.t0 + (share.end - pos));
       const int32_t* const row = a.table + (long long)sg.req * a.width;
       const int n_pages = (int)pages_for(r.n_keys, a.shift);
       int base = (int)(((long long)sg.t0 * kTileKeys) >> a.shift);
       int ids = nx_ids, next = nx_next;
-      pos += t1 - sg.t0;
+      pos += C::kWhole ? 1 : t1 - sg.t0;
       if (pos < share.end) {
-        next_place(a, s_pre, &nx);
+        next_place<C>(a, s_pre, &nx);
         read_ids();
       }
       const int qbuf = nq & 1;
@@ -260,17 +273,21 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         // boxes that hold keys below n_keys; the rest of the stage is masked
         const int live = r.n_keys <= k0 ? 0 : min(boxes, (r.n_keys - k0 + box - 1) / box);
-        const int bx = lane & 15;
-        const int id = __shfl_sync(0xffffffffu, ids, (page - base + (per_tile ? bx : 0)) & 31);
-        const bool fine = page_ok(id, a.pages);
-        const int at = fine ? id : a.pages;  // past the pool: reads as zero
         if (lane == 0) mbar_arrive_expect_tx(BAR(BAR_FULL + s), 2 * live * box * 128);
         __syncwarp();
-        if (bx < live) {
-          bad |= !fine;
-          tma_load_4d(sbase + s * kStage + (lane >> 4) * kHalf + bx * box * 128,
-                      lane < 16 ? &tm_k : &tm_v, BAR(BAR_FULL + s), 0,
-                      per_tile ? 0 : k0 & ((1 << a.shift) - 1), sg.kv, at);
+#pragma unroll
+        for (int b0 = 0; b0 < kTileKeys / 8; b0 += 16) {  // pages of 8 tokens make the most boxes
+          if (b0 >= boxes) break;
+          const int bx = b0 + (lane & 15);
+          const int id = __shfl_sync(0xffffffffu, ids, (page - base + (per_tile ? bx : 0)) & 31);
+          const bool fine = page_ok(id, a.pages);
+          if (bx < live) {
+            bad |= !fine;
+            tma_load_4d(sbase + s * kStage + (lane >> 4) * kHalf + bx * box * 128,
+                        lane < 16 ? &tm_k : &tm_v, BAR(BAR_FULL + s), 0,
+                        per_tile ? 0 : k0 & ((1 << a.shift) - 1), sg.kv,
+                        fine ? id : a.pages);  // past the pool: reads as zero
+          }
         }
       }
     }
@@ -289,11 +306,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     int it = 0, nq = 0;
     bool ok = true, tail = false;
     Place sg{};
-    if (share.begin < share.end) sg = place_at(a, s_pre, share.begin);
+    if (share.begin < share.end) sg = place_at<C>(a, s_pre, share.begin);
     for (long long pos = share.begin; pos < share.end;) {
       const Request r = sg.r;
-      const int t1 = (int)min((long long)sg.nt, sg.t0 + (share.end - pos));
-      pos += t1 - sg.t0;
+      const int t1 = C::kWhole ? sg.nt : (int)min((long long)sg.nt, sg.t0 + (share.end - pos));
+      pos += C::kWhole ? 1 : t1 - sg.t0;
       const int rows = r.n_new * a.G;
       const int qbuf = nq & 1;
       uint32_t q[4][4];
@@ -434,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       named_barrier_sync(1, kConsumers * 32);
       const int row = tid >> 3, c0 = (tid & 7) * 8;
-      if (ok && row < rows) {
+      if (ok && row < rows) {  // the first 128 threads have a row
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, s_ml[w * kDecodeRows + row].x);
@@ -451,53 +468,75 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int e = 0; e < 8; ++e) acc[e] = fmaf(d[e], f, acc[e]);
         }
         const int tok = r.q0 + row / a.G, h = sg.kv * a.G + row % a.G;
-        if (sg.t0 == 0 && t1 == sg.nt)
+        if (C::kWhole || (sg.t0 == 0 && t1 == sg.nt))
           write_row<BF16>(a.o, a.lse, a.tokens, tok, h, c0, acc, m, l);
         else
           store_part(a.part, blockIdx.x, sg.t0 == 0, row, c0, acc, m, l);
       }
-      if (sg.t0 == 0 && t1 < sg.nt) {
+      if (!C::kWhole && sg.t0 == 0 && t1 < sg.nt) {
         tail = true;
         if (tid == 0)
           a.part.desc[blockIdx.x] =
               PartDesc{r.q0, sg.kv, rows, last_block(share, pos - t1 + sg.nt - 1)};
       }
-      if (pos < share.end) next_place(a, s_pre, &sg);
+      if (pos < share.end) next_place<C>(a, s_pre, &sg);
       named_barrier_sync(1, kConsumers * 32);
     }
-    if (tid == 0 && !tail) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
+    if (!C::kWhole && tid == 0 && !tail) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
   }
 #undef BAR
 }
 
 }  // namespace
 
+constexpr int kWholeKeys = 256;
+
 int decode_tokens(int G) { return G > kDecodeRows ? 0 : kDecodeRows / G; }
 
+
+namespace {
+
+template <class C>
+int launch(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
+           const PoolArg& vc, const DecodeArgs& args, int blocks, int which, cudaStream_t stream) {
+  CUtensorMap tq, tk, tv;
+  const uint32_t box = (1u << d.shift) < C::kTileKeys ? (1u << d.shift) : C::kTileKeys;
+  const uint64_t P = 1ull << d.shift;
+  if (!encode_tmap_4d(&tq, d.bf16, q.p, d.G, d.Hkv, d.tokens, q.h, q.h * d.G, q.t, d.G, 1,
+                      args.ntok) ||
+      !encode_tmap_4d(&tk, d.bf16, kc.p, P, d.Hkv, d.pages, kc.r, kc.h, kc.pg, box, 1, 1) ||
+      !encode_tmap_4d(&tv, d.bf16, vc.p, P, d.Hkv, d.pages, vc.r, vc.h, vc.pg, box, 1, 1))
+    return ATTN_ERR_CUDA;
+  const size_t smem = C::kSmemPre + 8 * (size_t)(d.batch + 1) + 1024;
+  auto* kernel = d.bf16 ? paged_decode_kernel<true, C> : paged_decode_kernel<false, C>;
+  const int rc = allow_smem(which + d.bf16, reinterpret_cast<const void*>(kernel),
+                            C::kSmemPre + 8 * (C::kMaxBatch + 1) + 1024);
+  if (rc != ATTN_OK) return rc;
+  return cuda_status(launch_dependent(kernel, dim3(blocks), dim3(C::kThreads), smem, stream, tq,
+                                      tk, tv, args));
+}
+
+}  // namespace
+
+// Whole items where every item finds an SM and the table leaves room for no
+// more than kWholeKeys keys a request: eight warps are through with an item in
+// two steps, and the parts and the second launch fall away.  Split / whole, us:
+// one request of 100 keys 6.1 / 4.6, of 250 7.4 / 6.3, of 777 8.5 / 10.0; eight
+// of 256 8.3 / 6.0; 64 of 60 (512 items) 8.1 / 10.7.
+bool decode_whole(const PagedDims& d, int sm_count) {
+  return (long long)d.batch * d.Hkv <= sm_count && ((long long)d.width << d.shift) <= kWholeKeys;
+}
 
 int launch_paged_decode(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
                         const PoolArg& kc, const PoolArg& vc, const int32_t* table,
                         const int32_t* cu, const int32_t* lens, const PartArgs& part, int blocks,
                         const RowsArg& o, float* lse, cudaStream_t stream) {
-  CUtensorMap tq, tk, tv;
-  const int ntok = decode_tokens(d.G);
-  const uint32_t box = (1u << d.shift) < kTileKeys ? (1u << d.shift) : kTileKeys;
-  const uint64_t P = 1ull << d.shift;
-  if (!encode_tmap_4d(&tq, d.bf16, q.p, d.G, d.Hkv, d.tokens, q.h, q.h * d.G, q.t, d.G, 1, ntok) ||
-      !encode_tmap_4d(&tk, d.bf16, kc.p, P, d.Hkv, d.pages, kc.r, kc.h, kc.pg, box, 1, 1) ||
-      !encode_tmap_4d(&tv, d.bf16, vc.p, P, d.Hkv, d.pages, vc.r, vc.h, vc.pg, box, 1, 1))
-    return ATTN_ERR_CUDA;
-  const DecodeArgs args{d.batch, d.tokens, d.H,  d.Hkv, d.G, ntok, d.max_new, d.pages, d.width,
-                        d.shift, d.c,      cu,   lens,  table, o,  lse,       part,    ctx.err,
+  const DecodeArgs args{d.batch, d.tokens, d.H, d.Hkv, d.G,  decode_tokens(d.G), d.max_new,
+                        d.pages, d.width,  d.shift, d.c, cu, lens, table, o, lse, part, ctx.err,
                         ctx.wait_ns};
-  const size_t smem = kSmemPre + 8 * (size_t)(d.batch + 1) + 1024;
-  auto* kernel = d.bf16 ? paged_decode_kernel<true> : paged_decode_kernel<false>;
-  const int rc = allow_smem(d.bf16 ? kSmemDecodeBf16 : kSmemDecodeF16,
-                            reinterpret_cast<const void*>(kernel),
-                            kSmemPre + 8 * (4096 + 1) + 1024);
-  if (rc != ATTN_OK) return rc;
-  return cuda_status(launch_dependent(kernel, dim3(blocks), dim3(kThreads), smem, stream, tq, tk,
-                                      tv, args));
+  if (decode_whole(d, ctx.sm_count))
+    return launch<Whole>(d, ctx, q, kc, vc, args, d.batch * d.Hkv, kSmemWholeF16, stream);
+  return launch<Split>(d, ctx, q, kc, vc, args, blocks, kSmemDecodeF16, stream);
 }
 
 }  // namespace css

@@ -153,9 +153,9 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
   if (ntok > 0) {
     few = parts_at(at, 2 * kMaxSm, kDecodeRows, kLeastFew);
     at += parts_bytes(2 * kMaxSm, kDecodeRows);
-    n_few = 2 * sms;
-    rc = launch_paged_decode(d, ctx, q, kc, vc, table, cu, lens, few, n_few, o, lse, stream);
+    rc = launch_paged_decode(d, ctx, q, kc, vc, table, cu, lens, few, 2 * sms, o, lse, stream);
     if (rc != ATTN_OK) return rc;
+    if (!decode_whole(d, ctx.sm_count)) n_few = 2 * sms;
   }
   if (d.max_new > ntok) {
     rows = parts_at(at, kMaxSm, kItemRows, kLeastRows);
@@ -163,6 +163,7 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
     rc = launch_paged_rows(d, ctx, q, kc, vc, table, cu, lens, rows, n_rows, ntok, o, lse, stream);
     if (rc != ATTN_OK) return rc;
   }
+  if (n_few + n_rows == 0) return ATTN_OK;
   return launch_join(d, few, n_few, rows, n_rows, o, lse, stream);
 }
 

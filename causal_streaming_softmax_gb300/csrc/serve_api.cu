@@ -40,7 +40,7 @@ int validate_heads(int heads, int kv_heads, int head_dim, int dtype) {
 // The part of a paged shape that every call reads.
 int validate_paged(const attn_paged_shape* s, PagedDims* d) {
   if (!s) return ATTN_ERR_NULL;
-  if (s->batch < 1 || s->batch > 4096 || s->tokens < 0 || s->tokens > (1 << 30))
+  if (s->batch < 1 || s->batch > kMaxPagedBatch || s->tokens < 0 || s->tokens > (1 << 30))
     return ATTN_ERR_SHAPE;
   int shift = 3;
   while (shift < 10 && (1 << shift) != s->page_size) ++shift;

@@ -44,9 +44,12 @@ struct PartArgs {
 // Rows (new tokens x heads of a group) of a request that paged_decode takes,
 // and the new tokens that makes for a group of G heads (0: none).
 constexpr int kDecodeRows = 16;
+constexpr int kMaxPagedBatch = 4096;
 // Rows of a work item of the tile kernel: three tiles.
 constexpr int kItemRows = 384;
 int decode_tokens(int G);
+// Whether paged_decode finishes every item itself (no parts to join).
+bool decode_whole(const PagedDims& d, int sm_count);
 int launch_paged_decode(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
                         const PoolArg& kc, const PoolArg& vc, const int32_t* table,
                         const int32_t* cu, const int32_t* lens, const PartArgs& part, int blocks,
@@ -61,6 +64,8 @@ int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, c
 enum {
   kSmemDecodeF16,
   kSmemDecodeBf16,
+  kSmemWholeF16,
+  kSmemWholeBf16,
   kSmemPackedF16,
   kSmemPackedBf16,
   kSmemRowsF16,
