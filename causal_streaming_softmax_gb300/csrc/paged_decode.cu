@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
           next = base + 32 + lane < n_pages ? row[base + 32 + lane] : a.pages;
         }
         // boxes that hold keys below n_keys; the rest of the stage is masked
-        const int live = r.n_keys <= k0 ? 0 : min(boxes, (r.n_keys - k0 + box - 1) / box);
+        const int live = r.n_keys <= k0 ? 0 : min(boxes, (r.n_keys - k0 - 1) / box + 1);
         if (lane == 0) mbar_arrive_expect_tx(BAR(BAR_FULL + s), 2 * live * box * 128);
         __syncwarp();
 #pragma unroll

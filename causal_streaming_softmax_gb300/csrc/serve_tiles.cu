@@ -219,7 +219,7 @@ __device__ __forceinline__ void paged_unit(const TileArgs& a, const Place& p, in
   const int first = q0 + t * a.tpt, past = min(q_end, first + a.tpt);
   const bool some = t < kNT && first < past;
   const int keys = some ? lim + (past - 1 - q0) : 0;  // the last row's
-  const int n = keys <= 0 ? 0 : (keys + kBN - 1) / kBN;
+  const int n = keys <= 0 ? 0 : (keys - 1) / kBN + 1;
   const int mine = some ? max(0, min(n, t1) - p.t0) : 0;
   const int nj = __reduce_max_sync(0xffffffffu, mine);
   const int kend = __reduce_max_sync(0xffffffffu, max(keys, 0));
@@ -385,7 +385,7 @@ __device__ __forceinline__ bool any_nonfinite(const uint4& w) {
 // thread: P from its tensor-memory columns, V from the stage.  Rare.
 template <bool BF16>
 __device__ __noinline__ void row_product(uint32_t t_p, uint32_t t_o, const uint8_t* v, int lo,
-                                            int hi, bool first) {
+                                         int hi, bool first) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {  // 16 columns at a time
     uint32_t o[16];
@@ -498,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool b;
       const PagedReq r = paged_req(a, i, &b);
       bad |= b;
-      s_pre[i + 1] = sum += r.n_new > 0 ? tiles_before(r.n_keys, r.n_new, w, kBN, (r.n_new + w - 1) / w) : 0;
+      if (r.n_new > 0) sum += tiles_before(r.n_keys, r.n_new, w, kBN, (r.n_new + w - 1) / w);
+      s_pre[i + 1] = sum;
     }
     if (bad && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
     long long upto = sum;
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 15) {
       // ---------------- work items and loads ----------------
       int kt = 0, nu = 0, nq = 0;
-      bool ok = true, bad = false, tail = false;
+      bool ok = true, bad = false, tail = false, checks = false;
       const int q_rows = a.tpt * a.G;
       long long pos = share.begin;
       int block = blockIdx.x, taken = 0;  // packed: the window and head of this round
@@ -744,11 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           paged_unit(a, place, place.t0 + steps, nt, &u);
         } else {
           packed_unit(a, block, &u);
-          if (block == 0) {
-            // every pair of offsets is looked at once, whichever rows it spans
-            for (int i = lane; i < a.batch; i += 32)
-              bad |= row_range(a.cu[i], a.cu[i + 1], a.tokens).bad;
-          }
+          checks |= block == 0;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(BAR_UNIT + ub));
@@ -810,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ids = next;
               next = base + 32 + lane < n_pages ? row[base + 32 + lane] : a.pages;
             }
-            const int live = n_keys <= k0 ? 0 : min(boxes, (n_keys - k0 + box - 1) / box);
+            const int live = n_keys <= k0 ? 0 : min(boxes, (n_keys - k0 - 1) / box + 1);
             const int bx = lane & 15;
             const int id = __shfl_sync(0xffffffffu, ids, (page - base + (boxes > 1 ? bx : 0)) & 31);
             const bool fine = page_ok(id, a.pages);
@@ -830,6 +827,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (!ok) break;
+      }
+      if (checks) {
+        // every pair of offsets is looked at once, whichever rows it spans
+        for (int i = lane; i < a.batch; i += 32)
+          bad |= row_range(a.cu[i], a.cu[i + 1], a.tokens).bad;
       }
       if (bad) atomicOr(a.err, kErrIndex);
       if (PAGED) {

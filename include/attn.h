@@ -422,7 +422,8 @@ ATTN_API int attn_packed_fwd(const attn_packed_shape* shape, const void* q, cons
  * page table[i * table_width + p / page_size], row p % page_size.
  * tokens: rows of q, o (k, v, slots in the store), all requests' new tokens
  * one behind the other and perhaps padding.  max_new: the most new tokens any
- * request has in this call (the host's bound; 1 for a token step).
+ * request has in this call (the host's bound; 1 for a token step; a request
+ * with more is left out and reported as a bad length is).
  */
 typedef struct attn_paged_shape {
   int32_t batch;
