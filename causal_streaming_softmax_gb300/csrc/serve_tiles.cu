@@ -86,9 +86,9 @@ static_assert(kColO + 64 * kNT <= kTmemCols, "tensor memory");
 
 enum {
   BAR_Q = 0,                             // [Q buffer] the item's Q tiles landed
-  BAR_Q_FREE = BAR_Q + 2,                // [Q buffer] every tile's products done
+  BAR_Q_FREE = BAR_Q + 2,                // [Q buffer] every row tile's products done
   BAR_KV_FULL = BAR_Q_FREE + 2,          // [stage]
-  BAR_KV_EMPTY = BAR_KV_FULL + kStages,  // [stage] every tile's products done
+  BAR_KV_EMPTY = BAR_KV_FULL + kStages,  // [stage] every row tile's products done
   BAR_S_FULL = BAR_KV_EMPTY + kStages,   // [t]
   BAR_S_FREE = BAR_S_FULL + kNT,         // [t] read by the softmax (128 threads)
   BAR_P_FULL = BAR_S_FREE + kNT,         // [t] P stored, O rescaled (128 threads)
@@ -106,7 +106,7 @@ static_assert(BAR_COUNT * 8 <= 512, "barrier area");
 // A work item as warp 15 describes it.  Keys count from the item's first key.
 struct Unit {
   int more;      // 0: no further item
-  int q0;        // token row of tile A's first row
+  int q0;        // token row of the first row tile's first row
   int q_end;     // token rows from here on are not the item's
   int kv;
   int kbeg;      // packed: row of key 0
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, bad = false, tail = false, checks = false;
       const int q_rows = a.tpt * a.G;
       long long pos = share.begin;
-      int block = blockIdx.x, taken = 0;  // packed: the window and head of this round
+      int block = blockIdx.x, taken = 0;  // packed: the window and head in hand
       for (;; ++nu) {
         const int ub = nu & 1;
         if (!PAGED && nu > 0) {

@@ -129,19 +129,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Whether the phase with the given parity has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Waits for the phase with the given parity to complete.  Returns false (and
 // records the failure) once the limit has passed or another thread of the
 // block has already given up; the caller must then stop its role.
@@ -188,24 +175,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, co
   const bool ok = mbar_wait(bar, parity, w);
   return __all_sync(0xffffffffu, ok);
 }
-
-// A bound on a warp's polling of several barriers: reset by progress, it says
-// when to give up.
-struct PollBound {
-  uint64_t t0;
-  uint32_t idle;
-  __device__ __forceinline__ void reset() { idle = 0; }
-  __device__ __forceinline__ bool give_up(const WaitCtl& w) {
-    if ((++idle & 31u) != 0) return false;
-    const uint64_t now = global_timer_ns();
-    if (idle == 32u) t0 = now;
-    const bool late = now - t0 > w.limit_ns;
-    if (!__any_sync(0xffffffffu, late || *w.abort != 0)) return false;
-    *w.abort = 1;
-    if (late && w.err) atomicOr(w.err, kErrWaitTimeout);
-    return true;
-  }
-};
 
 // mbar_wait_warp without a call: for code that holds more registers than a
 // call preserves (a call there moves them through local memory).
