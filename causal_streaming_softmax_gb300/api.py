@@ -618,6 +618,20 @@ def _dense(t, name, dtype, shape, dev):
     _refuse(t, name, dtype, shape, dev, "contiguous")
 
 
+def _step_rows(t, name, dtype, shape, dev, written=False):
+    """What the entry points ask of rows [tokens][heads][64], asked ahead of the
+    first launch: the tensor's type, size and device, strides and alignment,
+    and, where they are written, rows apart from one another."""
+    p, (t0, t1, _) = _strided(t, name, dtype, shape, dev)
+    n, h, _ = shape
+    if p % 16 or any(d > 1 and not (64 <= x < 1 << 38 and x % 8 == 0)
+                     for d, x in ((n, t0), (h, t1))):
+        raise ValueError("%s must start on 16 bytes, its strides multiples of 8 and at least 64"
+                         % name)
+    if written and n > 1 and h > 1 and t0 < (h - 1) * t1 + 64 and t1 < (n - 1) * t0 + 64:
+        raise ValueError("rows of %s overlap" % name)
+
+
 def _device_of(t, name) -> int:
     """The tensor's device, on which all others have to be (_run refuses -1,
     host memory)."""
@@ -799,13 +813,16 @@ class PagedCache:
         n = q.shape[0]
         s = self.shape(n, max_new or max(n, 1))
         # everything is looked at before the plan moves the cache on
-        dev, dt, rows = _device_of(q, "q"), self.dtype, (n, self.heads, 64)
-        _strided(q, "q", dt, rows, dev)
-        _strided(k, "k", dt, (n, self.kv_heads, 64), dev)
-        _strided(v, "v", dt, (n, self.kv_heads, 64), dev)
-        _strided(o, "o", dt, rows, dev)
-        if lse is not None:
-            _dense(lse, "lse", torch.float32, (self.heads, n), dev)
+        if not 1 <= s.max_new <= 1 << 30:
+            raise ValueError("max_new must be from 1 to 2^30")
+        dev, dt, rows = self.k.get_device(), self.dtype, (n, self.heads, 64)
+        new = (n, self.kv_heads, 64)
+        _step_rows(q, "q", dt, rows, dev)
+        _step_rows(k, "k", dt, new, dev)
+        _step_rows(v, "v", dt, new, dev)
+        _step_rows(o, "o", dt, rows, dev, written=True)
+        if lse is not None and _dense(lse, "lse", torch.float32, (self.heads, n), dev) % 16:
+            raise ValueError("lse must start on 16 bytes")
         slots = torch.empty(n, dtype=torch.int32, device=self.k.device)
         attn_paged_plan(s, self.lens, fresh, self.ring, self.state, self.table, self.cu,
                         self._lens, slots, self._state)

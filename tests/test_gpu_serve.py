@@ -714,6 +714,32 @@ def test_step_refuses_before_it_plans(torch):
     assert cache.lens.tolist() == [10]
 
 
+def test_step_refuses_layouts_before_it_plans(torch):
+    """Strides, alignment, rows that overlap and max_new, which the entry points
+    behind the plan refuse too, leave the cache as it was."""
+    from causal_streaming_softmax_gb300 import api
+    q, k, v = packed_inputs(torch, 10, 4, 2, torch.float16, 17)
+    cache = api.PagedCache(1, 4, 2, num_pages=5)
+    o = torch.empty((10, 4, 64), dtype=torch.float16, device="cuda")
+    room = torch.empty(10 * 4 * 72 + 8, dtype=torch.float16, device="cuda")
+    floats = torch.empty(41, device="cuda")
+    for bad in (dict(k=k[:, :1].expand(10, 2, 64)),               # a stride of 0
+                dict(v=room.as_strided((10, 2, 64), (132, 66, 1))),  # not a multiple of 8
+                dict(q=room.as_strided((10, 4, 64), (256, 64, 1), 4)),  # starts on 8 bytes
+                dict(o=room.as_strided((10, 4, 64), (256, 64, 1), 1)),
+                dict(o=room.as_strided((10, 4, 64), (64, 72, 1))),   # rows overlap
+                dict(lse=floats[1:].view(4, 10)),
+                dict(max_new=-1), dict(max_new=(1 << 30) + 1)):
+        args = dict(dict(q=q, k=k, v=v, o=o), **bad)
+        with pytest.raises(ValueError):
+            cache.step(i32(torch, [10]), **args)
+        assert cache.lens.tolist() == [0] and cache.free_pages() == 5
+    lse = torch.empty((4, 10), device="cuda")
+    cache.step(i32(torch, [10]), q, k, v, o, lse)
+    assert cache.lens.tolist() == [10]
+    check_packed(torch, q, k, v, [0, 10], True, o, lse)
+
+
 FIRST_CALL = """
 import torch
 from causal_streaming_softmax_gb300 import api

@@ -385,3 +385,24 @@ def test_host_form_of_the_plan():
         assert sorted(held + free) == list(range(N))
         live = [s for s in slots if s >= 0]
         assert len(set(live)) == len(live) == cu[-1]
+
+
+def test_step_rows_are_checked_ahead():
+    """A cache step looks at strides, alignment and overlap before its first launch."""
+    f16 = torch.float16
+    room = torch.empty(10 * 4 * 72 + 8, dtype=f16)
+
+    def look(shape, strides, at=0, written=False):
+        api._step_rows(room.as_strided(shape, strides, at), "x", f16, shape, -1, written)
+
+    look((10, 4, 64), (256, 64, 1))
+    look((10, 4, 64), (64, 640, 1), written=True)          # head-major
+    look((10, 4, 64), (64, 72, 1))                         # rows that overlap may be read
+    look((1, 1, 64), (3, 5, 1), written=True)              # strides of ones are not read
+    look((10, 1, 64), (64, 0, 1), 8, written=True)
+    look((0, 4, 64), (256, 64, 1), written=True)
+    for bad in (((10, 4, 64), (0, 64, 1)), ((10, 4, 64), (256, 0, 1)), ((10, 4, 64), (256, 66, 1)),
+                ((10, 4, 64), (256, 56, 1)), ((10, 4, 64), (256, 64, 1), 4),
+                ((10, 4, 64), (64, 72, 1), 0, True)):
+        with pytest.raises(ValueError):
+            look(*bad)
