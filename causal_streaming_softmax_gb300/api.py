@@ -787,10 +787,14 @@ class PagedCache:
         self.table = torch.full((batch, self.table_width), -1, **i32)
         self.ring = torch.arange(num_pages, **i32)
         self.cu = torch.zeros(batch + 1, **i32)
-        # lengths and ring state, each read by a step and written for the next
-        self.lens, self._lens = torch.zeros(batch, **i32), torch.zeros(batch, **i32)
-        self.state = torch.tensor([0, num_pages, 0, 0], **i32)
-        self._state = torch.zeros(4, **i32)
+        # lengths and ring state, one behind the other: what a step starts from,
+        # and what its plan writes beside it.  The second is copied over the first
+        # on the device, so that every step, eager or replayed, starts from the
+        # same place whatever ran before it.
+        self._now = torch.tensor([0] * batch + [0, num_pages, 0, 0], **i32)
+        self._new = torch.zeros_like(self._now)
+        self.lens, self.state = self._now[:batch], self._now[batch:]
+        self._lens, self._state = self._new[:batch], self._new[batch:]
         # as large as any step needs: a captured step keeps reading it
         self.ws = alloc_paged_workspace(self.shape(1, 1 << 30), dev)
 
@@ -804,9 +808,8 @@ class PagedCache:
         (negative: finished, its pages go back), whose rows stand in q, k, v
         one behind the other; plans, stores K and V and writes o (and lse).
         ``max_new``: the most new tokens of a request (default: all of them).
-        Steps are ordered by their streams alone.  The lengths and the ring
-        state swap between two buffers from step to step, so a graph that is
-        replayed holds an even number of steps."""
+        Steps are ordered by their streams alone.  A graph may hold any number
+        of steps, and be replayed between eager ones."""
         if stream is not None:  # the step's own buffers belong to its stream
             with torch.cuda.stream(stream):
                 return self.step(fresh, q, k, v, o, lse, max_new)
@@ -826,8 +829,7 @@ class PagedCache:
         slots = torch.empty(n, dtype=torch.int32, device=self.k.device)
         attn_paged_plan(s, self.lens, fresh, self.ring, self.state, self.table, self.cu,
                         self._lens, slots, self._state)
-        self.lens, self._lens = self._lens, self.lens
-        self.state, self._state = self._state, self.state
+        self._now.copy_(self._new)
         if n:
             attn_paged_store(s, k, v, slots, self.k, self.v)
             attn_paged_fwd(s, q, self.k, self.v, self.table, self.cu, self.lens, self.ws, o, lse)

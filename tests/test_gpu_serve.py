@@ -874,3 +874,54 @@ def test_python_names_what_is_wrong(torch):
                            torch.empty((4, Hkv, 16, 64), dtype=torch.float16, device="cuda"),
                            i32(torch, [[0, 1, 2, 3]]), cu, i32(torch, [n]),
                            torch.empty(1 << 10, dtype=torch.uint8, device="cuda"), o)
+
+
+def step_rows(torch, n, seed, H=8, Hkv=2):
+    return [x.clone() for x in packed_inputs(torch, n, H, Hkv, torch.float16, seed)]
+
+
+@pytest.mark.parametrize("captured", [1, 2, 3])
+@pytest.mark.parametrize("between", [0, 1, 2, 3])
+def test_captured_steps_between_eager_ones(torch, captured, between):
+    """A graph of any number of steps replays after any number of eager steps:
+    each step goes on from the lengths and pages that the one before it left."""
+    from causal_streaming_softmax_gb300 import api
+    cache = api.PagedCache(2, 8, 2, num_pages=60)
+    hist = [[], []]
+
+    def note(fresh, k, v):
+        at = 0
+        for i, f in enumerate(fresh):
+            hist[i] += [(k[at + x], v[at + x]) for x in range(f)]
+            at += f
+
+    def eager(fresh, seed):
+        n = sum(fresh)
+        q, k, v = step_rows(torch, n, seed)
+        cache.step(i32(torch, fresh), q, k, v, torch.empty_like(q), max_new=max(fresh))
+        note(fresh, k, v)
+
+    eager([37, 5], 1)
+    one = i32(torch, [1, 1])
+    rows = [step_rows(torch, 2, 10 + i) for i in range(captured)]
+    outs = [torch.empty_like(r[0]) for r in rows]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for (q, k, v), o in zip(rows, outs):
+            cache.step(one, q, k, v, o, max_new=1)
+    for rep in range(3):
+        g.replay()
+        for (q, k, v), o in zip(rows, outs):
+            note([1, 1], k, v)
+        assert cache.lens.tolist() == [len(h) for h in hist], "replay %d" % rep
+        for i in range(2):
+            kk, vv = (torch.stack([h[j] for h in hist[i]]) for j in (0, 1))
+            seen = torch.tensor([len(hist[i])], device="cuda")
+            eo, _, to, _ = attend64(rows[-1][0][i:i + 1], kk, vv, seen)
+            check(outs[-1][i:i + 1], eo, to, "replay %d request %d" % (rep, i))
+        for x in range(between):
+            eager([19, 1], 100 * rep + x)
+        assert cache.lens.tolist() == [len(h) for h in hist]
+        assert cache.status() == 0
+        assert cache.free_pages() == 60 - sum(-(-len(h) // 16) for h in hist)
