@@ -795,6 +795,8 @@ class PagedCache:
         self._new = torch.zeros_like(self._now)
         self.lens, self.state = self._now[:batch], self._now[batch:]
         self._lens, self._state = self._new[:batch], self._new[batch:]
+        # the last step's stream (id, device index, device type)
+        self._stream = torch._C._cuda_getCurrentStream(self.k.get_device())
         # as large as any step needs: a captured step keeps reading it
         self.ws = alloc_paged_workspace(self.shape(1, 1 << 30), dev)
 
@@ -827,6 +829,8 @@ class PagedCache:
         if lse is not None and _dense(lse, "lse", torch.float32, (self.heads, n), dev) % 16:
             raise ValueError("lse must start on 16 bytes")
         slots = torch.empty(n, dtype=torch.int32, device=self.k.device)
+        if not torch.cuda.is_current_stream_capturing():  # a graph runs where it is replayed
+            self._stream = torch._C._cuda_getCurrentStream(dev)
         attn_paged_plan(s, self.lens, fresh, self.ring, self.state, self.table, self.cu,
                         self._lens, slots, self._state)
         self._now.copy_(self._new)
@@ -834,11 +838,19 @@ class PagedCache:
             attn_paged_store(s, k, v, slots, self.k, self.v)
             attn_paged_fwd(s, q, self.k, self.v, self.table, self.cu, self.lens, self.ws, o, lse)
 
+    def _read(self, i: int) -> int:
+        sid, index, kind = self._stream
+        torch.cuda.current_stream(index).wait_stream(
+            torch.cuda.Stream(stream_id=sid, device_index=index, device_type=kind))
+        return int(self.state[i])
+
     def status(self) -> int:
         """The last step's status (0, or a sum of PLAN_ bits: the step handed
-        out nothing, stored nothing and left o as it was).  Synchronises."""
-        return int(self.state[3])
+        out nothing, stored nothing and left o as it was).  Waits for that step,
+        whichever stream it was given, and for the current stream, on which or
+        behind which a replayed graph has to be."""
+        return self._read(3)
 
     def free_pages(self) -> int:
-        """Pages that are free after the last step.  Synchronises."""
-        return int(self.state[1])
+        """Pages that are free after the last step.  Waits as status() does."""
+        return self._read(1)

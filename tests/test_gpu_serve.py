@@ -925,3 +925,22 @@ def test_captured_steps_between_eager_ones(torch, captured, between):
         assert cache.lens.tolist() == [len(h) for h in hist]
         assert cache.status() == 0
         assert cache.free_pages() == 60 - sum(-(-len(h) // 16) for h in hist)
+
+
+def test_status_follows_a_step_on_another_stream(torch):
+    """status() and free_pages() wait for the last step, whichever stream it is on."""
+    from causal_streaming_softmax_gb300 import api
+    q, k, v = packed_inputs(torch, 50, 8, 2, torch.float16, 23)
+    o, fresh, gone = torch.empty_like(q), i32(torch, [50]), i32(torch, [500])
+    cache = api.PagedCache(1, 8, 2, num_pages=20)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # a tenth of a second
+    cache.step(fresh, q, k, v, o, stream=side)
+    assert cache.free_pages() == 20 - 4
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    cache.step(gone, q, k, v, o, stream=side)
+    assert cache.status() == api.PLAN_PAGES | api.PLAN_WIDTH | api.PLAN_TOKENS
+    assert cache.lens.tolist() == [50]
