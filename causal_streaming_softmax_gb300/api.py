@@ -809,7 +809,10 @@ class PagedCache:
         """One step of every request: ``fresh`` int32 [batch] new tokens each
         (negative: finished, its pages go back), whose rows stand in q, k, v
         one behind the other; plans, stores K and V and writes o (and lse).
-        ``max_new``: the most new tokens of a request (default: all of them).
+        ``max_new``: the most new tokens of a request (default: all of them,
+        which a step of single tokens pays for: give it 1 there).  A request with
+        more is stored and counted but its rows of o and lse stay as they were;
+        last_device_error() tells, status() does not.
         Steps are ordered by their streams alone.  A graph may hold any number
         of steps, and be replayed between eager ones."""
         if stream is not None:  # the step's own buffers belong to its stream

@@ -90,7 +90,7 @@ __device__ __forceinline__ Request request_at(const DecodeArgs& a, int i, bool* 
   bool b;
   Request q{r.begin, r.end - r.begin, key_count(a.lens[i], a.width, a.shift, &b)};
   *bad = r.bad || b || q.n_new > a.max_new;
-  if (q.n_new > a.ntok) q.n_new = 0;
+  if (q.n_new > min(a.ntok, a.max_new)) q.n_new = 0;
   return q;
 }
 

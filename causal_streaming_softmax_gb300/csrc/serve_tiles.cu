@@ -149,7 +149,7 @@ __device__ __forceinline__ PagedReq paged_req(const TileArgs& a, int i, bool* ba
   bool b;
   PagedReq q{r.begin, r.end - r.begin, key_count(a.lens[i], a.width, a.shift, &b)};
   *bad = r.bad || b || q.n_new > a.max_new;
-  if (q.n_new <= a.skip) q.n_new = 0;
+  if (q.n_new <= a.skip || q.n_new > a.max_new) q.n_new = 0;
   return q;
 }
 

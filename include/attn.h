@@ -423,7 +423,8 @@ ATTN_API int attn_packed_fwd(const attn_packed_shape* shape, const void* q, cons
  * tokens: rows of q, o (k, v, slots in the store), all requests' new tokens
  * one behind the other and perhaps padding.  max_new: the most new tokens any
  * request has in this call (the host's bound; 1 for a token step; a request
- * with more is left out and reported as a bad length is).
+ * with more is left out, its rows of o and lse as they were, and reported as a
+ * bad length is).
  */
 typedef struct attn_paged_shape {
   int32_t batch;

@@ -944,3 +944,23 @@ def test_status_follows_a_step_on_another_stream(torch):
     cache.step(gone, q, k, v, o, stream=side)
     assert cache.status() == api.PLAN_PAGES | api.PLAN_WIDTH | api.PLAN_TOKENS
     assert cache.lens.tolist() == [50]
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (4, 4), (17, 1)])
+@pytest.mark.parametrize("bound", [1, 3, 4, 5, 16, 20, 39])
+def test_requests_with_more_new_tokens_than_the_bound_are_left_out(torch, heads, bound):
+    """Their rows stay as they were, also where their keys are split over
+    blocks; the other requests are right."""
+    from causal_streaming_softmax_gb300 import api
+    reqs = [(2000, 40), (500, bound), (64, 1), (9000, bound + 1), (33, bound)]
+    q, kc, vc, table, cu, lens, _ = paged_problem(torch, reqs, heads[0], heads[1], 16,
+                                                  torch.float16, 24)
+    o, L = run_paged(torch, q, kc, vc, table, cu, lens, max_new=bound)
+    assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX
+    tt = torch.tensor(table, dtype=torch.int64, device="cuda")
+    for i, (rows, eo, el, to, tl) in enumerate(paged64(q, kc, vc, tt, cu, lens)):
+        if reqs[i][1] > bound:
+            assert (o[rows] == SENTINEL).all() and (L[:, rows] == SENTINEL).all(), i
+        else:
+            check(o[rows], eo, to, "O of request %d" % i)
+            check(L[:, rows], el, tl, "L of request %d" % i)
