@@ -154,8 +154,9 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs a) 
   }
   for (int y = first; y < total.back; y += step) {
     const int i = last_at_or_below(s_back, a.batch, y);
-    a.ring[ring_at(head, (long long)free + y, a.pages)] =
-        a.table[(long long)i * a.width + (y - s_back[i])];
+    const int id = a.table[(long long)i * a.width + (y - s_back[i])];
+    bad |= !page_ok(id, a.pages);  // told now, not by whom it is handed to later
+    a.ring[ring_at(head, (long long)free + y, a.pages)] = id;
   }
   if (bad) atomicOr(a.err, kErrIndex);
 }

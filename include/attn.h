@@ -458,6 +458,11 @@ typedef struct attn_paged_shape {
  * for the pages handed out (in order of requests, then positions, from the
  * ring's head; other entries stay); the pages of finished requests behind the
  * ring's tail; and next = {head', free', pages handed out, status}.
+ * Every page is in one place: in the ring's free part or held by one request.
+ * The plan does not check that: requests that share pages (attn_paged_fwd reads
+ * them) are the caller's to plan and to finish.  A page id outside the pool that
+ * is handed out or taken back is reported (ATTN_ERR_DEVICE_INDEX); it stays
+ * where it is, in the table or behind the ring's tail.
  * status 0, or a sum of ATTN_PLAN_ bits, in which case nothing is handed out
  * or taken back: the table and the ring stay, every offset is 0, every slot
  * -1, lens = cached and next = {head, free, 0, status}.

@@ -964,3 +964,14 @@ def test_requests_with_more_new_tokens_than_the_bound_are_left_out(torch, heads,
         else:
             check(o[rows], eo, to, "O of request %d" % i)
             check(L[:, rows], el, tl, "L of request %d" % i)
+
+
+@pytest.mark.parametrize("bad", [-1, 9, 2 ** 31 - 1, -2 ** 31])
+def test_plan_reports_a_retired_page_that_does_not_exist(torch, bad):
+    """A finished request whose table row names no page of the pool."""
+    from causal_streaming_softmax_gb300 import api
+    got = run_plan(torch, [20, 3], [-1, 1], [6, 7, 8, -4, -4, -4, -4, -4, -4], [0, 3, 0, 0],
+                   [[0, bad, 2], [4, 0, 0]], 1, 8, 3)
+    assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX
+    assert got[0] == [0, 0, 1] and got[1] == [0, 4] and got[2] == [4 * 8 + 3]
+    assert got[5] == [0, 6, 0, 0]
