@@ -326,8 +326,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
       }
       ++nq;
       // keys that this thread's two rows see
-      const int first_lim = r.n_keys - r.n_new + 1;
-      const int lim0 = first_lim + g / a.G, lim1 = first_lim + (g + 8) / a.G;
+      const int first_lim = row_limit(r.n_keys, r.n_new, 0);
+      const int lim0 = row_limit(r.n_keys, r.n_new, g / a.G),
+                lim1 = row_limit(r.n_keys, r.n_new, (g + 8) / a.G);
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
       float o[8][4];
 #pragma unroll
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
           mma_16816<BF16>(sc[0], q[kk], kf[0], kf[1]);
           mma_16816<BF16>(sc[1], q[kk], kf[2], kf[3]);
         }
-        const bool edge = k0 + 16 > first_lim;  // some row does not see every key
+        const bool edge = past_limit(k0, 16, first_lim);  // some row does not see every key
         if (edge) {
 #pragma unroll
           for (int n = 0; n < 2; ++n)

@@ -55,6 +55,16 @@ CSS_HD int key_count(int32_t len, int32_t table_width, int32_t page_shift, bool*
   return len < 0 ? 0 : ((long long)len > cap ? (int)cap : len);
 }
 
+// Keys that the row of new token tok of n_new sees, the last token's is n_keys;
+// a row past the last token counts as the last.  May be negative.
+CSS_HD int row_limit(int n_keys, int n_new, int tok) {
+  const int behind = n_new - 1 - tok;
+  return n_keys - (behind > 0 ? behind : 0);
+}
+
+// Whether the keys [k0, k0 + n) pass lim, for k0 < 2^31 and lim > k0 - 2^30.
+CSS_HD bool past_limit(int k0, int n, int lim) { return lim - k0 < n; }
+
 // Pages that hold n tokens.
 CSS_HD long long pages_for(long long n, int page_shift) {
   return (n + ((1ll << page_shift) - 1)) >> page_shift;

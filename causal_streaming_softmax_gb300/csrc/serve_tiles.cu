@@ -215,7 +215,7 @@ __device__ __forceinline__ void paged_unit(const TileArgs& a, const Place& p, in
                                            Unit* u) {
   const int w = kNT * a.tpt, lane = threadIdx.x & 31, t = lane;
   const int q0 = p.r.q0 + p.blk * w, q_end = min(p.r.q0 + p.r.n_new, q0 + w);
-  const int lim = p.r.n_keys - p.r.n_new + 1 + p.blk * w;
+  const int lim = row_limit(p.r.n_keys, p.r.n_new, p.blk * w);
   const int first = q0 + t * a.tpt, past = min(q_end, first + a.tpt);
   const bool some = t < kNT && first < past;
   const int keys = some ? lim + (past - 1 - q0) : 0;  // the last row's
@@ -560,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int j = j0; j < j1; ++j) {
         const int k0 = j * kBN;
-        const bool edge = k0 < lo_max || k0 + kBN > hi_min;  // the same for the whole tile
+        const bool edge =
+            k0 < lo_max || past_limit(k0, kBN, hi_min);  // the same for the whole tile
         const int lo_l = lo - k0, hi_l = hi - k0;
         if (!mbar_wait_inline(BAR(BAR_S_FULL + t), ns & 1, wc)) {
           ok = false;
@@ -909,8 +910,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t v_lo =
                   sdesc_lo(sbase + kSmemStage0 + s * kStageBytes + kHalfBytes, 8192);
               // on a masked tile the rows' threads may have formed the product
-              const bool by_rows = (i * kBN < lo_max || (i + 1) * kBN > hi_min) &&
-                                   s_odd[t][np & 1] == np + 1;
+              const bool by_rows =
+                  (i * kBN < lo_max || past_limit(i * kBN, kBN, hi_min)) &&
+                  s_odd[t][np & 1] == np + 1;
               if (elect_one()) {
                 if (!by_rows) {
 #pragma unroll

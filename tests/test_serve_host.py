@@ -406,3 +406,49 @@ def test_step_rows_are_checked_ahead():
                 ((10, 4, 64), (64, 72, 1), 0, True)):
         with pytest.raises(ValueError):
             look(*bad)
+
+
+LIMITS = r"""
+#include <stdio.h>
+#include "serve_index.h"
+using namespace css;
+int main() {
+  int what;
+  while (scanf("%d", &what) == 1) {
+    if (what == 0) {
+      int k, n, tok; scanf("%d %d %d", &k, &n, &tok);
+      printf("%d\n", row_limit(k, n, tok));
+    } else {
+      int k0, n, lim; scanf("%d %d %d", &k0, &n, &lim);
+      printf("%d\n", (int)past_limit(k0, n, lim));
+    }
+  }
+  return 0;
+}
+"""
+
+
+def test_row_limits_at_the_longest_lengths(tmp_path):
+    """Which keys a row sees, and whether a run of keys passes that, without
+    leaving 32 bits at the most keys a table may hold (2^28 - 1 pages of 8)."""
+    (tmp_path / "h.cpp").write_text(LIMITS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined",
+                    "-fno-sanitize-recover=undefined", "-I", build.CSRC, "-o", str(tmp_path / "h"),
+                    str(tmp_path / "h.cpp")], check=True)
+    most = 8 * (2 ** 28 - 1)
+    lens = [0, 1, 2, 15, 16, 63, 64, 65, 1000, most - 70, most - 17, most - 16, most - 1, most]
+    asks, want = [], []
+    for k in lens:
+        for n in (1, 2, 16, 2 ** 30):
+            for tok in {0, 1, 15, min(n - 1, 383)}:  # rows past the last one too
+                asks.append("0 %d %d %d" % (k, n, tok))
+                want.append(min(k, k - n + 1 + tok))
+        for k0 in {0, 16, max(0, k - 1) // 16 * 16, max(0, k - 1) // 64 * 64, max(0, k - 1) // 64 * 64 + 48}:
+            if k0 < 2 ** 31:
+                for n in (16, 64):
+                    for lim in (k, k - 15, k - 383):
+                        asks.append("1 %d %d %d" % (k0, n, lim))
+                        want.append(int(k0 + n > lim))
+    r = subprocess.run([str(tmp_path / "h")], input="\n".join(asks), capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert [int(x) for x in r.stdout.split()] == want
