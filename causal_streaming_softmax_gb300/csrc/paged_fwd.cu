@@ -21,18 +21,24 @@ constexpr int kJoinRows = 16;                 // rows of a block
 // on timing.
 template <bool BF16>
 __global__ void __launch_bounds__(kJoinThreads)
-    join_kernel(const PartArgs p1, int n1, const PartArgs p2, int chunks, const RowsArg o,
-                float* lse, int tokens, int G) {
+    join_kernel(const PartArgs p1, int n1, const PartArgs p2, int n2, int chunks, const RowsArg o,
+                float* lse, int tokens, int Hkv, int G, uint32_t* err) {
   __shared__ float s_sum[kJoinSlots][8][9];
   griddep_launch_dependents();
   griddep_wait();
   const bool one = (int)blockIdx.x < n1;
   const PartArgs& p = one ? p1 : p2;
   const int at_2 = blockIdx.x - n1, c = one ? blockIdx.x : at_2 / chunks;
-  const PartDesc d = p.desc[c];
+  const PartDesc d = part_desc(p, c);
+  if (d.rows == 0) return;  // block c left no part to join
+  if (!part_ok(d.q0, d.kv, d.rows, d.last, c, one ? n1 : n2, p.rows, tokens, Hkv, G)) {
+    // two calls share a workspace: wrong rows, but no access outside the tensors
+    if (threadIdx.x == 0) atomicOr(err, kErrIndex);
+    return;
+  }
   const int row0 = one ? 0 : at_2 % chunks * kJoinRows, rows = min(d.rows - row0, kJoinRows);
-  if (rows <= 0) return;  // the whole block
-  int span = 1;           // rows rounded up to a power of two
+  if (rows <= 0) return;
+  int span = 1;  // rows rounded up to a power of two
   while (span < rows) span <<= 1;
   const int slot = threadIdx.x >> 3, lane = threadIdx.x & 7, c0 = lane * 8;
   const int at_row = slot & (span - 1), group = slot / span, groups = kJoinSlots / span;
@@ -79,8 +85,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   write_row<BF16>(o, lse, tokens, d.q0 + row / G, d.kv * G + row % G, c0, acc, m, l);
 }
 
-int launch_join(const PagedDims& d, const PartArgs& p1, int n1, const PartArgs& p2, int n2,
-                const RowsArg& o, float* lse, cudaStream_t stream) {
+int launch_join(const PagedDims& d, const DevCtx& ctx, const PartArgs& p1, int n1,
+                const PartArgs& p2, int n2, const RowsArg& o, float* lse, cudaStream_t stream) {
   static_assert(kDecodeRows <= kJoinRows && kItemRows % kJoinRows == 0, "rows of a block");
   // no item has more rows than the largest request, nor than its tiles hold
   const long long most = (long long)d.max_new * d.G;
@@ -88,7 +94,7 @@ int launch_join(const PagedDims& d, const PartArgs& p1, int n1, const PartArgs& 
   const int chunks = (rows + kJoinRows - 1) / kJoinRows;
   return cuda_status(launch_dependent(d.bf16 ? join_kernel<true> : join_kernel<false>,
                                       dim3(n1 + n2 * chunks), dim3(kJoinThreads), 0, stream, p1,
-                                      n1, p2, chunks, o, lse, d.tokens, d.G));
+                                      n1, p2, n2, chunks, o, lse, d.tokens, d.Hkv, d.G, ctx.err));
 }
 
 // The largest grid of the split kernels on any device this library runs on:
@@ -164,7 +170,7 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
     if (rc != ATTN_OK) return rc;
   }
   if (n_few + n_rows == 0) return ATTN_OK;
-  return launch_join(d, few, n_few, rows, n_rows, o, lse, stream);
+  return launch_join(d, ctx, few, n_few, rows, n_rows, o, lse, stream);
 }
 
 }  // namespace css

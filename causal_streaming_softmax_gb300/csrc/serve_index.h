@@ -197,6 +197,15 @@ CSS_HD long long tiles_before(int n_keys, int n_new, int w, int bn, int nb) {
   return s + sum;
 }
 
+// Whether the description of a part, as block c of `blocks` left it in the
+// workspace, names rows of the output and parts that exist (room: rows a part
+// has room for).  It does unless something else wrote the workspace meanwhile.
+CSS_HD bool part_ok(int q0, int kv, int rows, int last, int c, int blocks, int room, int tokens,
+                    int Hkv, int G) {
+  return q0 >= 0 && q0 <= tokens && kv >= 0 && kv < Hkv && rows >= 0 && rows <= room &&
+         rows <= (long long)(tokens - q0) * G && last >= c && last < blocks;
+}
+
 CSS_HD int tiles_of_block(int n_keys, int n_new, int w, int bn, int b) {
   const long long past = (b + 1ll) * w;
   const long long end = (long long)n_keys - n_new + (past < n_new ? past : n_new);

@@ -25,6 +25,22 @@ __device__ __forceinline__ long long part_row(const PartArgs& p, int block, bool
   return ((long long)block * 2 + (tail ? 1 : 0)) * p.rows + row;
 }
 
+// The description that block c left, read once a warp: what is checked is what
+// is used, and a warp's lanes agree on it whatever else writes there.
+__device__ __forceinline__ PartDesc part_desc(const PartArgs& p, int c) {
+  static_assert(sizeof(PartDesc) == 16, "one load");
+  PartDesc d;
+  asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(d.q0), "=r"(d.kv), "=r"(d.rows), "=r"(d.last)
+               : "l"(p.desc + c)
+               : "memory");
+  d.q0 = __shfl_sync(0xffffffffu, d.q0, 0);
+  d.kv = __shfl_sync(0xffffffffu, d.kv, 0);
+  d.rows = __shfl_sync(0xffffffffu, d.rows, 0);
+  d.last = __shfl_sync(0xffffffffu, d.last, 0);
+  return d;
+}
+
 // Eight columns of a row's part; the thread of column 0 writes m and l.
 __device__ __forceinline__ void store_part(const PartArgs& p, int block, bool tail, int row,
                                            int c0, const float (&acc)[8], float m, float l) {

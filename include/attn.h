@@ -499,7 +499,9 @@ ATTN_API int attn_paged_store(const attn_paged_shape* shape, const void* k, cons
  * Bytes of the workspace of attn_paged_fwd (0 if the shape is invalid).  It
  * holds the parts of rows whose keys were split over several blocks; its
  * contents need not be initialised and mean nothing after the call.  Calls
- * that overlap on the GPU need workspaces of their own.
+ * that overlap on the GPU need workspaces of their own; where two share one, or
+ * anything else writes it meanwhile, their outputs are undefined (and reported
+ * as ATTN_ERR_DEVICE_INDEX where the kernels can tell).
  */
 ATTN_API size_t attn_paged_workspace_bytes(const attn_paged_shape* shape);
 

@@ -975,3 +975,34 @@ def test_plan_reports_a_retired_page_that_does_not_exist(torch, bad):
     assert api.last_device_error() == api.ATTN_ERR_DEVICE_INDEX
     assert got[0] == [0, 0, 1] and got[1] == [0, 4] and got[2] == [4 * 8 + 3]
     assert got[5] == [0, 6, 0, 0]
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_workspace_that_something_else_writes(torch, new):
+    """While another stream writes the workspace the outputs mean nothing, but
+    nothing outside the rows is written and the next call is right."""
+    from causal_streaming_softmax_gb300 import api
+    q, kc, vc, table, cu, lens, _ = paged_problem(torch, [(3000, new), (4000, new)] * 4, 8, 2, 16,
+                                                  torch.float16, 27)
+    t = q.shape[0]
+    s = api.PagedShape(8, t, 8, 2, 16, kc.shape[0], len(table[0]), max_new=new)
+    ws = api.alloc_paged_workspace(s)
+    room = torch.full((t + 64, 8, 64), SENTINEL, dtype=q.dtype, device="cuda")
+    floats = torch.full((8 * t + 64,), SENTINEL, device="cuda")
+    o, L = room[32:32 + t], floats[32:32 + 8 * t].view(8, t)
+    args = (s, q, kc, vc, i32(torch, table), i32(torch, cu), i32(torch, lens), ws, o, L)
+    junk = torch.randint(-2 ** 31, 2 ** 31 - 1, (ws.numel() // 4,), device="cuda", dtype=torch.int32,
+                         generator=torch.Generator(device="cuda").manual_seed(1))
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(60):
+        with torch.cuda.stream(other):
+            for j in range(4):
+                ws.view(torch.int32).copy_(junk if (i + j) % 2 else junk & 15)
+        api.attn_paged_fwd(*args)
+    torch.cuda.synchronize()
+    assert api.last_device_error() in (0, api.ATTN_ERR_DEVICE_INDEX)
+    for x in (room[:32], room[32 + t:], floats[:32], floats[32 + 8 * t:]):
+        assert (x == SENTINEL).all()
+    api.attn_paged_fwd(*args)
+    check_paged(torch, q, kc, vc, table, cu, lens, o, L)

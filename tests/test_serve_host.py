@@ -452,3 +452,46 @@ def test_row_limits_at_the_longest_lengths(tmp_path):
     r = subprocess.run([str(tmp_path / "h")], input="\n".join(asks), capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     assert [int(x) for x in r.stdout.split()] == want
+
+
+PARTS = r"""
+#include <stdio.h>
+#include "serve_index.h"
+using namespace css;
+int main() {
+  int a[10];
+  for (;;) {
+    for (int i = 0; i < 10; ++i)
+      if (scanf("%d", &a[i]) != 1) return 0;
+    printf("%d\n", (int)part_ok(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9]));
+  }
+}
+"""
+
+
+def test_descriptions_of_parts_are_checked(tmp_path):
+    """Whatever a workspace holds, a part that passes names rows of the output
+    and parts of the workspace."""
+    (tmp_path / "h.cpp").write_text(PARTS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined",
+                    "-fno-sanitize-recover=undefined", "-I", build.CSRC, "-o", str(tmp_path / "h"),
+                    str(tmp_path / "h.cpp")], check=True)
+    r = random.Random(7)
+    asks, want = [], []
+    for _ in range(4000):
+        blocks, room, hkv, g = r.choice([1, 152, 304]), r.choice([16, 384]), r.randint(1, 9), \
+            r.choice([1, 3, 4, 17, 128])
+        c, tokens = r.randrange(blocks), r.choice([1, 5, 100, 2 ** 30])
+        near = lambda *x: r.choice(EXTREMES + [y + z for y in x for z in (-1, 0, 1)])
+        q0, kv, rows, last = near(0, tokens), near(0, hkv), near(0, room, g), near(c, blocks)
+        if r.random() < 0.5:
+            kv, last = r.randrange(hkv), r.randrange(c, blocks)
+        asks.append((q0, kv, rows, last, c, blocks, room, tokens, hkv, g))
+        ok = 0 <= kv < hkv and 0 <= rows <= room and c <= last < blocks and q0 >= 0
+        ok = ok and all(q0 + x // g < tokens for x in range(rows)) and q0 <= tokens
+        want.append(int(ok))
+    got = subprocess.run([str(tmp_path / "h")], input="\n".join(
+        " ".join(map(str, a)) for a in asks), capture_output=True, text=True)
+    assert got.returncode == 0, got.stderr
+    assert [int(x) for x in got.stdout.split()] == want
+    assert 100 < sum(want) < 3900
