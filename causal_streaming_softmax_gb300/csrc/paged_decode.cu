@@ -30,8 +30,6 @@
 // chain of loads lengths -> page ids -> pages -> parts.
 #include <math.h>
 
-#include <mutex>
-
 #include "serve_index.h"
 #include "serve_internal.h"
 #include "serve_parts.cuh"
@@ -105,6 +103,14 @@ struct Place {
   int req, kv, t0, nt;
 };
 
+// What the producer hands the consumers beside an item's Q: they read no device
+// array themselves, so that the warps agree on an item whatever those hold.
+struct Item {
+  Request r;
+  int kv, t0, t1;
+  int whole;  // its rows are finished here; else a part
+};
+
 // The place at position pos.  pre[i] counts the tiles (whole: the items) of one
 // head of the requests before i.
 template <class C>
@@ -124,20 +130,22 @@ __device__ __forceinline__ Place place_at(const DecodeArgs& a, const long long* 
   bool b;
   p.r = request_at(a, p.req, &b);
   p.nt = tiles_of<C>(p.r.n_keys);
-  p.kv = C::kWhole ? (int)off : (int)quot(off, p.nt);
-  p.t0 = C::kWhole ? 0 : (int)(off - (long long)p.kv * p.nt);
+  const long long kv = C::kWhole ? off : quot(off, p.nt);
+  p.t0 = C::kWhole ? 0 : (int)(off - kv * p.nt);
+  p.kv = (int)min(kv, a.Hkv - 1ll);  // less already, unless lens changed meanwhile
   return p;
 }
 
 // The place behind an item: the next head or the next request with rows.
-// Called only where the list goes on.
+// Called only where the list goes on; never past the last request, also where
+// lens changed meanwhile.
 template <class C>
 __device__ __forceinline__ void next_place(const DecodeArgs& a, const long long* pre, Place* p) {
   p->t0 = 0;
   if (++p->kv < a.Hkv) return;
   p->kv = 0;
   do {
-    ++p->req;
+    p->req = min(p->req + 1, a.batch - 1);
   } while (pre[p->req + 1] == pre[p->req] && p->req + 1 < a.batch);
   bool b;
   p->r = request_at(a, p->req, &b);
@@ -156,6 +164,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
                 BAR_Q_FREE = C::kQFree;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int s_abort;
+  __shared__ Item s_item[2];  // [Q buffer]
   __shared__ long long s_scan[kThreads / 32];
   griddep_launch_dependents();
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
     const int boxes = kTileKeys / box;                    // copies a tile of K (and of V)
     const int per_tile = (1 << a.shift) >= kTileKeys ? 0 : boxes;
     int it = 0, nq = 0;
-    bool ok = true, bad = false;
+    bool ok = true, bad = false, tail = false;
     // page ids go 32 at a time: lane l of group g has page first + 32 g + l.
     // The first two groups of the next item are read while this one runs.
     Place nx{};
@@ -245,6 +254,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
       const int n_pages = (int)pages_for(r.n_keys, a.shift);
       int base = (int)(((long long)sg.t0 * kTileKeys) >> a.shift);
       int ids = nx_ids, next = nx_next;
+      const long long last = pos - sg.t0 + sg.nt - 1;  // the item's last position
       pos += C::kWhole ? 1 : t1 - sg.t0;
       if (pos < share.end) {
         next_place<C>(a, s_pre, &nx);
@@ -254,6 +264,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
       ok = !(nq >= 2) || mbar_wait_warp(BAR(BAR_Q_FREE + qbuf), ((nq >> 1) - 1) & 1, wc);
       if (!ok) break;
       if (lane == 0) {
+        s_item[qbuf] = Item{r, sg.kv, sg.t0, t1, C::kWhole || (sg.t0 == 0 && t1 == sg.nt)};
         mbar_arrive_expect_tx(BAR(BAR_Q + qbuf), a.ntok * a.G * 128);
         tma_load_4d(sbase + kSmemQ + qbuf * kQ, &tm_q, BAR(BAR_Q + qbuf), 0, 0, sg.kv, r.q0);
       }
@@ -290,7 +301,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
           }
         }
       }
+      if (!C::kWhole && sg.t0 == 0 && t1 < sg.nt) {
+        tail = true;
+        if (lane == 0)
+          a.part.desc[blockIdx.x] = PartDesc{r.q0, sg.kv, r.n_new * a.G, last_block(share, last)};
+      }
     }
+    if (!C::kWhole && lane == 0 && !tail) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
     if (bad) atomicOr(a.err, kErrIndex);
     // no copy may still be landing when the block exits (matters only when a
     // wait gave up)
@@ -304,18 +321,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
     const int g = lane >> 2, tq = lane & 3;
     const int mi = lane >> 3, mr = lane & 7;
     int it = 0, nq = 0;
-    bool ok = true, tail = false;
-    Place sg{};
-    if (share.begin < share.end) sg = place_at<C>(a, s_pre, share.begin);
     for (long long pos = share.begin; pos < share.end;) {
-      const Request r = sg.r;
-      const int t1 = C::kWhole ? sg.nt : (int)min((long long)sg.nt, sg.t0 + (share.end - pos));
-      pos += C::kWhole ? 1 : t1 - sg.t0;
-      const int rows = r.n_new * a.G;
       const int qbuf = nq & 1;
       uint32_t q[4][4];
-      ok = ok && mbar_wait_warp(BAR(BAR_Q + qbuf), (nq >> 1) & 1, wc);
+      Item sg{};
+      bool ok = mbar_wait_warp(BAR(BAR_Q + qbuf), (nq >> 1) & 1, wc);
       if (ok) {
+        sg = s_item[qbuf];
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           ldmatrix_x4(sbase + kSmemQ + qbuf * kQ +
@@ -325,6 +337,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
         if (lane == 0) mbar_arrive(BAR(BAR_Q_FREE + qbuf));
       }
       ++nq;
+      const Request r = sg.r;
+      const int t1 = sg.t1, rows = r.n_new * a.G;
+      pos += C::kWhole ? 1 : t1 - sg.t0;
       // keys that this thread's two rows see
       const int first_lim = row_limit(r.n_keys, r.n_new, 0);
       const int lim0 = row_limit(r.n_keys, r.n_new, g / a.G),
@@ -336,8 +351,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
 
       for (int t = sg.t0; t < t1; ++t, ++it) {
         const int s = it % kStages;
-        ok = ok && mbar_wait_warp(BAR(BAR_FULL + s), (it / kStages) & 1, wc);
-        if (!ok) continue;
+        ok = mbar_wait_warp(BAR(BAR_FULL + s), (it / kStages) & 1, wc);
+        if (!ok) break;
         const uint32_t ks = sbase + s * kStage + warp * 16 * 128, vs = ks + kHalf;
         const int k0 = t * kTileKeys + warp * 16;
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -435,7 +450,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
         if (lane == 0) mbar_arrive(BAR(BAR_EMPTY + s));
       }
 
-      // ---------------- the four warps meet ----------------
+      // ---------------- the consumer warps meet ----------------
       l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
       l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -450,9 +465,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
         *reinterpret_cast<float2*>(d) = make_float2(o[i][0], o[i][1]);
         *reinterpret_cast<float2*>(d + 8 * kLd) = make_float2(o[i][2], o[i][3]);
       }
-      named_barrier_sync(1, kConsumers * 32);
+      // where a wait gave up, all leave together
+      if (named_barrier_any(1, kConsumers * 32, !ok)) break;
       const int row = tid >> 3, c0 = (tid & 7) * 8;
-      if (ok && row < rows) {  // the first 128 threads have a row
+      if (row < rows) {  // the first 128 threads have a row
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, s_ml[w * kDecodeRows + row].x);
@@ -469,21 +485,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
           for (int e = 0; e < 8; ++e) acc[e] = fmaf(d[e], f, acc[e]);
         }
         const int tok = r.q0 + row / a.G, h = sg.kv * a.G + row % a.G;
-        if (C::kWhole || (sg.t0 == 0 && t1 == sg.nt))
+        if (sg.whole)
           write_row<BF16>(a.o, a.lse, a.tokens, tok, h, c0, acc, m, l);
         else
           store_part(a.part, blockIdx.x, sg.t0 == 0, row, c0, acc, m, l);
       }
-      if (!C::kWhole && sg.t0 == 0 && t1 < sg.nt) {
-        tail = true;
-        if (tid == 0)
-          a.part.desc[blockIdx.x] =
-              PartDesc{r.q0, sg.kv, rows, last_block(share, pos - t1 + sg.nt - 1)};
-      }
-      if (pos < share.end) next_place<C>(a, s_pre, &sg);
       named_barrier_sync(1, kConsumers * 32);
     }
-    if (!C::kWhole && tid == 0 && !tail) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
   }
 #undef BAR
 }

@@ -196,7 +196,8 @@ __device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pr
 }
 
 // The place behind a block: the next block, head or request with rows.  Called
-// only where the list goes on.
+// only where the list goes on; never past the last request, also where lens
+// changed meanwhile.
 __device__ __forceinline__ void next_block(const TileArgs& a, Place* p) {
   p->t0 = 0;
   if (++p->blk * kNT * a.tpt < p->r.n_new) return;
@@ -205,7 +206,8 @@ __device__ __forceinline__ void next_block(const TileArgs& a, Place* p) {
   p->kv = 0;
   do {
     bool b;
-    p->r = paged_req(a, ++p->req, &b);
+    p->req = min(p->req + 1, a.batch - 1);
+    p->r = paged_req(a, p->req, &b);
   } while (p->r.n_new == 0 && p->req + 1 < a.batch);
 }
 
@@ -742,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) u.more = 0;
         } else if (PAGED) {
           nt = tiles_of_block(place.r.n_keys, place.r.n_new, kNT * a.tpt, kBN, place.blk);
+          place.t0 = min(place.t0, nt - 1);  // it is less, unless lens changed meanwhile
           steps = (int)min((long long)(nt - place.t0), share.end - pos);
           paged_unit(a, place, place.t0 + steps, nt, &u);
         } else {

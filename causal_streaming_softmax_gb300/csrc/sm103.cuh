@@ -73,6 +73,20 @@ __device__ __forceinline__ void named_barrier_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The same, and whether any of its threads came with v set: one answer for all.
+__device__ __forceinline__ bool named_barrier_any(int id, int nthreads, bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(nthreads), "r"((uint32_t)v)
+      : "memory");
+  return any != 0;
+}
+
 // Programmatic dependent launch.  A kernel launched with programmatic stream
 // serialization may start while the kernel before it in the stream is still
 // running; griddep_wait blocks the calling thread until that kernel has

@@ -375,7 +375,9 @@ ATTN_API int attn_bwd_noalloc(const attn_shape* shape, const uint16_t* q,
  * read there.  A value outside its range never leads to an access outside the
  * tensors: the kernel leaves the row or key out and sets the device error
  * word (attn_last_device_error then returns ATTN_ERR_DEVICE_INDEX); the
- * outputs of that sequence are then undefined.
+ * outputs of that sequence are then undefined.  The arrays do not change while
+ * a call reads them: where something writes them meanwhile the call's outputs
+ * are undefined, but it ends and stays inside the tensors all the same.
  *
  * An output row depends on the keys that its row sees and on nothing else:
  * infinities and NaN in masked keys, in pages past a length or in other

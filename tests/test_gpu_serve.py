@@ -1006,3 +1006,45 @@ def test_a_workspace_that_something_else_writes(torch, new):
         assert (x == SENTINEL).all()
     api.attn_paged_fwd(*args)
     check_paged(torch, q, kc, vc, table, cu, lens, o, L)
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (16, 1), (3, 3)])
+@pytest.mark.parametrize("hi", [1, 5, 120])
+def test_arrays_that_something_else_writes(torch, heads, hi):
+    """While another stream writes the lengths, offsets and pages of a call its
+    outputs mean nothing, but it ends, and nothing outside the rows is written;
+    the next call is right."""
+    from causal_streaming_softmax_gb300 import api
+    H, Hkv = heads
+    r = random.Random(hi)
+    reqs = [(r.randint(hi, 3000), r.randint(1, hi)) for _ in range(40)]
+    q, kc, vc, table, cu, lens, width = paged_problem(torch, reqs, H, Hkv, 16, torch.float16, 28)
+    t, pages = q.shape[0], kc.shape[0]
+    s = api.PagedShape(40, t, H, Hkv, 16, pages, width, max_new=hi)
+    ws = api.alloc_paged_workspace(s)
+    room = torch.full((t + 64, H, 64), SENTINEL, dtype=q.dtype, device="cuda")
+    floats = torch.full((H * t + 64,), SENTINEL, device="cuda")
+    o, L = room[32:32 + t], floats[32:32 + H * t].view(H, t)
+    good = [i32(torch, x) for x in (table, cu, lens)]
+    live = [x.clone() for x in good]
+    others = []  # other lengths, offsets and pages, right and wrong ones
+    for _ in range(6):
+        at = sorted(r.randint(0, t) for _ in range(39))
+        others.append([i32(torch, x) for x in (
+            [[r.randint(-1, pages) for _ in range(width)] for _ in reqs],
+            r.choice([[0] + at + [t], [r.randint(-9, t + 9) for _ in range(41)]]),
+            [r.choice([0, 1, 16 * width, r.randint(0, 16 * width), -5, 2 ** 31 - 1]) for _ in reqs])])
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(60):
+        with torch.cuda.stream(other):
+            for j in range(5):
+                for a, b in zip(live, others[(i + j) % 6]):
+                    a.copy_(b)
+        api.attn_paged_fwd(s, q, kc, vc, *live, ws, o, L)
+    torch.cuda.synchronize()
+    assert api.last_device_error() in (0, api.ATTN_ERR_DEVICE_INDEX)
+    for x in (room[:32], room[32 + t:], floats[:32], floats[32 + H * t:]):
+        assert (x == SENTINEL).all()
+    api.attn_paged_fwd(s, q, kc, vc, *good, ws, o, L)
+    check_paged(torch, q, kc, vc, table, cu, lens, o, L)
