@@ -14,6 +14,8 @@
 // bisection of the scanned offsets in shared memory.  The pages read are at
 // the ring's head and the table's old entries, those written behind its tail
 // and in the table's new entries, so no block reads what another writes.
+// cached is read again where a token or page is placed; should another stream
+// write it meanwhile, the place is checked, not trusted.
 // Measured (GB300): 64 requests of one token 3.6 us, 512 requests with 110,000
 // slots 5.8 us, of which about 2 are the launch.
 #include "serve_index.h"
@@ -136,12 +138,17 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs a) 
     int slot = -1;
     if (t < total.add) {
       const int i = last_at_or_below(s_cu, a.batch, t);
-      const int c = a.cached[i], pos = c + (t - s_cu[i]);
-      const int have = (int)pages_for(c, a.shift), pg = pos >> a.shift;
-      const int id = pg < have ? a.table[(long long)i * a.width + pg]
-                               : a.ring[ring_at(head, s_need[i] + (pg - have), a.pages)];
+      const long long c = a.cached[i], pos = c + (t - s_cu[i]);
+      const long long have = pages_for(c, a.shift), pg = pos >> a.shift;
+      const long long x = s_need[i] + (pg - have);  // handed out: place behind the head
+      int id = -1;
+      if (pg < have) {
+        if (pg >= 0 && pg < a.width) id = a.table[(long long)i * a.width + pg];
+      } else if (x < total.need) {
+        id = a.ring[ring_at(head, x, a.pages)];
+      }
       if (page_ok(id, a.pages))
-        slot = (id << a.shift) + (pos & ((1 << a.shift) - 1));
+        slot = (id << a.shift) + ((int)pos & ((1 << a.shift) - 1));
       else
         bad = true;
     }
@@ -149,8 +156,11 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs a) 
   }
   for (int x = first; x < total.need; x += step) {
     const int i = last_at_or_below(s_need, a.batch, x);
-    const int have = (int)pages_for(a.cached[i], a.shift);
-    a.table[(long long)i * a.width + have + (x - s_need[i])] = a.ring[ring_at(head, x, a.pages)];
+    const long long at = pages_for(a.cached[i], a.shift) + (x - s_need[i]);
+    if (at >= 0 && at < a.width)
+      a.table[(long long)i * a.width + at] = a.ring[ring_at(head, x, a.pages)];
+    else
+      bad = true;
   }
   for (int y = first; y < total.back; y += step) {
     const int i = last_at_or_below(s_back, a.batch, y);

@@ -1048,3 +1048,40 @@ def test_arrays_that_something_else_writes(torch, heads, hi):
         assert (x == SENTINEL).all()
     api.attn_paged_fwd(s, q, kc, vc, *good, ws, o, L)
     check_paged(torch, q, kc, vc, table, cu, lens, o, L)
+
+
+def test_plan_of_lengths_that_something_else_writes(torch):
+    from causal_streaming_softmax_gb300 import api
+    r = random.Random(30)
+    B, page, width, N, tokens = 300, 8, 20, 4000, 9000
+    s = api.PagedShape(B, tokens, 1, 1, page, N, width)
+    room = torch.full((B * width + N + 2 * B + tokens + 600,), -77, dtype=torch.int32, device="cuda")
+    at, parts, guards = 0, [], []
+    for n in (B * width, N, B + 1, B, tokens, 4):
+        guards.append(room[at:at + 64])
+        parts.append(room[at + 64:at + 64 + n])
+        at += 64 + n
+    guards.append(room[at:])
+    table, ring, cu, lens, slots, nxt = parts
+    table.fill_(0), ring.copy_(torch.arange(N))
+    state, fresh = i32(torch, [5, 2000, 0, 0]), i32(torch, [r.choice([0, 1, 30, -1]) for _ in range(B)])
+    good = i32(torch, [3] * B)
+    live, others = good.clone(), [i32(torch, [r.choice([0, 8, 100, 129, 130, -4, 2 ** 31 - 1, 7])
+                                              for _ in range(B)]) for _ in range(6)]
+    others += [i32(torch, [r.randint(0, 130) for _ in range(B)]) for _ in range(6)]
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(200):
+        with torch.cuda.stream(other):
+            for j in range(3):
+                live.copy_(others[(i + j) % 12])
+        api.attn_paged_plan(s, live, fresh, ring, state, table.view(B, width), cu, lens, slots, nxt)
+    torch.cuda.synchronize()
+    assert api.last_device_error() in (0, api.ATTN_ERR_DEVICE_INDEX)
+    assert all((g == -77).all() for g in guards)
+    ring.copy_(torch.arange(N)), table.fill_(0)
+    api.attn_paged_plan(s, good, fresh, ring, state, table.view(B, width), cu, lens, slots, nxt)
+    want = plan_host([3] * B, fresh.tolist(), list(range(N)), [5, 2000], [[0] * width] * B, tokens,
+                     page, width)
+    for g, w in zip((cu, lens, slots, ring, table.view(B, width), nxt), want):
+        assert g.tolist() == list(w)
