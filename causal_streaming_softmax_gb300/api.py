@@ -816,6 +816,8 @@ class PagedCache:
         Steps are ordered by their streams alone.  A graph may hold any number
         of steps, and be replayed between eager ones."""
         if stream is not None:  # the step's own buffers belong to its stream
+            if stream.device_index != self.k.get_device():
+                raise ValueError("the stream belongs to another device than the cache")
             with torch.cuda.stream(stream):
                 return self.step(fresh, q, k, v, o, lse, max_new)
         n = q.shape[0]

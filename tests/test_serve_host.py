@@ -495,3 +495,14 @@ def test_descriptions_of_parts_are_checked(tmp_path):
     assert got.returncode == 0, got.stderr
     assert [int(x) for x in got.stdout.split()] == want
     assert 100 < sum(want) < 3900
+
+
+def test_step_refuses_a_stream_of_another_device():
+    """It would run on the current stream of the cache's own device instead."""
+    class Stream:
+        device_index = 3
+
+    cache = api.PagedCache.__new__(api.PagedCache)  # a cache without a GPU: its device is -1
+    cache.k = torch.zeros(1)
+    with pytest.raises(ValueError, match="another device"):
+        cache.step(None, None, None, None, None, stream=Stream())
