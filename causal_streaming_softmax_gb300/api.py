@@ -164,6 +164,11 @@ def _bind_native(lib) -> None:
     except ImportError as e:
         raise ImportError("_marshal.so could not be loaded (%s): build it with "
                           "causal_streaming_softmax_gb300.build.build()" % e) from e
+    key = _build.marshal_key(torch.__version__, torch.version.cuda, torch.version.git_version)
+    if getattr(_marshal, "built_for", None) != key:
+        raise ImportError("_marshal.so was built for %s, this is %s: build it with "
+                          "causal_streaming_softmax_gb300.build.build()"
+                          % (getattr(_marshal, "built_for", "another PyTorch"), key))
     _marshal.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                     for n in ("attn_packed_fwd", "attn_paged_plan", "attn_paged_store",
                               "attn_paged_fwd")))

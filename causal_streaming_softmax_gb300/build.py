@@ -7,12 +7,16 @@ source or header is newer than the library.
 
 ``_marshal.so`` beside it is a small Python extension (host code) that hands
 PyTorch tensors to the library's serving calls; it is compiled by g++ against
-the installed PyTorch's headers in the same way.
+the installed PyTorch's headers in the same way.  It reads PyTorch's objects
+through those headers, so it belongs to one build of PyTorch and Python: it
+carries that build's key, and is made again, or left alone, where another is
+installed.  The library does not need it.
 """
 import concurrent.futures
 import glob
 import importlib.util
 import os
+import runpy
 import shutil
 import subprocess
 import sys
@@ -26,6 +30,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libattn.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL_KEY = os.path.join(BUILD, "marshal.key")  # what MARSHAL was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -56,12 +61,25 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def marshal_key(version=None, cuda=None, git_version=None) -> str:
+    """What _marshal.so is built for: the installed (or the given) PyTorch's
+    version, CUDA version and revision, and this Python's ABI."""
+    if version is None:
+        v = runpy.run_path(os.path.join(_torch(), "version.py"))
+        version, cuda, git_version = v["__version__"], v.get("cuda"), v.get("git_version")
+    return "torch %s cuda %s %s %s" % (version, cuda, git_version,
+                                       sysconfig.get_config_var("SOABI"))
+
+
 def marshal_up_to_date() -> bool:
-    if not os.path.exists(MARSHAL):
+    if not os.path.exists(MARSHAL) or not os.path.exists(MARSHAL_KEY):
         return False
+    with open(MARSHAL_KEY) as f:
+        if f.read() != marshal_key():
+            return False
     t = os.path.getmtime(MARSHAL)
     return all(os.path.getmtime(p) <= t for p in (MARSHAL_SRC, os.path.join(INCLUDE, "attn.h"),
-                                                  os.path.join(_torch(), "version.py"), __file__))
+                                                  __file__))
 
 
 def _torch() -> str:
@@ -75,13 +93,14 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
     """Compile the Python extension that marshals the serving calls."""
     if not force and marshal_up_to_date():
         return MARSHAL
-    torch, cuda = _torch(), os.path.dirname(os.path.dirname(_nvcc()))
+    torch, cuda, key = _torch(), os.path.dirname(os.path.dirname(_nvcc())), marshal_key()
     inc = [os.path.join(torch, "include"),
            os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
     lib = os.path.join(torch, "lib")
     tmp = MARSHAL + ".tmp.%d" % os.getpid()
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden"] + \
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           '-DCSS_BUILT_FOR="%s"' % key] + \
         [x for p in inc for x in ("-isystem", p)] + [MARSHAL_SRC, "-o", tmp, "-L" + lib,
          "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:
@@ -89,7 +108,12 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed on %s:\n%s%s" % (MARSHAL_SRC, r.stdout, r.stderr))
+    os.makedirs(BUILD, exist_ok=True)
+    if os.path.exists(MARSHAL_KEY):
+        os.remove(MARSHAL_KEY)  # never a key beside another build's library
     os.replace(tmp, MARSHAL)
+    with open(MARSHAL_KEY, "w") as f:
+        f.write(key)
     return MARSHAL
 
 

@@ -8,6 +8,10 @@
 // where one fails, or the case is not the ordinary one, they return None
 // without having done anything, and api.py's own path goes on from there: it
 // names what is wrong, or handles the rest.
+//
+// The objects are read through PyTorch's headers: built_for names the PyTorch
+// and Python that they belong to, and api.py binds the entry points only where
+// those are the ones that run.
 #include <Python.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -290,5 +294,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
 PyMODINIT_FUNC PyInit__marshal(void) {
   for (int i = 0; i < NAMES; ++i)
     if (!(names[i] = PyUnicode_InternFromString(kNames[i]))) return nullptr;
-  return PyModule_Create(&module);
+  PyObject* const m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", CSS_BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
 }

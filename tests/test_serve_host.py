@@ -506,3 +506,21 @@ def test_step_refuses_a_stream_of_another_device():
     cache.k = torch.zeros(1)
     with pytest.raises(ValueError, match="another device"):
         cache.step(None, None, None, None, None, stream=Stream())
+
+
+def test_the_marshaller_is_built_for_one_pytorch(lib, monkeypatch):
+    """One made for another PyTorch or Python is made again, whatever the
+    files' times say, and is not bound."""
+    assert build.marshal_up_to_date()
+    key = build.marshal_key()
+    assert api._native.built_for == key
+    for part in (torch.__version__, str(torch.version.cuda), torch.version.git_version):
+        assert part in key
+    with monkeypatch.context() as m:
+        m.setattr(build, "marshal_key", lambda *a: key.replace("torch ", "torch 1"))
+        assert not build.marshal_up_to_date()
+        m.setattr(api, "_native", None)
+        with pytest.raises(ImportError, match="built for"):
+            api._bind_native(lib)
+        assert api._native is None
+    assert build.marshal_up_to_date()
