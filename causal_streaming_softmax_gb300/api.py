@@ -8,8 +8,10 @@ same name on the current stream (or the one given).  There is no fallback:
 if the library is missing or a call fails, an exception is raised.
 """
 import ctypes
+import importlib
 import os
 import struct
+import warnings
 from dataclasses import dataclass
 from typing import Optional
 
@@ -146,7 +148,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "attn_paged_plan", "attn_paged_store", "attn_paged_fwd"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
-        _bind_native(lib)
+        try:
+            _bind_native(lib)
+        except ImportError as e:  # no call needs it: api's own checks and ctypes do the same
+            warnings.warn("%s; until then the serving calls take some 5 us longer on the host" % e,
+                          RuntimeWarning, stacklevel=2)
         _lib = lib
     return lib
 
@@ -160,7 +166,7 @@ _native = None
 def _bind_native(lib) -> None:
     global _native
     try:
-        from . import _marshal
+        _marshal = importlib.import_module("._marshal", __package__)
     except ImportError as e:
         raise ImportError("_marshal.so could not be loaded (%s): build it with "
                           "causal_streaming_softmax_gb300.build.build()" % e) from e

@@ -89,6 +89,17 @@ def _torch() -> str:
     return spec.submodule_search_locations[0]
 
 
+def marshal_missing():
+    """What keeps _marshal.so from being built here (None: nothing)."""
+    if importlib.util.find_spec("torch") is None:
+        return "PyTorch"
+    if not os.path.exists(os.path.join(_torch(), "lib", "libc10_cuda.so")):
+        return "a PyTorch with CUDA"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return None
+
+
 def build_marshal(force: bool = False, verbose: bool = False) -> str:
     """Compile the Python extension that marshals the serving calls."""
     if not force and marshal_up_to_date():
@@ -118,7 +129,10 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date() and marshal_up_to_date():
+    missing = marshal_missing()
+    if missing and verbose:
+        print("_marshal.so is left out: it needs %s" % missing, file=sys.stderr)
+    if not force and up_to_date() and (missing or marshal_up_to_date()):
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -137,11 +151,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     srcs = sources()
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        marshal = ex.submit(build_marshal, force, verbose)
+        marshal = None if missing else ex.submit(build_marshal, force, verbose)
         objs = [] if not force and up_to_date() else list(ex.map(compile_one, srcs))
-        marshal.result()
-    if not objs:
-        return LIB
+    if objs:
+        _link(nvcc, objs, verbose)
+    if marshal is not None:
+        marshal.result()  # raises what stopped it, the library being there
+    return LIB
+
+
+def _link(nvcc: str, objs, verbose: bool) -> None:
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     if verbose:
@@ -150,7 +169,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

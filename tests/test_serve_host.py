@@ -6,6 +6,7 @@ import itertools
 import os
 import random
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -524,3 +525,37 @@ def test_the_marshaller_is_built_for_one_pytorch(lib, monkeypatch):
             api._bind_native(lib)
         assert api._native is None
     assert build.marshal_up_to_date()
+
+
+def test_the_library_does_not_need_the_marshaller(lib, monkeypatch):
+    """Without it, or with one of another PyTorch, the library loads, says so
+    once, and every call goes through api's own checks."""
+    name = api.__package__ + "._marshal"
+    for how in (lambda m: m.setitem(sys.modules, name, None),
+                lambda m: m.setattr(build, "marshal_key", lambda *a: "another")):
+        with monkeypatch.context() as m:
+            m.setattr(api, "_lib", None)
+            m.setattr(api, "_native", None)
+            how(m)
+            with pytest.warns(RuntimeWarning, match="_marshal.so"):
+                assert api.load_library() is not None
+            assert api._native is None and api.load_library() is api._lib
+            assert api.paged_workspace_bytes(api.PagedShape(1, 1, 4, 2, 16, 4, 4)) > 0
+            i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+            with pytest.raises(ValueError, match="CUDA tensors"):
+                api.attn_paged_plan(api.PagedShape(2, 4, 2, 1, 16, 4, 4), i(2), i(2), i(4), i(4),
+                                    i(2, 4), i(3), i(2), i(4), i(4))
+
+
+def test_build_leaves_out_a_marshaller_that_cannot_be_built(lib, monkeypatch, tmp_path):
+    """A PyTorch without CUDA, or none, does not stop the library's build."""
+    assert build.marshal_missing() is None
+    with monkeypatch.context() as m:
+        m.setattr(build, "MARSHAL", str(tmp_path / "_marshal.so"))
+        m.setattr(build, "MARSHAL_KEY", str(tmp_path / "marshal.key"))
+        m.setattr(build, "_torch", lambda: str(tmp_path))
+        assert build.marshal_missing() == "a PyTorch with CUDA"
+        assert build.build() == build.LIB and not os.path.exists(build.MARSHAL)
+        m.setattr(build.importlib.util, "find_spec", lambda n: None)
+        assert build.marshal_missing() == "PyTorch"
+        assert build.build() == build.LIB and not os.path.exists(build.MARSHAL)
