@@ -1085,3 +1085,61 @@ def test_plan_of_lengths_that_something_else_writes(torch):
                      page, width)
     for g, w in zip((cu, lens, slots, ring, table.view(B, width), nxt), want):
         assert g.tolist() == list(w)
+
+
+def test_the_native_marshaller_takes_ordinary_calls(torch):
+    """Called directly: it makes the ordinary calls itself, and leaves alone,
+    without doing anything, what it has to leave."""
+    from causal_streaming_softmax_gb300 import api
+    api.load_library()
+    nat, H, Hkv, n = api._native, 8, 2, 40
+    q, k, v = packed_inputs(torch, n, H, Hkv, torch.float16, 25)
+    cu, o, L = i32(torch, [0, n]), torch.zeros_like(q), torch.zeros((H, n), device="cuda")
+    s = api.PackedShape(n, 1, H, Hkv)
+    assert nat.packed_fwd(s, q, k, v, cu, o, L) == 0
+    assert nat.packed_fwd(s, q, k, v, cu, o, None) == 0
+    check_packed(torch, q, k, v, [0, n], True, o, L)
+    p = api.PagedShape(1, n, H, Hkv, 16, 5, 4, max_new=n)
+    state = [i32(torch, x) for x in ([0], [n], list(range(5)), [0, 5, 0, 0], [[-1] * 4])]
+    step = [torch.empty(x, dtype=torch.int32, device="cuda") for x in (2, 1, n, 4)]
+    assert nat.paged_plan(p, *state, *step) == 0
+    pools = [torch.zeros((5, Hkv, 16, 64), dtype=torch.float16, device="cuda") for _ in range(2)]
+    assert nat.paged_store(p, k, v, step[2], *pools) == 0
+    ws, o2, L2 = api.alloc_paged_workspace(p), torch.zeros_like(q), torch.zeros_like(L)
+    assert nat.paged_fwd(p, q, *pools, state[4], step[0], step[1], ws, o2, L2) == 0
+    check_packed(torch, q, k, v, [0, n], True, o2, L2)
+    # an entry point's refusal comes back as its code
+    assert nat.packed_fwd(s, q, k, v, cu, o[:1].expand(n, H, 64), None) == api.ATTN_ERR_SHAPE
+    before = o.clone()
+    for bad in (dict(q=q.cpu()), dict(q=q.bfloat16()), dict(k=k[:9]), dict(v=None),
+                dict(cu=cu.long()), dict(cu=i32(torch, [0, 3, n])), dict(q=q.transpose(1, 2)),
+                dict(L=L.t()), dict(s=api.PackedShape(1 << 40, 1, H, Hkv)), dict(s=None),
+                dict(s=api.PackedShape(n, 1, H, Hkv, dtype=torch.float32)),
+                dict(s=api.PackedShape(n, 1, H, Hkv, scale="1"))):
+        a = dict(dict(s=s, q=q, k=k, v=v, cu=cu, o=o, L=L), **bad)
+        assert nat.packed_fwd(*(a[x] for x in ("s", "q", "k", "v", "cu", "o", "L"))) is None, bad
+    assert nat.paged_plan(p, state[0].cpu(), *state[1:], *step) is None
+    assert nat.paged_store(p, k, v, step[2].long(), *pools) is None
+    assert nat.paged_fwd(p, q, *pools, state[4], step[0], step[1], ws.float(), o2, L2) is None
+    assert nat.paged_fwd(p, q) is None and torch.equal(before, o)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("new", [1, 2, 4])
+@pytest.mark.parametrize("page", [8, 64, 256])
+def test_bad_values_in_short_tables(torch, dtype, new, page):
+    """NaN and infinities among visible keys where the table holds at most 256
+    keys and every request is finished by one block."""
+    reqs = [(200, new), (new, new), (129, 1), (128, new), (240, 1)]
+    q, kc, vc, table, cu, lens, _ = paged_problem(torch, reqs, 8, 2, page, getattr(torch, dtype),
+                                                  26, stale=NAN)
+    table = [r[:256 // page] for r in table]
+    for req, back, head, what in ((0, 1, 0, NAN), (0, 2, 1, math.inf), (1, 1, 1, -math.inf),
+                                  (2, 1, 0, math.inf), (3, new, 1, NAN), (4, 240, 0, math.inf)):
+        pos = lens[req] - back
+        if pos >= 0:
+            vc[table[req][pos // page], head, pos % page, 3 + back % 50] = what
+    pos = lens[3] - 1
+    kc[table[3][pos // page], 0, pos % page, 3] = NAN
+    o, L = run_paged(torch, q, kc, vc, table, cu, lens)
+    check_paged(torch, q, kc, vc, table, cu, lens, o, L)
