@@ -381,7 +381,8 @@ ATTN_API int attn_bwd_noalloc(const attn_shape* shape, const uint16_t* q,
  *
  * An output row depends on the keys that its row sees and on nothing else:
  * infinities and NaN in masked keys, in pages past a length or in other
- * sequences do not reach it.  A row that sees no key gives O = 0, L = -inf.
+ * sequences do not reach it.  A row that sees no key, or whose every
+ * score is -infinity, gives O = 0, L = -inf.
  */
 enum { ATTN_F16 = 0, ATTN_BF16 = 1 };
 
@@ -491,7 +492,7 @@ ATTN_API int attn_paged_plan(const attn_paged_shape* shape, const int32_t* cache
  * goes to slot slots[t]; a negative slot is skipped.  Slots of one call are
  * distinct (attn_paged_plan's are): where one is given twice, which row it
  * ends with is not determined.  The pools' rows must not overlap one another
- * within a pool (ATTN_ERR_SHAPE).  Uses batch, tokens, kv_heads, page_size,
+ * within a pool (ATTN_ERR_SHAPE), nor the other pool's, nor k and v.  Uses batch, tokens, kv_heads, page_size,
  * num_pages, dtype and the k, v, kc and vc strides.
  */
 ATTN_API int attn_paged_store(const attn_paged_shape* shape, const void* k, const void* v,

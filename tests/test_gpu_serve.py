@@ -1143,3 +1143,57 @@ def test_bad_values_in_short_tables(torch, dtype, new, page):
     kc[table[3][pos // page], 0, pos % page, 3] = NAN
     o, L = run_paged(torch, q, kc, vc, table, cu, lens)
     check_paged(torch, q, kc, vc, table, cu, lens, o, L)
+
+
+def test_offsets_that_something_else_writes(torch):
+    """The same of packed prompts."""
+    from causal_streaming_softmax_gb300 import api
+    H, Hkv, t, B = 8, 2, 3000, 50
+    r = random.Random(31)
+    q, k, v = packed_inputs(torch, t, H, Hkv, torch.float16, 32)
+    room = torch.full((t + 64, H, 64), SENTINEL, dtype=q.dtype, device="cuda")
+    floats = torch.full((H * t + 64,), SENTINEL, device="cuda")
+    o, L = room[32:32 + t], floats[32:32 + H * t].view(H, t)
+    ways = [[0] + sorted(r.randint(0, t) for _ in range(B - 1)) + [t] for _ in range(4)]
+    good = i32(torch, ways[0])
+    others = [i32(torch, w) for w in ways]
+    others += [i32(torch, [r.choice([0, t, t + 1, -1, 2 ** 31 - 1, -2 ** 31, r.randint(0, t)])
+                           for _ in range(B + 1)]) for _ in range(4)]
+    live, other = good.clone(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(60):
+        with torch.cuda.stream(other):
+            for j in range(8):
+                live.copy_(others[(3 * i + j) % 8])
+        api.attn_packed_fwd(api.PackedShape(t, B, H, Hkv, causal=bool(i % 2)), q, k, v, live, o, L)
+    torch.cuda.synchronize()
+    assert api.last_device_error() in (0, api.ATTN_ERR_DEVICE_INDEX)
+    for x in (room[:32], room[32 + t:], floats[:32], floats[32 + H * t:]):
+        assert (x == SENTINEL).all()
+    api.attn_packed_fwd(api.PackedShape(t, B, H, Hkv), q, k, v, good, o, L)
+    check_packed(torch, q, k, v, ways[0], True, o, L)
+
+
+@pytest.mark.parametrize("n", [1, 3, 40, 200])
+def test_rows_whose_every_score_is_minus_infinity(torch, n):
+    """Like rows that see no key; the rows that see another key too go on
+    without the infinite one."""
+    H, Hkv = 8, 2
+    q, k, v = packed_inputs(torch, n, H, Hkv, torch.bfloat16, 33, "dense")
+    q[..., 5] = -1.0
+    k[0, :, 5] = math.inf
+    outs = [run_packed(torch, q, k, v, [0, n])]
+    if n > 1:
+        outs.append(run_packed(torch, q, k, v, [0, 1, n]))
+    pool = [torch.zeros((15, Hkv, 16, 64), dtype=q.dtype, device="cuda") for _ in range(2)]
+    for p, x in zip(pool, (k, v)):
+        for j in range(n):
+            p[j // 16, :, j % 16] = x[j]
+    outs.append(run_paged(torch, q, *pool, [list(range(15))], [0, n], [n]))
+    for i, (o, L) in enumerate(outs):
+        assert (o[0] == 0).all() and (L[:, 0] == -math.inf).all(), i
+        assert torch.isfinite(o).all() and torch.isfinite(L[:, 1:]).all(), i
+        if n > 1:
+            eo, el, to, tl = attend64(q[1:], k[1:], v[1:], torch.arange(1, n, device="cuda"))
+            check(o[1:], eo, to, "O")
+            check(L[:, 1:], el, tl, "L")
