@@ -4,7 +4,10 @@
 // For each request and K/V head: S = Q K^T, t = S c in base 2, per key block
 // m' = max(m, max t), P = 2^(t - m'), l = l 2^(m - m') + sum P (binary32, P
 // unrounded), O = O 2^(m - m') + P V with P rounded to the operands' type;
-// O / l and L = m + log2 l.
+// O / l and L = m + log2 l.  P is rounded because the matrix product takes
+// 16-bit operands, as it is in every forward pass of the library, so that a
+// token gives the same through either kernel; next to the rounding of O it adds
+// a tenth to the error against 64 bits (binary16 2.2e-4, bfloat16 1.8e-3).
 //
 // Bound by memory: 256 bytes of K and V a key and K/V head, 4 * 64 * 16
 // operations on a padded 16-row tile, a twentieth of what the matrix units
@@ -15,19 +18,23 @@
 //    parts, in a fixed order);
 //  * a producer warp copies tiles by TMA into a ring of stages, its page ids
 //    read 32 at a time ahead of their use; two blocks a SM keep 2 x 5 x 16 KB
-//    under way;
-//  * four consumer warps take 16 keys each of every tile with their own
-//    running maximum, in registers from S to O (warp-level matrix products:
-//    with 16 rows and a handful of keys a warp, a tensor-memory round trip
-//    would be the longer path), and meet once a work item;
+//    under way.  The 8 bytes a request of the tile counts (s_pre) end that
+//    between 1,024 and 1,280 requests, from where one block fits: 6.7 TB/s at
+//    1,024 requests of 512..3500 keys (32 / 4 heads), 3.9 at 1,280 and at 4,096;
+//  * four consumer warps (eight where a block takes whole items) take 16 keys
+//    each of every tile with their own running maximum, in registers from S to
+//    O (warp-level matrix products: with 16 rows and a handful of keys a warp, a
+//    tensor-memory round trip would be the longer path), and meet once a work
+//    item, which the producer describes to them beside its Q;
 //  * the next item's request and page ids are read while this one's tiles
 //    arrive, so that short requests do not wait for them.
 //
-// Measured (GB300, join included): 256 requests over 1024..16384 keys, 32 / 4
-// heads 309 us = 6.84 TB/s, 101% of the measured copy rate; 64 over 17..8192,
-// 32 / 8 heads 92 us = 6.02 TB/s; 2 over 50000..65536, 16 / 16 heads 75 us =
-// 6.26 TB/s; one over 777 keys 9 us, of which about 8 are two launches and the
-// chain of loads lengths -> page ids -> pages -> parts.
+// Measured (GB300, join included; boxes differ by 2%): 256 requests over
+// 1024..16384 keys, 32 / 4 heads 310 to 317 us = 6.7 to 6.8 TB/s, 98 to 101% of
+// the measured copy rate; 64 over 17..8192, 32 / 8 heads 93 us = 5.97 TB/s; 2 over
+// 50000..65536, 16 / 16 heads 75 us = 6.25 TB/s; one over 777 keys 7.9 us, nearly
+// all of it two launches and the chain of loads lengths -> page ids -> pages ->
+// parts.
 #include <math.h>
 
 #include "serve_index.h"
@@ -530,8 +537,10 @@ int launch(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolAr
 // Whole items where every item finds an SM and the table leaves room for no
 // more than kWholeKeys keys a request: eight warps are through with an item in
 // two steps, and the parts and the second launch fall away.  Split / whole, us:
-// one request of 100 keys 6.1 / 4.6, of 250 7.4 / 6.3, of 777 8.5 / 10.0; eight
-// of 256 8.3 / 6.0; 64 of 60 (512 items) 8.1 / 10.7.
+// one request of 100 keys 5.8 / 4.4, of 250 7.2 / 5.4, of 777 7.8 / 9.6, of 4000
+// 9.5 / 32; eight of 256 7.9 / 5.5; 64 of 60 (512 items) 7.7 / 16.7.  The width
+// stands for the lengths, which the host does not see: short requests in a wide
+// table take the split form and its 1.4 to 3 us.
 bool decode_whole(const PagedDims& d, int sm_count) {
   return (long long)d.batch * d.Hkv <= sm_count && ((long long)d.width << d.shift) <= kWholeKeys;
 }

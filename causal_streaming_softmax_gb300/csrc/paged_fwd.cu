@@ -135,8 +135,8 @@ PartArgs parts_at(void* ws, size_t blocks, int rows, int min_tiles) {
 
 // A block takes at least so many tiles: below, starting it and joining its
 // parts costs more than its tiles.  Few rows (64-key tiles), us with at least
-// 1 / 2 / 4: one request of 100 keys 7.0 / 6.1 / 8.1, of 777 8.3 / 8.7 / 9.4, of
-// 4000 12.8 / 10.6 / 10.8, eight of 256 7.9 / 8.3 / 7.2.
+// 1 / 2 / 4: one request of 100 keys 6.6 / 5.8 / 7.7, of 777 7.8 / 7.8 / 9.0, of
+// 4000 11.2 / 9.5 / 10.6, eight of 256 7.7 / 7.9 / 7.3, 64 of 60 7.8 / 7.7 / 11.1.
 constexpr int kLeastFew = 2, kLeastRows = 2;
 
 }  // namespace

@@ -40,9 +40,12 @@
 // phased and however many warps issued the products (1.25 ms for a prompt of
 // 16384 tokens, 32 / 4 heads); three tiles of 64 keys take 0.95 ms.
 //
-// Measured (GB300): that prompt 952 us = 1155 TFLOP/s, 62% of the measured
-// dense rate; 16 prompts of 256..4096 tokens, 32 / 8 heads, 504 us = 861
-// TFLOP/s.  The matrix pipe is busy 45% of the time and the issue slots 58%:
+// Measured (GB300): that prompt 951 to 959 us in a captured graph and 977 to 992
+// call by call = 1108 to 1156 TFLOP/s, 59 to 62% of the measured dense rate; 16
+// prompts of 256..4096 tokens, 32 / 8 heads, 508 us = 854 TFLOP/s, of which five
+// to six tile steps a window are its border: the last products, the epilogue and
+// the next window's first steps, one behind the other.
+// The matrix pipe is busy 46% of the time and the issue slots 59%:
 // what bounds is the latency of a tile step (wait for S, load, maximum,
 // exponentials, store of P, wait of the products) times the three in flight.
 // Slower were: a warp for S and one for O += P V (1.38 ms, the second's own
