@@ -5,9 +5,9 @@
 // m' = max(m, max t), P = 2^(t - m'), l = l 2^(m - m') + sum P (binary32, P
 // unrounded), O = O 2^(m - m') + P V with P rounded to the operands' type;
 // O / l and L = m + log2 l.  P is rounded because the matrix product takes
-// 16-bit operands, as it is in every forward pass of the library, so that a
-// token gives the same through either kernel; next to the rounding of O it adds
-// a tenth to the error against 64 bits (binary16 2.2e-4, bfloat16 1.8e-3).
+// 16-bit operands, as in every forward pass of the library; next to the rounding
+// of O that adds up to a tenth to the error against 64 bits (binary16 2.2e-4,
+// bfloat16 1.8e-3, relative to the outputs' norm).
 //
 // Bound by memory: 256 bytes of K and V a key and K/V head, 4 * 64 * 16
 // operations on a padded 16-row tile, a twentieth of what the matrix units

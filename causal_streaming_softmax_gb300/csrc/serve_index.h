@@ -62,7 +62,7 @@ CSS_HD int row_limit(int n_keys, int n_new, int tok) {
   return n_keys - (behind > 0 ? behind : 0);
 }
 
-// Whether the keys [k0, k0 + n) pass lim, for k0 < 2^31 and lim > k0 - 2^30.
+// Whether the keys [k0, k0 + n) pass lim, without forming k0 + n.
 CSS_HD bool past_limit(int k0, int n, int lim) { return lim - k0 < n; }
 
 // Pages that hold n tokens.

@@ -3,7 +3,9 @@
 //
 // Method: for every key tile that a row tile sees, S = Q K^T; t = S c in base
 // 2; P = 2^(t - m); l += sum P (binary32, P unrounded); O += P V with P
-// rounded to the operands' type; O / l and L = m + log2 l.  m follows the
+// rounded to the operands' type, which the matrix product takes (error against
+// 64 bits 2.2e-4 to 2.9e-4 in binary16 and 2.1e-3 to 2.3e-3 in bfloat16, where
+// rounding O alone gives 2.0e-4 and 1.7e-3); O / l and L = m + log2 l.  m follows the
 // running maximum only when that has grown by more than kSlack: P may then
 // reach 2^kSlack, which changes no relative rounding (binary16 holds it, sums
 // are binary32), and O is rescaled a few times a row instead of at nearly

@@ -492,8 +492,9 @@ ATTN_API int attn_paged_plan(const attn_paged_shape* shape, const int32_t* cache
  * goes to slot slots[t]; a negative slot is skipped.  Slots of one call are
  * distinct (attn_paged_plan's are): where one is given twice, which row it
  * ends with is not determined.  The pools' rows must not overlap one another
- * within a pool (ATTN_ERR_SHAPE), nor the other pool's, nor k and v.  Uses batch, tokens, kv_heads, page_size,
- * num_pages, dtype and the k, v, kc and vc strides.
+ * within a pool (ATTN_ERR_SHAPE), nor the other pool's, nor k and v.  Uses
+ * batch, tokens, kv_heads, page_size, num_pages, dtype and the k, v, kc and vc
+ * strides.
  */
 ATTN_API int attn_paged_store(const attn_paged_shape* shape, const void* k, const void* v,
                               const int32_t* slots, void* k_cache, void* v_cache, void* stream);
