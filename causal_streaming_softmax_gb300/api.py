@@ -38,6 +38,7 @@ ATTN_STEP_FUSED = 1
 MIN_WAIT_LIMIT_NS = 10_000_000
 
 HEAD_DIM = 64
+UNIT4_BYTES = 288  # eight rows of a 4-bit pool
 
 
 class AttnShape(ctypes.Structure):
@@ -143,9 +144,14 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.attn_paged_workspace_bytes.argtypes = [gp]
     lib.attn_paged_workspace_bytes.restype = sz
     lib.attn_paged_fwd.argtypes = [gp] + [vp] * 7 + [sz, vp, vp, vp]
+    lib.attn_paged_append.argtypes = [gp] + [vp] * 5 + [ctypes.c_int32] + [vp] * 7
+    lib.attn_paged_append4.argtypes = lib.attn_paged_append.argtypes
+    lib.attn_paged_load4.argtypes = [gp] + [vp] * 6
+    lib.attn_paged_fwd4.argtypes = lib.attn_paged_fwd.argtypes
     for name in ("attn_fwd", "attn_row_terms", "attn_bwd_keys", "attn_bwd_queries",
                  "attn_last_device_error", "attn_selftest_wait_timeout", "attn_packed_fwd",
-                 "attn_paged_plan", "attn_paged_store", "attn_paged_fwd"):
+                 "attn_paged_plan", "attn_paged_store", "attn_paged_fwd", "attn_paged_append",
+                 "attn_paged_append4", "attn_paged_load4", "attn_paged_fwd4"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         try:
@@ -177,7 +183,8 @@ def _bind_native(lib) -> None:
                           % (getattr(_marshal, "built_for", "another PyTorch"), key))
     _marshal.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                     for n in ("attn_packed_fwd", "attn_paged_plan", "attn_paged_store",
-                              "attn_paged_fwd")))
+                              "attn_paged_fwd", "attn_paged_append", "attn_paged_append4",
+                              "attn_paged_load4", "attn_paged_fwd4")))
     _native = _marshal
 
 
@@ -739,6 +746,104 @@ def attn_paged_store(s: PagedShape, k, v, slots, k_cache, v_cache, stream=None) 
          vc)
 
 
+def _pool4(t, name, s, dev):
+    """Pointer and strides of a 4-bit pool, its last two dimensions dense."""
+    shape = (s.num_pages, s.kv_heads, s.page_size // 8, UNIT4_BYTES)
+    p, st = _strided(t, name, torch.uint8, shape, dev)
+    if st[2] != UNIT4_BYTES and shape[2] > 1:
+        raise ValueError("%s must be dense in its last two dimensions" % name)
+    return p, (st[0], st[1], 0)
+
+
+def alloc_paged_pool4(s: PagedShape, device=None) -> torch.Tensor:
+    """A pool of a 4-bit cache, every row zero: uint8
+    [num_pages][kv_heads][page_size / 8][288] (see attn.h)."""
+    return torch.zeros((s.num_pages, s.kv_heads, s.page_size // 8, UNIT4_BYTES),
+                       dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def _append(name, s, q, k, v, cos, sin, slots, cu, lens, q_out, k_cache, v_cache, stream):
+    n, H, Hkv, B, dt = s.tokens, s.heads, s.kv_heads, s.batch, s.dtype
+    four = name == "attn_paged_append4"
+    dev = _device_of(k, "k")
+    kp, ks = _strided(k, "k", dt, (n, Hkv, 64), dev)
+    vp, vs = _strided(v, "v", dt, (n, Hkv, 64), dev)
+    sp = _dense(slots, "slots", torch.int32, (n,), dev)
+    qp = cp = sn = op = cup = lp = None
+    qs = os_ = (0, 0)
+    angles = 0
+    if not (four and cos is None and sin is None):
+        qp, qs = _strided(q, "q", dt, (n, H, 64), dev)
+        op, os_ = _strided(q_out, "q_out", dt, (n, H, 64), dev)
+        angles = cos.shape[0] if isinstance(cos, torch.Tensor) and cos.dim() else 0
+        cp = _dense(cos, "cos", torch.float32, (angles, 32), dev)
+        sn = _dense(sin, "sin", torch.float32, (angles, 32), dev)
+        cup = _dense(cu, "cu", torch.int32, (B + 1,), dev)
+        lp = _dense(lens, "lens", torch.int32, (B,), dev)
+        if not 0 < angles < 1 << 31:
+            raise ValueError("cos and sin must have from 1 to 2^31 - 1 rows")
+    if four:
+        kc, kcs = _pool4(k_cache, "k_cache", s, dev)
+        vc, vcs = _pool4(v_cache, "v_cache", s, dev)
+    else:
+        dims = (s.num_pages, Hkv, s.page_size, 64)
+        kc, kcs = _strided(k_cache, "k_cache", dt, dims, dev)
+        vc, vcs = _strided(v_cache, "v_cache", dt, dims, dev)
+    _run(name, dev, stream,
+         s.c_bytes((qs[0], qs[1], os_[0], os_[1], ks[0], ks[1], vs[0], vs[1]) + kcs[:3] + vcs[:3]),
+         qp, kp, vp, cp, sn, angles, sp, cup, lp, op, kc, vc)
+
+
+def attn_paged_append(s: PagedShape, q, k, v, cos, sin, slots, cu, lens, q_out, k_cache, v_cache,
+                      stream=None) -> None:
+    """Stores rows of k and v [tokens][kv_heads][64] at slots int32 [tokens], k
+    turned by the rotation of its position, and writes the turned q
+    [tokens][heads][64] to q_out (q itself, or rows apart from all others).  cos, sin
+    float32 [angles][32]; cu, lens as attn_paged_fwd takes them."""
+    if stream is None and _native is not None:
+        rc = _native.paged_append(s, q, k, v, cos, sin, slots, cu, lens, q_out, k_cache, v_cache)
+        if rc == ATTN_OK:
+            return
+        if rc is not None:
+            raise AttnError("attn_paged_append", rc)
+    _append("attn_paged_append", s, q, k, v, cos, sin, slots, cu, lens, q_out, k_cache, v_cache,
+            stream)
+
+
+def attn_paged_append4(s: PagedShape, q, k, v, cos, sin, slots, cu, lens, q_out, k_cache, v_cache,
+                       stream=None) -> None:
+    """The same into 4-bit pools (alloc_paged_pool4).  With cos and sin None nothing
+    is turned, and q, cu, lens and q_out are not looked at."""
+    if stream is None and _native is not None:
+        rc = _native.paged_append4(s, q, k, v, cos, sin, slots, cu, lens, q_out, k_cache, v_cache)
+        if rc == ATTN_OK:
+            return
+        if rc is not None:
+            raise AttnError("attn_paged_append4", rc)
+    _append("attn_paged_append4", s, q, k, v, cos, sin, slots, cu, lens, q_out, k_cache, v_cache,
+            stream)
+
+
+def attn_paged_load4(s: PagedShape, slots, k_cache, v_cache, k, v, stream=None) -> None:
+    """Rows of 4-bit pools at slots int32 [tokens] into k, v [tokens][kv_heads][64]
+    (rows with a negative slot stay as they are)."""
+    if stream is None and _native is not None:
+        rc = _native.paged_load4(s, slots, k_cache, v_cache, k, v)
+        if rc == ATTN_OK:
+            return
+        if rc is not None:
+            raise AttnError("attn_paged_load4", rc)
+    dev, rows = _device_of(slots, "slots"), (s.tokens, s.kv_heads, 64)
+    sp = _dense(slots, "slots", torch.int32, (s.tokens,), dev)
+    kc, kcs = _pool4(k_cache, "k_cache", s, dev)
+    vc, vcs = _pool4(v_cache, "v_cache", s, dev)
+    kp, ks = _strided(k, "k", s.dtype, rows, dev)
+    vp, vs = _strided(v, "v", s.dtype, rows, dev)
+    _run("attn_paged_load4", dev, stream,
+         s.c_bytes((0, 0, 0, 0, ks[0], ks[1], vs[0], vs[1]) + kcs + vcs),
+         sp, kc, vc, kp, vp)
+
+
 def paged_workspace_bytes(s: PagedShape) -> int:
     n = load_library().attn_paged_workspace_bytes(s.c_bytes())
     if n == 0:
@@ -747,7 +852,8 @@ def paged_workspace_bytes(s: PagedShape) -> int:
 
 
 def alloc_paged_workspace(s: PagedShape, device=None) -> torch.Tensor:
-    """A uint8 CUDA tensor large enough for attn_paged_fwd's workspace."""
+    """A uint8 CUDA tensor large enough for attn_paged_fwd's and attn_paged_fwd4's
+    workspace."""
     return torch.empty(paged_workspace_bytes(s), dtype=torch.uint8,
                        device=device or torch.device("cuda"))
 
@@ -762,13 +868,33 @@ def attn_paged_fwd(s: PagedShape, q, k_cache, v_cache, table, cu, lens, ws, o, l
             return
         if rc is not None:
             raise AttnError("attn_paged_fwd", rc)
+    _attend("attn_paged_fwd", s, q, k_cache, v_cache, table, cu, lens, ws, o, lse, stream)
+
+
+def attn_paged_fwd4(s: PagedShape, q, k_cache, v_cache, table, cu, lens, ws, o, lse=None,
+                    stream=None) -> None:
+    """The same over 4-bit pools (alloc_paged_pool4)."""
+    if stream is None and _native is not None:
+        rc = _native.paged_fwd4(s, q, k_cache, v_cache, table, cu, lens, ws, o, lse)
+        if rc == ATTN_OK:
+            return
+        if rc is not None:
+            raise AttnError("attn_paged_fwd4", rc)
+    _attend("attn_paged_fwd4", s, q, k_cache, v_cache, table, cu, lens, ws, o, lse, stream)
+
+
+def _attend(name, s, q, k_cache, v_cache, table, cu, lens, ws, o, lse, stream):
     n, H, B, dt = s.tokens, s.heads, s.batch, s.dtype
     dev = _device_of(q, "q")
-    dims = (s.num_pages, s.kv_heads, s.page_size, 64)
     qp, qs = _strided(q, "q", dt, (n, H, 64), dev)
     op, os_ = _strided(o, "o", dt, (n, H, 64), dev)
-    kc, kcs = _strided(k_cache, "k_cache", dt, dims, dev)
-    vc, vcs = _strided(v_cache, "v_cache", dt, dims, dev)
+    if name == "attn_paged_fwd4":
+        kc, kcs = _pool4(k_cache, "k_cache", s, dev)
+        vc, vcs = _pool4(v_cache, "v_cache", s, dev)
+    else:
+        dims = (s.num_pages, s.kv_heads, s.page_size, 64)
+        kc, kcs = _strided(k_cache, "k_cache", dt, dims, dev)
+        vc, vcs = _strided(v_cache, "v_cache", dt, dims, dev)
     tp = _dense(table, "table", torch.int32, (B, s.table_width), dev)
     cup = _dense(cu, "cu", torch.int32, (B + 1,), dev)
     lenp = _dense(lens, "lens", torch.int32, (B,), dev)
@@ -776,24 +902,31 @@ def attn_paged_fwd(s: PagedShape, q, k_cache, v_cache, table, cu, lens, ws, o, l
     if not (isinstance(ws, torch.Tensor) and ws.dtype is torch.uint8 and ws.is_contiguous()
             and ws.get_device() == dev):
         raise TypeError("ws must be a contiguous uint8 CUDA tensor on the device of the others")
-    _run("attn_paged_fwd", dev, stream,
+    _run(name, dev, stream,
          s.c_bytes((qs[0], qs[1], os_[0], os_[1], 0, 0, 0, 0) + kcs[:3] + vcs[:3]), qp, kc, vc, tp,
          cup, lenp, ws.data_ptr(), ws.numel(), op, lp)
 
 
 class PagedCache:
     """The device state of a server's cache: pools of K and V pages, the block
-    table, the requests' lengths and the ring of free pages."""
+    table, the requests' lengths and the ring of free pages.  ``bits``: 16, or 4
+    for pools that hold K and V quantised (28% of the memory; see attn.h)."""
 
     def __init__(self, batch: int, heads: int, kv_heads: int, num_pages: int, page_size: int = 16,
                  table_width: Optional[int] = None, dtype=torch.float16, scale: float = 0.125,
-                 device=None):
+                 device=None, bits: int = 16):
+        if bits not in (4, 16):
+            raise ValueError("bits must be 4 or 16")
         dev = torch.device(device or "cuda")
+        self.bits = bits
         self.batch, self.heads, self.kv_heads = batch, heads, kv_heads
         self.num_pages, self.page_size, self.scale, self.dtype = num_pages, page_size, scale, dtype
         self.table_width = table_width or num_pages
         i32 = dict(dtype=torch.int32, device=dev)
-        self.k = torch.zeros((num_pages, kv_heads, page_size, 64), dtype=dtype, device=dev)
+        if bits == 4:
+            self.k = alloc_paged_pool4(self.shape(1, 1), dev)
+        else:
+            self.k = torch.zeros((num_pages, kv_heads, page_size, 64), dtype=dtype, device=dev)
         self.v = torch.zeros_like(self.k)
         self.table = torch.full((batch, self.table_width), -1, **i32)
         self.ring = torch.arange(num_pages, **i32)
@@ -816,7 +949,7 @@ class PagedCache:
                           self.num_pages, self.table_width, max_new, self.scale, self.dtype)
 
     def step(self, fresh, q, k, v, o, lse=None, max_new: Optional[int] = None,
-             stream=None) -> None:
+             stream=None, cos=None, sin=None) -> None:
         """One step of every request: ``fresh`` int32 [batch] new tokens each
         (negative: finished, its pages go back), whose rows stand in q, k, v
         one behind the other; plans, stores K and V and writes o (and lse).
@@ -824,13 +957,17 @@ class PagedCache:
         which a step of single tokens pays for: give it 1 there).  A request with
         more is stored and counted but its rows of o and lse stay as they were;
         last_device_error() tells, status() does not.
+        ``cos``, ``sin``: float32 [angles][32], to turn q and k by their positions
+        (q, k and v themselves stay as they are); a token at a position that the
+        tables do not have is not stored, its row of o then means nothing, and
+        last_device_error() tells.
         Steps are ordered by their streams alone.  A graph may hold any number
         of steps, and be replayed between eager ones."""
         if stream is not None:  # the step's own buffers belong to its stream
             if stream.device_index != self.k.get_device():
                 raise ValueError("the stream belongs to another device than the cache")
             with torch.cuda.stream(stream):
-                return self.step(fresh, q, k, v, o, lse, max_new)
+                return self.step(fresh, q, k, v, o, lse, max_new, None, cos, sin)
         n = q.shape[0]
         s = self.shape(n, max_new or max(n, 1))
         # everything is looked at before the plan moves the cache on
@@ -844,15 +981,37 @@ class PagedCache:
         _step_rows(o, "o", dt, rows, dev, written=True)
         if lse is not None and _dense(lse, "lse", torch.float32, (self.heads, n), dev) % 16:
             raise ValueError("lse must start on 16 bytes")
+        if cos is not None or sin is not None:
+            angles = cos.shape[0] if isinstance(cos, torch.Tensor) and cos.dim() else 0
+            for t, name in ((cos, "cos"), (sin, "sin")):
+                if _dense(t, name, torch.float32, (angles, 32), dev) % 16 or angles < 1:
+                    raise ValueError("%s must start on 16 bytes and have rows" % name)
         slots = torch.empty(n, dtype=torch.int32, device=self.k.device)
         if not torch.cuda.is_current_stream_capturing():  # a graph runs where it is replayed
             self._stream = torch._C._cuda_getCurrentStream(dev)
         attn_paged_plan(s, self.lens, fresh, self.ring, self.state, self.table, self.cu,
                         self._lens, slots, self._state)
         self._now.copy_(self._new)
-        if n:
+        if not n:
+            return
+        if cos is not None:
+            q_in, q = q, torch.empty(rows, dtype=dt, device=self.k.device)
+            append = attn_paged_append4 if self.bits == 4 else attn_paged_append
+            append(s, q_in, k, v, cos, sin, slots, self.cu, self.lens, q, self.k, self.v)
+        elif self.bits == 4:
+            attn_paged_append4(s, None, k, v, None, None, slots, None, None, None, self.k, self.v)
+        else:
             attn_paged_store(s, k, v, slots, self.k, self.v)
-            attn_paged_fwd(s, q, self.k, self.v, self.table, self.cu, self.lens, self.ws, o, lse)
+        attend = attn_paged_fwd4 if self.bits == 4 else attn_paged_fwd
+        attend(s, q, self.k, self.v, self.table, self.cu, self.lens, self.ws, o, lse)
+
+    def load(self, slots, k, v, stream=None) -> None:
+        """What a 4-bit cache holds at slots int32 [tokens], as rows of k, v
+        [tokens][kv_heads][64]; rows with a negative slot stay as they are."""
+        if self.bits != 4:
+            raise ValueError("the pools of a 16-bit cache hold the rows themselves")
+        n = _device_of(slots, "slots") >= 0 and slots.numel()
+        attn_paged_load4(self.shape(int(n), 1), slots, self.k, self.v, k, v, stream)
 
     def _read(self, i: int) -> int:
         sid, index, kind = self._stream

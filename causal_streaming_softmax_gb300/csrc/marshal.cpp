@@ -18,6 +18,8 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <utility>
+
 #include "attn.h"
 
 namespace {
@@ -27,6 +29,10 @@ struct {
   decltype(&attn_paged_plan) paged_plan;
   decltype(&attn_paged_store) paged_store;
   decltype(&attn_paged_fwd) paged_fwd;
+  decltype(&attn_paged_append) paged_append;
+  decltype(&attn_paged_append4) paged_append4;
+  decltype(&attn_paged_load4) paged_load4;
+  decltype(&attn_paged_fwd4) paged_fwd4;
 } entry;
 
 enum Name {
@@ -112,6 +118,19 @@ struct Call {
     *s1 = s[1];
     *s2 = s[2];
     return t->data_ptr();
+  }
+
+  // uint8 [pages][kv heads][page size / 8][288], any strides over the first two
+  uint8_t* pool4(PyObject* o, const attn_paged_shape& p, int64_t* s0, int64_t* s1) {
+    const at::Tensor* t = tensor(o, at::kByte);
+    if (!t) return nullptr;
+    const auto z = t->sizes(), s = t->strides();
+    if (z.size() != 4 || z[0] != p.num_pages || z[1] != p.kv_heads || z[2] != p.page_size / 8 ||
+        z[3] != ATTN_UNIT4_BYTES || s[3] != 1 || (z[2] > 1 && s[2] != ATTN_UNIT4_BYTES))
+      return ok = false, nullptr;
+    *s0 = s[0];
+    *s1 = s[1];
+    return static_cast<uint8_t*>(t->data_ptr());
   }
 
   // a contiguous tensor [d0] or, with d1 >= 0, [d0][d1]
@@ -240,17 +259,16 @@ PyObject* paged_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// paged_fwd(shape, q, k_cache, v_cache, table, cu, lens, ws, o, lse)
-PyObject* paged_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 10 || !entry.paged_fwd) return none();
+// What paged_fwd and paged_fwd4 share; pools: the caches of the shape.
+template <class F, class G>
+PyObject* attend(PyObject* const* a, F entry_point, G pools) {
   return guarded([&]() -> PyObject* {
     attn_paged_shape p;
     at::ScalarType type;
     if (!paged_shape(a[0], &p, &type)) return none();
     Call c;
     void* const q = c.rows(a[1], type, p.tokens, p.heads, &p.q_token, &p.q_head);
-    void* const kc = c.pool(a[2], type, p, &p.kc_page, &p.kc_head, &p.kc_row);
-    void* const vc = c.pool(a[3], type, p, &p.vc_page, &p.vc_head, &p.vc_row);
+    const auto cache = pools(c, a + 2, type, &p);
     int32_t* const table = c.ints(a[4], p.batch, p.table_width);
     int32_t* const cu = c.ints(a[5], p.batch + 1ll);
     int32_t* const lens = c.ints(a[6], p.batch);
@@ -264,28 +282,121 @@ PyObject* paged_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* const work = ws->data_ptr();
     const size_t bytes = static_cast<size_t>(ws->numel());
     return launched([&] {
-      return entry.paged_fwd(&p, q, kc, vc, table, cu, lens, work, bytes, o, lse, stream);
+      return entry_point(&p, q, cache.first, cache.second, table, cu, lens, work, bytes, o, lse,
+                         stream);
     });
   });
 }
 
-// bind(packed_fwd, paged_plan, paged_store, paged_fwd): the entry points'
-// addresses in the loaded libattn.so
+std::pair<void*, void*> pools16(Call& c, PyObject* const* a, at::ScalarType type,
+                                attn_paged_shape* p) {
+  void* const k = c.pool(a[0], type, *p, &p->kc_page, &p->kc_head, &p->kc_row);
+  return {k, c.pool(a[1], type, *p, &p->vc_page, &p->vc_head, &p->vc_row)};
+}
+std::pair<uint8_t*, uint8_t*> pools4(Call& c, PyObject* const* a, at::ScalarType,
+                                     attn_paged_shape* p) {
+  uint8_t* const k = c.pool4(a[0], *p, &p->kc_page, &p->kc_head);
+  return {k, c.pool4(a[1], *p, &p->vc_page, &p->vc_head)};
+}
+
+// paged_fwd(shape, q, k_cache, v_cache, table, cu, lens, ws, o, lse)
+PyObject* paged_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 10 || !entry.paged_fwd) return none();
+  return attend(a, entry.paged_fwd, pools16);
+}
+PyObject* paged_fwd4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 10 || !entry.paged_fwd4) return none();
+  return attend(a, entry.paged_fwd4, pools4);
+}
+
+// What paged_append and paged_append4 share; plain: nothing is turned.
+template <class F, class G>
+PyObject* append(PyObject* const* a, F entry_point, G pools, bool plain) {
+  return guarded([&]() -> PyObject* {
+    attn_paged_shape p;
+    at::ScalarType type;
+    if (!paged_shape(a[0], &p, &type)) return none();
+    Call c;
+    void* const k = c.rows(a[2], type, p.tokens, p.kv_heads, &p.k_token, &p.k_head);
+    void* const v = c.rows(a[3], type, p.tokens, p.kv_heads, &p.v_token, &p.v_head);
+    int32_t* const slots = c.ints(a[6], p.tokens);
+    const auto cache = pools(c, a + 10, type, &p);
+    void *q = nullptr, *q_out = nullptr;
+    float *cos_tab = nullptr, *sin_tab = nullptr;
+    int32_t *cu = nullptr, *lens = nullptr;
+    int64_t angles = 0;
+    if (!plain) {
+      q = c.rows(a[1], type, p.tokens, p.heads, &p.q_token, &p.q_head);
+      q_out = c.rows(a[9], type, p.tokens, p.heads, &p.o_token, &p.o_head);
+      const at::Tensor* const t = c.tensor(a[4], at::kFloat);
+      if (!t || t->dim() != 2 || (angles = t->size(0)) < 1 || angles > INT32_MAX) return none();
+      cos_tab = static_cast<float*>(c.dense(a[4], at::kFloat, angles, 32));
+      sin_tab = static_cast<float*>(c.dense(a[5], at::kFloat, angles, 32));
+      cu = c.ints(a[7], p.batch + 1ll);
+      lens = c.ints(a[8], p.batch);
+    }
+    if (!c.ok) return none();
+    void* const stream = c.stream();
+    return launched([&] {
+      return entry_point(&p, q, k, v, cos_tab, sin_tab, static_cast<int32_t>(angles), slots, cu,
+                         lens, q_out, cache.first, cache.second, stream);
+    });
+  });
+}
+
+// paged_append(shape, q, k, v, cos, sin, slots, cu, lens, q_out, k_cache, v_cache)
+PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 12 || !entry.paged_append) return none();
+  return append(a, entry.paged_append, pools16, false);
+}
+PyObject* paged_append4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 12 || !entry.paged_append4) return none();
+  return append(a, entry.paged_append4, pools4, a[4] == Py_None && a[5] == Py_None);
+}
+
+// paged_load4(shape, slots, k_cache, v_cache, k, v)
+PyObject* paged_load4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 6 || !entry.paged_load4) return none();
+  return guarded([&]() -> PyObject* {
+    attn_paged_shape p;
+    at::ScalarType type;
+    if (!paged_shape(a[0], &p, &type)) return none();
+    Call c;
+    int32_t* const slots = c.ints(a[1], p.tokens);
+    const auto cache = pools4(c, a + 2, type, &p);
+    void* const k = c.rows(a[4], type, p.tokens, p.kv_heads, &p.k_token, &p.k_head);
+    void* const v = c.rows(a[5], type, p.tokens, p.kv_heads, &p.v_token, &p.v_head);
+    if (!c.ok) return none();
+    void* const stream = c.stream();
+    return launched([&] {
+      return entry.paged_load4(&p, slots, cache.first, cache.second, k, v, stream);
+    });
+  });
+}
+
+// bind(packed_fwd, paged_plan, paged_store, paged_fwd, paged_append, paged_append4,
+// paged_load4, paged_fwd4): the entry points' addresses in the loaded libattn.so
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* p[4] = {};
-  for (Py_ssize_t i = 0; i < n && i < 4; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+  void* p[8] = {};
+  for (Py_ssize_t i = 0; i < n && i < 8; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) return nullptr;
   entry.packed_fwd = reinterpret_cast<decltype(entry.packed_fwd)>(p[0]);
   entry.paged_plan = reinterpret_cast<decltype(entry.paged_plan)>(p[1]);
   entry.paged_store = reinterpret_cast<decltype(entry.paged_store)>(p[2]);
   entry.paged_fwd = reinterpret_cast<decltype(entry.paged_fwd)>(p[3]);
+  entry.paged_append = reinterpret_cast<decltype(entry.paged_append)>(p[4]);
+  entry.paged_append4 = reinterpret_cast<decltype(entry.paged_append4)>(p[5]);
+  entry.paged_load4 = reinterpret_cast<decltype(entry.paged_load4)>(p[6]);
+  entry.paged_fwd4 = reinterpret_cast<decltype(entry.paged_fwd4)>(p[7]);
   Py_RETURN_NONE;
 }
 
 #define METHOD(f) \
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr }
-PyMethodDef methods[] = {METHOD(bind),        METHOD(packed_fwd), METHOD(paged_plan),
-                         METHOD(paged_store), METHOD(paged_fwd),  {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(bind),          METHOD(packed_fwd),   METHOD(paged_plan),
+                         METHOD(paged_store),   METHOD(paged_fwd),    METHOD(paged_append),
+                         METHOD(paged_append4), METHOD(paged_load4),  METHOD(paged_fwd4),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr,               nullptr,    nullptr, nullptr};
 

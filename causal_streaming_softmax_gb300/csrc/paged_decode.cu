@@ -37,6 +37,7 @@
 // parts.
 #include <math.h>
 
+#include "serve_decode.cuh"
 #include "serve_index.h"
 #include "serve_internal.h"
 #include "serve_parts.cuh"
@@ -73,91 +74,6 @@ static_assert(Split::kSmemPre + 8 * (Split::kMaxBatch + 1) + 1024 <= 227 * 1024 
                   Whole::kSmemPre + 8 * (Whole::kMaxBatch + 1) + 1024 <= 227 * 1024 - 2048,
               "shared memory of a block");
 constexpr int kLd = 68;  // floats a row of the joining buffer (bank spread)
-
-struct DecodeArgs {
-  int batch, tokens, H, Hkv, G, ntok, max_new, pages, width, shift;
-  float c;
-  const int32_t *cu, *lens, *table;
-  RowsArg o;
-  float* lse;
-  PartArgs part;
-  uint32_t* err;
-  uint64_t wait_ns;
-};
-
-// A request's rows and keys; n_new 0 for one that this kernel does not take.
-struct Request {
-  int q0, n_new, n_keys;
-};
-
-__device__ __forceinline__ Request request_at(const DecodeArgs& a, int i, bool* bad) {
-  const RowRange r = row_range(a.cu[i], a.cu[i + 1], a.tokens);
-  bool b;
-  Request q{r.begin, r.end - r.begin, key_count(a.lens[i], a.width, a.shift, &b)};
-  *bad = r.bad || b || q.n_new > a.max_new;
-  if (q.n_new > min(a.ntok, a.max_new)) q.n_new = 0;
-  return q;
-}
-
-template <class C>
-__device__ __forceinline__ int tiles_of(int n_keys) {
-  return n_keys <= 0 ? 1 : (n_keys - 1) / C::kTileKeys + 1;
-}
-
-// A place in the tile list: tile t0 of nt of a request and K/V head.
-struct Place {
-  Request r;
-  int req, kv, t0, nt;
-};
-
-// What the producer hands the consumers beside an item's Q: they read no device
-// array themselves, so that the warps agree on an item whatever those hold.
-struct Item {
-  Request r;
-  int kv, t0, t1;
-  int whole;  // its rows are finished here; else a part
-};
-
-// The place at position pos.  pre[i] counts the tiles (whole: the items) of one
-// head of the requests before i.
-template <class C>
-__device__ __forceinline__ Place place_at(const DecodeArgs& a, const long long* pre,
-                                          long long pos) {
-  int lo = 0, hi = a.batch;  // the last i with pre[i] * Hkv <= pos: never an empty request
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] * a.Hkv <= pos)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  Place p;
-  p.req = lo - 1;
-  const long long off = pos - pre[p.req] * a.Hkv;
-  bool b;
-  p.r = request_at(a, p.req, &b);
-  p.nt = tiles_of<C>(p.r.n_keys);
-  const long long kv = C::kWhole ? off : quot(off, p.nt);
-  p.t0 = C::kWhole ? 0 : (int)(off - kv * p.nt);
-  p.kv = (int)min(kv, a.Hkv - 1ll);  // less already, unless lens changed meanwhile
-  return p;
-}
-
-// The place behind an item: the next head or the next request with rows.
-// Called only where the list goes on; never past the last request, also where
-// lens changed meanwhile.
-template <class C>
-__device__ __forceinline__ void next_place(const DecodeArgs& a, const long long* pre, Place* p) {
-  p->t0 = 0;
-  if (++p->kv < a.Hkv) return;
-  p->kv = 0;
-  do {
-    p->req = min(p->req + 1, a.batch - 1);
-  } while (pre[p->req + 1] == pre[p->req] && p->req + 1 < a.batch);
-  bool b;
-  p->r = request_at(a, p->req, &b);
-  p->nt = tiles_of<C>(p->r.n_keys);
-}
 
 template <bool BF16, class C>
 __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
@@ -202,33 +118,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kWhole ? 1 : 2)
   fence_proxy_async_shared();
   griddep_wait();
 
-  // tiles of one head before each request, every block for itself
-  {
-    const int per = (a.batch + kThreads - 1) / kThreads;
-    const int i0 = tid * per, i1 = min(a.batch, i0 + per);
-    long long sum = 0;
-    bool bad = false;
-    for (int i = i0; i < i1; ++i) {
-      bool b;
-      const Request r = request_at(a, i, &b);
-      bad |= b;
-      s_pre[i + 1] = sum += r.n_new > 0 ? (C::kWhole ? 1 : tiles_of<C>(r.n_keys)) : 0;
-    }
-    if (bad && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
-    long long upto = sum;
-#pragma unroll
-    for (int by = 1; by < 32; by <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, by);
-      if (lane >= by) upto += x;
-    }
-    if (lane == 31) s_scan[warp] = upto;
-    __syncthreads();
-    long long before = upto - sum;
-    for (int w = 0; w < warp; ++w) before += s_scan[w];
-    for (int i = i0; i < i1; ++i) s_pre[i + 1] += before;
-    if (tid == 0) s_pre[0] = 0;
-    __syncthreads();
-  }
+  tiles_before_each<C>(a, s_pre, s_scan);
   const Share share = share_of(s_pre[a.batch] * a.Hkv, C::kWhole ? 1 : a.part.min_tiles, gridDim.x, blockIdx.x);
 
   if (warp == kConsumers) {

@@ -138,6 +138,7 @@ PartArgs parts_at(void* ws, size_t blocks, int rows, int min_tiles) {
 // 1 / 2 / 4: one request of 100 keys 6.6 / 5.8 / 7.7, of 777 7.8 / 7.8 / 9.0, of
 // 4000 11.2 / 9.5 / 10.6, eight of 256 7.7 / 7.9 / 7.3, 64 of 60 7.8 / 7.7 / 11.1.
 constexpr int kLeastFew = 2, kLeastRows = 2;
+constexpr int kLeastFew4 = 1;  // 256-key tiles of a 4-bit cache
 
 }  // namespace
 
@@ -149,7 +150,7 @@ size_t paged_workspace_bytes(const PagedDims& d) {
 
 int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
                      const PoolArg& vc, const int32_t* table, const int32_t* cu,
-                     const int32_t* lens, void* ws, const RowsArg& o, float* lse,
+                     const int32_t* lens, void* ws, bool four, const RowsArg& o, float* lse,
                      cudaStream_t stream) {
   const int ntok = decode_tokens(d.G);
   const int sms = ctx.sm_count < kMaxSm ? ctx.sm_count : kMaxSm;
@@ -157,16 +158,18 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
   PartArgs few{}, rows{};
   int n_few = 0, n_rows = 0, rc;
   if (ntok > 0) {
-    few = parts_at(at, 2 * kMaxSm, kDecodeRows, kLeastFew);
+    few = parts_at(at, 2 * kMaxSm, kDecodeRows, four ? kLeastFew4 : kLeastFew);
     at += parts_bytes(2 * kMaxSm, kDecodeRows);
-    rc = launch_paged_decode(d, ctx, q, kc, vc, table, cu, lens, few, 2 * sms, o, lse, stream);
+    rc = (four ? launch_paged_decode4 : launch_paged_decode)(d, ctx, q, kc, vc, table, cu, lens,
+                                                             few, 2 * sms, o, lse, stream);
     if (rc != ATTN_OK) return rc;
-    if (!decode_whole(d, ctx.sm_count)) n_few = 2 * sms;
+    if (!(four ? decode4_whole(d) : decode_whole(d, ctx.sm_count))) n_few = 2 * sms;
   }
   if (d.max_new > ntok) {
     rows = parts_at(at, kMaxSm, kItemRows, kLeastRows);
     n_rows = sms;
-    rc = launch_paged_rows(d, ctx, q, kc, vc, table, cu, lens, rows, n_rows, ntok, o, lse, stream);
+    rc = launch_paged_rows(d, ctx, q, kc, vc, table, cu, lens, rows, n_rows, ntok,
+                           four, o, lse, stream);
     if (rc != ATTN_OK) return rc;
   }
   if (n_few + n_rows == 0) return ATTN_OK;

@@ -1,0 +1,147 @@
+// pool4.cuh - the rows of a 4-bit cache.
+//
+// A row of 64 channels is 32 bytes of codes and two 16-bit scales.  Byte c holds
+// channel c in its low half and channel c + 32 in its high half, each as code + 8
+// with code in -8..7; the value is code * scale of the channel's group (0..31,
+// 32..63).  A scale has three significant bits fewer than the cache's type, so
+// that code * scale is exact in that type: the attention kernels form the 16-bit
+// operands of their matrix products without rounding, and a row read back is the
+// row that they see.
+//
+// Eight rows make a unit of 288 bytes, their codes before their scales: any run of
+// units in a page is one contiguous copy, and the shared-memory layout of a key
+// tile does not depend on the page size.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+#include "sm103.cuh"
+#include "warp_mma.cuh"
+
+namespace css {
+
+constexpr int kUnitBytes = 288, kUnitScales = 256;
+
+// Bytes of a page of one K/V head.
+__host__ __device__ constexpr int page4_bytes(int shift) { return (kUnitBytes / 8) << shift; }
+
+// Where row r of a page has its codes; its scales.
+__device__ __forceinline__ int code_at(int r) { return (r >> 3) * kUnitBytes + (r & 7) * 32; }
+__device__ __forceinline__ int scale_at(int r) {
+  return (r >> 3) * kUnitBytes + kUnitScales + (r & 7) * 4;
+}
+
+// max and min that keep a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// The scale of a group with the largest value mx and the smallest mn, as 16 bits of
+// the type: -e / 8 for the extremum e, which then has the code -8, to nearest (its
+// code comes out between -8.25 and -7.75, so cutting it off at -8 costs less than a
+// rounding).  The largest scale keeps 8 s (binary16) and 24 s (bfloat16, where the
+// attention kernels form that) finite.  A group that holds an infinity or a NaN has
+// the scale NaN and reads as NaN throughout.
+template <bool BF16>
+__device__ __forceinline__ uint32_t group_scale(float mx, float mn) {
+  constexpr int kDrop = BF16 ? 19 : 16;  // significand bits left out, of 24
+  constexpr float kMost = BF16 ? 0x1p123f : 8160.f;
+  const float e = (mx > -mn ? -mx : -mn) * 0.125f + 0.f;  // a group of zeros: +0
+  const float s = __uint_as_float((__float_as_uint(e) + (1u << (kDrop - 1))) & (~0u << kDrop));
+  const uint32_t h = pack2<BF16>(fminf(fmaxf(s, -kMost), kMost), 0.f) & 0xffffu;
+  return fabsf(mx) < INFINITY && fabsf(mn) < INFINITY ? h : (BF16 ? 0x7fc0u : 0x7e00u);
+}
+
+// code + 8 of x in a group of scale s; 8 where the group is zero or NaN.  The
+// quotient is rounded correctly, as a tie between two codes is common with so few
+// bits on both sides and goes to the even one.
+__device__ __forceinline__ uint32_t code_of(float x, float s) {
+  const float q = fminf(fmaxf(rintf(__fdiv_rn(x, s)), -8.f), 7.f);
+  return s != 0.f && s == s ? (uint32_t)((int)q + 8) : 8u;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (BF16)
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  if (BF16)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// The bits of 16 + code of the half bytes that `shift` brings to bits 3..6 of each
+// 16-bit half, as bfloat16.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  return (w & 0x00780078u) | 0x41804180u;
+}
+
+// A word of codes as pairs of operands: the low and high halves of bytes 0 and 2,
+// then of bytes 1 and 3.  binary16: code' * 2^-24 and code' * 2^-20; bfloat16:
+// 16 + code' (code' = code + 8).
+template <bool BF16>
+__device__ __forceinline__ void raw_codes(uint32_t w, uint32_t& lo0, uint32_t& hi0, uint32_t& lo1,
+                                          uint32_t& hi1) {
+  if (BF16) {
+    lo0 = codes_bf16(w << 3);
+    hi0 = codes_bf16(w >> 1);
+    lo1 = codes_bf16(w >> 5);
+    hi1 = codes_bf16(w >> 9);
+  } else {
+    const uint32_t v = w >> 8;
+    lo0 = w & 0x000f000fu;
+    hi0 = w & 0x00f000f0u;
+    lo1 = v & 0x000f000fu;
+    hi1 = v & 0x00f000f0u;
+  }
+}
+// What stands in a product for code -8, low and high half, and what a score is
+// multiplied by beside the scale.
+template <bool BF16>
+struct Raw {
+  static constexpr float kLoZero = BF16 ? 24.f : 0x1p-21f, kHiZero = BF16 ? 24.f : 0x1p-17f;
+  static constexpr float kLoUnit = BF16 ? 1.f : 0x1p24f, kHiUnit = BF16 ? 1.f : 0x1p20f;
+};
+
+// The same word as code * scale; the scales are those of the two keys of a pair.
+template <bool BF16>
+__device__ __forceinline__ void scaled_codes(uint32_t w, uint32_t s_lo, uint32_t s_hi, uint32_t& lo0,
+                                             uint32_t& hi0, uint32_t& lo1, uint32_t& hi1) {
+  if (BF16) {
+    // (16 + code') s - 24 s: both exact, as s has five significant bits
+    const uint32_t z_lo = mul2<true>(s_lo, 0xc1c0c1c0u), z_hi = mul2<true>(s_hi, 0xc1c0c1c0u);
+    raw_codes<true>(w, lo0, hi0, lo1, hi1);
+    lo0 = fma2<true>(lo0, s_lo, z_lo);
+    hi0 = fma2<true>(hi0, s_hi, z_hi);
+    lo1 = fma2<true>(lo1, s_lo, z_lo);
+    hi1 = fma2<true>(hi1, s_hi, z_hi);
+  } else {
+    // 1024 + code' - 1032 and (1024 + 16 code') / 16 - 72, then times s
+    constexpr uint32_t kOne = 0x3c003c00u, kSixteenth = 0x2c002c00u, kM = 0x64006400u,
+                       k1032 = 0xe408e408u, k72 = 0xd480d480u;
+    const uint32_t v = w >> 8;
+    lo0 = mul2<false>(fma2<false>((w & 0x000f000fu) | kM, kOne, k1032), s_lo);
+    hi0 = mul2<false>(fma2<false>((w & 0x00f000f0u) | kM, kSixteenth, k72), s_hi);
+    lo1 = mul2<false>(fma2<false>((v & 0x000f000fu) | kM, kOne, k1032), s_lo);
+    hi1 = mul2<false>(fma2<false>((v & 0x00f000f0u) | kM, kSixteenth, k72), s_hi);
+  }
+}
+
+}  // namespace css

@@ -102,6 +102,117 @@ int pools(const attn_paged_shape* s, const void* kc, const void* vc, PoolArg* k,
   return ATTN_OK;
 }
 
+// A stride of a 4-bit pool, in bytes.
+bool fix_stride4(int64_t* s, int64_t dim, int64_t page) {
+  if (dim <= 1) {
+    *s = page;
+    return true;
+  }
+  return *s >= page && *s % 16 == 0 && *s < (1ll << 40);
+}
+
+int pools4(const attn_paged_shape* s, int shift, const void* kc, const void* vc, PoolArg* k,
+           PoolArg* v) {
+  *k = PoolArg{const_cast<void*>(kc), s->kc_page, s->kc_head, 0};
+  *v = PoolArg{const_cast<void*>(vc), s->vc_page, s->vc_head, 0};
+  const int64_t page = 36ll << shift;
+  for (PoolArg* p : {k, v}) {
+    int64_t pg = p->pg, h = p->h;
+    if (!fix_stride4(&pg, s->num_pages, page) || !fix_stride4(&h, s->kv_heads, page))
+      return ATTN_ERR_SHAPE;
+    // no two pages of a head share a byte
+    if (s->num_pages > 1 && s->kv_heads > 1 && pg < (s->kv_heads - 1) * h + page &&
+        h < (s->num_pages - 1) * pg + page)
+      return ATTN_ERR_SHAPE;
+    p->pg = pg, p->h = h;
+  }
+  return ATTN_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// attn_paged_append and attn_paged_append4.
+int append(const attn_paged_shape* s, bool four, const void* q, const void* k, const void* v,
+           const float* cos_tab, const float* sin_tab, int32_t angles, const int32_t* slots,
+           const int32_t* cu, const int32_t* lens, void* q_out, void* k_cache, void* v_cache,
+           void* stream) {
+  PagedDims d;
+  int rc = validate_paged(s, &d);
+  if (rc != ATTN_OK) return rc;
+  const bool rotate = !four || cos_tab || sin_tab;
+  if ((rc = validate_heads(rotate ? s->heads : s->kv_heads, s->kv_heads, s->head_dim,
+                           s->dtype)) != ATTN_OK)
+    return rc;
+  d.Hkv = s->kv_heads;
+  d.H = rotate ? s->heads : 0;
+  d.bf16 = s->dtype == ATTN_BF16;
+  int64_t st[8] = {s->k_token, s->k_head, s->v_token, s->v_head,
+                   s->q_token, s->q_head, s->o_token, s->o_head};
+  for (int i = 0; i < (rotate ? 8 : 4); ++i)
+    if (!fix_stride(&st[i], (i & 1) ? (i > 3 ? s->heads : s->kv_heads) : s->tokens))
+      return ATTN_ERR_SHAPE;
+  if (rotate && (angles < 1 || !rows_apart(st[6], st[7], s->tokens, s->heads)))
+    return ATTN_ERR_SHAPE;
+  AppendArgs a{};
+  if (four) {
+    if ((rc = pools4(s, d.shift, k_cache, v_cache, &a.kc, &a.vc)) != ATTN_OK) return rc;
+  } else {
+    if ((rc = pools(s, k_cache, v_cache, &a.kc, &a.vc)) != ATTN_OK) return rc;
+    if (!pool_apart(a.kc, d.pages, d.Hkv, 1 << d.shift) ||
+        !pool_apart(a.vc, d.pages, d.Hkv, 1 << d.shift))
+      return ATTN_ERR_SHAPE;
+  }
+  if (s->tokens == 0) return ATTN_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache) return ATTN_ERR_NULL;
+  if (rotate && (!q || !cos_tab || !sin_tab || !cu || !lens || !q_out)) return ATTN_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(slots))
+    return ATTN_ERR_ALIGN;
+  if (rotate && (!aligned16(q) || !aligned16(q_out) || !aligned16(cos_tab) ||
+                 !aligned16(sin_tab) || !aligned4(cu) || !aligned4(lens)))
+    return ATTN_ERR_ALIGN;
+  // q is turned in place row by row, or lies elsewhere
+  if (rotate && q == q_out && (st[4] != st[6] || st[5] != st[7])) return ATTN_ERR_SHAPE;
+  DevCtx ctx;
+  if ((rc = device_context(&ctx)) != ATTN_OK) return rc;
+  a.k = RowsArg{const_cast<void*>(k), st[0], st[1]};
+  a.v = RowsArg{const_cast<void*>(v), st[2], st[3]};
+  a.q = RowsArg{const_cast<void*>(q), st[4], st[5]};
+  a.q_out = RowsArg{q_out, st[6], st[7]};
+  a.cos_tab = cos_tab, a.sin_tab = sin_tab;
+  a.angles = angles;
+  a.slots = slots, a.cu = cu, a.lens = lens;
+  return launch_paged_append(d, ctx, a, rotate, four, static_cast<cudaStream_t>(stream));
+}
+
+// attn_paged_fwd and attn_paged_fwd4.
+int attend(const attn_paged_shape* s, bool four, const void* q, const void* k_cache,
+           const void* v_cache, const int32_t* table, const int32_t* cu, const int32_t* lens,
+           void* ws, size_t ws_bytes, void* o, float* lse, void* stream) {
+  PagedDims d;
+  int rc = validate_attend(s, &d);
+  if (rc != ATTN_OK) return rc;
+  int64_t st[4] = {s->q_token, s->q_head, s->o_token, s->o_head};
+  for (int i = 0; i < 4; ++i)
+    if (!fix_stride(&st[i], (i & 1) ? s->heads : s->tokens)) return ATTN_ERR_SHAPE;
+  if (!rows_apart(st[2], st[3], s->tokens, s->heads)) return ATTN_ERR_SHAPE;
+  PoolArg kc, vc;
+  rc = four ? pools4(s, d.shift, k_cache, v_cache, &kc, &vc) : pools(s, k_cache, v_cache, &kc, &vc);
+  if (rc != ATTN_OK) return rc;
+  if (s->tokens == 0) return ATTN_OK;
+  if (!q || !k_cache || !v_cache || !table || !cu || !lens || !ws || !o) return ATTN_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(ws) ||
+      !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(table) & 3) ||
+      (reinterpret_cast<uintptr_t>(cu) & 3) || (reinterpret_cast<uintptr_t>(lens) & 3))
+    return ATTN_ERR_ALIGN;
+  if (ws_bytes < paged_workspace_bytes(d)) return ATTN_ERR_WORKSPACE;
+  DevCtx ctx;
+  if ((rc = device_context(&ctx)) != ATTN_OK) return rc;
+  return launch_paged_fwd(d, ctx, RowsArg{const_cast<void*>(q), st[0], st[1]}, kc, vc, table, cu,
+                          lens, ws, four, RowsArg{o, st[2], st[3]}, lse,
+                          static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 }  // namespace css
 
@@ -200,6 +311,50 @@ int attn_paged_store(const attn_paged_shape* s, const void* k, const void* v,
                             static_cast<cudaStream_t>(stream));
 }
 
+int attn_paged_append(const attn_paged_shape* s, const void* q, const void* k, const void* v,
+                      const float* cos_tab, const float* sin_tab, int32_t angles,
+                      const int32_t* slots, const int32_t* cu, const int32_t* lens, void* q_out,
+                      void* k_cache, void* v_cache, void* stream) {
+  return append(s, false, q, k, v, cos_tab, sin_tab, angles, slots, cu, lens, q_out, k_cache,
+                v_cache, stream);
+}
+
+int attn_paged_append4(const attn_paged_shape* s, const void* q, const void* k, const void* v,
+                       const float* cos_tab, const float* sin_tab, int32_t angles,
+                       const int32_t* slots, const int32_t* cu, const int32_t* lens, void* q_out,
+                       uint8_t* k_cache, uint8_t* v_cache, void* stream) {
+  return append(s, true, q, k, v, cos_tab, sin_tab, angles, slots, cu, lens, q_out, k_cache,
+                v_cache, stream);
+}
+
+int attn_paged_load4(const attn_paged_shape* s, const int32_t* slots, const uint8_t* k_cache,
+                     const uint8_t* v_cache, void* k, void* v, void* stream) {
+  PagedDims d;
+  int rc = validate_paged(s, &d);
+  if (rc != ATTN_OK) return rc;
+  if ((rc = validate_heads(s->kv_heads, s->kv_heads, s->head_dim, s->dtype)) != ATTN_OK)
+    return rc;
+  d.Hkv = s->kv_heads;
+  d.bf16 = s->dtype == ATTN_BF16;
+  int64_t st[4] = {s->k_token, s->k_head, s->v_token, s->v_head};
+  for (int i = 0; i < 4; ++i)
+    if (!fix_stride(&st[i], (i & 1) ? s->kv_heads : s->tokens)) return ATTN_ERR_SHAPE;
+  if (!rows_apart(st[0], st[1], s->tokens, s->kv_heads) ||
+      !rows_apart(st[2], st[3], s->tokens, s->kv_heads))
+    return ATTN_ERR_SHAPE;
+  PoolArg kc, vc;
+  if ((rc = pools4(s, d.shift, k_cache, v_cache, &kc, &vc)) != ATTN_OK) return rc;
+  if (s->tokens == 0) return ATTN_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache) return ATTN_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(slots))
+    return ATTN_ERR_ALIGN;
+  DevCtx ctx;
+  if ((rc = device_context(&ctx)) != ATTN_OK) return rc;
+  return launch_paged_load4(d, ctx, kc, vc, slots, RowsArg{k, st[0], st[1]},
+                            RowsArg{v, st[2], st[3]}, static_cast<cudaStream_t>(stream));
+}
+
 size_t attn_paged_workspace_bytes(const attn_paged_shape* s) {
   PagedDims d;
   if (validate_attend(s, &d) != ATTN_OK) return 0;
@@ -210,27 +365,14 @@ int attn_paged_fwd(const attn_paged_shape* s, const void* q, const void* k_cache
                    const void* v_cache, const int32_t* table, const int32_t* cu,
                    const int32_t* lens, void* ws, size_t ws_bytes, void* o, float* lse,
                    void* stream) {
-  PagedDims d;
-  int rc = validate_attend(s, &d);
-  if (rc != ATTN_OK) return rc;
-  int64_t st[4] = {s->q_token, s->q_head, s->o_token, s->o_head};
-  for (int i = 0; i < 4; ++i)
-    if (!fix_stride(&st[i], (i & 1) ? s->heads : s->tokens)) return ATTN_ERR_SHAPE;
-  if (!rows_apart(st[2], st[3], s->tokens, s->heads)) return ATTN_ERR_SHAPE;
-  PoolArg kc, vc;
-  if ((rc = pools(s, k_cache, v_cache, &kc, &vc)) != ATTN_OK) return rc;
-  if (s->tokens == 0) return ATTN_OK;
-  if (!q || !k_cache || !v_cache || !table || !cu || !lens || !ws || !o) return ATTN_ERR_NULL;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(ws) ||
-      !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(table) & 3) ||
-      (reinterpret_cast<uintptr_t>(cu) & 3) || (reinterpret_cast<uintptr_t>(lens) & 3))
-    return ATTN_ERR_ALIGN;
-  if (ws_bytes < paged_workspace_bytes(d)) return ATTN_ERR_WORKSPACE;
-  DevCtx ctx;
-  if ((rc = device_context(&ctx)) != ATTN_OK) return rc;
-  return launch_paged_fwd(d, ctx, RowsArg{const_cast<void*>(q), st[0], st[1]}, kc, vc, table, cu,
-                          lens, ws, RowsArg{o, st[2], st[3]}, lse,
-                          static_cast<cudaStream_t>(stream));
+  return attend(s, false, q, k_cache, v_cache, table, cu, lens, ws, ws_bytes, o, lse, stream);
+}
+
+int attn_paged_fwd4(const attn_paged_shape* s, const void* q, const uint8_t* k_cache,
+                    const uint8_t* v_cache, const int32_t* table, const int32_t* cu,
+                    const int32_t* lens, void* ws, size_t ws_bytes, void* o, float* lse,
+                    void* stream) {
+  return attend(s, true, q, k_cache, v_cache, table, cu, lens, ws, ws_bytes, o, lse, stream);
 }
 
 }  // extern "C"

@@ -57,7 +57,13 @@ int launch_paged_decode(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
 int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
                       const PoolArg& vc, const int32_t* table, const int32_t* cu,
                       const int32_t* lens, const PartArgs& part, int blocks, int skip,
-                      const RowsArg& o, float* lse, cudaStream_t stream);
+                      bool four, const RowsArg& o, float* lse, cudaStream_t stream);
+// The same over a 4-bit cache (the pools' strides in bytes).
+bool decode4_whole(const PagedDims& d);
+int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
+                         const PoolArg& kc, const PoolArg& vc, const int32_t* table,
+                         const int32_t* cu, const int32_t* lens, const PartArgs& part, int blocks,
+                         const RowsArg& o, float* lse, cudaStream_t stream);
 
 // Lets `kernel` (known by an index of its own) use `bytes` of dynamic shared
 // memory on the current device; set once a device.
@@ -70,6 +76,12 @@ enum {
   kSmemPackedBf16,
   kSmemRowsF16,
   kSmemRowsBf16,
+  kSmemDecode4F16,
+  kSmemDecode4Bf16,
+  kSmemDecode4WideF16,
+  kSmemDecode4WideBf16,
+  kSmemRows4F16,
+  kSmemRows4Bf16,
   kSmemKernels
 };
 int allow_smem(int which, const void* kernel, size_t bytes);
@@ -90,10 +102,26 @@ int launch_paged_plan(const PagedDims& d, const DevCtx& ctx, const int32_t* cach
 int launch_paged_store(const PagedDims& d, const DevCtx& ctx, const RowsArg& k, const RowsArg& v,
                        const int32_t* slots, const PoolArg& kc, const PoolArg& vc,
                        cudaStream_t stream);
+// What the append reads and writes; sizes are the launcher's to fill in.
+struct AppendArgs {
+  RowsArg q, k, v, q_out;
+  const float *cos_tab, *sin_tab;  // [angles][32]
+  int angles;
+  const int32_t *slots, *cu, *lens;
+  PoolArg kc, vc;  // strides in elements (16-bit pools) or bytes (4-bit)
+  int tokens, batch, H, Hkv, pages, shift;
+  int per, parts;  // rows of a token that a warp takes, warps a token
+  uint32_t* err;
+};
+int launch_paged_append(const PagedDims& d, const DevCtx& ctx, AppendArgs args, bool rotate,
+                        bool four, cudaStream_t stream);
+int launch_paged_load4(const PagedDims& d, const DevCtx& ctx, const PoolArg& kc, const PoolArg& vc,
+                       const int32_t* slots, const RowsArg& k, const RowsArg& v,
+                       cudaStream_t stream);
 size_t paged_workspace_bytes(const PagedDims& d);
 int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
                      const PoolArg& vc, const int32_t* table, const int32_t* cu,
-                     const int32_t* lens, void* ws, const RowsArg& o, float* lse,
+                     const int32_t* lens, void* ws, bool four, const RowsArg& o, float* lse,
                      cudaStream_t stream);
 
 }  // namespace css

@@ -62,6 +62,7 @@
 // is formed by the row's own thread over the keys that it sees.
 #include <math.h>
 
+#include "pool4.cuh"
 #include "serve_index.h"
 #include "serve_internal.h"
 #include "serve_parts.cuh"
@@ -71,7 +72,10 @@
 namespace css {
 namespace {
 
-constexpr int kNT = 3;   // row tiles of a work item
+// What a kernel reads: packed prompts, a paged cache, a paged cache of 4 bits.
+enum Mode { kPacked, kPaged, kPaged4 };
+constexpr int kMaxNT = 3;  // row tiles of a work item, at most
+__host__ __device__ constexpr int row_tiles(int mode) { return mode == kPaged4 ? 2 : kMaxNT; }
 constexpr int kBN = 64;  // keys a tile
 constexpr int kStages = 6;
 constexpr int kThreads = 512;
@@ -79,15 +83,20 @@ constexpr float kSlack = 8.f;
 constexpr uint32_t kTileBytes = 128 * 128;
 constexpr uint32_t kHalfBytes = kBN * 128;         // K (or V) of a stage
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
-constexpr uint32_t kSmemStage0 = 2 * kNT * kTileBytes;  // behind two Q buffers
+constexpr uint32_t kSmemStage0 = 2 * kMaxNT * kTileBytes;  // behind two Q buffers
+// 4 bits: packed rows lie where the third row tile's Q would
+constexpr int kRaw = 6;
+constexpr uint32_t kRawHalf = kBN / 8 * kUnitBytes;  // K (or V) of a raw stage
+constexpr uint32_t kSmemRaw = 2 * row_tiles(kPaged4) * kTileBytes;
+static_assert(kSmemRaw + kRaw * 2 * kRawHalf <= kSmemStage0, "raw stages");
 constexpr uint32_t kSmemBar = kSmemStage0 + kStages * kStageBytes;
 constexpr uint32_t kSmemPre = kSmemBar + 512;  // paged: prefix of tiles
 
 constexpr uint32_t kColS = 0;                // + 64 t
-constexpr uint32_t kColP = kColS + 64 * kNT;  // + 32 t
-constexpr uint32_t kColO = kColP + 32 * kNT;  // + 64 t
+constexpr uint32_t kColP = kColS + 64 * kMaxNT;  // + 32 t
+constexpr uint32_t kColO = kColP + 32 * kMaxNT;  // + 64 t
 constexpr uint32_t kTmemCols = 512;
-static_assert(kColO + 64 * kNT <= kTmemCols, "tensor memory");
+static_assert(kColO + 64 * kMaxNT <= kTmemCols, "tensor memory");
 
 enum {
   BAR_Q = 0,                             // [Q buffer] the item's Q tiles landed
@@ -95,16 +104,18 @@ enum {
   BAR_KV_FULL = BAR_Q_FREE + 2,          // [stage]
   BAR_KV_EMPTY = BAR_KV_FULL + kStages,  // [stage] every row tile's products done
   BAR_S_FULL = BAR_KV_EMPTY + kStages,   // [t]
-  BAR_S_FREE = BAR_S_FULL + kNT,         // [t] read by the softmax (128 threads)
-  BAR_P_FULL = BAR_S_FREE + kNT,         // [t] P stored, O rescaled (128 threads)
-  BAR_P_FREE = BAR_P_FULL + kNT,         // [t] O += P V done
-  BAR_O_FREE = BAR_P_FREE + kNT,         // [t] the epilogue has read O (128 threads)
-  BAR_V_OK = BAR_O_FREE + kNT,           // [t] rows of V looked at (128 threads)
-  BAR_UNIT = BAR_V_OK + kNT,             // [item buffer] description written
-  BAR_UNIT_FREE = BAR_UNIT + 2,          // [item buffer] read by 5 kNT warps
+  BAR_S_FREE = BAR_S_FULL + kMaxNT,         // [t] read by the softmax (128 threads)
+  BAR_P_FULL = BAR_S_FREE + kMaxNT,         // [t] P stored, O rescaled (128 threads)
+  BAR_P_FREE = BAR_P_FULL + kMaxNT,         // [t] O += P V done
+  BAR_O_FREE = BAR_P_FREE + kMaxNT,         // [t] the epilogue has read O (128 threads)
+  BAR_V_OK = BAR_O_FREE + kMaxNT,           // [t] rows of V looked at (128 threads)
+  BAR_UNIT = BAR_V_OK + kMaxNT,             // [item buffer] description written
+  BAR_UNIT_FREE = BAR_UNIT + 2,          // [item buffer] read by 5 warps a row tile, and those that unpack
   BAR_MMA_DONE = BAR_UNIT_FREE + 2,      // every product of the block done (kNT commits)
   BAR_TAKE = BAR_MMA_DONE + 1,           // an answer of take_block
-  BAR_COUNT
+  BAR_RAW_FULL = BAR_TAKE + 1,           // [raw stage] 4-bit rows landed
+  BAR_RAW_EMPTY = BAR_RAW_FULL + kRaw,   // [raw stage] unpacked (128 threads)
+  BAR_COUNT = BAR_RAW_EMPTY + kRaw
 };
 static_assert(BAR_COUNT * 8 <= 512, "barrier area");
 
@@ -116,8 +127,8 @@ struct Unit {
   int kv;
   int kbeg;      // packed: row of key 0
   int j0, nj;    // key tiles j0 .. j0 + nj - 1
-  int t0[kNT], t1[kNT];          // those of row tile t: [t0, t1), counted from j0
-  int lo_max[kNT], hi_min[kNT];  // keys that every row of tile t sees: [lo_max, hi_min)
+  int t0[kMaxNT], t1[kMaxNT];    // those of row tile t: [t0, t1), counted from j0
+  int lo_max[kMaxNT], hi_min[kMaxNT];  // keys that every row of tile t sees: [lo_max, hi_min)
   int kend;      // no row sees a key from here on
   int s0, s1;    // packed: first and last sequence in the window
   int lim;       // paged: keys that the first token of the item sees
@@ -135,6 +146,7 @@ struct TileArgs {
   PartArgs part;
   uint32_t* err;
   uint64_t wait_ns;
+  PoolArg kc, vc;  // 4 bits
 };
 
 __device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
@@ -166,6 +178,7 @@ struct Place {
 
 // The place at position pos of the list; pre[i] counts the tiles of one head
 // of the requests before i.  Called by a whole warp.
+template <int kNT>
 __device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pre, long long pos) {
   int lo = 0, hi = a.batch;
   while (lo < hi) {
@@ -203,6 +216,7 @@ __device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pr
 // The place behind a block: the next block, head or request with rows.  Called
 // only where the list goes on; never past the last request, also where lens
 // changed meanwhile.
+template <int kNT>
 __device__ __forceinline__ void next_block(const TileArgs& a, Place* p) {
   p->t0 = 0;
   if (++p->blk * kNT * a.tpt < p->r.n_new) return;
@@ -218,6 +232,7 @@ __device__ __forceinline__ void next_block(const TileArgs& a, Place* p) {
 
 // Describes the item at a place, tiles [t0, t1) of nt; lane t looks after row
 // tile t.
+template <int kNT>
 __device__ __forceinline__ void paged_unit(const TileArgs& a, const Place& p, int t1, int nt,
                                            Unit* u) {
   const int w = kNT * a.tpt, lane = threadIdx.x & 31, t = lane;
@@ -257,6 +272,7 @@ __device__ __forceinline__ void paged_unit(const TileArgs& a, const Place& p, in
 // Kept short: a block runs it once or a few times, and code that has to be
 // fetched first takes some ten clocks an instruction.
 __device__ __forceinline__ void packed_unit(const TileArgs& a, int block, Unit* u) {
+  constexpr int kNT = row_tiles(kPacked);
   const int w = kNT * a.tpt, win_rev = block / a.Hkv;
   const int lane = threadIdx.x & 31, t = lane >> 1;
   const int q0 = (a.windows - 1 - win_rev) * w, q_end = min(a.tokens, q0 + w);
@@ -434,10 +450,66 @@ __device__ __noinline__ void row_product(uint32_t t_p, uint32_t t_o, const uint8
   tmem_st_wait();
 }
 
-template <bool PAGED, bool BF16>
+// Warps 8 to 11 of a 4-bit call: packed rows of a raw stage to 16-bit rows of a K/V
+// stage, as TMA would have written them.  A thread has one row of K or of V.
+template <bool BF16>
+__device__ __forceinline__ void unpack_rows(const TileArgs& a, uint8_t* smem, uint32_t bar0,
+                                            const Unit* s_unit, const WaitCtl& wc) {
+#define BAR(i) (bar0 + 8u * (uint32_t)(i))
+  const int lane = threadIdx.x & 31, row = threadIdx.x & (kBN - 1);
+  const bool is_v = (threadIdx.x & 127) >= kBN;
+  int kt = 0;
+  for (int nu = 0;; ++nu) {
+    if (!mbar_wait_inline(BAR(BAR_UNIT + (nu & 1)), (nu >> 1) & 1, wc)) return;
+    const int more = s_unit[nu & 1].more, nj = s_unit[nu & 1].nj;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(BAR(BAR_UNIT_FREE + (nu & 1)));
+    if (!more) return;
+    for (int j = 0; j < nj; ++j, ++kt) {
+      const int from = kt % kRaw, s = kt % kStages;
+      if (!mbar_wait_inline(BAR(BAR_RAW_FULL + from), (kt / kRaw) & 1, wc)) return;
+      const uint8_t* const unit = smem + kSmemRaw + from * 2 * kRawHalf +
+                                  (is_v ? kRawHalf : 0) + (row >> 3) * kUnitBytes;
+      const uint4 c0 = *reinterpret_cast<const uint4*>(unit + (row & 7) * 32);
+      const uint4 c1 = *reinterpret_cast<const uint4*>(unit + (row & 7) * 32 + 16);
+      const uint32_t sw = *reinterpret_cast<const uint32_t*>(unit + kUnitScales + (row & 7) * 4);
+      mbar_arrive(BAR(BAR_RAW_EMPTY + from));
+      if (kt >= kStages && !mbar_wait_inline(BAR(BAR_KV_EMPTY + s), (kt / kStages - 1) & 1, wc))
+        return;
+      const uint32_t s_lo = __byte_perm(sw, sw, 0x1010), s_hi = __byte_perm(sw, sw, 0x3232);
+      uint8_t* const to =
+          smem + kSmemStage0 + s * kStageBytes + (is_v ? kHalfBytes : 0) + row * 128;
+      const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // channels 8 c .. and 32 + 8 c ..
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t l0, h0, l1, h1;
+          scaled_codes<BF16>(w[2 * c + i], s_lo, s_hi, l0, h0, l1, h1);
+          lo[2 * i] = __byte_perm(l0, l1, 0x5410);
+          lo[2 * i + 1] = __byte_perm(l0, l1, 0x7632);
+          hi[2 * i] = __byte_perm(h0, h1, 0x5410);
+          hi[2 * i + 1] = __byte_perm(h0, h1, 0x7632);
+        }
+        *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) =
+            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(to + (((c + 4) ^ (row & 7)) << 4)) =
+            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      }
+      fence_proxy_async_shared();
+      mbar_arrive(BAR(BAR_KV_FULL + s));
+    }
+  }
+#undef BAR
+}
+
+template <int MODE, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const TileArgs a) {
+  constexpr bool PAGED = MODE != kPacked, FOUR = MODE == kPaged4;
+  constexpr int kNT = row_tiles(MODE);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -461,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(BAR_Q + i), 1);
       mbar_init(BAR(BAR_Q_FREE + i), kNT);
       mbar_init(BAR(BAR_UNIT + i), 1);
-      mbar_init(BAR(BAR_UNIT_FREE + i), 5 * kNT);
+      mbar_init(BAR(BAR_UNIT_FREE + i), 5 * kNT + (FOUR ? 4 : 0));
     }
     for (int i = 0; i < kNT; ++i) {
       s_turn[i] = 0;
@@ -474,11 +546,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(BAR_V_OK + i), 128);
     }
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(BAR(BAR_KV_FULL + s), 1);
+      mbar_init(BAR(BAR_KV_FULL + s), FOUR ? 128 : 1);
       mbar_init(BAR(BAR_KV_EMPTY + s), kNT);
     }
     mbar_init(BAR(BAR_MMA_DONE), kNT);
     mbar_init(BAR(BAR_TAKE), 1);
+    for (int s = 0; FOUR && s < kRaw; ++s) {
+      mbar_init(BAR(BAR_RAW_FULL + s), 1);
+      mbar_init(BAR(BAR_RAW_EMPTY + s), 128);
+    }
     fence_mbarrier_init();
   }
   if (warp == 15) tmem_alloc(smem_u32(&s_tmem), kTmemCols);
@@ -526,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   Place place{};
-  if (PAGED && warp == 15 && share.begin < share.end) place = place_at(a, s_pre, share.begin);
+  if (PAGED && warp == 15 && share.begin < share.end) place = place_at<kNT>(a, s_pre, share.begin);
 
   if (warp < 4 * kNT) {
     // ---------------- softmax: thread = row of tile t ----------------
@@ -711,12 +787,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(BAR_UNIT_FREE + (nu & 1)));
     }
+  } else if (FOUR && warp < 12) {
+    unpack_rows<BF16>(a, smem, bar0, s_unit, wc);
   } else {
     if (warp == 15) {
       // ---------------- work items and loads ----------------
       int kt = 0, nu = 0, nq = 0;
       bool ok = true, bad = false, tail = false, checks = false;
       const int q_rows = a.tpt * a.G;
+      // the stages that the copies land in
+      constexpr int kLand = FOUR ? kRaw : kStages, BAR_FULL = FOUR ? BAR_RAW_FULL : BAR_KV_FULL,
+                    BAR_EMPTY = FOUR ? BAR_RAW_EMPTY : BAR_KV_EMPTY;
       long long pos = share.begin;
       int block = blockIdx.x, taken = 0;  // packed: the window and head in hand
       for (;; ++nu) {
@@ -751,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           nt = tiles_of_block(place.r.n_keys, place.r.n_new, kNT * a.tpt, kBN, place.blk);
           place.t0 = min(place.t0, nt - 1);  // it is less, unless lens changed meanwhile
           steps = (int)min((long long)(nt - place.t0), share.end - pos);
-          paged_unit(a, place, place.t0 + steps, nt, &u);
+          paged_unit<kNT>(a, place, place.t0 + steps, nt, &u);
         } else {
           packed_unit(a, block, &u);
           checks |= block == 0;
@@ -768,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  last_block(share, pos + nt - 1)};
           }
           pos += steps;
-          if (pos < share.end) next_block(a, &place);
+          if (pos < share.end) next_block<kNT>(a, &place);
         }
         if (u.nj == 0) continue;
         const int qbuf = nq & 1;
@@ -802,12 +883,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           next = base + 32 + lane < n_pages ? row[base + 32 + lane] : a.pages;
         }
         for (int j = 0; j < u.nj; ++j, ++kt) {
-          const int s = kt % kStages;
-          if (kt >= kStages && !mbar_wait_warp(BAR(BAR_KV_EMPTY + s), (kt / kStages - 1) & 1, wc)) {
+          const int s = kt % kLand;
+          if (kt >= kLand && !mbar_wait_warp(BAR(BAR_EMPTY + s), (kt / kLand - 1) & 1, wc)) {
             ok = false;
             break;
           }
-          const uint32_t st = sbase + kSmemStage0 + s * kStageBytes;
+          const uint32_t st = FOUR ? sbase + kSmemRaw + s * 2 * kRawHalf
+                                   : sbase + kSmemStage0 + s * kStageBytes;
           const int k0 = (u.j0 + j) * kBN;
           if (PAGED) {
             const int page = k0 >> a.shift;
@@ -820,6 +902,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int bx = lane & 15;
             const int id = __shfl_sync(0xffffffffu, ids, (page - base + (boxes > 1 ? bx : 0)) & 31);
             const bool fine = page_ok(id, a.pages);
+            if (FOUR) {
+              // units that hold keys below n_keys; the rest of the stage is masked
+              const int units = n_keys <= k0 ? 0 : min(kBN / 8, (n_keys - k0 - 1) / 8 + 1);
+              if (lane == 0) mbar_arrive_expect_tx(BAR(BAR_RAW_FULL + s), 2 * units * kUnitBytes);
+              __syncwarp();
+              if (bx < live) {
+                bad |= !fine;
+                // of a page that does not exist the first one takes the place
+                const PoolArg& pool = lane < 16 ? a.kc : a.vc;
+                const int u0 = bx * (box / 8),
+                          off = boxes > 1 ? 0 : (k0 & ((1 << a.shift) - 1)) / 8 * kUnitBytes;
+                bulk_load(st + (lane >> 4) * kRawHalf + u0 * kUnitBytes,
+                          static_cast<const uint8_t*>(pool.p) + (fine ? id : 0) * pool.pg +
+                              u.kv * pool.h + off,
+                          min(box / 8, units - u0) * kUnitBytes, BAR(BAR_RAW_FULL + s));
+              }
+              __syncwarp();
+              continue;
+            }
             if (lane == 0) mbar_arrive_expect_tx(BAR(BAR_KV_FULL + s), 2 * live * box * 128);
             __syncwarp();
             if (bx < live) {
@@ -851,12 +952,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         if (taken > 0) drain_wait(BAR(BAR_TAKE), (taken - 1) & 1);
         for (int q = 0; q < 2 && q < nq; ++q) drain_wait(BAR(BAR_Q + q), ((nq - q + 1) / 2 - 1) & 1);
-        for (int k = kt > kStages ? kt - kStages : 0; k < kt; ++k)
-          drain_wait(BAR(BAR_KV_FULL + k % kStages), (k / kStages) & 1);
+        for (int k = kt > kLand ? kt - kLand : 0; k < kt; ++k)
+          drain_wait(BAR(BAR_FULL + k % kLand), (k / kLand) & 1);
       }
-    } else {
+    } else if (warp < 12 + kNT) {
       // ---------------- products of row tile t ----------------
-      const int t = warp - 4 * kNT;
+      const int t = warp - 12;
       const uint32_t d_s = tmem + kColS + 64 * t, d_p = tmem + kColP + 32 * t,
                      d_o = tmem + kColO + 64 * t;
       int kt = 0, nq = 0, ns = 0, np = 0, no = 0;
@@ -987,10 +1088,11 @@ int launch_packed_fwd(const PackedDims& d, const DevCtx& ctx, const RowsArg& q, 
       !encode_tmap_4d(&tk, d.bf16, k.p, d.tokens, d.Hkv, 1, k.t, k.h, 64, kBN, 1, 1) ||
       !encode_tmap_4d(&tv, d.bf16, v.p, d.tokens, d.Hkv, 1, v.t, v.h, 64, kBN, 1, 1))
     return ATTN_ERR_CUDA;
-  a.windows = (d.tokens + kNT * a.tpt - 1) / (kNT * a.tpt);
+  const int window = row_tiles(kPacked) * a.tpt;
+  a.windows = (d.tokens + window - 1) / window;
   const long long units = (long long)d.Hkv * a.windows;
   if (units > 0x7fffffffLL) return ATTN_ERR_SHAPE;
-  auto* kernel = d.bf16 ? tiles_kernel<false, true> : tiles_kernel<false, false>;
+  auto* kernel = d.bf16 ? tiles_kernel<kPacked, true> : tiles_kernel<kPacked, false>;
   const size_t smem = kSmemPre + 1024;
   const int rc = allow_smem(d.bf16 ? kSmemPackedBf16 : kSmemPackedF16,
                             reinterpret_cast<const void*>(kernel), smem);
@@ -1002,7 +1104,7 @@ int launch_packed_fwd(const PackedDims& d, const DevCtx& ctx, const RowsArg& q, 
 int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
                       const PoolArg& vc, const int32_t* table, const int32_t* cu,
                       const int32_t* lens, const PartArgs& part, int blocks, int skip,
-                      const RowsArg& o, float* lse, cudaStream_t stream) {
+                      bool four, const RowsArg& o, float* lse, cudaStream_t stream) {
   CUtensorMap tq, tk, tv;
   TileArgs a{};
   a.tokens = d.tokens;
@@ -1026,16 +1128,23 @@ int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, c
   a.part = part;
   a.err = ctx.err;
   a.wait_ns = ctx.wait_ns;
+  a.kc = kc;
+  a.vc = vc;
   const uint32_t box = (1u << d.shift) < kBN ? (1u << d.shift) : kBN;
   const uint64_t P = 1ull << d.shift;
-  if (!encode_tmap_4d(&tq, d.bf16, q.p, d.G, d.Hkv, d.tokens, q.h, q.h * d.G, q.t, d.G, 1, a.tpt) ||
-      !encode_tmap_4d(&tk, d.bf16, kc.p, P, d.Hkv, d.pages, kc.r, kc.h, kc.pg, box, 1, 1) ||
-      !encode_tmap_4d(&tv, d.bf16, vc.p, P, d.Hkv, d.pages, vc.r, vc.h, vc.pg, box, 1, 1))
+  if (!encode_tmap_4d(&tq, d.bf16, q.p, d.G, d.Hkv, d.tokens, q.h, q.h * d.G, q.t, d.G, 1, a.tpt))
     return ATTN_ERR_CUDA;
-  auto* kernel = d.bf16 ? tiles_kernel<true, true> : tiles_kernel<true, false>;
+  tk = tv = tq;  // 4 bits: not used
+  if (!four &&
+      (!encode_tmap_4d(&tk, d.bf16, kc.p, P, d.Hkv, d.pages, kc.r, kc.h, kc.pg, box, 1, 1) ||
+       !encode_tmap_4d(&tv, d.bf16, vc.p, P, d.Hkv, d.pages, vc.r, vc.h, vc.pg, box, 1, 1)))
+    return ATTN_ERR_CUDA;
+  auto* kernel = d.bf16 ? tiles_kernel<kPaged, true> : tiles_kernel<kPaged, false>;
+  if (four) kernel = d.bf16 ? tiles_kernel<kPaged4, true> : tiles_kernel<kPaged4, false>;
   const size_t smem = kSmemPre + 8 * (size_t)(d.batch + 1) + 1024;
   const int rc =
-      allow_smem(d.bf16 ? kSmemRowsBf16 : kSmemRowsF16, reinterpret_cast<const void*>(kernel),
+      allow_smem((four ? kSmemRows4F16 : kSmemRowsF16) + (d.bf16 ? 1 : 0),
+                 reinterpret_cast<const void*>(kernel),
                  kSmemPre + 8 * (size_t)(4096 + 1) + 1024);
   if (rc != ATTN_OK) return rc;
   return cuda_status(launch_dependent(kernel, dim3(blocks), dim3(kThreads), smem, stream, tq, tk,

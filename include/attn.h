@@ -443,7 +443,7 @@ typedef struct attn_paged_shape {
   float scale;
   int64_t q_token, q_head, o_token, o_head;              /* attn_paged_fwd   */
   int64_t k_token, k_head, v_token, v_head;              /* attn_paged_store */
-  int64_t kc_page, kc_head, kc_row, vc_page, vc_head, vc_row;
+  int64_t kc_page, kc_head, kc_row, vc_page, vc_head, vc_row; /* 4 bits: bytes */
 } attn_paged_shape;
 
 /*
@@ -500,7 +500,79 @@ ATTN_API int attn_paged_store(const attn_paged_shape* shape, const void* k, cons
                               const int32_t* slots, void* k_cache, void* v_cache, void* stream);
 
 /*
- * Bytes of the workspace of attn_paged_fwd (0 if the shape is invalid).  It
+ * The append with the position rotation: attn_paged_store that turns q and k on
+ * the way.  Token t is row t of q, k, v, q_out and slots; a token with a negative
+ * slot is left out (its row of q_out as it was).  cu and lens are those that
+ * attn_paged_fwd takes after it: token t of request i, rows cu[i] .. cu[i+1] - 1,
+ * stands at position p = lens[i] - (cu[i+1] - cu[i]) + (t - cu[i]).  For c < 32
+ *   y[c]      = x[c] cos[p][c] - x[c + 32] sin[p][c]
+ *   y[c + 32] = x[c + 32] cos[p][c] + x[c] sin[p][c]
+ * (the rotation whose inverse attn_bwd_queries_rotated applies; both products
+ * rounded to binary32, then added), rounded to the type: q to q_out, k to its slot
+ * of the K pool; v goes to its slot as it is.  cos_tab, sin_tab: device [angles][32]
+ * binary32, 16-byte aligned.  A token outside every request, or at a position that
+ * is negative or not below `angles`, is left out and reported
+ * (ATTN_ERR_DEVICE_INDEX).
+ * q_out is q itself (the same pointer and strides: q is turned in place) or
+ * overlaps nothing else; what attn_paged_store says of slots and pools holds.  Uses
+ * batch, tokens, heads, kv_heads, page_size, num_pages, dtype and the q, k, v, kc
+ * and vc strides; o_token and o_head are q_out's.
+ */
+ATTN_API int attn_paged_append(const attn_paged_shape* shape, const void* q, const void* k,
+                               const void* v, const float* cos_tab, const float* sin_tab,
+                               int32_t angles, const int32_t* slots, const int32_t* cu,
+                               const int32_t* lens, void* q_out, void* k_cache, void* v_cache,
+                               void* stream);
+
+/*
+ * The paged cache in 4 bits.  A row of 64 channels is kept as 36 bytes: 32 of
+ * codes, byte c with channel c in its low and channel c + 32 in its high half, each
+ * code + 8, and two 16-bit scales in `dtype`, of channels 0..31 and 32..63.  The
+ * value is code * scale, which is exact in the type.  Eight rows make a unit of
+ * ATTN_UNIT4_BYTES, their codes one behind the other and then their scales; the
+ * units of a page and K/V head lie one behind the other (ATTN_UNIT4_BYTES / 8 *
+ * page_size bytes).  In the calls below kc_page, kc_head, vc_page and vc_head count
+ * BYTES: multiples of 16, at least a page of one head in a dimension longer than
+ * one; kc_row and vc_row are not read.
+ *
+ * The scale of 32 values with the extremum e (of largest magnitude; the negative
+ * one of a tie) is -e / 8, to nearest (ties away from zero) with eight significant
+ * bits in binary16 and five in bfloat16 (there a multiple of 2^-130), at most 8160
+ * and 2^123 in magnitude, then in the type.  A code is the binary32 quotient value /
+ * scale, to the nearest whole number (ties to even), cut off at -8 and 7; 0 where
+ * the scale is zero.  So a value comes back
+ * within half a scale, or within one at the far end from the extremum, where 7 is
+ * the last code.  (Beyond 65280 in binary16 and 2^126 in bfloat16 it comes back as
+ * that.)  Where a group holds an infinity or a NaN, its scale is NaN and all its 32
+ * values come back as NaN.  A scale is finite or NaN; with an infinite one, which
+ * no call writes, its values read as infinities or NaN.
+ */
+#define ATTN_UNIT4_BYTES 288
+
+/*
+ * Appends to a 4-bit cache: attn_paged_append with k and v quantised, k after its
+ * rotation and from the unrounded binary32 values.  With cos_tab and sin_tab both
+ * NULL nothing is turned: q, q_out, cu and lens are not read, and k is stored as it
+ * is (attn_paged_store into 4 bits).
+ */
+ATTN_API int attn_paged_append4(const attn_paged_shape* shape, const void* q, const void* k,
+                                const void* v, const float* cos_tab, const float* sin_tab,
+                                int32_t angles, const int32_t* slots, const int32_t* cu,
+                                const int32_t* lens, void* q_out, uint8_t* k_cache,
+                                uint8_t* v_cache, void* stream);
+
+/*
+ * Reads rows of a 4-bit cache back: row t of k and v (all K/V heads) becomes what
+ * slot slots[t] holds, exactly; with a negative slot it stays as it was.  A slot may
+ * be given any number of times.  k and v overlap neither one another nor the pools.
+ * Uses tokens, kv_heads, page_size, num_pages, dtype and the k, v, kc and vc strides.
+ */
+ATTN_API int attn_paged_load4(const attn_paged_shape* shape, const int32_t* slots,
+                              const uint8_t* k_cache, const uint8_t* v_cache, void* k, void* v,
+                              void* stream);
+
+/*
+ * Bytes of the workspace of attn_paged_fwd and attn_paged_fwd4 (0 if the shape is invalid).  It
  * holds the parts of rows whose keys were split over several blocks; its
  * contents need not be initialised and mean nothing after the call.  Calls
  * that overlap on the GPU need workspaces of their own; where two share one, or
@@ -521,6 +593,16 @@ ATTN_API int attn_paged_fwd(const attn_paged_shape* shape, const void* q, const 
                             const void* v_cache, const int32_t* table, const int32_t* cu,
                             const int32_t* lens, void* ws, size_t ws_bytes, void* o, float* lse,
                             void* stream);
+
+/*
+ * The same over a 4-bit cache: attn_paged_fwd on the values that the pools hold
+ * (exact in 16 bits, so only the order of sums is another), with the workspace of
+ * attn_paged_workspace_bytes.  A row of q that holds an infinity or a NaN gives NaN.
+ */
+ATTN_API int attn_paged_fwd4(const attn_paged_shape* shape, const void* q, const uint8_t* k_cache,
+                             const uint8_t* v_cache, const int32_t* table, const int32_t* cu,
+                             const int32_t* lens, void* ws, size_t ws_bytes, void* o, float* lse,
+                             void* stream);
 
 /* A static, human-readable message for an ATTN_ code. */
 ATTN_API const char* attn_error_string(int code);
