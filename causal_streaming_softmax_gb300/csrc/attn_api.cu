@@ -163,6 +163,20 @@ bool encode_tmap_4d(CUtensorMap* map, bool bf16, const void* base, uint64_t d1, 
   return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_units(CUtensorMap* map, const void* base, uint64_t units, uint64_t heads,
+                       uint64_t pages, uint64_t head_bytes, uint64_t page_bytes, uint32_t box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {ATTN_UNIT4_BYTES / 8, units, heads, pages};
+  cuuint64_t strides[3] = {ATTN_UNIT4_BYTES, head_bytes, page_bytes};
+  cuuint32_t boxes[4] = {ATTN_UNIT4_BYTES / 8, box, 1, 1};
+  cuuint32_t estride[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 4, const_cast<void*>(base), dims, strides,
+                  boxes, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace css
 
 using namespace css;

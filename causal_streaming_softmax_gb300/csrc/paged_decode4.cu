@@ -29,6 +29,8 @@
 // the 16-bit kernel (serve_decode.cuh, serve_parts.cuh).
 #include <math.h>
 
+#include <type_traits>
+
 #include "pool4.cuh"
 #include "serve_decode.cuh"
 #include "serve_index.h"
@@ -40,34 +42,51 @@
 namespace css {
 namespace {
 
-constexpr float kSlack = 8.f;
+// A weight counts 2^kBias where the score is m, so that binary16 holds small ones
+// too.  Binary orders that a score may pass m by, and a scale of V its unit, before
+// both are followed: a weight times a scale stays at or below 2^15.
+constexpr float kBias = 10.f, kMost = 0x1p13f;
+constexpr int kVSlack = 2;
+constexpr int kTileKeys = 64;
+constexpr int kGroup = 4;  // tiles that the producer hands out at a time, eight lanes each
+// Pages of so many rows (their logarithm) are copied by tensor maps, whose boxes have
+// to start on 128 bytes of shared memory: four units.  Smaller ones are plain copies.
+constexpr int kTiledShift = 5;
+static_assert(kTiledShift >= 5 && (32 / 8 * kUnitBytes) % 128 == 0, "a box of 32 rows");
 constexpr int kLd = 68;  // floats a row of the joining buffer (bank spread)
 
 // A block's shape.  COLS: column tiles of eight query rows.
 template <int COLS>
 struct Config {
   static constexpr bool kWhole = false;
+  static constexpr int kTileKeys = css::kTileKeys;
   static constexpr int kCols = COLS, kRows = 8 * COLS;
-  static constexpr int kBlocks = COLS == 1 ? 2 : 1;  // a SM
-  static constexpr int kConsumers = 8, kStages = COLS == 1 ? 4 : 3;
+  static constexpr int kBlocks = COLS == 1 ? 3 : 2;  // a SM
+  // The tiles go round the consumer warps, each with a ring of its own: the phases of
+  // a stage's barriers are told apart by their parity, so a warp may look at a stage
+  // only in the order in which it is used.
+  static constexpr int kConsumers = 4, kRing = COLS == 1 ? 3 : 4;
+  static constexpr int kStages = kConsumers * kRing;
   static constexpr int kThreads = 32 * (kConsumers + 1);
-  static constexpr int kWarpKeys = 32, kTileKeys = kWarpKeys * kConsumers;
   static constexpr uint32_t kHalf = kTileKeys / 8 * kUnitBytes;  // K (or V) of a stage
   static constexpr uint32_t kStage = 2 * kHalf;
   static constexpr uint32_t kQ = kDecodeRows * 128;
   static constexpr uint32_t kSmemStage = 2 * kQ;  // behind two Q buffers
   static constexpr uint32_t kSmemJoin = kSmemStage + kStages * kStage;
-  static constexpr uint32_t kSmemMl = kSmemJoin + kConsumers * kRows * kLd * 4;
+  // a warp's place in the joining buffer holds its scales before
+  static constexpr uint32_t kScales = kTileKeys * 32;
+  static constexpr uint32_t kJoin = kRows * kLd * 4 > kScales ? kRows * kLd * 4 : kScales;
+  static constexpr uint32_t kSmemMl = kSmemJoin + kConsumers * kJoin;
   static constexpr uint32_t kSmemBar = kSmemMl + kConsumers * kRows * 8;
-  static constexpr uint32_t kSmemPre = kSmemBar + 128;  // + 8 (batch + 1), + alignment slack
   // barriers
   static constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQFree = kQFull + 2;
-  static_assert((kQFree + 2) * 8 <= 128, "barrier area");
-  static_assert(kHalf % 16 == 0 && kSmemMl % 16 == 0 && kSmemBar % 16 == 0, "alignment");
+  static constexpr uint32_t kSmemPre = kSmemBar + 8 * (kQFree + 2);  // + 8 (batch + 1), + slack
+  static_assert(kConsumers >= kGroup, "a group goes round the warps once at most");
+  static_assert(kSmemStage % 128 == 0 && kHalf % 128 == 0, "boxes start on 128 bytes");
+  static_assert(kSmemMl % 16 == 0 && kSmemBar % 16 == 0, "layout");
   static_assert(kSmemPre + 8 * (kMaxPagedBatch + 1) + 1024 <= 227 * 1024 - 2048,
                 "shared memory of a block");
 };
-constexpr int kTileKeys = Config<1>::kTileKeys;
 
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   uint32_t r;
@@ -87,6 +106,58 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
+// d = a b + c on the tensor cores, binary16 in, binary32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4],
+                                        const uint32_t (&b)[2], const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c[0]), "f"(c[1]),
+        "f"(c[2]), "f"(c[3]));
+}
+
+__device__ __forceinline__ uint32_t add_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// A word of codes as pairs of binary16 operands: the low and high halves of bytes 0
+// and 2, then of bytes 1 and 3, as the subnormal numbers (code + 8) 2^-24 and
+// (code + 8) 2^-20.
+__device__ __forceinline__ void raw_codes(uint32_t w, uint32_t& lo0, uint32_t& hi0, uint32_t& lo1,
+                                          uint32_t& hi1) {
+  const uint32_t v = w >> 8;
+  lo0 = w & 0x000f000fu;
+  hi0 = w & 0x00f000f0u;
+  lo1 = v & 0x000f000fu;
+  hi1 = v & 0x00f000f0u;
+}
+constexpr float kLoZero = 0x1p-21f, kHiZero = 0x1p-17f;  // what stands for code 0
+
+// The same as code 2^-24 and code 2^-20.
+__device__ __forceinline__ void signed_codes(uint32_t w, uint32_t& lo0, uint32_t& hi0,
+                                             uint32_t& lo1, uint32_t& hi1) {
+  raw_codes(w, lo0, hi0, lo1, hi1);
+  lo0 = add_f16(lo0, 0x80088008u);
+  hi0 = add_f16(hi0, 0x80808080u);
+  lo1 = add_f16(lo1, 0x80088008u);
+  hi1 = add_f16(hi1, 0x80808080u);
+}
+
+// A row's m follows its largest score x (in units of `unit`) where that is higher;
+// f: what its sums are multiplied by.
+__device__ __forceinline__ void follow(float x, float unit, float* neg_m, float* most, float* l,
+                                       float* f) {
+  const float to = kBias - x * unit;
+  if (x > -INFINITY && (*most < 0.f || to < *neg_m)) {
+    *f = *most < 0.f ? 0.f : ex2_approx(to - *neg_m);
+    *neg_m = to;
+    *most = kMost;
+    *l *= *f;
+  }
+}
+
 // Whether one of the two scales of a row is an infinity or NaN.
 template <bool BF16>
 __device__ __forceinline__ bool odd_scale(uint32_t s) {
@@ -96,11 +167,13 @@ __device__ __forceinline__ bool odd_scale(uint32_t s) {
 
 template <bool BF16, class C>
 __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
-    paged_decode4_kernel(const __grid_constant__ CUtensorMap tm_q, const DecodeArgs a,
+    paged_decode4_kernel(const __grid_constant__ CUtensorMap tm_q,
+                         const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a,
                          const PoolArg kc, const PoolArg vc) {
   constexpr int kConsumers = C::kConsumers, kStages = C::kStages, kThreads = C::kThreads,
-                kTileKeys = C::kTileKeys, kCols = C::kCols, kRows = C::kRows,
-                kWarpKeys = C::kWarpKeys, kSteps = kWarpKeys / 16;
+                kCols = C::kCols, kRows = C::kRows, kRing = C::kRing,
+                kSteps = kTileKeys / 16;
   constexpr uint32_t kHalf = C::kHalf, kStage = C::kStage, kQ = C::kQ;
   constexpr int BAR_FULL = C::kFull, BAR_EMPTY = C::kEmpty, BAR_Q = C::kQFull,
                 BAR_Q_FREE = C::kQFree;
@@ -116,21 +189,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
   long long* const s_pre = reinterpret_cast<long long*>(smem + C::kSmemPre);
   const uint32_t bar0 = sbase + C::kSmemBar;
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = (tid >> 5) - 1;  // of the consumers; the producer comes first
   const WaitCtl wc{a.err, a.wait_ns, &s_abort};
 
-  if (tid == 0) {
-    s_abort = 0;
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(BAR(BAR_FULL + s), 1);
-      mbar_init(BAR(BAR_EMPTY + s), kConsumers);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(BAR(BAR_Q + s), 1);
-      mbar_init(BAR(BAR_Q_FREE + s), kConsumers);
-    }
+  if (tid < kStages) {
+    mbar_init(BAR(BAR_FULL + tid), 1);
+    mbar_init(BAR(BAR_EMPTY + tid), 1);
+    fence_mbarrier_init();
+  } else if (tid < kStages + 2) {
+    mbar_init(BAR(BAR_Q + tid - kStages), 1);
+    mbar_init(BAR(BAR_Q_FREE + tid - kStages), kConsumers);
     fence_mbarrier_init();
   }
+  if (tid == 0) s_abort = 0;
   // rows of the query tile that no copy fills read as zero
   for (int i = tid; i < (int)(2 * kQ / 16); i += kThreads)
     reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
@@ -140,11 +212,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
   tiles_before_each<C>(a, s_pre, s_scan);
   const Share share = share_of(s_pre[a.batch] * a.Hkv, a.part.min_tiles, gridDim.x, blockIdx.x);
 
-  if (warp == kConsumers) {
+  if (warp < 0) {
     // ---------------- producer ----------------
-    const int box = min(1 << a.shift, kTileKeys);  // rows a copy, at most
-    const int boxes = kTileKeys / box;             // copies a tile of K (and of V)
-    const bool small = boxes > 1;                  // a copy a page
+    const int box_shift = min(a.shift, 6), box = 1 << box_shift;  // rows a copy, at most
+    const bool tiled = a.shift >= kTiledShift;
+    // eight lanes look after a tile of a group, a box each; ring, slot and turn: the
+    // next tile's warp, its place in the warp's ring, the parity of the phase before
+    const int tile = lane >> 3, in_tile = (lane & 7) << box_shift;
+    int ring = 0, slot = 0, turn = 1;
     int it = 0, nq = 0;
     bool ok = true, bad = false, tail = false;
     // page ids go 32 at a time: lane l of group g has page first + 32 g + l.
@@ -177,7 +252,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         read_ids();
       }
       const int qbuf = nq & 1;
-      ok = !(nq >= 2) || mbar_wait_warp(BAR(BAR_Q_FREE + qbuf), ((nq >> 1) - 1) & 1, wc);
+      ok = !(nq >= 2) || mbar_nap_warp(BAR(BAR_Q_FREE + qbuf), ((nq >> 1) - 1) & 1, wc);
       if (!ok) break;
       if (lane == 0) {
         s_item[qbuf] = Item{r, sg.kv, sg.t0, t1, sg.t0 == 0 && t1 == sg.nt};
@@ -187,43 +262,60 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
       ++nq;
       const uint8_t* const kp = static_cast<const uint8_t*>(kc.p) + sg.kv * kc.h;
       const uint8_t* const vp = static_cast<const uint8_t*>(vc.p) + sg.kv * vc.h;
-      for (int t = sg.t0; t < t1; ++t, ++it) {
-        const int s = it % kStages;
-        if (it >= kStages && !mbar_wait_warp(BAR(BAR_EMPTY + s), (it / kStages - 1) & 1, wc)) {
-          ok = false;
-          break;
+      for (int t = sg.t0; t < t1; t += kGroup) {
+        const int n = min(kGroup, t1 - t);
+        const bool has = tile < n;
+        int to_ring = ring + tile, to_slot = slot, to_turn = turn;
+        if (to_ring >= kConsumers) {
+          to_ring -= kConsumers;
+          if (++to_slot == kRing) to_slot = 0, to_turn ^= 1;
         }
-        const int k0 = t * kTileKeys;
-        const int page = k0 >> a.shift;  // the tile's first page
-        if (page - base >= 32) {
+        const int s = to_ring * kRing + to_slot;
+        ok = !has || mbar_try_wait(BAR(BAR_EMPTY + s), to_turn) ||
+             mbar_nap(BAR(BAR_EMPTY + s), to_turn, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if ((ring += n) >= kConsumers) {
+          ring -= kConsumers;
+          if (++slot == kRing) slot = 0, turn ^= 1;
+        }
+        it += n;
+        const int k0 = (t + tile) * kTileKeys, at = k0 + in_tile;  // the lane's first key
+        if (((t * kTileKeys) >> a.shift) - base >= 32) {
           base += 32;
           ids = next;
           next = base + 32 + lane < n_pages ? row[base + 32 + lane] : a.pages;
         }
-        // units that hold keys below n_keys; the rest of the stage is masked
-        const int live = r.n_keys <= k0 ? 0 : min(kTileKeys / 8, (r.n_keys - k0 - 1) / 8 + 1);
-        const uint32_t st = sbase + C::kSmemStage + s * kStage;
-        if (lane == 0) mbar_arrive_expect_tx(BAR(BAR_FULL + s), 2 * live * kUnitBytes);
+        const int which = (at >> a.shift) - base;  // below 64 where there are keys
+        const int id0 = __shfl_sync(0xffffffffu, ids, which & 31);
+        const int id1 = __shfl_sync(0xffffffffu, next, which & 31);
+        // boxes, and units of eight, that hold keys below n_keys; the rest of the
+        // stage is masked
+        const int keys = has ? min(max(r.n_keys - k0, 0), kTileKeys) : 0;
+        const uint32_t full = BAR(BAR_FULL + s);
+        if (has && (lane & 7) == 0)
+          mbar_arrive_expect_tx(
+              full, 2 * kUnitBytes *
+                        (tiled ? ((keys + box - 1) & -box) / 8 : (keys + 7) / 8));
         __syncwarp();
-#pragma unroll 1
-        for (int b0 = 0; b0 < boxes; b0 += 32) {
-          const int bx = b0 + lane;
-          // a tile of the smallest pages needs all 32 ids of a group
-          const int id = __shfl_sync(0xffffffffu, ids, (page - base + (small ? bx : 0)) & 31);
+        if (in_tile < keys) {
+          int id = which < 32 ? id0 : id1;
           const bool fine = page_ok(id, a.pages);
-          const int u0 = bx * (box / 8), units = min(box / 8, live - u0);
-          if (bx < boxes && units > 0) {
-            bad |= !fine;
-            // of a page that does not exist the first one takes the place
-            const long long p = fine ? id : 0;
-            const int off = small ? 0 : (k0 & ((1 << a.shift) - 1)) / 8 * kUnitBytes;
-            bulk_load(st + u0 * kUnitBytes, kp + p * kc.pg + off, units * kUnitBytes,
-                      BAR(BAR_FULL + s));
-            bulk_load(st + kHalf + u0 * kUnitBytes, vp + p * vc.pg + off, units * kUnitBytes,
-                      BAR(BAR_FULL + s));
+          bad |= !fine;
+          if (!fine) id = 0;  // the first page takes the place of one that does not exist
+          const uint32_t to = sbase + C::kSmemStage + s * kStage + in_tile / 8 * kUnitBytes;
+          const int unit = (at & ((1 << a.shift) - 1)) / 8;
+          if (tiled) {
+            tma_load_4d(to, &tm_k, full, 0, unit, sg.kv, id);
+            tma_load_4d(to + kHalf, &tm_v, full, 0, unit, sg.kv, id);
+          } else {
+            const uint32_t bytes = (min(box, keys - in_tile) + 7) / 8 * kUnitBytes;
+            bulk_load(to, kp + id * kc.pg + unit * kUnitBytes, bytes, full);
+            bulk_load(to + kHalf, vp + id * vc.pg + unit * kUnitBytes, bytes, full);
           }
         }
       }
+      if (!ok) break;
       if (sg.t0 == 0 && t1 < sg.nt) {
         tail = true;
         if (lane == 0)
@@ -236,207 +328,267 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
     // wait gave up)
     if (lane == 0) {
       for (int q = 0; q < 2 && q < nq; ++q) drain_wait(BAR(BAR_Q + q), ((nq - q + 1) / 2 - 1) & 1);
-      for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
-        drain_wait(BAR(BAR_FULL + k % kStages), (k / kStages) & 1);
+      for (int w = 0; w < kConsumers; ++w) {
+        const int uses = (it + kConsumers - 1 - w) / kConsumers;  // tiles of warp w
+        for (int k = max(uses - kRing, 0); k < uses; ++k)
+          drain_wait(BAR(BAR_FULL + w * kRing + k % kRing), k / kRing & 1);
+      }
     }
   } else {
     // ---------------- consumers ----------------
     const int g = lane >> 2, tq = lane & 3;
     const int mi = lane >> 3, mr = lane & 7;
-    int it = 0, nq = 0;
+    // the warp's scales of K, then of V, [key] {low, low, high, high}
+    float4* const s_scale = reinterpret_cast<float4*>(smem + C::kSmemJoin + warp * C::kJoin);
+    int it = 0, nq = 0, slot = 0, turn = 0;
     for (long long pos = share.begin; pos < share.end;) {
       const int qbuf = nq & 1;
       // Q's fragments: products 0 and 1 take the low channels (words 0 and 1 of a
       // lane's codes), 2 and 3 the high ones
       uint32_t q[kCols][4][2];
-      float z_lo[kCols][2], z_hi[kCols][2];  // where the scores of rows 2 tq, 2 tq + 1 start
+      float z_lo[kCols][4], z_hi[kCols][4];  // where scores start
+      float2 unit[kCols];                    // of the scores of rows 2 tq, 2 tq + 1
       Item sg{};
       bool ok = mbar_wait_warp(BAR(BAR_Q + qbuf), (nq >> 1) & 1, wc);
       if (ok) {
         sg = s_item[qbuf];
 #pragma unroll
         for (int n = 0; n < kCols; ++n) {
-          float sum[2];
+          float x[2][8], top = 0.f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // channels 32 h + 8 tq .. + 7 of row 8 n + g
             const uint4 w = *reinterpret_cast<const uint4*>(
                 smem + qbuf * kQ + sw128_offset(8 * n + g, 4 * h + tq));
-            q[n][2 * h][0] = __byte_perm(w.x, w.y, 0x5410);
-            q[n][2 * h][1] = __byte_perm(w.x, w.y, 0x7632);
-            q[n][2 * h + 1][0] = __byte_perm(w.z, w.w, 0x5410);
-            q[n][2 * h + 1][1] = __byte_perm(w.z, w.w, 0x7632);
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[h][2 * i] = half_to_f32<BF16>((uint16_t)u[i]);
+              x[h][2 * i + 1] = half_to_f32<BF16>((uint16_t)(u[i] >> 16));
+              top = fmaxf(top, fmaxf(fabsf(x[h][2 * i]), fabsf(x[h][2 * i + 1])));
+            }
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int sh = min(9 - ((int)(__float_as_uint(top) >> 23) - 127), 120);
+          float sum[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f = __uint_as_float((uint32_t)(sh + 127 + (h ? 0 : 4)) << 23);
             sum[h] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sum[h] += half_to_f32<BF16>((uint16_t)u[i]) + half_to_f32<BF16>((uint16_t)(u[i] >> 16));
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t w = pack_f16x2(x[h][4 * i + j] * f, x[h][4 * i + j + 2] * f);
+                q[n][2 * h + i][j] = w;
+                sum[h] += f16_bits_to_f32((uint16_t)w) + f16_bits_to_f32((uint16_t)(w >> 16));
+              }
             sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
             sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
           }
+          // scores that may leave binary32 are NaN, not something else
+          float back = sh < -107 ? INFINITY : a.c * __uint_as_float((uint32_t)(147 - sh) << 23);
+          if (!(back < INFINITY)) back = __uint_as_float(0x7fc00000u);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            z_lo[n][e] = -Raw<BF16>::kLoZero * __shfl_sync(0xffffffffu, sum[0], 8 * tq + 4 * e);
-            z_hi[n][e] = -Raw<BF16>::kHiZero * __shfl_sync(0xffffffffu, sum[1], 8 * tq + 4 * e);
+            z_lo[n][e] = z_lo[n][2 + e] =
+                -kLoZero * __shfl_sync(0xffffffffu, sum[0], 8 * tq + 4 * e);
+            z_hi[n][e] = z_hi[n][2 + e] =
+                -kHiZero * __shfl_sync(0xffffffffu, sum[1], 8 * tq + 4 * e);
           }
+          unit[n].x = __shfl_sync(0xffffffffu, back, 8 * tq);
+          unit[n].y = __shfl_sync(0xffffffffu, back, 8 * tq + 4);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(BAR_Q_FREE + qbuf));
       }
       ++nq;
-      const Request r = sg.r;
-      const int t1 = sg.t1, rows = r.n_new * a.G;
+      const int t1 = sg.t1, n_keys = sg.r.n_keys;
       pos += t1 - sg.t0;
-      // keys that this lane's rows see
-      const int first_lim = row_limit(r.n_keys, r.n_new, 0);
-      int lim[kCols][2];
-      float m[kCols][2], l[kCols][2];
+      const int first_lim = row_limit(n_keys, sg.r.n_new, 0);  // keys that every row sees
+      // neg_m: kBias - m in base 2; most: what a lane's weights of a row in a step may
+      // add up to.  V's scales count in a unit of their own: v_inv is its inverse,
+      // v_most what a scale may reach
+      float2 neg_m[kCols], most[kCols], l[kCols];
+      float v_inv = 1.f, v_most = 0.f;
       float o[kCols][4][4];
 #pragma unroll
-      for (int n = 0; n < kCols; ++n)
+      for (int n = 0; n < kCols; ++n) {
+        most[n] = make_float2(-1.f, -1.f);  // no m yet
+        neg_m[n] = l[n] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          lim[n][e] = row_limit(r.n_keys, r.n_new, (8 * n + 2 * tq + e) / a.G);
-          m[n][e] = -INFINITY;
-          l[n][e] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[n][j][e] = o[n][j][2 + e] = 0.f;
-        }
+        for (int j = 0; j < 4; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+      }
 
-      for (int t = sg.t0; t < t1; ++t, ++it) {
-        const int s = it % kStages;
-        ok = mbar_wait_warp(BAR(BAR_FULL + s), (it / kStages) & 1, wc);
-        if (!ok) break;
-        const uint32_t ks =
-            sbase + C::kSmemStage + s * kStage + warp * (kWarpKeys / 8) * kUnitBytes;
+      // the warp's keys of a tile; EDGE: some row misses one of them
+      const auto walk = [&](auto edge_tag, uint32_t ks, int k0) {
+        constexpr bool EDGE = decltype(edge_tag)::value;
         const uint32_t vs = ks + kHalf;
-        const int k0 = t * kTileKeys + warp * kWarpKeys;
-        const bool edge = past_limit(k0, kWarpKeys, first_lim);  // some row misses a key
-
-        // scores in base 2: [.][step][key g, key g + 8 of the step][row 2 tq, 2 tq + 1]
-        float p[kCols][kSteps][2][2];
+        // scales, each twice, to where the lanes of a key find them: keys `lane` and 32 on
+        bool odd = false;  // a scale of the edge that some row must not meet
+        float2 v_s[2];     // low and high channels
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int key = lane + 32 * x;
+          const int at = (key >> 3) * kUnitBytes + kUnitScales + (key & 7) * 4;
+          const uint32_t kw = lds32(ks + at);
+          uint32_t vw = lds32(vs + at);
+          if (EDGE) {
+            // keys that no row sees count as zero whatever stands there, and so, for
+            // now, does one that some row misses and that is not finite
+            if (k0 + key >= n_keys) vw = 0;
+            if (k0 + key >= first_lim && odd_scale<BF16>(vw)) vw = 0, odd = true;
+          }
+          const float lo = half_to_f32<BF16>((uint16_t)kw),
+                      hi = half_to_f32<BF16>((uint16_t)(kw >> 16));
+          v_s[x] = make_float2(half_to_f32<BF16>((uint16_t)vw),
+                               half_to_f32<BF16>((uint16_t)(vw >> 16)));
+          const float2 v = make_float2(v_s[x].x * v_inv, v_s[x].y * v_inv);
+          s_scale[key] = make_float4(lo, lo, hi, hi);
+          s_scale[kTileKeys + key] = make_float4(v.x, v.x, v.y, v.y);
+        }
+        __syncwarp();
+        // scores: [.][step][key g, key g + 8 of the step], rows 2 tq and 2 tq + 1
+        float2 sc[kCols][kSteps][2];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
           uint32_t x[4][4];  // product, fragment register
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {  // keys g and g + 8
-            const uint2 w = lds64(ks + (2 * i + u) * kUnitBytes + lane * 8);
-            raw_codes<BF16>(w.x, x[0][u], x[2][u], x[0][2 + u], x[2][2 + u]);
-            raw_codes<BF16>(w.y, x[1][u], x[3][u], x[1][2 + u], x[3][2 + u]);
-          }
-          float s_lo[2], s_hi[2];
-#pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t w = lds32(ks + (2 * i + u) * kUnitBytes + kUnitScales + g * 4);
-            s_lo[u] = half_to_f32<BF16>((uint16_t)w) * (a.c * Raw<BF16>::kLoUnit);
-            s_hi[u] = half_to_f32<BF16>((uint16_t)(w >> 16)) * (a.c * Raw<BF16>::kHiUnit);
+            const uint2 w = lds64(ks + (2 * i + u) * kUnitBytes + lane * 8);  // key g, g + 8
+            raw_codes(w.x, x[0][u], x[2][u], x[0][2 + u], x[2][2 + u]);
+            raw_codes(w.y, x[1][u], x[3][u], x[1][2 + u], x[3][2 + u]);
           }
+          const float4 s4[2] = {s_scale[16 * i + g], s_scale[16 * i + 8 + g]};
 #pragma unroll
           for (int n = 0; n < kCols; ++n) {
-            float lo[4] = {z_lo[n][0], z_lo[n][1], z_lo[n][0], z_lo[n][1]};
-            float hi[4] = {z_hi[n][0], z_hi[n][1], z_hi[n][0], z_hi[n][1]};
-            mma_16816<BF16>(lo, x[0], q[n][0][0], q[n][0][1]);
-            mma_16816<BF16>(hi, x[2], q[n][2][0], q[n][2][1]);
-            mma_16816<BF16>(lo, x[1], q[n][1][0], q[n][1][1]);
-            mma_16816<BF16>(hi, x[3], q[n][3][0], q[n][3][1]);
+            float lo[4], hi[4];
+            mma_f16(lo, x[0], q[n][0], z_lo[n]);
+            mma_f16(hi, x[2], q[n][2], z_hi[n]);
+            mma_f16(lo, x[1], q[n][1], lo);
+            mma_f16(hi, x[3], q[n][3], hi);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                p[n][i][u][e] = fmaf(lo[2 * u + e], s_lo[u], hi[2 * u + e] * s_hi[u]);
+              sc[n][i][u] = __ffma2_rn(
+                  make_float2(lo[2 * u], lo[2 * u + 1]), make_float2(s4[u].x, s4[u].y),
+                  __fmul2_rn(make_float2(hi[2 * u], hi[2 * u + 1]),
+                             make_float2(s4[u].z, s4[u].w)));
           }
         }
-        if (edge) {
+        if (EDGE) {
+          const int n_new = s_item[qbuf].r.n_new;
 #pragma unroll
-          for (int n = 0; n < kCols; ++n)
+          for (int n = 0; n < kCols; ++n) {
+            const int lim0 = row_limit(n_keys, n_new, (8 * n + 2 * tq) / a.G),
+                      lim1 = row_limit(n_keys, n_new, (8 * n + 2 * tq + 1) / a.G);
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-              for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (k0 + 16 * i + 8 * u + g >= lim[n][e]) p[n][i][u][e] = -INFINITY;
-        }
-        float top[kCols][2];
-        bool grew = false;
-#pragma unroll
-        for (int n = 0; n < kCols; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            top[n][e] = fmaxf(p[n][0][0][e], p[n][0][1][e]);
-#pragma unroll
-            for (int i = 1; i < kSteps; ++i)
-              top[n][e] = fmax3(top[n][e], p[n][i][0][e], p[n][i][1][e]);
-            grew |= top[n][e] > m[n][e] + kSlack;
-          }
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-          for (int n = 0; n < kCols; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = top[n][e];
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              if (x > m[n][e]) {
-                const float f = ex2_approx(m[n][e] - x);
-                m[n][e] = x;
-                l[n][e] *= f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[n][j][e] *= f, o[n][j][2 + e] *= f;
+              for (int u = 0; u < 2; ++u) {
+                const int key = k0 + 16 * i + 8 * u + g;
+                if (key >= lim0) sc[n][i][u].x = -INFINITY;
+                if (key >= lim1) sc[n][i][u].y = -INFINITY;
               }
+          }
+        }
+        float2 p[kCols][kSteps][2], sum[kCols];
+        const auto weigh = [&] {
+          bool big = false;
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float2 x = __ffma2_rn(sc[n][i][u], unit[n], neg_m[n]);
+                p[n][i][u] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                sum[n] = i + u ? __fadd2_rn(sum[n], p[n][i][u]) : p[n][i][u];
+              }
+            big |= sum[n].x > most[n].x || sum[n].y > most[n].y;
+          }
+          return big;
+        };
+        const float v_top = fmaxf(fmaxf(fabsf(v_s[0].x), fabsf(v_s[0].y)),
+                                  fmaxf(fabsf(v_s[1].x), fabsf(v_s[1].y)));  // less NaN
+        const bool big = weigh();
+        if (__any_sync(0xffffffffu, big || v_top > v_most)) {
+          // V's unit: a power of two at the largest scale that is finite
+          float v = 0.f, fv = 1.f;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (fabsf(v_s[x].x) < INFINITY) v = fmaxf(v, fabsf(v_s[x].x));
+            if (fabsf(v_s[x].y) < INFINITY) v = fmaxf(v, fabsf(v_s[x].y));
+          }
+          v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+          if (v > v_most) {
+            const int ex = max((int)(__float_as_uint(v) >> 23) - 127, -110);
+            const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+            fv = inv / v_inv;  // O is zero before the first
+            v_inv = inv;
+            v_most = __uint_as_float((uint32_t)(min(ex + kVSlack, 127) + 127) << 23);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float2 y = make_float2(v_s[x].x * v_inv, v_s[x].y * v_inv);
+              s_scale[kTileKeys + lane + 32 * x] = make_float4(y.x, y.x, y.y, y.y);
             }
+          }
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) {
+            float2 x = make_float2(-INFINITY, -INFINITY), f = make_float2(1.f, 1.f);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              x.x = fmax3(x.x, sc[n][i][0].x, sc[n][i][1].x);
+              x.y = fmax3(x.y, sc[n][i][0].y, sc[n][i][1].y);
+            }
+#pragma unroll
+            for (int by = 4; by < 32; by <<= 1) {
+              x.x = fmaxf(x.x, __shfl_xor_sync(0xffffffffu, x.x, by));
+              x.y = fmaxf(x.y, __shfl_xor_sync(0xffffffffu, x.y, by));
+            }
+            follow(x.x, unit[n].x, &neg_m[n].x, &most[n].x, &l[n].x, &f.x);
+            follow(x.y, unit[n].y, &neg_m[n].y, &most[n].y, &l[n].y, &f.y);
+            f.x *= fv, f.y *= fv;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              o[n][j][0] *= f.x, o[n][j][2] *= f.x;
+              o[n][j][1] *= f.y, o[n][j][3] *= f.y;
+            }
+          }
           __syncwarp();
+          weigh();
         }
-        uint32_t pf[kCols][kSteps][2];
 #pragma unroll
-        for (int n = 0; n < kCols; ++n) {
-          const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
-          const float u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              p[n][i][u][0] = ex2_approx(p[n][i][u][0] - u0);
-              p[n][i][u][1] = ex2_approx(p[n][i][u][1] - u1);
-              l[n][0] += p[n][i][u][0];
-              l[n][1] += p[n][i][u][1];
-              pf[n][i][u] = transpose8(pack2<BF16>(p[n][i][u][0], p[n][i][u][1]));
-            }
-        }
-        bool odd = false;  // a scale of the edge that some row must not meet
+        for (int n = 0; n < kCols; ++n) l[n] = __fadd2_rn(l[n], sum[n]);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
+          uint32_t pf[kCols][2][2];  // [.][low, high channels][keys]
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float4 s4 = s_scale[kTileKeys + 16 * i + 8 * u + g];
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) {
+              const float2 lo = __fmul2_rn(p[n][i][u], make_float2(s4.x, s4.y)),
+                           hi = __fmul2_rn(p[n][i][u], make_float2(s4.z, s4.w));
+              pf[n][0][u] = transpose8(pack_f16x2(lo.x, lo.y));
+              pf[n][1][u] = transpose8(pack_f16x2(hi.x, hi.y));
+            }
+          }
           uint32_t w[4];
           ldmatrix_x4_trans(vs + (2 * i + (mi & 1)) * kUnitBytes + mr * 32 + (mi >> 1) * 16, w);
-          uint32_t s_lo[2], s_hi[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {  // keys 2 tq and the next of either unit
-            uint2 sw = lds64(vs + (2 * i + u) * kUnitBytes + kUnitScales + tq * 8);
-            if (edge) {
-              // keys that no row sees count as zero whatever stands there, and so, for
-              // now, does one that some row misses and that is not finite
-              const int key = k0 + 16 * i + 8 * u + 2 * tq;
-              if (key >= r.n_keys) sw.x = 0;
-              if (key + 1 >= r.n_keys) sw.y = 0;
-              if (key >= first_lim && odd_scale<BF16>(sw.x)) sw.x = 0, odd = true;
-              if (key + 1 >= first_lim && odd_scale<BF16>(sw.y)) sw.y = 0, odd = true;
-            }
-            s_lo[u] = __byte_perm(sw.x, sw.y, 0x5410);
-            s_hi[u] = __byte_perm(sw.x, sw.y, 0x7632);
-          }
           // channel tiles 2 g, 32 + 2 g, 2 g + 1, 33 + 2 g (rows g; + 16 in rows g + 8)
           uint32_t x[4][4];
-          scaled_codes<BF16>(w[0], s_lo[0], s_hi[0], x[0][0], x[1][0], x[2][0], x[3][0]);
-          scaled_codes<BF16>(w[2], s_lo[0], s_hi[0], x[0][1], x[1][1], x[2][1], x[3][1]);
-          scaled_codes<BF16>(w[1], s_lo[1], s_hi[1], x[0][2], x[1][2], x[2][2], x[3][2]);
-          scaled_codes<BF16>(w[3], s_lo[1], s_hi[1], x[0][3], x[1][3], x[2][3], x[3][3]);
+          signed_codes(w[0], x[0][0], x[1][0], x[2][0], x[3][0]);
+          signed_codes(w[2], x[0][1], x[1][1], x[2][1], x[3][1]);
+          signed_codes(w[1], x[0][2], x[1][2], x[2][2], x[3][2]);
+          signed_codes(w[3], x[0][3], x[1][3], x[2][3], x[3][3]);
 #pragma unroll
           for (int n = 0; n < kCols; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_16816<BF16>(o[n][j], x[j], pf[n][i][0], pf[n][i][1]);
+            for (int j = 0; j < 4; ++j) mma_f16(o[n][j], x[j], pf[n][j & 1], o[n][j]);
         }
-        if (edge && __any_sync(0xffffffffu, odd)) {
-          // what those keys give the rows that see them
+        if (EDGE && __any_sync(0xffffffffu, odd)) {
+          // what those keys give the rows that see them: infinities and NaN, of
+          // whatever unit
+          const int n_new = s_item[qbuf].r.n_new;
 #pragma unroll
           for (int i = 0; i < kSteps; ++i)
 #pragma unroll
@@ -444,57 +596,82 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
 #pragma unroll 1
               for (int k = 0; k < 8; ++k) {
                 const int key = k0 + 16 * i + 8 * u + k;
-                const uint32_t unit = vs + (2 * i + u) * kUnitBytes;
-                const uint32_t sw = lds32(unit + kUnitScales + 4 * k);
-                float wt[kCols][2];
+                const uint32_t at = vs + (2 * i + u) * kUnitBytes;
+                const uint32_t sw = lds32(at + kUnitScales + 4 * k);
+                if (key < first_lim || key >= n_keys || !odd_scale<BF16>(sw)) continue;
 #pragma unroll
                 for (int n = 0; n < kCols; ++n)
 #pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    wt[n][e] = __shfl_sync(0xffffffffu, p[n][i][u][e], 4 * k + tq);
-                if (key < first_lim || key >= r.n_keys || !odd_scale<BF16>(sw)) continue;
+                  for (int e = 0; e < 2; ++e) {
+                    const float wt = __shfl_sync(0xffffffffu, e ? p[n][i][u].y : p[n][i][u].x, 4 * k + tq);
+                    const int lim = row_limit(n_keys, n_new, (8 * n + 2 * tq + e) / a.G);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {  // row g + 8 h of channel tile j
-                    const int byte = 16 * h + 2 * g + (j >> 1);
-                    const uint32_t b = smem[unit - sbase + k * 32 + byte] >> (4 * (j & 1));
-                    const float v = (float)((int)(b & 15) - 8) *
-                                    half_to_f32<BF16>((uint16_t)(sw >> (16 * (j & 1))));
-#pragma unroll
-                    for (int n = 0; n < kCols; ++n)
-#pragma unroll
-                      for (int e = 0; e < 2; ++e)
-                        if (key < lim[n][e])
-                          o[n][j][2 * h + e] = fmaf(wt[n][e], v, o[n][j][2 * h + e]);
+                      for (int h = 0; h < 2; ++h) {  // row g + 8 h of channel tile j
+                        const int byte = 16 * h + 2 * g + (j >> 1);
+                        const uint32_t b = smem[at - sbase + k * 32 + byte] >> (4 * (j & 1));
+                        const float v = (float)((int)(b & 15) - 8) *
+                                        half_to_f32<BF16>((uint16_t)(sw >> (16 * (j & 1))));
+                        // the row's other group, if finite, was dropped as well
+                        const float f = v * v_inv * ((j & 1) ? 0x1p-20f : 0x1p-24f);
+                        if (key < lim) o[n][j][2 * h + e] = fmaf(wt, f, o[n][j][2 * h + e]);
+                      }
                   }
               }
         }
+      };
+      for (int t = sg.t0 + (warp + kConsumers - it % kConsumers) % kConsumers; t < t1;
+           t += kConsumers) {
+        const int s = warp * kRing + slot;
+        ok = mbar_nap_warp(BAR(BAR_FULL + s), turn, wc);
+        if (!ok) break;
+        if (++slot == kRing) slot = 0, turn ^= 1;
+        const uint32_t ks = sbase + C::kSmemStage + s * kStage;
+        if (__builtin_expect(past_limit(t * kTileKeys, kTileKeys, first_lim), 0))
+          walk(std::true_type{}, ks, t * kTileKeys);
+        else
+          walk(std::false_type{}, ks, t * kTileKeys);
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(BAR_EMPTY + s));
       }
+      it += t1 - sg.t0;
+      const Request r = sg.r;
+      const int rows = r.n_new * a.G;
 
       // ---------------- the consumer warps meet ----------------
+      constexpr int kWarpLd = C::kJoin / 4;
+      __syncwarp();  // the scales have been read
 #pragma unroll
-      for (int n = 0; n < kCols; ++n)
+      for (int n = 0; n < kCols; ++n) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
-          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
-          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
-          const int row = warp * kRows + 8 * n + 2 * tq + e;
-          if (g == 0) s_ml[row] = make_float2(m[n][e], l[n][e]);
+        for (int by = 4; by < 32; by <<= 1) {
+          l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, by);
+          l[n].y += __shfl_xor_sync(0xffffffffu, l[n].y, by);
+        }
+        const int row = 8 * n + 2 * tq;
+        if (g == 0) {
+          s_ml[warp * kRows + row] =
+              make_float2(most[n].x < 0.f ? -INFINITY : -neg_m[n].x, l[n].x);
+          s_ml[warp * kRows + row + 1] =
+              make_float2(most[n].y < 0.f ? -INFINITY : -neg_m[n].y, l[n].y);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)  // low and high channels
-              *reinterpret_cast<float2*>(s_join + row * kLd + 32 * x + 16 * h + 2 * g) =
-                  make_float2(o[n][x][2 * h + e], o[n][2 + x][2 * h + e]);
-        }
+            for (int x = 0; x < 2; ++x) {  // low and high channels
+              const float f = (x ? 0x1p20f : 0x1p24f) / v_inv;
+              *reinterpret_cast<float2*>(s_join + warp * kWarpLd + (row + e) * kLd + 32 * x + 16 * h +
+                                         2 * g) =
+                  make_float2(o[n][x][2 * h + e] * f, o[n][2 + x][2 * h + e] * f);
+            }
+      }
       // where a wait gave up, all leave together
       if (named_barrier_any(1, kConsumers * 32, !ok)) break;
-      const int row = tid >> 3, c0 = (tid & 7) * 8;
-      if (row < rows && row < kRows) {
+      const int c0 = (tid & 7) * 8;
+      for (int row = (tid - 32) >> 3; row < min(rows, kRows); row += kConsumers * 4) {
         float mm = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) mm = fmaxf(mm, s_ml[w * kRows + row].x);
@@ -506,7 +683,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
           if (ml.x == -INFINITY && ml.y == 0.f) continue;
           const float f = ex2_approx(ml.x - mm);
           ll = fmaf(ml.y, f, ll);
-          const float* const d = s_join + (w * kRows + row) * kLd + c0;
+          const float* const d = s_join + w * kWarpLd + row * kLd + c0;
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e] = fmaf(d[e], f, acc[e]);
         }
@@ -517,6 +694,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
           store_part(a.part, blockIdx.x, sg.t0 == 0, row, c0, acc, mm, ll);
       }
       named_barrier_sync(1, kConsumers * 32);
+      if (lane == 0) mbar_arrive(BAR(BAR_Q_FREE + qbuf));
     }
   }
 #undef BAR
@@ -525,9 +703,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
 template <class C>
 int launch(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
            const PoolArg& vc, const DecodeArgs& args, int blocks, int which, cudaStream_t stream) {
-  CUtensorMap tq;
+  CUtensorMap tq, tk, tv;
+  const uint32_t units = (1u << d.shift) / 8;
+  const uint32_t box = units < kTileKeys / 8 ? units : kTileKeys / 8;
   if (!encode_tmap_4d(&tq, d.bf16, q.p, d.G, d.Hkv, d.tokens, q.h, q.h * d.G, q.t, d.G, 1,
-                      args.ntok))
+                      args.ntok) ||
+      !encode_tmap_units(&tk, kc.p, units, d.Hkv, d.pages, kc.h, kc.pg, box) ||
+      !encode_tmap_units(&tv, vc.p, units, d.Hkv, d.pages, vc.h, vc.pg, box))
     return ATTN_ERR_CUDA;
   const size_t smem = C::kSmemPre + 8 * (size_t)(d.batch + 1) + 1024;
   auto* kernel = d.bf16 ? paged_decode4_kernel<true, C> : paged_decode4_kernel<false, C>;
@@ -535,7 +717,7 @@ int launch(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolAr
                             C::kSmemPre + 8 * (kMaxPagedBatch + 1) + 1024);
   if (rc != ATTN_OK) return rc;
   return cuda_status(launch_dependent(kernel, dim3(blocks), dim3(C::kThreads), smem, stream, tq,
-                                      args, kc, vc));
+                                      tk, tv, args, kc, vc));
 }
 
 }  // namespace
@@ -543,13 +725,23 @@ int launch(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolAr
 // A table that leaves a request one tile gives every item to one block.
 bool decode4_whole(const PagedDims& d) { return ((long long)d.width << d.shift) <= kTileKeys; }
 
+namespace {
+// Column tiles of a call: as many tokens as it has at most, so that a token step of
+// up to eight heads a group needs one.
+int tokens4(const PagedDims& d) {
+  return d.max_new < decode_tokens(d.G) ? d.max_new : decode_tokens(d.G);
+}
+}  // namespace
+
+int decode4_blocks(const PagedDims& d) {
+  return tokens4(d) * d.G <= 8 ? Config<1>::kBlocks : Config<2>::kBlocks;
+}
+
 int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
                          const PoolArg& kc, const PoolArg& vc, const int32_t* table,
                          const int32_t* cu, const int32_t* lens, const PartArgs& part, int blocks,
                          const RowsArg& o, float* lse, cudaStream_t stream) {
-  // as many tokens as a call has at most: a token step of up to eight heads a group
-  // needs one column tile
-  const int ntok = d.max_new < decode_tokens(d.G) ? d.max_new : decode_tokens(d.G);
+  const int ntok = tokens4(d);
   const DecodeArgs args{d.batch, d.tokens, d.H, d.Hkv, d.G, ntok, d.max_new, d.pages, d.width,
                         d.shift, d.c, cu, lens, table, o, lse, part, ctx.err, ctx.wait_ns};
   if (ntok * d.G <= 8)

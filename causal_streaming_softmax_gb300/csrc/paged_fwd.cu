@@ -100,6 +100,7 @@ int launch_join(const PagedDims& d, const DevCtx& ctx, const PartArgs& p1, int n
 // The largest grid of the split kernels on any device this library runs on:
 // the workspace's size must not depend on the current device.
 constexpr int kMaxSm = 160;
+constexpr int kFewBlocks = 3;  // blocks a SM of the kernels for few rows, at most
 
 }  // namespace
 
@@ -137,14 +138,16 @@ PartArgs parts_at(void* ws, size_t blocks, int rows, int min_tiles) {
 // parts costs more than its tiles.  Few rows (64-key tiles), us with at least
 // 1 / 2 / 4: one request of 100 keys 6.6 / 5.8 / 7.7, of 777 7.8 / 7.8 / 9.0, of
 // 4000 11.2 / 9.5 / 10.6, eight of 256 7.7 / 7.9 / 7.3, 64 of 60 7.8 / 7.7 / 11.1.
+// The same of 4 bits, us with at least 1 / 2 / 4: one request of 777 keys 8.9 / 9.5 /
+// 9.7, of 4000 14.3 / 11.4 / 11.1, eight of 250 8.5 / 8.4 / 7.4, 64 of 17..512 13.9 /
+// 13.8 / 16.2.
 constexpr int kLeastFew = 2, kLeastRows = 2;
-constexpr int kLeastFew4 = 1;  // 256-key tiles of a 4-bit cache
 
 }  // namespace
 
 size_t paged_workspace_bytes(const PagedDims& d) {
   const int ntok = decode_tokens(d.G);
-  return (ntok > 0 ? parts_bytes(2 * kMaxSm, kDecodeRows) : 0) +
+  return (ntok > 0 ? parts_bytes(kFewBlocks * kMaxSm, kDecodeRows) : 0) +
          (d.max_new > ntok ? parts_bytes(kMaxSm, kItemRows) : 0);
 }
 
@@ -158,12 +161,13 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
   PartArgs few{}, rows{};
   int n_few = 0, n_rows = 0, rc;
   if (ntok > 0) {
-    few = parts_at(at, 2 * kMaxSm, kDecodeRows, four ? kLeastFew4 : kLeastFew);
-    at += parts_bytes(2 * kMaxSm, kDecodeRows);
+    const int blocks = (four ? decode4_blocks(d) : 2) * sms;
+    few = parts_at(at, kFewBlocks * kMaxSm, kDecodeRows, kLeastFew);
+    at += parts_bytes(kFewBlocks * kMaxSm, kDecodeRows);
     rc = (four ? launch_paged_decode4 : launch_paged_decode)(d, ctx, q, kc, vc, table, cu, lens,
-                                                             few, 2 * sms, o, lse, stream);
+                                                             few, blocks, o, lse, stream);
     if (rc != ATTN_OK) return rc;
-    if (!(four ? decode4_whole(d) : decode_whole(d, ctx.sm_count))) n_few = 2 * sms;
+    if (!(four ? decode4_whole(d) : decode_whole(d, ctx.sm_count))) n_few = blocks;
   }
   if (d.max_new > ntok) {
     rows = parts_at(at, kMaxSm, kItemRows, kLeastRows);

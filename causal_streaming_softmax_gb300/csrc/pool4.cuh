@@ -87,51 +87,24 @@ __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
   return r;
 }
 
-// The bits of 16 + code of the half bytes that `shift` brings to bits 3..6 of each
+// The bits of 16 + code of the half bytes that a shift brought to bits 3..6 of each
 // 16-bit half, as bfloat16.
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
   return (w & 0x00780078u) | 0x41804180u;
 }
 
-// A word of codes as pairs of operands: the low and high halves of bytes 0 and 2,
-// then of bytes 1 and 3.  binary16: code' * 2^-24 and code' * 2^-20; bfloat16:
-// 16 + code' (code' = code + 8).
-template <bool BF16>
-__device__ __forceinline__ void raw_codes(uint32_t w, uint32_t& lo0, uint32_t& hi0, uint32_t& lo1,
-                                          uint32_t& hi1) {
-  if (BF16) {
-    lo0 = codes_bf16(w << 3);
-    hi0 = codes_bf16(w >> 1);
-    lo1 = codes_bf16(w >> 5);
-    hi1 = codes_bf16(w >> 9);
-  } else {
-    const uint32_t v = w >> 8;
-    lo0 = w & 0x000f000fu;
-    hi0 = w & 0x00f000f0u;
-    lo1 = v & 0x000f000fu;
-    hi1 = v & 0x00f000f0u;
-  }
-}
-// What stands in a product for code -8, low and high half, and what a score is
-// multiplied by beside the scale.
-template <bool BF16>
-struct Raw {
-  static constexpr float kLoZero = BF16 ? 24.f : 0x1p-21f, kHiZero = BF16 ? 24.f : 0x1p-17f;
-  static constexpr float kLoUnit = BF16 ? 1.f : 0x1p24f, kHiUnit = BF16 ? 1.f : 0x1p20f;
-};
-
-// The same word as code * scale; the scales are those of the two keys of a pair.
+// A word of codes as pairs of code * scale: the low and high halves of bytes 0 and
+// 2, then of bytes 1 and 3.
 template <bool BF16>
 __device__ __forceinline__ void scaled_codes(uint32_t w, uint32_t s_lo, uint32_t s_hi, uint32_t& lo0,
                                              uint32_t& hi0, uint32_t& lo1, uint32_t& hi1) {
   if (BF16) {
     // (16 + code') s - 24 s: both exact, as s has five significant bits
     const uint32_t z_lo = mul2<true>(s_lo, 0xc1c0c1c0u), z_hi = mul2<true>(s_hi, 0xc1c0c1c0u);
-    raw_codes<true>(w, lo0, hi0, lo1, hi1);
-    lo0 = fma2<true>(lo0, s_lo, z_lo);
-    hi0 = fma2<true>(hi0, s_hi, z_hi);
-    lo1 = fma2<true>(lo1, s_lo, z_lo);
-    hi1 = fma2<true>(hi1, s_hi, z_hi);
+    lo0 = fma2<true>(codes_bf16(w << 3), s_lo, z_lo);
+    hi0 = fma2<true>(codes_bf16(w >> 1), s_hi, z_hi);
+    lo1 = fma2<true>(codes_bf16(w >> 5), s_lo, z_lo);
+    hi1 = fma2<true>(codes_bf16(w >> 9), s_hi, z_hi);
   } else {
     // 1024 + code' - 1032 and (1024 + 16 code') / 16 - 72, then times s
     constexpr uint32_t kOne = 0x3c003c00u, kSixteenth = 0x2c002c00u, kM = 0x64006400u,

@@ -60,6 +60,7 @@ int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, c
                       bool four, const RowsArg& o, float* lse, cudaStream_t stream);
 // The same over a 4-bit cache (the pools' strides in bytes).
 bool decode4_whole(const PagedDims& d);
+int decode4_blocks(const PagedDims& d);  // a SM
 int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
                          const PoolArg& kc, const PoolArg& vc, const int32_t* table,
                          const int32_t* cu, const int32_t* lens, const PartArgs& part, int blocks,
@@ -91,6 +92,11 @@ int allow_smem(int which, const void* kernel, size_t bytes);
 bool encode_tmap_4d(CUtensorMap* map, bool bf16, const void* base, uint64_t d1, uint64_t d2,
                     uint64_t d3, uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b1, uint32_t b2,
                     uint32_t b3);
+
+// A rank-4 tiled tensor map of a 4-bit pool: a unit of eight rows, units of a page,
+// heads, pages, boxes of `box` units.
+bool encode_tmap_units(CUtensorMap* map, const void* base, uint64_t units, uint64_t heads,
+                       uint64_t pages, uint64_t head_bytes, uint64_t page_bytes, uint32_t box);
 
 int launch_packed_fwd(const PackedDims& d, const DevCtx& ctx, const RowsArg& q, const RowsArg& k,
                       const RowsArg& v, const int32_t* cu, const RowsArg& o, float* lse,

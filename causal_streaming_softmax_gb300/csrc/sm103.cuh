@@ -190,6 +190,37 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, co
   return __all_sync(0xffffffffu, ok);
 }
 
+// mbar_wait_warp that sleeps up to kNapNs at a time in the hardware: a warp that
+// waits for most of its life polls some ten times a microsecond otherwise, on issue
+// slots that the block's other warps want.
+constexpr uint32_t kNapNs = 20000;
+
+static __device__ __noinline__ bool mbar_nap(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kNapNs)
+        : "memory");
+    if (ok) return true;
+    if (*w.abort) return false;
+    if (global_timer_ns() - t0 > w.limit_ns) {
+      *w.abort = 1;
+      if (w.err) atomicOr(w.err, kErrWaitTimeout);
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ bool mbar_nap_warp(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  const bool ok = mbar_try_wait(bar, parity) || mbar_nap(bar, parity, w);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // mbar_wait_warp without a call: for code that holds more registers than a
 // call preserves (a call there moves them through local memory).
 __device__ __forceinline__ bool mbar_wait_inline(uint32_t bar, uint32_t parity, const WaitCtl& w) {

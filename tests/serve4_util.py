@@ -5,15 +5,20 @@ Rows in and out are compared bit for bit: the rotation's products and sums and a
 code's quotient are single binary32 operations, a scale's roundings are exact in
 64 bits, and code * scale is exact in the type.
 
-Attention: the bound of serve_util with another error of the scores.  The kernel
-for few rows sums q * x over codes x as they stand in its operands (binary16 code +
-8 from a start of -8 sum q, so |x| + 8 <= 23; bfloat16 16 + code + 8 from -24 sum q,
-so at most 31 + 24 = 55) and applies the scale afterwards: 64 products, two starts
-and the sum of q (32 and two shuffles), each rounded or cut to 24 bits, three
-roundings of the scaling: (64 + 2 + 34 + 3) 2^-23 sum_d |q_d| X s_d c with X = 23
-or 55.  The kernel for many rows forms exact 16-bit values first, which is less.
-Its maximum may stand back by 2^8 behind the true one: weights are then larger,
-never smaller, so the spacing of small binary16 weights is what it was.
+Attention: the bound of serve_util with another error of the scores and of small
+weights.  The kernel for few rows sums q * (code + 8) from a start of -8 sum q, so
+that a term has up to |q| (15 + 8), and applies the scale afterwards: 64 products,
+two starts and the sum of q (32 and two shuffles), each rounded or cut to 24 bits,
+three roundings of the scaling: 103 * 2^-23 sum_d |q_d| 23 s_d c; q itself goes in
+as binary16 with the row's largest element between 2^9 and 2^10, whose spacing of
+2^-24 at the small end is 2^-34 of that: with the binary32 roundings above, 2^-33
+max |q| sum_d 23 s_d c more.  The kernel for many rows forms exact 16-bit values
+first, which is less.
+Weights times V's scales are binary16 in the kernel for few rows, a weight of 1
+counting 2^10 and the scales in a unit of at most the largest of them, S: spacing
+2^-24, so a key's share of O is off by up to 2^-25 2^-10 8 S, the sum of weights
+being at least one: 2^-32 n S.  The kernel for many rows rounds weights to the type
+(binary16: 2^-25 sum |v_j|).
 Weights below 2^-126 count as zero (the exponential gives no subnormal numbers), and
 so may a subnormal product: 2^-126 (sum |v_j| + 1), which only an element whose
 large values all have such weights comes near (one of 1.27e-38 did, where the bound
@@ -94,9 +99,10 @@ def pool_of(x, dtype):
     return torch.cat([b[..., :32].flatten(-2), b[..., 32:].flatten(-2)], -1).contiguous()
 
 
-def attend4(q, k, ks, v, seen, scale=0.125):
-    """q [n, H, 64] 16-bit; k, ks, v [m, Hkv, 64] in 64 bits; row i sees the first
-    seen[i] keys.  Returns O, L (base 2) and their tolerances."""
+def attend4(q, k, ks, v, vs, seen, scale=0.125):
+    """q [n, H, 64] 16-bit; k, v [m, Hkv, 64] in 64 bits and ks, vs their scales'
+    magnitudes; row i sees the first seen[i] keys.  Returns O, L (base 2) and their
+    tolerances."""
     n, H, _ = q.shape
     m, Hkv, _ = k.shape
     g = H // Hkv
@@ -117,7 +123,9 @@ def attend4(q, k, ks, v, seen, scale=0.125):
         kd, sd, vd = (torch.where(used, x[:, h // g], 0.0) for x in (k, ks, v))
         t = (qd @ kd.T) * c
         sd = torch.nan_to_num(sd, 0.0, 0.0, 0.0)
-        terr = 103 * 2.0 ** -23 * (23 if f16 else 55) * c * (qd.abs() @ sd.T)
+        terr = 103 * 2.0 ** -23 * 23 * c * (torch.nan_to_num(qd, 0.0, 0.0, 0.0).abs() @ sd.T)
+        big = torch.nan_to_num(qd, 0.0, 0.0, 0.0).abs().amax(1, keepdim=True)
+        terr = terr + 2.0 ** -33 * 23 * c * big * sd.sum(1)
         terr = terr + 2 * 2.0 ** -23 * torch.nan_to_num(t, 0.0, 0.0, 0.0).abs()
         terr = terr.masked_fill(mask, 0.0).amax(1)
         t = t.masked_fill(mask, -math.inf)
@@ -137,6 +145,8 @@ def attend4(q, k, ks, v, seen, scale=0.125):
                     s_h[i] = vd[:x].abs().sum(0)
         d = LN2 * terr + 2.0 ** -21
         tol = u * o_h.abs() + (u + 2 * d[:, None]) * a_h + 2.0 ** -126 * (s_h + 1)
+        top = torch.nan_to_num(torch.where(used, vs[:, h // g], 0.0), 0.0, 0.0, 0.0).max()
+        tol = tol + 2.0 ** -32 * m * top
         if f16:
             tol = tol + 2.0 ** -25 * s_h + 2.0 ** -25
         o[:, h] = torch.where(some[:, None], o_h, 0.0)
@@ -159,12 +169,12 @@ def gather(pool, row, n):
 def paged4_64(q, kc, vc, table, cu, lens, scale=0.125):
     """[(rows, O, L, tolerances)] of every request over 4-bit pools."""
     k, ks = values(kc, q.dtype)
-    v, _ = values(vc, q.dtype)
+    v, vs = values(vc, q.dtype)
     out = []
     for i, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
         n, m = b - a, lens[i]
         seen = (m - n + 1 + torch.arange(n, device=q.device)).clamp(min=0)
         out.append((slice(a, b),) + attend4(q[a:b], gather(k, table[i], m),
-                                            gather(ks, table[i], m), gather(v, table[i], m), seen,
-                                            scale))
+                                            gather(ks, table[i], m), gather(v, table[i], m),
+                                            gather(vs, table[i], m), seen, scale))
     return out

@@ -558,10 +558,10 @@ def test_paged4_the_largest_batch(torch, heads):
     q, kc, vc, table, cu, lens, _ = paged4_problem(torch, reqs, H, Hkv, 16, torch.float16, 2)
     o, L = run_paged4(torch, q, kc, vc, table, cu, lens)
     pick = [0, 1, 59, 60, 2047, 3333, 4095]
-    k, ks, v = values(kc, q.dtype) + values(vc, q.dtype)[:1]
+    pools = values(kc, q.dtype) + values(vc, q.dtype)
     tt = torch.tensor(table, dtype=torch.int64, device="cuda")
     for i in pick:
-        eo, el, to, tl = attend4(q[i:i + 1], *(gather(x, tt[i], lens[i]) for x in (k, ks, v)),
+        eo, el, to, tl = attend4(q[i:i + 1], *(gather(x, tt[i], lens[i]) for x in pools),
                                  torch.tensor([lens[i]], device="cuda"))
         check(o[i:i + 1], eo, to, "O of %d" % i)
         check(L[:, i:i + 1], el, tl, "L of %d" % i)
@@ -590,8 +590,9 @@ def test_pools_beyond_32_bits(torch):
         q = rnd(torch, (new, 8, 64), dt, 3, 2.0)
         o, L = run_paged4(torch, q, kc, vc, [ids], [0, new], [n])
         kd, vd = ko.double(), vo.double()
-        sc = quantise(k.float(), dt)[1].double().abs().repeat_interleave(32, -1)
-        eo, el, to, tl = attend4(q, kd, sc, vd,
+        sk, sv = (quantise(x.float(), dt)[1].double().abs().repeat_interleave(32, -1)
+                  for x in (k, v))
+        eo, el, to, tl = attend4(q, kd, sk, vd, sv,
                                  torch.arange(n - new + 1, n + 1, device="cuda"))
         check(o, eo, to, "O")
         check(L, el, tl, "L")
@@ -606,7 +607,7 @@ def serve(torch, bits, turn, dtype, steps=14):
                            bits=bits)
     cos, sin = angles(torch, 640)
     r = random.Random(11)
-    hist = [[] for _ in range(B)]  # of each token: K, V, K's scales
+    hist = [[] for _ in range(B)]  # of each token: K, V, their scales
     for step in range(steps):
         fresh = [r.choice([1, 1, 1, r.randint(0, 70), -1 if len(hist[i]) > 150 else 1])
                  for i in range(B)]
@@ -635,13 +636,13 @@ def serve(torch, bits, turn, dtype, steps=14):
                 if bits == 4:
                     (kq, ks), (vq, vs) = quantise(kf, dt), quantise(v[rows].float(), dt)
                     ks, vs = (y.double().repeat_interleave(32, -1) for y in (ks, vs))
-                    hist[i] += list(zip(kq * ks, vq * vs, ks.abs()))
+                    hist[i] += list(zip(kq * ks, vq * vs, ks.abs(), vs.abs()))
                 else:
-                    hist[i] += list(zip(kf.to(dt), v[rows], kf))
-                kk, vv, ss = (torch.stack([h[j] for h in hist[i]]) for j in range(3))
+                    hist[i] += list(zip(kf.to(dt), v[rows], kf, kf))
+                kk, vv, ss, vss = (torch.stack([h[j] for h in hist[i]]) for j in range(4))
                 m = len(hist[i])
                 seen = torch.arange(m - f + 1, m + 1, device="cuda")
-                eo, el, to, tl = attend4(qr, kk, ss, vv, seen) if bits == 4 else \
+                eo, el, to, tl = attend4(qr, kk, ss, vv, vss, seen) if bits == 4 else \
                     attend64(qr, kk, vv, seen)
                 check(o[rows], eo, to, "step %d request %d" % (step, i))
                 check(L[:, rows], el, tl, "L of step %d request %d" % (step, i))
@@ -722,7 +723,7 @@ def test_a_position_past_the_tables_in_a_step(torch):
     vq, vs = quantise(x[11:, 6:].float(), torch.float16)
     ks, vs = (y.double().repeat_interleave(32, -1) for y in (ks, vs))
     eo, _, to, _ = attend4(rotate(x[11:, :4], cos[:3], sin[:3]).half(), kq * ks, ks.abs(), vq * vs,
-                           torch.arange(1, 4, device="cuda"))
+                           vs.abs(), torch.arange(1, 4, device="cuda"))
     check(o[11:], eo, to, "the other request")
 
 
