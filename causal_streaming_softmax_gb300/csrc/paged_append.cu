@@ -44,46 +44,62 @@ __device__ __forceinline__ int position_of(const AppendArgs& a, int t) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
+__device__ __forceinline__ void widen8(const uint4& w, float2 (&x)[4]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = half_to_f32<BF16>((uint16_t)u[i]);
-    x[2 * i + 1] = half_to_f32<BF16>((uint16_t)(u[i] >> 16));
-  }
+  for (int i = 0; i < 4; ++i)
+    x[i] = make_float2(half_to_f32<BF16>((uint16_t)u[i]), half_to_f32<BF16>((uint16_t)(u[i] >> 16)));
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
-  return make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]),
-                    pack2<BF16>(x[6], x[7]));
+__device__ __forceinline__ uint4 narrow8(const float2 (&x)[4]) {
+  return make_uint4(pack2<BF16>(x[0].x, x[0].y), pack2<BF16>(x[1].x, x[1].y),
+                    pack2<BF16>(x[2].x, x[2].y), pack2<BF16>(x[3].x, x[3].y));
 }
 
 // The four lanes of a row: extrema over the row's group.
-__device__ __forceinline__ void extrema(const float (&x)[8], float* mx, float* mn) {
-  *mx = *mn = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) *mx = max_nan(*mx, x[i]), *mn = min_nan(*mn, x[i]);
-#pragma unroll
-  for (int by = 1; by < 4; by <<= 1) {
-    *mx = max_nan(*mx, __shfl_xor_sync(0xffffffffu, *mx, by));
-    *mn = min_nan(*mn, __shfl_xor_sync(0xffffffffu, *mn, by));
-  }
+__device__ __forceinline__ void extrema(const float2 (&x)[4], float* mx, float* mn) {
+  *mx = *mn = x[0].x;
+  *mx = max3_nan(*mx, x[0].y, x[1].x), *mn = min3_nan(*mn, x[0].y, x[1].x);
+  *mx = max3_nan(*mx, x[1].y, x[2].x), *mn = min3_nan(*mn, x[1].y, x[2].x);
+  *mx = max3_nan(*mx, x[2].y, x[3].x), *mn = min3_nan(*mn, x[2].y, x[3].x);
+  // the last value and two lanes beside
+  const float a = max3_nan(*mx, x[3].y, x[3].y), b = min3_nan(*mn, x[3].y, x[3].y);
+  *mx = max3_nan(a, __shfl_xor_sync(0xffffffffu, a, 1), a);
+  *mn = min3_nan(b, __shfl_xor_sync(0xffffffffu, b, 1), b);
+  *mx = max3_nan(*mx, __shfl_xor_sync(0xffffffffu, *mx, 2), *mx);
+  *mn = min3_nan(*mn, __shfl_xor_sync(0xffffffffu, *mn, 2), *mn);
 }
 
-template <bool BF16, bool ROTATE, bool FOUR>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+// kSets: sets of eight rows that a warp takes of a token, their loads under way
+// before the position is known.
+template <bool BF16, bool ROTATE, bool FOUR, int kSets>
+__global__ void __launch_bounds__(kThreads, FOUR ? 3 : 4) append_kernel(const AppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, c0 = (lane & 3) * 8;
-  const int first = ROTATE ? 0 : a.H, rows = a.H + 2 * a.Hkv;  // without rotation q stays
-  const long long warps = (long long)gridDim.x * (kThreads / 32);
-  const long long n = (long long)a.tokens * a.parts;
+  const int rows = a.H + 2 * a.Hkv;  // without rotation q stays, and H is 0
+  const int warps = gridDim.x * (kThreads / 32);
+  const int first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   bool bad = false;
-  for (long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < n;
-       i += warps) {
+  for (long long i = first; i < (long long)a.tokens * a.parts; i += warps) {
     const int t = (int)quot(i, a.parts), part = (int)(i - (long long)t * a.parts);
     const int slot = a.slots[t];
+    uint4 w_lo[kSets], w_hi[kSets];
+    const int set0 = part * kSets;
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+      const int row = (set0 + j) * 8 + (lane >> 2);
+      w_lo[j] = w_hi[j] = make_uint4(0, 0, 0, 0);
+      if (row < rows) {
+        const bool is_q = row < a.H, is_v = row >= a.H + a.Hkv;
+        const int h = row - (is_q ? 0 : (is_v ? a.H + a.Hkv : a.H));
+        const RowsArg& src = is_q ? a.q : (is_v ? a.v : a.k);
+        const uint16_t* const p = static_cast<const uint16_t*>(src.p) + t * src.t + h * src.h + c0;
+        w_lo[j] = *reinterpret_cast<const uint4*>(p);
+        w_hi[j] = *reinterpret_cast<const uint4*>(p + 32);
+      }
+    }
     if (slot < 0) continue;
     const int page = slot >> a.shift, r = slot & ((1 << a.shift) - 1);
     const int pos = ROTATE ? position_of(a, t) : 0;
@@ -91,65 +107,62 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
       bad = true;
       continue;
     }
-    float co[8], si[8];
+    float2 co[4], si[4];
     if (ROTATE) {
       const float4* const c = reinterpret_cast<const float4*>(a.cos_tab + pos * 32ll + c0);
       const float4* const s = reinterpret_cast<const float4*>(a.sin_tab + pos * 32ll + c0);
-      const float4 c_lo = c[0], c_hi = c[1], s_lo = s[0], s_hi = s[1];
-      co[0] = c_lo.x, co[1] = c_lo.y, co[2] = c_lo.z, co[3] = c_lo.w;
-      co[4] = c_hi.x, co[5] = c_hi.y, co[6] = c_hi.z, co[7] = c_hi.w;
-      si[0] = s_lo.x, si[1] = s_lo.y, si[2] = s_lo.z, si[3] = s_lo.w;
-      si[4] = s_hi.x, si[5] = s_hi.y, si[6] = s_hi.z, si[7] = s_hi.w;
-    }
-    for (int row0 = first + part * a.per; row0 < min(rows, first + (part + 1) * a.per);
-         row0 += 8) {
-      const int row = row0 + (lane >> 2);
-      const bool live = row < rows, is_q = row < a.H, is_v = row >= a.H + a.Hkv;
-      const int h = live ? row - (is_q ? 0 : (is_v ? a.H + a.Hkv : a.H)) : 0;
-      const RowsArg& src = is_q ? a.q : (is_v ? a.v : a.k);
-      uint4 w_lo = make_uint4(0, 0, 0, 0), w_hi = w_lo;
-      if (live) {
-        const uint16_t* const p =
-            static_cast<const uint16_t*>(src.p) + t * src.t + h * src.h + c0;
-        w_lo = *reinterpret_cast<const uint4*>(p);
-        w_hi = *reinterpret_cast<const uint4*>(p + 32);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 cw = c[e], sw = s[e];
+        co[2 * e] = make_float2(cw.x, cw.y), co[2 * e + 1] = make_float2(cw.z, cw.w);
+        si[2 * e] = make_float2(sw.x, sw.y), si[2 * e + 1] = make_float2(sw.z, sw.w);
       }
-      float x[8], y[8];
-      widen8<BF16>(w_lo, x);
-      widen8<BF16>(w_hi, y);
+    }
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+      const int row0 = (set0 + j) * 8, row = row0 + (lane >> 2);
+      if (row0 >= rows) break;  // the same for the whole warp
+      const bool live = row < rows, is_q = row < a.H, is_v = row >= a.H + a.Hkv;
+      const int h = row - (is_q ? 0 : (is_v ? a.H + a.Hkv : a.H));
+      float2 x[4], y[4];
+      widen8<BF16>(w_lo[j], x);
+      widen8<BF16>(w_hi[j], y);
       if (ROTATE && !is_v) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float u = __fsub_rn(__fmul_rn(x[e], co[e]), __fmul_rn(y[e], si[e]));
-          y[e] = __fadd_rn(__fmul_rn(y[e], co[e]), __fmul_rn(x[e], si[e]));
+        for (int e = 0; e < 4; ++e) {
+          // one by one: pairs of products and sums are fused
+          const float2 u =
+              make_float2(__fsub_rn(__fmul_rn(x[e].x, co[e].x), __fmul_rn(y[e].x, si[e].x)),
+                          __fsub_rn(__fmul_rn(x[e].y, co[e].y), __fmul_rn(y[e].y, si[e].y)));
+          y[e] = make_float2(__fadd_rn(__fmul_rn(y[e].x, co[e].x), __fmul_rn(x[e].x, si[e].x)),
+                             __fadd_rn(__fmul_rn(y[e].y, co[e].y), __fmul_rn(x[e].y, si[e].y)));
           x[e] = u;
         }
-        w_lo = narrow8<BF16>(x);
-        w_hi = narrow8<BF16>(y);
+        w_lo[j] = narrow8<BF16>(x);
+        w_hi[j] = narrow8<BF16>(y);
       }
       const PoolArg& pool = is_v ? a.vc : a.kc;
-      if (is_q || !FOUR) {
-        uint16_t* const p = is_q ? static_cast<uint16_t*>(a.q_out.p) + t * a.q_out.t + h * a.q_out.h
-                                 : static_cast<uint16_t*>(pool.p) + page * pool.pg + h * pool.h +
-                                       r * pool.r;
-        if (live) {
-          *reinterpret_cast<uint4*>(p + c0) = w_lo;
-          *reinterpret_cast<uint4*>(p + c0 + 32) = w_hi;
-        }
+      if (live && (is_q || !FOUR)) {
+        uint16_t* const p = (is_q ? static_cast<uint16_t*>(a.q_out.p) + t * a.q_out.t +
+                                        h * a.q_out.h
+                                  : static_cast<uint16_t*>(pool.p) + page * pool.pg + h * pool.h +
+                                        r * pool.r) +
+                            c0;
+        *reinterpret_cast<uint4*>(p) = w_lo[j];
+        *reinterpret_cast<uint4*>(p + 32) = w_hi[j];
       }
       if (FOUR && row0 + 8 > a.H) {  // the same for the whole warp
         float mx0, mn0, mx1, mn1;
         extrema(x, &mx0, &mn0);
         extrema(y, &mx1, &mn1);
         const uint32_t h0 = group_scale<BF16>(mx0, mn0), h1 = group_scale<BF16>(mx1, mn1);
-        const float s0 = half_to_f32<BF16>((uint16_t)h0), s1 = half_to_f32<BF16>((uint16_t)h1);
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          w[e >> 2] |= (code_of(x[e], s0) | code_of(y[e], s1) << 4) << (8 * (e & 3));
+        const Quotient lo = quotient(half_to_f32<BF16>((uint16_t)h0)),
+                       hi = quotient(half_to_f32<BF16>((uint16_t)h1));
+        const uint2 w = make_uint2(lo.codes(x[0], x[1]) | hi.codes(y[0], y[1]) << 4,
+                                   lo.codes(x[2], x[3]) | hi.codes(y[2], y[3]) << 4);
         if (live && !is_q) {
           uint8_t* const p = static_cast<uint8_t*>(pool.p) + page * pool.pg + h * pool.h;
-          *reinterpret_cast<uint2*>(p + code_at(r) + c0) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(p + code_at(r) + c0) = w;
           if (c0 == 0) *reinterpret_cast<uint32_t*>(p + scale_at(r)) = h0 | h1 << 16;
         }
       }
@@ -166,68 +179,94 @@ struct LoadArgs {
   uint32_t* err;
 };
 
-// Four threads have a row of K and of V, as above.
-template <bool BF16>
+// Four threads have a row of K and of V, as above; kMoves such rows of a thread are
+// under way together.
+template <bool BF16, int kMoves>
 __global__ void __launch_bounds__(kThreads) load4_kernel(const LoadArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   const long long n = (long long)a.tokens * a.Hkv * 4;
+  const long long step = (long long)gridDim.x * kThreads * kMoves;
   bool bad = false;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n;
-       i += (long long)gridDim.x * kThreads) {
-    const int c0 = (int)(i & 3) * 8;
-    const int t = (int)quot(i >> 2, a.Hkv), h = (int)((i >> 2) - (long long)t * a.Hkv);
-    const int slot = a.slots[t];
-    if (slot < 0) continue;
-    const int page = slot >> a.shift, r = slot & ((1 << a.shift) - 1);
-    if (!page_ok(page, a.pages)) {
-      bad = true;
-      continue;
-    }
-    const uint8_t* const kp = static_cast<const uint8_t*>(a.kc.p) + page * a.kc.pg + h * a.kc.h;
-    const uint8_t* const vp = static_cast<const uint8_t*>(a.vc.p) + page * a.vc.pg + h * a.vc.h;
-    const uint2 code[2] = {*reinterpret_cast<const uint2*>(kp + code_at(r) + c0),
-                           *reinterpret_cast<const uint2*>(vp + code_at(r) + c0)};
-    const uint32_t scale[2] = {*reinterpret_cast<const uint32_t*>(kp + scale_at(r)),
-                               *reinterpret_cast<const uint32_t*>(vp + scale_at(r))};
+  for (long long i0 = (long long)blockIdx.x * kThreads * kMoves + threadIdx.x; i0 < n; i0 += step) {
+    uint2 code[kMoves][2];
+    uint32_t scale[kMoves][2];
+    long long k_at[kMoves], v_at[kMoves];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float s0 = half_to_f32<BF16>((uint16_t)scale[j]),
-                  s1 = half_to_f32<BF16>((uint16_t)(scale[j] >> 16));
-      float x[8], y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = ((e & 4) ? code[j].y : code[j].x) >> (8 * (e & 3));
-        x[e] = (float)((int)(b & 15) - 8) * s0;
-        y[e] = (float)((int)(b >> 4 & 15) - 8) * s1;
+    for (int u = 0; u < kMoves; ++u) {
+      const long long i = i0 + u * kThreads;
+      k_at[u] = -1;
+      if (i >= n) continue;
+      const int c0 = (int)(i & 3) * 8;
+      const int t = (int)quot(i >> 2, a.Hkv), h = (int)((i >> 2) - (long long)t * a.Hkv);
+      const int slot = a.slots[t];
+      if (slot < 0) continue;
+      const int page = slot >> a.shift, r = slot & ((1 << a.shift) - 1);
+      if (!page_ok(page, a.pages)) {
+        bad = true;
+        continue;
       }
-      const RowsArg& to = j ? a.v : a.k;
-      uint16_t* const p = static_cast<uint16_t*>(to.p) + t * to.t + h * to.h + c0;
-      *reinterpret_cast<uint4*>(p) = narrow8<BF16>(x);
-      *reinterpret_cast<uint4*>(p + 32) = narrow8<BF16>(y);
+      const uint8_t* const kp = static_cast<const uint8_t*>(a.kc.p) + page * a.kc.pg + h * a.kc.h;
+      const uint8_t* const vp = static_cast<const uint8_t*>(a.vc.p) + page * a.vc.pg + h * a.vc.h;
+      code[u][0] = *reinterpret_cast<const uint2*>(kp + code_at(r) + c0);
+      code[u][1] = *reinterpret_cast<const uint2*>(vp + code_at(r) + c0);
+      scale[u][0] = *reinterpret_cast<const uint32_t*>(kp + scale_at(r));
+      scale[u][1] = *reinterpret_cast<const uint32_t*>(vp + scale_at(r));
+      k_at[u] = t * a.k.t + h * a.k.h + c0;
+      v_at[u] = t * a.v.t + h * a.v.h + c0;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      if (k_at[u] < 0) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float s0 = half_to_f32<BF16>((uint16_t)scale[u][j]),
+                    s1 = half_to_f32<BF16>((uint16_t)(scale[u][j] >> 16));
+        float2 x[4], y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t b = ((e & 2) ? code[u][j].y : code[u][j].x) >> (16 * (e & 1));
+          x[e] = make_float2((float)((int)(b & 15) - 8) * s0, (float)((int)(b >> 8 & 15) - 8) * s0);
+          y[e] = make_float2((float)((int)(b >> 4 & 15) - 8) * s1,
+                             (float)((int)(b >> 12 & 15) - 8) * s1);
+        }
+        uint16_t* const p =
+            static_cast<uint16_t*>(j ? a.v.p : a.k.p) + (j ? v_at[u] : k_at[u]);
+        *reinterpret_cast<uint4*>(p) = narrow8<BF16>(x);
+        *reinterpret_cast<uint4*>(p + 32) = narrow8<BF16>(y);
+      }
     }
   }
   if (bad) atomicOr(a.err, kErrIndex);
 }
 
+template <int kSets>
+void (*append_of(bool bf16, bool rotate, bool four))(AppendArgs) {
+  if (!four)
+    return bf16 ? append_kernel<true, true, false, kSets> : append_kernel<false, true, false, kSets>;
+  if (rotate)
+    return bf16 ? append_kernel<true, true, true, kSets> : append_kernel<false, true, true, kSets>;
+  return bf16 ? append_kernel<true, false, true, kSets> : append_kernel<false, false, true, kSets>;
+}
+
+constexpr int kManySets = 2, kManyMoves = 4;
+// Blocks of a full SM, and how many times over the threads of all SMs there has to be
+// work before a thread takes several pieces.
+constexpr int kBlocks = 8, kMany = 4;
+
 }  // namespace
 
 int launch_paged_append(const PagedDims& d, const DevCtx& ctx, AppendArgs a, bool rotate,
                         bool four, cudaStream_t stream) {
-  const int rows = (rotate ? d.H : 0) + 2 * d.Hkv;
   a.tokens = d.tokens, a.batch = d.batch, a.H = d.H, a.Hkv = d.Hkv;
   a.pages = d.pages, a.shift = d.shift;
   a.err = ctx.err;
-  a.per = 8;
-  a.parts = (rows + a.per - 1) / a.per;
-  void (*kernel)(AppendArgs);
-  if (!four)
-    kernel = d.bf16 ? append_kernel<true, true, false> : append_kernel<false, true, false>;
-  else if (rotate)
-    kernel = d.bf16 ? append_kernel<true, true, true> : append_kernel<false, true, true>;
-  else
-    kernel = d.bf16 ? append_kernel<true, false, true> : append_kernel<false, false, true>;
-  const long long per = kThreads / 32, most = 8LL * ctx.sm_count;
+  const int sets = (d.H + 2 * d.Hkv + 7) / 8;  // of eight rows, a token
+  const bool many = (long long)d.tokens * sets >= (long long)kMany * kBlocks * (kThreads / 32) * ctx.sm_count;
+  a.parts = many ? (sets + kManySets - 1) / kManySets : sets;
+  auto* kernel =
+      many ? append_of<kManySets>(d.bf16, rotate, four) : append_of<1>(d.bf16, rotate, four);
+  const long long per = kThreads / 32, most = (long long)kBlocks * ctx.sm_count;
   const long long blocks = ((long long)d.tokens * a.parts + per - 1) / per;
   return cuda_status(launch_dependent(kernel, dim3((unsigned)(blocks > most ? most : blocks)),
                                       dim3(kThreads), 0, stream, a));
@@ -237,10 +276,17 @@ int launch_paged_load4(const PagedDims& d, const DevCtx& ctx, const PoolArg& kc,
                        const int32_t* slots, const RowsArg& k, const RowsArg& v,
                        cudaStream_t stream) {
   const LoadArgs args{d.tokens, d.Hkv, d.pages, d.shift, kc, vc, slots, k, v, ctx.err};
-  const long long blocks = ((long long)d.tokens * d.Hkv * 4 + kThreads - 1) / kThreads;
-  const long long most = 8LL * ctx.sm_count;
-  return cuda_status(launch_dependent(d.bf16 ? load4_kernel<true> : load4_kernel<false>,
-                                      dim3((unsigned)(blocks > most ? most : blocks)),
+  const long long threads = (long long)d.tokens * d.Hkv * 4;
+  const bool many = threads >= (long long)kMany * kBlocks * kThreads * ctx.sm_count;
+  const long long per = (many ? kManyMoves : 1) * kThreads;
+  const long long most = (long long)kBlocks * ctx.sm_count;
+  const long long blocks = (threads + per - 1) / per;
+  void (*kernel)(LoadArgs);
+  if (many)
+    kernel = d.bf16 ? load4_kernel<true, kManyMoves> : load4_kernel<false, kManyMoves>;
+  else
+    kernel = d.bf16 ? load4_kernel<true, 1> : load4_kernel<false, 1>;
+  return cuda_status(launch_dependent(kernel, dim3((unsigned)(blocks > most ? most : blocks)),
                                       dim3(kThreads), 0, stream, args));
 }
 

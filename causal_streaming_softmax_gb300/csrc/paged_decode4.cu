@@ -55,10 +55,11 @@ constexpr int kTiledShift = 5;
 static_assert(kTiledShift >= 5 && (32 / 8 * kUnitBytes) % 128 == 0, "a box of 32 rows");
 constexpr int kLd = 68;  // floats a row of the joining buffer (bank spread)
 
-// A block's shape.  COLS: column tiles of eight query rows.
-template <int COLS>
+// A block's shape.  COLS: column tiles of eight query rows.  WHOLE: a block takes
+// whole items, so that nothing is joined.
+template <int COLS, bool WHOLE>
 struct Config {
-  static constexpr bool kWhole = false;
+  static constexpr bool kWhole = WHOLE;
   static constexpr int kTileKeys = css::kTileKeys;
   static constexpr int kCols = COLS, kRows = 8 * COLS;
   static constexpr int kBlocks = COLS == 1 ? 3 : 2;  // a SM
@@ -210,7 +211,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
   griddep_wait();
 
   tiles_before_each<C>(a, s_pre, s_scan);
-  const Share share = share_of(s_pre[a.batch] * a.Hkv, a.part.min_tiles, gridDim.x, blockIdx.x);
+  const Share share =
+      share_of(s_pre[a.batch] * a.Hkv, C::kWhole ? 1 : a.part.min_tiles, gridDim.x, blockIdx.x);
 
   if (warp < 0) {
     // ---------------- producer ----------------
@@ -240,13 +242,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
     for (long long pos = share.begin; ok && pos < share.end;) {
       const Place sg = nx;
       const Request r = sg.r;
-      const int t1 = (int)min((long long)sg.nt, sg.t0 + (share.end - pos));
+      const int t1 = C::kWhole ? sg.nt : (int)min((long long)sg.nt, sg.t0 + (share.end - pos));
       const int32_t* const row = a.table + (long long)sg.req * a.width;
       const int n_pages = (int)pages_for(r.n_keys, a.shift);
       int base = (int)(((long long)sg.t0 * kTileKeys) >> a.shift);
       int ids = nx_ids, next = nx_next;
       const long long last = pos - sg.t0 + sg.nt - 1;  // the item's last position
-      pos += t1 - sg.t0;
+      pos += C::kWhole ? 1 : t1 - sg.t0;
       if (pos < share.end) {
         next_place<C>(a, s_pre, &nx);
         read_ids();
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
       ok = !(nq >= 2) || mbar_nap_warp(BAR(BAR_Q_FREE + qbuf), ((nq >> 1) - 1) & 1, wc);
       if (!ok) break;
       if (lane == 0) {
-        s_item[qbuf] = Item{r, sg.kv, sg.t0, t1, sg.t0 == 0 && t1 == sg.nt};
+        s_item[qbuf] = Item{r, sg.kv, sg.t0, t1, C::kWhole || (sg.t0 == 0 && t1 == sg.nt)};
         mbar_arrive_expect_tx(BAR(BAR_Q + qbuf), a.ntok * a.G * 128);
         tma_load_4d(sbase + qbuf * kQ, &tm_q, BAR(BAR_Q + qbuf), 0, 0, sg.kv, r.q0);
       }
@@ -316,13 +318,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         }
       }
       if (!ok) break;
-      if (sg.t0 == 0 && t1 < sg.nt) {
+      if (!C::kWhole && sg.t0 == 0 && t1 < sg.nt) {
         tail = true;
         if (lane == 0)
           a.part.desc[blockIdx.x] = PartDesc{r.q0, sg.kv, r.n_new * a.G, last_block(share, last)};
       }
     }
-    if (lane == 0 && !tail) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
+    if (!C::kWhole && lane == 0 && !tail) a.part.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
     if (bad) atomicOr(a.err, kErrIndex);
     // no copy may still be landing when the block exits (matters only when a
     // wait gave up)
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
       }
       ++nq;
       const int t1 = sg.t1, n_keys = sg.r.n_keys;
-      pos += t1 - sg.t0;
+      pos += C::kWhole ? 1 : t1 - sg.t0;
       const int first_lim = row_limit(n_keys, sg.r.n_new, 0);  // keys that every row sees
       // neg_m: kBias - m in base 2; most: what a lane's weights of a row in a step may
       // add up to.  V's scales count in a unit of their own: v_inv is its inverse,
@@ -722,19 +724,37 @@ int launch(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolAr
 
 }  // namespace
 
-// A table that leaves a request one tile gives every item to one block.
-bool decode4_whole(const PagedDims& d) { return ((long long)d.width << d.shift) <= kTileKeys; }
+constexpr int kWholeKeys = 1024;
 
 namespace {
-// Column tiles of a call: as many tokens as it has at most, so that a token step of
-// up to eight heads a group needs one.
+// The most new tokens of a request that a call has for this kernel.
 int tokens4(const PagedDims& d) {
   return d.max_new < decode_tokens(d.G) ? d.max_new : decode_tokens(d.G);
 }
+
+template <int COLS>
+int launch_cols(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
+                const PoolArg& vc, const DecodeArgs& args, int blocks, int which,
+                cudaStream_t stream) {
+  if (decode4_whole(d, ctx.sm_count))
+    return launch<Config<COLS, true>>(d, ctx, q, kc, vc, args, d.batch * d.Hkv, which + 2, stream);
+  return launch<Config<COLS, false>>(d, ctx, q, kc, vc, args, blocks, which, stream);
+}
 }  // namespace
 
+// Whole items where each finds a block at once and the table leaves room for no more
+// than kWholeKeys keys a request: the parts and the second launch fall away.  Split /
+// whole, us (8 K/V heads): one request of 100 keys 6.4 / 4.8, of 777 9.5 / 8.4, of 1500
+// 9.0 / 12.3; eight of 250 9.2 / 5.9, of 777 10.9 / 8.9, of 1500 10.1 / 12.9; fifty of
+// 500 17.4 / 9.1.  The width stands for the lengths, which the host does not see.
+bool decode4_whole(const PagedDims& d, int sm_count) {
+  return (long long)d.batch * d.Hkv <= decode4_blocks(d) * sm_count &&
+         ((long long)d.width << d.shift) <= kWholeKeys;
+}
+
+// One column tile serves a token step of up to eight heads a group.
 int decode4_blocks(const PagedDims& d) {
-  return tokens4(d) * d.G <= 8 ? Config<1>::kBlocks : Config<2>::kBlocks;
+  return tokens4(d) * d.G <= 8 ? Config<1, false>::kBlocks : Config<2, false>::kBlocks;
 }
 
 int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
@@ -745,8 +765,8 @@ int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q
   const DecodeArgs args{d.batch, d.tokens, d.H, d.Hkv, d.G, ntok, d.max_new, d.pages, d.width,
                         d.shift, d.c, cu, lens, table, o, lse, part, ctx.err, ctx.wait_ns};
   if (ntok * d.G <= 8)
-    return launch<Config<1>>(d, ctx, q, kc, vc, args, blocks, kSmemDecode4F16, stream);
-  return launch<Config<2>>(d, ctx, q, kc, vc, args, blocks, kSmemDecode4WideF16, stream);
+    return launch_cols<1>(d, ctx, q, kc, vc, args, blocks, kSmemDecode4F16, stream);
+  return launch_cols<2>(d, ctx, q, kc, vc, args, blocks, kSmemDecode4WideF16, stream);
 }
 
 }  // namespace css

@@ -167,7 +167,7 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
     rc = (four ? launch_paged_decode4 : launch_paged_decode)(d, ctx, q, kc, vc, table, cu, lens,
                                                              few, blocks, o, lse, stream);
     if (rc != ATTN_OK) return rc;
-    if (!(four ? decode4_whole(d) : decode_whole(d, ctx.sm_count))) n_few = blocks;
+    if (!(four ? decode4_whole : decode_whole)(d, ctx.sm_count)) n_few = blocks;
   }
   if (d.max_new > ntok) {
     rows = parts_at(at, kMaxSm, kItemRows, kLeastRows);

@@ -32,15 +32,15 @@ __device__ __forceinline__ int scale_at(int r) {
   return (r >> 3) * kUnitBytes + kUnitScales + (r & 7) * 4;
 }
 
-// max and min that keep a NaN.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// max and min of three that keep a NaN.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
   float d;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -60,12 +60,35 @@ __device__ __forceinline__ uint32_t group_scale(float mx, float mn) {
   return fabsf(mx) < INFINITY && fabsf(mn) < INFINITY ? h : (BF16 ? 0x7fc0u : 0x7e00u);
 }
 
-// code + 8 of x in a group of scale s; 8 where the group is zero or NaN.  The
-// quotient is rounded correctly, as a tie between two codes is common with so few
-// bits on both sides and goes to the even one.
-__device__ __forceinline__ uint32_t code_of(float x, float s) {
-  const float q = fminf(fmaxf(rintf(__fdiv_rn(x, s)), -8.f), 7.f);
-  return s != 0.f && s == s ? (uint32_t)((int)q + 8) : 8u;
+// The quotients of a group's values by its scale, correctly rounded: a tie between
+// two codes is common with so few bits on both sides, and goes to the even one.  After
+// Markstein (1990): with y = 1 / s correctly rounded, q0 = x y and r = x - q0 s, the
+// sum q0 + r y is.  That wants s away from the smallest numbers: there both sides are
+// first multiplied by 2^64.
+struct Quotient {
+  float s, y, up;
+  // code + 8 of two values in the low bytes
+  __device__ __forceinline__ uint2 codes(float2 x) const {
+    const float2 y2 = make_float2(y, y);
+    x = __fmul2_rn(x, make_float2(up, up));
+    float2 q = __fmul2_rn(x, y2);
+    q = __ffma2_rn(__ffma2_rn(q, make_float2(-s, -s), x), y2, q);
+    // 1.5 2^23 + 8: the sum's last bit counts one, halves go to even
+    q = __fadd2_rn(make_float2(fminf(fmaxf(q.x, -8.f), 7.f), fminf(fmaxf(q.y, -8.f), 7.f)),
+                   make_float2(12582920.f, 12582920.f));
+    return make_uint2(__float_as_uint(q.x), __float_as_uint(q.y));
+  }
+  // four of them, a byte each; 8 in a group that is zero or reads as NaN
+  __device__ __forceinline__ uint32_t codes(float2 a, float2 b) const {
+    const uint2 u = codes(a), v = codes(b);
+    const uint32_t w =
+        __byte_perm(__byte_perm(u.x, u.y, 0x0040), __byte_perm(v.x, v.y, 0x0040), 0x5410);
+    return fabsf(y) < INFINITY ? w : 0x08080808u;
+  }
+};
+__device__ __forceinline__ Quotient quotient(float s) {
+  const float up = fabsf(s) < 0x1p-60f ? 0x1p64f : 1.f;
+  return Quotient{s * up, __fdiv_rn(1.f, s * up), up};
 }
 
 template <bool BF16>

@@ -59,7 +59,7 @@ int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, c
                       const int32_t* lens, const PartArgs& part, int blocks, int skip,
                       bool four, const RowsArg& o, float* lse, cudaStream_t stream);
 // The same over a 4-bit cache (the pools' strides in bytes).
-bool decode4_whole(const PagedDims& d);
+bool decode4_whole(const PagedDims& d, int sm_count);
 int decode4_blocks(const PagedDims& d);  // a SM
 int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
                          const PoolArg& kc, const PoolArg& vc, const int32_t* table,
@@ -79,8 +79,12 @@ enum {
   kSmemRowsBf16,
   kSmemDecode4F16,
   kSmemDecode4Bf16,
+  kSmemDecode4WholeF16,
+  kSmemDecode4WholeBf16,
   kSmemDecode4WideF16,
   kSmemDecode4WideBf16,
+  kSmemDecode4WideWholeF16,
+  kSmemDecode4WideWholeBf16,
   kSmemRows4F16,
   kSmemRows4Bf16,
   kSmemKernels
@@ -116,7 +120,7 @@ struct AppendArgs {
   const int32_t *slots, *cu, *lens;
   PoolArg kc, vc;  // strides in elements (16-bit pools) or bytes (4-bit)
   int tokens, batch, H, Hkv, pages, shift;
-  int per, parts;  // rows of a token that a warp takes, warps a token
+  int parts;  // warps a token
   uint32_t* err;
 };
 int launch_paged_append(const PagedDims& d, const DevCtx& ctx, AppendArgs args, bool rotate,
