@@ -6,8 +6,9 @@
 // over values code * scale, which are exact in 16 bits (pool4.cuh).
 //
 // 72 bytes a key and K/V head come from memory where the 16-bit cache has 256, so
-// the same arithmetic has less than a third of the time, and the number of
-// instructions a key decides.  Hence:
+// the same arithmetic has less than a third of the time: for 16 keys of a K/V head
+// the schedulers of a SM have some 200 issue slots at the copy rate, and the kernel
+// takes about 140.  Hence:
 //  * S^T = K Q^T and O^T = V^T P^T: the 16-row side of the warp-level product holds
 //    keys and channels, the 8-column side the query rows, so that a group of up to
 //    eight rows pads nothing and half the products, maxima and exponentials of the
@@ -18,15 +19,32 @@
 //  * ldmatrix takes V's codes two bytes at a time as 16-bit elements and transposes
 //    them, which puts the same channel of two keys side by side in a word: the four
 //    codes of an element are the four channel tiles of O^T;
-//  * K's codes go into the product unscaled and unsigned and the scale of a key is
-//    applied to its scores: binary16 as subnormals, code * 2^-24 (or 2^-20) being
-//    the bits of the code themselves, bfloat16 as 16 + code; the offset times the
-//    sum of q is where the accumulators start;
-//  * V's codes become code * scale (the scale varies along the sum): exact;
-//  * the maximum is followed only when a score passes it by kSlack, so that a step
-//    has one vote instead of a reduction over the keys' lanes.
-// The list of key tiles, the producer warp and the joining of parts are those of
-// the 16-bit kernel (serve_decode.cuh, serve_parts.cuh).
+//  * all products take binary16: the bits of code + 8 are the subnormal number
+//    (code + 8) 2^-24 (2^-20 in the high half of a byte), which costs an AND and no
+//    conversion.  q goes in with its row's largest element at 2^9.  K's scale is
+//    applied to the scores, the offset of 8 times the sum of q is where they start.
+//    V's scale, which varies along the sum, goes into the weights, the offset comes
+//    off V's codes (left in, it would be taken off a sum ten times the result);
+//  * weights times V's scales are binary16 too, a weight of 1 counting 2^kBias and the
+//    scales in a unit near the largest so far: spacing 2^-35 of that;
+//  * m and the unit are followed only when a lane's sum of a step's weights passes
+//    kMost or a scale v_most: one vote a step, no maximum over the keys' lanes;
+//  * a lane converts the scales of two keys and passes them on through shared memory,
+//    each twice, as operands of the paired binary32 instructions.
+// Tiles of 64 keys go round four consumer warps a block, each with a ring of three;
+// the producer hands out four at a time, eight lanes each.  Items, places and the
+// joining of parts are those of the 16-bit kernel (serve_decode.cuh,
+// serve_parts.cuh).
+//
+// Measured (GB300, join included): 256 requests over 1024..16384 keys, 32 / 4 heads,
+// 130 us = 4.75 TB/s, 70% of the measured copy rate; 2 over 50000..65536, 16 / 16 heads,
+// 37 us = 3.8 TB/s; one over 777 keys 8.4 us.  The copies alone take 105 us of the 130
+// with two blocks a SM and rings of five (copies of 2304 bytes, 26 clocks each beside
+// their bytes: pages of 16 rows 1.3 times the time of pages of 64), the arithmetic alone
+// about 100: neither hides all of the other.  What was slower: 8 warps of 32 keys in
+// step 163 us; seven warps a block, two blocks, 151; four, two blocks, rings of five 140;
+// a product of its own for the offset of 8 147; the scores of one tile beside the
+// product of the one before 144; both operands as code * scale, exact, 201.
 #include <math.h>
 
 #include <type_traits>
@@ -43,8 +61,9 @@ namespace css {
 namespace {
 
 // A weight counts 2^kBias where the score is m, so that binary16 holds small ones
-// too.  Binary orders that a score may pass m by, and a scale of V its unit, before
-// both are followed: a weight times a scale stays at or below 2^15.
+// too.  What a lane's weights of a row in a step may add up to, and the binary orders
+// that a scale of V may pass its unit by, before m and the unit are followed: a weight
+// times a scale stays at or below 2^15.
 constexpr float kBias = 10.f, kMost = 0x1p13f;
 constexpr int kVSlack = 2;
 constexpr int kTileKeys = 64;
@@ -522,7 +541,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
           }
           v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
           if (v > v_most) {
-            const int ex = max((int)(__float_as_uint(v) >> 23) - 127, -110);
+            const int ex = min(max((int)(__float_as_uint(v) >> 23) - 127, -110), 125);
             const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
             fv = inv / v_inv;  // O is zero before the first
             v_inv = inv;
@@ -605,7 +624,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
                 for (int n = 0; n < kCols; ++n)
 #pragma unroll
                   for (int e = 0; e < 2; ++e) {
-                    const float wt = __shfl_sync(0xffffffffu, e ? p[n][i][u].y : p[n][i][u].x, 4 * k + tq);
+                    const float wt = __shfl_sync(0xffffffffu, e ? p[n][i][u].y : p[n][i][u].x,
+                                                 4 * k + tq);
                     const int lim = row_limit(n_keys, n_new, (8 * n + 2 * tq + e) / a.G);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -652,23 +672,26 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
           l[n].y += __shfl_xor_sync(0xffffffffu, l[n].y, by);
         }
         const int row = 8 * n + 2 * tq;
+        constexpr float kOne = 0x1p-10f;  // of a weight that counts 2^kBias
+        static_assert(kBias == 10.f, "kOne");
         if (g == 0) {
-          s_ml[warp * kRows + row] =
-              make_float2(most[n].x < 0.f ? -INFINITY : -neg_m[n].x, l[n].x);
-          s_ml[warp * kRows + row + 1] =
-              make_float2(most[n].y < 0.f ? -INFINITY : -neg_m[n].y, l[n].y);
+          s_ml[warp * kRows + row] = make_float2(
+              most[n].x < 0.f ? -INFINITY : kBias - neg_m[n].x, l[n].x * kOne);
+          s_ml[warp * kRows + row + 1] = make_float2(
+              most[n].y < 0.f ? -INFINITY : kBias - neg_m[n].y, l[n].y * kOne);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int x = 0; x < 2; ++x) {  // low and high channels, back to units of one
+          const float raw = (x ? 0x1p20f : 0x1p24f) * kOne, v_unit = 1.f / v_inv;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {  // low and high channels
-              const float f = (x ? 0x1p20f : 0x1p24f) / v_inv;
-              *reinterpret_cast<float2*>(s_join + warp * kWarpLd + (row + e) * kLd + 32 * x + 16 * h +
-                                         2 * g) =
-                  make_float2(o[n][x][2 * h + e] * f, o[n][2 + x][2 * h + e] * f);
-            }
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<float2*>(s_join + warp * kWarpLd + (row + e) * kLd + 32 * x +
+                                         16 * h + 2 * g) =
+                  make_float2(o[n][x][2 * h + e] * raw * v_unit,
+                              o[n][2 + x][2 * h + e] * raw * v_unit);
+        }
       }
       // where a wait gave up, all leave together
       if (named_barrier_any(1, kConsumers * 32, !ok)) break;

@@ -553,7 +553,8 @@ ATTN_API int attn_paged_append(const attn_paged_shape* shape, const void* q, con
  * Appends to a 4-bit cache: attn_paged_append with k and v quantised, k after its
  * rotation and from the unrounded binary32 values.  With cos_tab and sin_tab both
  * NULL nothing is turned: q, q_out, cu and lens are not read, and k is stored as it
- * is (attn_paged_store into 4 bits).
+ * is (attn_paged_store into 4 bits).  A slot that is given twice ends with codes and
+ * scales of either row.
  */
 ATTN_API int attn_paged_append4(const attn_paged_shape* shape, const void* q, const void* k,
                                 const void* v, const float* cos_tab, const float* sin_tab,
@@ -597,7 +598,8 @@ ATTN_API int attn_paged_fwd(const attn_paged_shape* shape, const void* q, const 
 /*
  * The same over a 4-bit cache: attn_paged_fwd on the values that the pools hold
  * (exact in 16 bits, so only the order of sums is another), with the workspace of
- * attn_paged_workspace_bytes.  A row of q that holds an infinity or a NaN gives NaN.
+ * attn_paged_workspace_bytes.  A row of q that holds an infinity or a NaN (or, in
+ * bfloat16, an element of 2^110 or more) may give NaN; no other row does.
  */
 ATTN_API int attn_paged_fwd4(const attn_paged_shape* shape, const void* q, const uint8_t* k_cache,
                              const uint8_t* v_cache, const int32_t* table, const int32_t* cu,

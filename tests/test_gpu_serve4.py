@@ -436,6 +436,35 @@ def test_paged4_scales_and_large_scores(torch, dtype, scale, std, reqs):
     check_paged4(torch, q, kc, vc, table, cu, lens, o, L, scale)
 
 
+# the type, and the binary orders of K and V
+MAGNITUDES = [("float16", -8, -14), ("float16", 3, 8), ("float16", 0, 12), ("bfloat16", -60, -100),
+              ("bfloat16", 20, 100), ("bfloat16", 0, -120), ("bfloat16", 0, 120)]
+
+
+@pytest.mark.parametrize("dtype,ke,ve", MAGNITUDES)
+@pytest.mark.parametrize("reqs", [[(700, 1), (33, 2)], [(300, 40)]])
+def test_paged4_small_and_large_magnitudes(torch, dtype, ke, ve, reqs):
+    """K and V far from one; the scale of the scores takes K's back."""
+    dt = getattr(torch, dtype)
+    q, _, _, table, cu, lens, _ = paged4_problem(torch, reqs, 8, 2, 16, dt, 13)
+    pages = max(p for row in table for p in row if 0 <= p < 10 ** 6) + 1
+    kc, vc = (pool_of((rnd(torch, (pages, 2, 16, 64), torch.float32, 80 + e % 7) * 2.0 ** e).to(dt),
+                      dt) for e in (ke, ve))
+    scale = 0.125 * 2.0 ** -ke
+    o, L = run_paged4(torch, q, kc, vc, table, cu, lens, scale=scale)
+    check_paged4(torch, q, kc, vc, table, cu, lens, o, L, scale)
+
+
+@pytest.mark.parametrize("B", [1, 57, 58])
+@pytest.mark.parametrize("keys", [1007, 1008, 1009, 1030])
+def test_paged4_around_whole_items(torch, B, keys):
+    """Tables that hold just 1024 keys and just more, with as many items as blocks."""
+    reqs = [(keys - 13 * i % 500, 1) for i in range(B)]
+    q, kc, vc, table, cu, lens, _ = paged4_problem(torch, reqs, 8, 8, 16, torch.float16, keys + B)
+    o, L = run_paged4(torch, q, kc, vc, table, cu, lens)
+    check_paged4(torch, q, kc, vc, table, cu, lens, o, L)
+
+
 @pytest.mark.parametrize("bound", [1, 2, 4, 40, 1000])
 def test_paged4_whatever_the_bound_on_new_tokens(torch, bound):
     p = paged4_problem(torch, [(900, 1), (33, 1), (1, 1)], 8, 2, 32, torch.bfloat16, 4)
