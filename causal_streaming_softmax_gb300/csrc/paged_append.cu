@@ -13,9 +13,19 @@
 // Four threads have a row, each eight channels of its low half and the eight that
 // belong to them of its high half: the rotation, the byte that holds a channel of
 // either half, and both groups' extrema (two shuffles) need no other thread.  A
-// warp has one token, whose position it finds by trying 32 offsets at a time, and
-// walks through its rows (q, k, v heads) eight by eight with the angles in
-// registers.
+// warp has eight or sixteen rows (q, k, v heads) of one token, whose position it finds
+// by trying 32 offsets at a time while its rows are under way.
+//
+// Bound by memory: 128 bytes read and written a row of q, k and v, 36 written into 4
+// bits.  36,000 tokens of 32 / 8 heads in bfloat16 take 68 us = 6.5 TB/s, 96% of the
+// measured copy rate (one set of eight rows a warp 90 us, three 71, six 74; blocks for
+// all the work instead of a full SM's 75).  24,600 tokens into 4 bits 53 us, 69% of it:
+// the arithmetic of a K or V row, some 200 instructions a thread, takes as long as its
+// bytes (1700 instructions a token, issue slots 69% busy; three blocks a SM 52.8 us,
+// four 53.3, two 62).  64 tokens 2.4 us, one 1.9: launch and the chain offsets ->
+// length -> angles.  Rows read back: 150,000 random slots, 4 heads, 39 us = 4.6 TB/s (a
+// row's 36 bytes lie in two sectors, so that 64 come from memory for each); a whole
+// pool in order 14 us of a floor of 11.6.
 #include "pool4.cuh"
 #include "serve_index.h"
 #include "serve_internal.h"
@@ -48,7 +58,8 @@ __device__ __forceinline__ void widen8(const uint4& w, float2 (&x)[4]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    x[i] = make_float2(half_to_f32<BF16>((uint16_t)u[i]), half_to_f32<BF16>((uint16_t)(u[i] >> 16)));
+    x[i] = make_float2(half_to_f32<BF16>((uint16_t)u[i]),
+                       half_to_f32<BF16>((uint16_t)(u[i] >> 16)));
 }
 
 template <bool BF16>
@@ -180,7 +191,7 @@ struct LoadArgs {
 };
 
 // Four threads have a row of K and of V, as above; kMoves such rows of a thread are
-// under way together.
+// under way together (150,000 random slots: one 44 us, two 40, four 39).
 template <bool BF16, int kMoves>
 __global__ void __launch_bounds__(kThreads) load4_kernel(const LoadArgs a) {
   griddep_launch_dependents();
@@ -243,16 +254,21 @@ __global__ void __launch_bounds__(kThreads) load4_kernel(const LoadArgs a) {
 template <int kSets>
 void (*append_of(bool bf16, bool rotate, bool four))(AppendArgs) {
   if (!four)
-    return bf16 ? append_kernel<true, true, false, kSets> : append_kernel<false, true, false, kSets>;
+    return bf16 ? append_kernel<true, true, false, kSets>
+                : append_kernel<false, true, false, kSets>;
   if (rotate)
     return bf16 ? append_kernel<true, true, true, kSets> : append_kernel<false, true, true, kSets>;
   return bf16 ? append_kernel<true, false, true, kSets> : append_kernel<false, false, true, kSets>;
 }
 
 constexpr int kManySets = 2, kManyMoves = 4;
-// Blocks of a full SM, and how many times over the threads of all SMs there has to be
-// work before a thread takes several pieces.
-constexpr int kBlocks = 8, kMany = 4;
+// A thread takes several pieces where there is more than so many blocks a SM of work.
+// Of 16 bits (32 / 8 heads; one set, two): 800 tokens 3.1, 3.3 us; 1200 4.5, 3.9; 1600
+// 5.0, 4.1; 6400 17.5, 15.8: once not all warps of one set are resident.  Into 4 bits
+// (with the rows read back): 3200 tokens 19.3, 22.2; 12800 44.2, 46.2; 25600 79.0, 76.8.
+// Rows read back (4 heads, random slots; one, four): 80,000 22.2, 23.0; 150,000 44, 39.
+constexpr int kMany = 4, kMany4 = 80, kManyLoad = 48;
+constexpr int kBlocks = 8;  // a full SM
 
 }  // namespace
 
@@ -262,7 +278,8 @@ int launch_paged_append(const PagedDims& d, const DevCtx& ctx, AppendArgs a, boo
   a.pages = d.pages, a.shift = d.shift;
   a.err = ctx.err;
   const int sets = (d.H + 2 * d.Hkv + 7) / 8;  // of eight rows, a token
-  const bool many = (long long)d.tokens * sets >= (long long)kMany * kBlocks * (kThreads / 32) * ctx.sm_count;
+  const long long warps = (long long)(four ? kMany4 : kMany) * (kThreads / 32) * ctx.sm_count;
+  const bool many = sets > 1 && (long long)d.tokens * sets > warps;
   a.parts = many ? (sets + kManySets - 1) / kManySets : sets;
   auto* kernel =
       many ? append_of<kManySets>(d.bf16, rotate, four) : append_of<1>(d.bf16, rotate, four);
@@ -277,7 +294,7 @@ int launch_paged_load4(const PagedDims& d, const DevCtx& ctx, const PoolArg& kc,
                        cudaStream_t stream) {
   const LoadArgs args{d.tokens, d.Hkv, d.pages, d.shift, kc, vc, slots, k, v, ctx.err};
   const long long threads = (long long)d.tokens * d.Hkv * 4;
-  const bool many = threads >= (long long)kMany * kBlocks * kThreads * ctx.sm_count;
+  const bool many = threads > (long long)kManyLoad * kThreads * ctx.sm_count;
   const long long per = (many ? kManyMoves : 1) * kThreads;
   const long long most = (long long)kBlocks * ctx.sm_count;
   const long long blocks = (threads + per - 1) / per;

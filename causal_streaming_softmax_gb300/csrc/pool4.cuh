@@ -119,8 +119,9 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
 // A word of codes as pairs of code * scale: the low and high halves of bytes 0 and
 // 2, then of bytes 1 and 3.
 template <bool BF16>
-__device__ __forceinline__ void scaled_codes(uint32_t w, uint32_t s_lo, uint32_t s_hi, uint32_t& lo0,
-                                             uint32_t& hi0, uint32_t& lo1, uint32_t& hi1) {
+__device__ __forceinline__ void scaled_codes(uint32_t w, uint32_t s_lo, uint32_t s_hi,
+                                             uint32_t& lo0, uint32_t& hi0, uint32_t& lo1,
+                                             uint32_t& hi1) {
   if (BF16) {
     // (16 + code') s - 24 s: both exact, as s has five significant bits
     const uint32_t z_lo = mul2<true>(s_lo, 0xc1c0c1c0u), z_hi = mul2<true>(s_hi, 0xc1c0c1c0u);

@@ -55,6 +55,14 @@
 // (1.13 ms, the waiting warps' polls), P tested against the last maximum
 // first and the maximum taken only where it grew (1.06 ms).
 //
+// A 4-bit cache (pool4.cuh): warps 8 to 11 turn the packed rows that land in raw
+// stages into the 16-bit rows of a K/V stage, exactly, and two row tiles remain.  Four
+// chunks of 301..1024 tokens over 2048..8192 keys, 32 / 8 heads, take 134 us where the
+// 16-bit cache takes 108, a prompt of 16384 tokens 1.56 ms against 1.07: the third row
+// tile is missed more than the bytes are saved.  Twenty warps, three row tiles and
+// registers moved between them is not possible: the softmax does not fit 128 of them
+// under such a split.
+//
 // What a mask excludes cannot reach a row, infinities and NaN included: S is
 // replaced by -inf, and on tiles where some row misses a key the rows of V
 // are looked at.  Rows of V past the last key of the item are set to zero;
@@ -110,7 +118,7 @@ enum {
   BAR_O_FREE = BAR_P_FREE + kMaxNT,         // [t] the epilogue has read O (128 threads)
   BAR_V_OK = BAR_O_FREE + kMaxNT,           // [t] rows of V looked at (128 threads)
   BAR_UNIT = BAR_V_OK + kMaxNT,             // [item buffer] description written
-  BAR_UNIT_FREE = BAR_UNIT + 2,          // [item buffer] read by 5 warps a row tile, and those that unpack
+  BAR_UNIT_FREE = BAR_UNIT + 2,          // [item buffer] read by 5 kNT warps (4 bits: and 4)
   BAR_MMA_DONE = BAR_UNIT_FREE + 2,      // every product of the block done (kNT commits)
   BAR_TAKE = BAR_MMA_DONE + 1,           // an answer of take_block
   BAR_RAW_FULL = BAR_TAKE + 1,           // [raw stage] 4-bit rows landed
