@@ -55,13 +55,16 @@
 // (1.13 ms, the waiting warps' polls), P tested against the last maximum
 // first and the maximum taken only where it grew (1.06 ms).
 //
-// A 4-bit cache (pool4.cuh): warps 8 to 11 turn the packed rows that land in raw
-// stages into the 16-bit rows of a K/V stage, exactly, and two row tiles remain.  Four
-// chunks of 301..1024 tokens over 2048..8192 keys, 32 / 8 heads, take 134 us where the
-// 16-bit cache takes 108, a prompt of 16384 tokens 1.56 ms against 1.07: the third row
-// tile is missed more than the bytes are saved.  Twenty warps, three row tiles and
-// registers moved between them is not possible: the softmax does not fit 128 of them
-// under such a split.
+// A 4-bit cache (pool4.cuh): packed rows land in raw stages, and the softmax of row
+// tile n mod 3 turns those of key tile n into the 16-bit rows of a K/V stage, exactly,
+// two steps before their use.  Four chunks of 301..1024 tokens over 2048..8192 keys, 32 / 8
+// heads, take 128 us where the 16-bit cache takes 108, a prompt of 16384 tokens 1.40 ms
+// against 1.07: some 180 instructions a thread on the chain of every third step.
+// Slower were: two row tiles and four warps that unpack beside them (134 us, 1.56 ms),
+// warp 15 for all tiles (163, 1.98) or every fourth (154, 1.69), warps 12 to 15 for a
+// quarter of each (159, 1.73: products come late).  Four warps more beside three row
+// tiles leave 96 registers a thread, too few for the softmax also where registers are
+// moved to it.
 //
 // What a mask excludes cannot reach a row, infinities and NaN included: S is
 // replaced by -inf, and on tiles where some row misses a key the rows of V
@@ -82,47 +85,47 @@ namespace {
 
 // What a kernel reads: packed prompts, a paged cache, a paged cache of 4 bits.
 enum Mode { kPacked, kPaged, kPaged4 };
-constexpr int kMaxNT = 3;  // row tiles of a work item, at most
-__host__ __device__ constexpr int row_tiles(int mode) { return mode == kPaged4 ? 2 : kMaxNT; }
+constexpr int kNT = 3;   // row tiles of a work item
 constexpr int kBN = 64;  // keys a tile
-constexpr int kStages = 6;
+constexpr int kMaxStages = 6;
 constexpr int kThreads = 512;
 constexpr float kSlack = 8.f;
 constexpr uint32_t kTileBytes = 128 * 128;
 constexpr uint32_t kHalfBytes = kBN * 128;         // K (or V) of a stage
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
-constexpr uint32_t kSmemStage0 = 2 * kMaxNT * kTileBytes;  // behind two Q buffers
-// 4 bits: packed rows lie where the third row tile's Q would
-constexpr int kRaw = 6;
+constexpr uint32_t kSmemStage0 = 2 * kNT * kTileBytes;  // behind two Q buffers
+// 4 bits: one stage less, packed rows in its place
+constexpr int kStages4 = kMaxStages - 1, kRaw = kNT;
+constexpr int kAhead = 2;  // steps between unpacking a tile and its use
 constexpr uint32_t kRawHalf = kBN / 8 * kUnitBytes;  // K (or V) of a raw stage
-constexpr uint32_t kSmemRaw = 2 * row_tiles(kPaged4) * kTileBytes;
-static_assert(kSmemRaw + kRaw * 2 * kRawHalf <= kSmemStage0, "raw stages");
-constexpr uint32_t kSmemBar = kSmemStage0 + kStages * kStageBytes;
+constexpr uint32_t kSmemRaw = kSmemStage0 + kStages4 * kStageBytes;
+static_assert(kRaw * 2 * kRawHalf <= kStageBytes, "raw stages");
+constexpr uint32_t kSmemBar = kSmemStage0 + kMaxStages * kStageBytes;
 constexpr uint32_t kSmemPre = kSmemBar + 512;  // paged: prefix of tiles
 
 constexpr uint32_t kColS = 0;                // + 64 t
-constexpr uint32_t kColP = kColS + 64 * kMaxNT;  // + 32 t
-constexpr uint32_t kColO = kColP + 32 * kMaxNT;  // + 64 t
+constexpr uint32_t kColP = kColS + 64 * kNT;  // + 32 t
+constexpr uint32_t kColO = kColP + 32 * kNT;  // + 64 t
 constexpr uint32_t kTmemCols = 512;
-static_assert(kColO + 64 * kMaxNT <= kTmemCols, "tensor memory");
+static_assert(kColO + 64 * kNT <= kTmemCols, "tensor memory");
 
 enum {
   BAR_Q = 0,                             // [Q buffer] the item's Q tiles landed
   BAR_Q_FREE = BAR_Q + 2,                // [Q buffer] every row tile's products done
-  BAR_KV_FULL = BAR_Q_FREE + 2,          // [stage]
-  BAR_KV_EMPTY = BAR_KV_FULL + kStages,  // [stage] every row tile's products done
-  BAR_S_FULL = BAR_KV_EMPTY + kStages,   // [t]
-  BAR_S_FREE = BAR_S_FULL + kMaxNT,         // [t] read by the softmax (128 threads)
-  BAR_P_FULL = BAR_S_FREE + kMaxNT,         // [t] P stored, O rescaled (128 threads)
-  BAR_P_FREE = BAR_P_FULL + kMaxNT,         // [t] O += P V done
-  BAR_O_FREE = BAR_P_FREE + kMaxNT,         // [t] the epilogue has read O (128 threads)
-  BAR_V_OK = BAR_O_FREE + kMaxNT,           // [t] rows of V looked at (128 threads)
-  BAR_UNIT = BAR_V_OK + kMaxNT,             // [item buffer] description written
-  BAR_UNIT_FREE = BAR_UNIT + 2,          // [item buffer] read by 5 kNT warps (4 bits: and 4)
+  BAR_KV_FULL = BAR_Q_FREE + 2,          // [stage] (4 bits: unpacked by four warps)
+  BAR_KV_EMPTY = BAR_KV_FULL + kMaxStages,  // [stage] every row tile's products done
+  BAR_S_FULL = BAR_KV_EMPTY + kMaxStages,   // [t]
+  BAR_S_FREE = BAR_S_FULL + kNT,         // [t] read by the softmax (128 threads)
+  BAR_P_FULL = BAR_S_FREE + kNT,         // [t] P stored, O rescaled (128 threads)
+  BAR_P_FREE = BAR_P_FULL + kNT,         // [t] O += P V done
+  BAR_O_FREE = BAR_P_FREE + kNT,         // [t] the epilogue has read O (128 threads)
+  BAR_V_OK = BAR_O_FREE + kNT,           // [t] rows of V looked at (128 threads)
+  BAR_UNIT = BAR_V_OK + kNT,             // [item buffer] description written
+  BAR_UNIT_FREE = BAR_UNIT + 2,          // [item buffer] read by 5 kNT warps
   BAR_MMA_DONE = BAR_UNIT_FREE + 2,      // every product of the block done (kNT commits)
   BAR_TAKE = BAR_MMA_DONE + 1,           // an answer of take_block
   BAR_RAW_FULL = BAR_TAKE + 1,           // [raw stage] 4-bit rows landed
-  BAR_RAW_EMPTY = BAR_RAW_FULL + kRaw,   // [raw stage] unpacked (128 threads)
+  BAR_RAW_EMPTY = BAR_RAW_FULL + kRaw,   // [raw stage] read (4 warps)
   BAR_COUNT = BAR_RAW_EMPTY + kRaw
 };
 static_assert(BAR_COUNT * 8 <= 512, "barrier area");
@@ -135,8 +138,8 @@ struct Unit {
   int kv;
   int kbeg;      // packed: row of key 0
   int j0, nj;    // key tiles j0 .. j0 + nj - 1
-  int t0[kMaxNT], t1[kMaxNT];    // those of row tile t: [t0, t1), counted from j0
-  int lo_max[kMaxNT], hi_min[kMaxNT];  // keys that every row of tile t sees: [lo_max, hi_min)
+  int t0[kNT], t1[kNT];          // those of row tile t: [t0, t1), counted from j0
+  int lo_max[kNT], hi_min[kNT];  // keys that every row of tile t sees: [lo_max, hi_min)
   int kend;      // no row sees a key from here on
   int s0, s1;    // packed: first and last sequence in the window
   int lim;       // paged: keys that the first token of the item sees
@@ -186,7 +189,6 @@ struct Place {
 
 // The place at position pos of the list; pre[i] counts the tiles of one head
 // of the requests before i.  Called by a whole warp.
-template <int kNT>
 __device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pre, long long pos) {
   int lo = 0, hi = a.batch;
   while (lo < hi) {
@@ -224,7 +226,6 @@ __device__ __forceinline__ Place place_at(const TileArgs& a, const long long* pr
 // The place behind a block: the next block, head or request with rows.  Called
 // only where the list goes on; never past the last request, also where lens
 // changed meanwhile.
-template <int kNT>
 __device__ __forceinline__ void next_block(const TileArgs& a, Place* p) {
   p->t0 = 0;
   if (++p->blk * kNT * a.tpt < p->r.n_new) return;
@@ -240,7 +241,6 @@ __device__ __forceinline__ void next_block(const TileArgs& a, Place* p) {
 
 // Describes the item at a place, tiles [t0, t1) of nt; lane t looks after row
 // tile t.
-template <int kNT>
 __device__ __forceinline__ void paged_unit(const TileArgs& a, const Place& p, int t1, int nt,
                                            Unit* u) {
   const int w = kNT * a.tpt, lane = threadIdx.x & 31, t = lane;
@@ -280,7 +280,6 @@ __device__ __forceinline__ void paged_unit(const TileArgs& a, const Place& p, in
 // Kept short: a block runs it once or a few times, and code that has to be
 // fetched first takes some ten clocks an instruction.
 __device__ __forceinline__ void packed_unit(const TileArgs& a, int block, Unit* u) {
-  constexpr int kNT = row_tiles(kPacked);
   const int w = kNT * a.tpt, win_rev = block / a.Hkv;
   const int lane = threadIdx.x & 31, t = lane >> 1;
   const int q0 = (a.windows - 1 - win_rev) * w, q_end = min(a.tokens, q0 + w);
@@ -458,58 +457,52 @@ __device__ __noinline__ void row_product(uint32_t t_p, uint32_t t_o, const uint8
   tmem_st_wait();
 }
 
-// Warps 8 to 11 of a 4-bit call: packed rows of a raw stage to 16-bit rows of a K/V
-// stage, as TMA would have written them.  A thread has one row of K or of V.
+// 4 bits: key tile n's packed rows to the 16-bit rows of its K/V stage, as TMA would
+// have written them, by the 128 threads of a row tile's softmax: a row of K or of V a
+// thread.  Parities tell two uses of a stage apart, not three: a raw stage always
+// belongs to the same row tile, and who unpacks tile n has waited for the end of tile
+// n - 3 - kStages4, stages coming free in order, also for a row tile that sees no key of
+// them.
 template <bool BF16>
-__device__ __forceinline__ void unpack_rows(const TileArgs& a, uint8_t* smem, uint32_t bar0,
-                                            const Unit* s_unit, const WaitCtl& wc) {
-#define BAR(i) (bar0 + 8u * (uint32_t)(i))
-  const int lane = threadIdx.x & 31, row = threadIdx.x & (kBN - 1);
+__device__ __forceinline__ bool unpack_tile(uint8_t* smem, uint32_t bar0, int n,
+                                            const WaitCtl& wc) {
+  const int row = threadIdx.x & (kBN - 1), from = n % kRaw, s = n % kStages4;
   const bool is_v = (threadIdx.x & 127) >= kBN;
-  int kt = 0;
-  for (int nu = 0;; ++nu) {
-    if (!mbar_wait_inline(BAR(BAR_UNIT + (nu & 1)), (nu >> 1) & 1, wc)) return;
-    const int more = s_unit[nu & 1].more, nj = s_unit[nu & 1].nj;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(BAR(BAR_UNIT_FREE + (nu & 1)));
-    if (!more) return;
-    for (int j = 0; j < nj; ++j, ++kt) {
-      const int from = kt % kRaw, s = kt % kStages;
-      if (!mbar_wait_inline(BAR(BAR_RAW_FULL + from), (kt / kRaw) & 1, wc)) return;
-      const uint8_t* const unit = smem + kSmemRaw + from * 2 * kRawHalf +
-                                  (is_v ? kRawHalf : 0) + (row >> 3) * kUnitBytes;
-      const uint4 c0 = *reinterpret_cast<const uint4*>(unit + (row & 7) * 32);
-      const uint4 c1 = *reinterpret_cast<const uint4*>(unit + (row & 7) * 32 + 16);
-      const uint32_t sw = *reinterpret_cast<const uint32_t*>(unit + kUnitScales + (row & 7) * 4);
-      mbar_arrive(BAR(BAR_RAW_EMPTY + from));
-      if (kt >= kStages && !mbar_wait_inline(BAR(BAR_KV_EMPTY + s), (kt / kStages - 1) & 1, wc))
-        return;
-      const uint32_t s_lo = __byte_perm(sw, sw, 0x1010), s_hi = __byte_perm(sw, sw, 0x3232);
-      uint8_t* const to =
-          smem + kSmemStage0 + s * kStageBytes + (is_v ? kHalfBytes : 0) + row * 128;
-      const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  if (!mbar_wait_inline(bar0 + 8u * (BAR_RAW_FULL + from), (n / kRaw) & 1, wc)) return false;
+  const uint8_t* const unit = smem + kSmemRaw + from * 2 * kRawHalf + (is_v ? kRawHalf : 0) +
+                              (row >> 3) * kUnitBytes;
+  const uint4 c0 = *reinterpret_cast<const uint4*>(unit + (row & 7) * 32);
+  const uint4 c1 = *reinterpret_cast<const uint4*>(unit + (row & 7) * 32 + 16);
+  const uint32_t sw = *reinterpret_cast<const uint32_t*>(unit + kUnitScales + (row & 7) * 4);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar0 + 8u * (BAR_RAW_EMPTY + from));
+  if (n >= kStages4 &&
+      !mbar_wait_inline(bar0 + 8u * (BAR_KV_EMPTY + s), (n / kStages4 - 1) & 1, wc))
+    return false;
+  const uint32_t s_lo = __byte_perm(sw, sw, 0x1010), s_hi = __byte_perm(sw, sw, 0x3232);
+  uint8_t* const to = smem + kSmemStage0 + s * kStageBytes + (is_v ? kHalfBytes : 0) + row * 128;
+  const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {  // channels 8 c .. and 32 + 8 c ..
-        uint32_t lo[4], hi[4];
+  for (int c = 0; c < 4; ++c) {  // channels 8 c .. and 32 + 8 c ..
+    uint32_t lo[4], hi[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t l0, h0, l1, h1;
-          scaled_codes<BF16>(w[2 * c + i], s_lo, s_hi, l0, h0, l1, h1);
-          lo[2 * i] = __byte_perm(l0, l1, 0x5410);
-          lo[2 * i + 1] = __byte_perm(l0, l1, 0x7632);
-          hi[2 * i] = __byte_perm(h0, h1, 0x5410);
-          hi[2 * i + 1] = __byte_perm(h0, h1, 0x7632);
-        }
-        *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) =
-            make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4*>(to + (((c + 4) ^ (row & 7)) << 4)) =
-            make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      }
-      fence_proxy_async_shared();
-      mbar_arrive(BAR(BAR_KV_FULL + s));
+    for (int i = 0; i < 2; ++i) {
+      uint32_t l0, h0, l1, h1;
+      scaled_codes<BF16>(w[2 * c + i], s_lo, s_hi, l0, h0, l1, h1);
+      lo[2 * i] = __byte_perm(l0, l1, 0x5410);
+      lo[2 * i + 1] = __byte_perm(l0, l1, 0x7632);
+      hi[2 * i] = __byte_perm(h0, h1, 0x5410);
+      hi[2 * i + 1] = __byte_perm(h0, h1, 0x7632);
     }
+    *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) =
+        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(to + (((c + 4) ^ (row & 7)) << 4)) =
+        make_uint4(hi[0], hi[1], hi[2], hi[3]);
   }
-#undef BAR
+  fence_proxy_async_shared();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar0 + 8u * (BAR_KV_FULL + s));
+  return true;
 }
 
 template <int MODE, bool BF16>
@@ -517,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const TileArgs a) {
   constexpr bool PAGED = MODE != kPacked, FOUR = MODE == kPaged4;
-  constexpr int kNT = row_tiles(MODE);
+  constexpr int kStages = FOUR ? kStages4 : kMaxStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -541,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(BAR_Q + i), 1);
       mbar_init(BAR(BAR_Q_FREE + i), kNT);
       mbar_init(BAR(BAR_UNIT + i), 1);
-      mbar_init(BAR(BAR_UNIT_FREE + i), 5 * kNT + (FOUR ? 4 : 0));
+      mbar_init(BAR(BAR_UNIT_FREE + i), 5 * kNT);
     }
     for (int i = 0; i < kNT; ++i) {
       s_turn[i] = 0;
@@ -554,14 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(BAR_V_OK + i), 128);
     }
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(BAR(BAR_KV_FULL + s), FOUR ? 128 : 1);
+      mbar_init(BAR(BAR_KV_FULL + s), FOUR ? 4 : 1);
       mbar_init(BAR(BAR_KV_EMPTY + s), kNT);
     }
     mbar_init(BAR(BAR_MMA_DONE), kNT);
     mbar_init(BAR(BAR_TAKE), 1);
     for (int s = 0; FOUR && s < kRaw; ++s) {
       mbar_init(BAR(BAR_RAW_FULL + s), 1);
-      mbar_init(BAR(BAR_RAW_EMPTY + s), 128);
+      mbar_init(BAR(BAR_RAW_EMPTY + s), 4);
     }
     fence_mbarrier_init();
   }
@@ -610,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   Place place{};
-  if (PAGED && warp == 15 && share.begin < share.end) place = place_at<kNT>(a, s_pre, share.begin);
+  if (PAGED && warp == 15 && share.begin < share.end) place = place_at(a, s_pre, share.begin);
 
   if (warp < 4 * kNT) {
     // ---------------- softmax: thread = row of tile t ----------------
@@ -649,7 +642,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int lo_max = su.lo_max[t] - su.j0 * kBN, hi_min = su.hi_min[t] - su.j0 * kBN;
       float m = -INFINITY, l = 0.f;
-      for (int j = j0; j < j1; ++j) {
+      if (FOUR)  // the item's first tiles; the others kAhead steps before their use
+        for (int j = 0; ok && j < min(kAhead, su.nj); ++j)
+          if ((kt + j) % kNT == t) ok = unpack_tile<BF16>(smem, bar0, kt + j, wc);
+      for (int j = FOUR ? 0 : j0; ok && j < (FOUR ? su.nj : j1); ++j) {
+        if (FOUR) {
+          if (j + kAhead < su.nj && (kt + j + kAhead) % kNT == t &&
+              !unpack_tile<BF16>(smem, bar0, kt + j + kAhead, wc)) {
+            ok = false;
+            break;
+          }
+          if (j >= j1) continue;  // j0 is 0
+        }
         const int k0 = j * kBN;
         const bool edge =
             k0 < lo_max || past_limit(k0, kBN, hi_min);  // the same for the whole tile
@@ -795,8 +799,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(BAR_UNIT_FREE + (nu & 1)));
     }
-  } else if (FOUR && warp < 12) {
-    unpack_rows<BF16>(a, smem, bar0, s_unit, wc);
   } else {
     if (warp == 15) {
       // ---------------- work items and loads ----------------
@@ -840,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           nt = tiles_of_block(place.r.n_keys, place.r.n_new, kNT * a.tpt, kBN, place.blk);
           place.t0 = min(place.t0, nt - 1);  // it is less, unless lens changed meanwhile
           steps = (int)min((long long)(nt - place.t0), share.end - pos);
-          paged_unit<kNT>(a, place, place.t0 + steps, nt, &u);
+          paged_unit(a, place, place.t0 + steps, nt, &u);
         } else {
           packed_unit(a, block, &u);
           checks |= block == 0;
@@ -857,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  last_block(share, pos + nt - 1)};
           }
           pos += steps;
-          if (pos < share.end) next_block<kNT>(a, &place);
+          if (pos < share.end) next_block(a, &place);
         }
         if (u.nj == 0) continue;
         const int qbuf = nq & 1;
@@ -1042,6 +1044,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
               ++np;
+            } else if (FOUR) {
+              // behind the products before, so that stages come free in their order
+              if (elect_one()) mma_commit(BAR(BAR_KV_EMPTY + s));
+              __syncwarp();
             } else if (lane == 0) {
               mbar_arrive(BAR(BAR_KV_EMPTY + s));
             }
@@ -1096,7 +1102,7 @@ int launch_packed_fwd(const PackedDims& d, const DevCtx& ctx, const RowsArg& q, 
       !encode_tmap_4d(&tk, d.bf16, k.p, d.tokens, d.Hkv, 1, k.t, k.h, 64, kBN, 1, 1) ||
       !encode_tmap_4d(&tv, d.bf16, v.p, d.tokens, d.Hkv, 1, v.t, v.h, 64, kBN, 1, 1))
     return ATTN_ERR_CUDA;
-  const int window = row_tiles(kPacked) * a.tpt;
+  const int window = kNT * a.tpt;
   a.windows = (d.tokens + window - 1) / window;
   const long long units = (long long)d.Hkv * a.windows;
   if (units > 0x7fffffffLL) return ATTN_ERR_SHAPE;
