@@ -19,7 +19,7 @@
 // Bound by memory: 128 bytes read and written a row of q, k and v, 36 written into 4
 // bits.  36,000 tokens of 32 / 8 heads in bfloat16 take 68 us = 6.5 TB/s, 96% of the
 // measured copy rate (one set of eight rows a warp 90 us, three 71, six 74; blocks for
-// all the work instead of a full SM's 75).  24,600 tokens into 4 bits 53 us, 69% of it:
+// all the work instead of a full SM's 75).  22,900 tokens into 4 bits 53 us, 69% of it:
 // the arithmetic of a K or V row, some 200 instructions a thread, takes as long as its
 // bytes (1700 instructions a token, issue slots 69% busy; three blocks a SM 52.8 us,
 // four 53.3, two 62).  64 tokens 2.4 us, one 1.9: launch and the chain offsets ->
