@@ -190,6 +190,59 @@ def test_append4(torch, dtype, heads, turn, case):
         same(got, want, "read back")
 
 
+@pytest.mark.parametrize("bits,turn", [(16, True), (4, True), (4, False)])
+def test_append_and_load_of_many_tokens(torch, bits, turn):
+    """So many that a thread takes several rows; an odd number of eights of rows."""
+    from causal_streaming_softmax_gb300 import api
+    H = Hkv = 17
+    dt, page = torch.bfloat16, 64
+    q, k, v, slots, cu, lens, pages = append_problem(torch, [(7, 11000), (0, 8000), (50, 1001)],
+                                                     H, Hkv, page, dt, 77, pad=5)
+    t = q.shape[0]
+    cos, sin = angles(torch, max(lens))
+    rows = torch.tensor([i for i in range(cu[-1]) if slots[i] >= 0], device="cuda")
+    pos = torch.tensor(positions(cu, lens), device="cuda")[rows]
+    at = torch.tensor(slots, device="cuda")[rows]
+    s = api.PagedShape(len(lens), t, H, Hkv, page, pages, 1, dtype=dt)
+    out = torch.full((t, H, 64), SENTINEL, dtype=dt, device="cuda")
+    args = (i32(torch, slots), i32(torch, cu), i32(torch, lens), out)
+    turned = rotate(k[rows], cos[pos], sin[pos]) if turn else k[rows].float()
+    if turn:
+        want_q = torch.full_like(out, SENTINEL)
+        want_q[rows] = rotate(q[rows], cos[pos], sin[pos]).to(dt)
+    if bits == 16:
+        kc, vc = (rnd(torch, (pages, Hkv, page, 64), dt, 5 + i) for i in range(2))
+        want_k, want_v = kc.clone(), vc.clone()
+        want_k[at // page, :, at % page] = turned.to(dt)
+        want_v[at // page, :, at % page] = v[rows]
+        api.attn_paged_append(s, q, k, v, cos, sin, *args, kc, vc)
+        same(kc, want_k, "K")
+        same(vc, want_v, "V")
+        same(out, want_q, "q")
+        return
+    kc, vc = (bytes_pool(torch, pages, Hkv, page, 9 + i) for i in range(2))
+    want_k, want_v = row_bytes(kc), row_bytes(vc)
+    want_k[at // page, :, at % page] = pack(*quantise(turned, dt))
+    want_v[at // page, :, at % page] = pack(*quantise(v[rows].float(), dt))
+    if turn:
+        api.attn_paged_append4(s, q, k, v, cos, sin, *args, kc, vc)
+        same(out, want_q, "q")
+    else:
+        api.attn_paged_append4(s, None, k, v, None, None, args[0], None, None, None, kc, vc)
+    same(row_bytes(kc), want_k, "K")
+    same(row_bytes(vc), want_v, "V")
+    # and back, every slot twice
+    twice = torch.cat([args[0], args[0].flip(0)])
+    both = torch.cat([rows, 2 * t - 1 - rows])
+    s = api.PagedShape(1, 2 * t, H, Hkv, page, pages, 1, dtype=dt)
+    ko, vo = (torch.full((2 * t, Hkv, 64), SENTINEL, dtype=dt, device="cuda") for _ in range(2))
+    api.attn_paged_load4(s, twice, kc, vc, ko, vo)
+    for got, pool in ((ko, kc), (vo, vc)):
+        want = torch.full_like(got, SENTINEL)
+        want[both] = values(pool, dt)[0][at // page, :, at % page].to(dt).repeat(2, 1, 1)
+        same(got, want, "read back")
+
+
 @pytest.mark.parametrize("n", [1, 31, 32, 33, 1023, 1024, 1025, 4096])
 def test_append_finds_every_request(torch, n):
     """As many requests as the search for a token's request takes steps."""
@@ -523,6 +576,38 @@ def test_paged4_queries_that_are_not_finite(torch):
     q[0, 3, 5], q[1, 7, 40], q[9, 0, 63] = 0, 0, 0
     o2, _ = run_paged4(torch, q, kc, vc, table, cu, lens)
     same(o[~bad], o2[~bad])
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("heads,first", [((16, 1), 2), ((8, 2), 5), ((33, 1), 1), ((24, 3), 3)])
+def test_paged4_chunks_of_unequal_row_tiles(torch, dtype, heads, first):
+    """Many chunks whose last row tiles are short or empty, over short and long caches:
+    items of one key tile and of many follow one another in a block."""
+    r = random.Random(first)
+    reqs = []
+    for i in range(120):
+        n = r.choice([first, first + 1, 8, 9, 17, 25, 33, 65, 70])
+        reqs.append((max(n, r.choice([1, 30, 64, 65, 129, 400, 1500])), n))
+    reqs[60] = (9000, 100)
+    page = [8, 16, 64, 32][first % 4]
+    p = paged4_problem(torch, reqs, heads[0], heads[1], page, getattr(torch, dtype), 21 + first)
+    q, kc, vc, table, cu, lens, _ = p
+    o, L = run_paged4(torch, q, kc, vc, table, cu, lens)
+    check_paged4(torch, q, kc, vc, table, cu, lens, o, L)
+    for _ in range(4):
+        o2, L2 = run_paged4(torch, q, kc, vc, table, cu, lens)
+        assert torch.equal(o, o2) and torch.equal(L, L2)
+
+
+@pytest.mark.parametrize("heads", [(8, 1), (12, 4), (5, 1)])
+def test_paged4_one_and_several_tokens_in_a_call(torch, heads):
+    """Items of up to eight rows, and of up to sixteen, in one call."""
+    n = 16 // (heads[0] // heads[1])
+    reqs = [(5000, 1), (4000, n), (700, 1), (n, n), (65, 1), (64, n), (300, 1)] * 5
+    q, kc, vc, table, cu, lens, _ = paged4_problem(torch, reqs, heads[0], heads[1], 16,
+                                                   torch.bfloat16, 31)
+    o, L = run_paged4(torch, q, kc, vc, table, cu, lens)
+    check_paged4(torch, q, kc, vc, table, cu, lens, o, L)
 
 
 def test_paged4_is_deterministic(torch):
