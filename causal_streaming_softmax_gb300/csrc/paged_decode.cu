@@ -51,7 +51,7 @@ namespace {
 // memory.  kWhole: a block takes whole items, so that nothing is joined.
 template <int CONSUMERS, int STAGES, bool WHOLE>
 struct Config {
-  static constexpr bool kWhole = WHOLE;
+  static constexpr bool kWhole = WHOLE, kSplit = false;
   static constexpr int kMaxBatch = WHOLE ? 1024 : kMaxPagedBatch;  // whole: <= the SMs
   static constexpr int kConsumers = CONSUMERS, kStages = STAGES;
   static constexpr int kThreads = 32 * (CONSUMERS + 1);

@@ -75,10 +75,11 @@ static_assert(kTiledShift >= 5 && (32 / 8 * kUnitBytes) % 128 == 0, "a box of 32
 constexpr int kLd = 68;  // floats a row of the joining buffer (bank spread)
 
 // A block's shape.  COLS: column tiles of eight query rows.  WHOLE: a block takes
-// whole items, so that nothing is joined.
-template <int COLS, bool WHOLE>
+// whole items, so that nothing is joined.  SPLIT: a request may be several items.
+template <int COLS, bool WHOLE, bool SPLIT = false>
 struct Config {
-  static constexpr bool kWhole = WHOLE;
+  static constexpr bool kWhole = WHOLE, kSplit = SPLIT;
+  static_assert(!(WHOLE && SPLIT), "a block for each item of a batch");
   static constexpr int kTileKeys = css::kTileKeys;
   static constexpr int kCols = COLS, kRows = 8 * COLS;
   static constexpr int kBlocks = COLS == 1 ? 3 : 2;  // a SM
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
       if (!ok) break;
       if (lane == 0) {
         s_item[qbuf] = Item{r, sg.kv, sg.t0, t1, C::kWhole || (sg.t0 == 0 && t1 == sg.nt)};
-        mbar_arrive_expect_tx(BAR(BAR_Q + qbuf), a.ntok * a.G * 128);
+        mbar_arrive_expect_tx(BAR(BAR_Q + qbuf), a.split * a.G * 128);
         tma_load_4d(sbase + qbuf * kQ, &tm_q, BAR(BAR_Q + qbuf), 0, 0, sg.kv, r.q0);
       }
       ++nq;
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         const uint32_t ks = sbase + C::kSmemStage + s * kStage;
         if (__builtin_expect(past_limit(t * kTileKeys, kTileKeys, first_lim), 0))
           walk(std::true_type{}, AllCols{}, ks, t * kTileKeys);
-        else if (kCols > 1 && sg.r.n_new * a.G <= 8)  // 32 beside chunks: 199 -> 191 us in all
+        else if (kCols > 1 && sg.r.n_new * a.G <= 8)
           walk(std::false_type{}, OneCol{}, ks, t * kTileKeys);
         else
           walk(std::false_type{}, AllCols{}, ks, t * kTileKeys);
@@ -738,7 +739,7 @@ int launch(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolAr
   const uint32_t units = (1u << d.shift) / 8;
   const uint32_t box = units < kTileKeys / 8 ? units : kTileKeys / 8;
   if (!encode_tmap_4d(&tq, d.bf16, q.p, d.G, d.Hkv, d.tokens, q.h, q.h * d.G, q.t, d.G, 1,
-                      args.ntok) ||
+                      args.split) ||
       !encode_tmap_units(&tk, kc.p, units, d.Hkv, d.pages, kc.h, kc.pg, box) ||
       !encode_tmap_units(&tv, vc.p, units, d.Hkv, d.pages, vc.h, vc.pg, box))
     return ATTN_ERR_CUDA;
@@ -761,6 +762,12 @@ int tokens4(const PagedDims& d) {
   return d.max_new < decode_tokens(d.G) ? d.max_new : decode_tokens(d.G);
 }
 
+// Beside chunks, requests of nine to sixteen rows are rare and go as items of up to
+// eight, which read K and V again (from L2 for the most part): 32 requests over
+// 2048..8192 keys, 32 / 8 heads, and a chunk of 300 tokens, us with two column tiles for
+// all / with items of eight: one token each 84 / 76, four 90 / 99.
+bool splits(const PagedDims& d) { return d.G <= 8 && d.max_new > decode_tokens(d.G); }
+
 template <int COLS>
 int launch_cols(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolArg& kc,
                 const PoolArg& vc, const DecodeArgs& args, int blocks, int which,
@@ -777,13 +784,13 @@ int launch_cols(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const P
 // 9.0 / 12.3; eight of 250 9.2 / 5.9, of 777 10.9 / 8.9, of 1500 10.1 / 12.9; fifty of
 // 500 17.4 / 9.1.  The width stands for the lengths, which the host does not see.
 bool decode4_whole(const PagedDims& d, int sm_count) {
-  return (long long)d.batch * d.Hkv <= decode4_blocks(d) * sm_count &&
+  return !splits(d) && (long long)d.batch * d.Hkv <= decode4_blocks(d) * sm_count &&
          ((long long)d.width << d.shift) <= kWholeKeys;
 }
 
 // One column tile serves a token step of up to eight heads a group.
 int decode4_blocks(const PagedDims& d) {
-  return tokens4(d) * d.G <= 8 ? Config<1, false>::kBlocks : Config<2, false>::kBlocks;
+  return splits(d) || tokens4(d) * d.G <= 8 ? Config<1, false>::kBlocks : Config<2, false>::kBlocks;
 }
 
 int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
@@ -792,7 +799,11 @@ int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q
                          const RowsArg& o, float* lse, cudaStream_t stream) {
   const int ntok = tokens4(d);
   const DecodeArgs args{d.batch, d.tokens, d.H, d.Hkv, d.G, ntok, d.max_new, d.pages, d.width,
-                        d.shift, d.c, cu, lens, table, o, lse, part, ctx.err, ctx.wait_ns};
+                        d.shift, d.c, cu, lens, table, o, lse, part, ctx.err, ctx.wait_ns,
+                        splits(d) ? 8 / d.G : ntok};
+  if (splits(d))
+    return launch<Config<1, false, true>>(d, ctx, q, kc, vc, args, blocks, kSmemDecode4SplitF16,
+                                          stream);
   if (ntok * d.G <= 8)
     return launch_cols<1>(d, ctx, q, kc, vc, args, blocks, kSmemDecode4F16, stream);
   return launch_cols<2>(d, ctx, q, kc, vc, args, blocks, kSmemDecode4WideF16, stream);

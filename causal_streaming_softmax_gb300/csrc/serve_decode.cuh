@@ -17,6 +17,7 @@ struct DecodeArgs {
   PartArgs part;
   uint32_t* err;
   uint64_t wait_ns;
+  int split;  // C::kSplit: tokens of an item, at most; else all of a request
 };
 
 // A request's rows and keys; n_new 0 for one that this kernel does not take.
@@ -38,10 +39,25 @@ __device__ __forceinline__ int tiles_of(int n_keys) {
   return n_keys <= 0 ? 1 : (n_keys - 1) / C::kTileKeys + 1;
 }
 
+// C::kSplit: a request with more tokens than an item has rows for is several: its
+// first `split` tokens over the keys that they see, and so on.
+template <class C>
+__device__ __forceinline__ int sub_count(const DecodeArgs& a, const Request& r) {
+  return C::kSplit ? (r.n_new + a.split - 1) / a.split : 1;
+}
+template <class C>
+__device__ __forceinline__ Request sub_request(const DecodeArgs& a, const Request& r, int i) {
+  if (!C::kSplit) return r;
+  const int first = i * a.split, n = min(a.split, r.n_new - first);
+  return Request{r.q0 + first, n, r.n_keys - (r.n_new - first - n)};
+}
+
 // A place in the tile list: tile t0 of nt of a request and K/V head.
 struct Place {
   Request r;
   int req, kv, t0, nt;
+  Request all;  // C::kSplit: r is part `sub` of it
+  int sub;
 };
 
 // What the producer hands the consumers beside an item's Q: they read no device
@@ -69,11 +85,23 @@ __device__ __forceinline__ Place place_at(const DecodeArgs& a, const long long* 
   p.req = lo - 1;
   const long long off = pos - pre[p.req] * a.Hkv;
   bool b;
-  p.r = request_at(a, p.req, &b);
+  p.all = request_at(a, p.req, &b);
+  p.sub = 0;
+  p.r = sub_request<C>(a, p.all, 0);
   p.nt = tiles_of<C>(p.r.n_keys);
-  const long long kv = C::kWhole ? off : quot(off, p.nt);
-  p.t0 = C::kWhole ? 0 : (int)(off - kv * p.nt);
+  const int subs = sub_count<C>(a, p.all);
+  long long per = p.nt;  // tiles of a head
+  if (C::kSplit)
+    for (int i = 1; i < subs; ++i) per += tiles_of<C>(sub_request<C>(a, p.all, i).n_keys);
+  const long long kv = C::kWhole ? off : quot(off, per);
+  p.t0 = C::kWhole ? 0 : (int)(off - kv * per);
   p.kv = (int)min(kv, a.Hkv - 1ll);  // less already, unless lens changed meanwhile
+  if (C::kSplit)
+    while (p.t0 >= p.nt && p.sub + 1 < subs) {
+      p.t0 -= p.nt;
+      p.r = sub_request<C>(a, p.all, ++p.sub);
+      p.nt = tiles_of<C>(p.r.n_keys);
+    }
   return p;
 }
 
@@ -83,13 +111,24 @@ __device__ __forceinline__ Place place_at(const DecodeArgs& a, const long long* 
 template <class C>
 __device__ __forceinline__ void next_place(const DecodeArgs& a, const long long* pre, Place* p) {
   p->t0 = 0;
-  if (++p->kv < a.Hkv) return;
+  if (C::kSplit && sub_count<C>(a, p->all) > 1) {
+    if (++p->sub == sub_count<C>(a, p->all)) p->sub = 0, ++p->kv;
+    if (p->kv < a.Hkv) {
+      p->r = sub_request<C>(a, p->all, p->sub);
+      p->nt = tiles_of<C>(p->r.n_keys);
+      return;
+    }
+  } else if (++p->kv < a.Hkv) {
+    return;
+  }
   p->kv = 0;
   do {
     p->req = min(p->req + 1, a.batch - 1);
   } while (pre[p->req + 1] == pre[p->req] && p->req + 1 < a.batch);
   bool b;
-  p->r = request_at(a, p->req, &b);
+  p->all = request_at(a, p->req, &b);
+  p->sub = 0;
+  p->r = sub_request<C>(a, p->all, 0);
   p->nt = tiles_of<C>(p->r.n_keys);
 }
 
@@ -108,7 +147,10 @@ __device__ __forceinline__ void tiles_before_each(const DecodeArgs& a, long long
     bool b;
     const Request r = request_at(a, i, &b);
     bad |= b;
-    s_pre[i + 1] = sum += r.n_new > 0 ? (C::kWhole ? 1 : tiles_of<C>(r.n_keys)) : 0;
+    int subs = r.n_new > 0 ? sub_count<C>(a, r) : 0;
+    while (--subs >= 0)
+      sum += C::kWhole ? 1 : tiles_of<C>(sub_request<C>(a, r, subs).n_keys);
+    s_pre[i + 1] = sum;
   }
   if (bad && blockIdx.x == 0) atomicOr(a.err, kErrIndex);
   long long upto = sum;

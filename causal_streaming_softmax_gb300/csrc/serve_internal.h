@@ -85,6 +85,8 @@ enum {
   kSmemDecode4WideBf16,
   kSmemDecode4WideWholeF16,
   kSmemDecode4WideWholeBf16,
+  kSmemDecode4SplitF16,
+  kSmemDecode4SplitBf16,
   kSmemRows4F16,
   kSmemRows4Bf16,
   kSmemKernels
