@@ -599,6 +599,23 @@ def test_paged4_chunks_of_unequal_row_tiles(torch, dtype, heads, first):
         assert torch.equal(o, o2) and torch.equal(L, L2)
 
 
+@pytest.mark.parametrize("heads", [(2, 2), (4, 2), (15, 5), (8, 2), (5, 1), (12, 2), (7, 1),
+                                   (8, 1)])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_paged4_several_tokens_beside_a_chunk(torch, heads, dtype):
+    """Requests of nine to sixteen rows are several items there; some see no key."""
+    most = 16 // (heads[0] // heads[1])
+    reqs = [(900, 40)]
+    for n in range(1, most + 1):
+        reqs += [(4000 - 7 * n, n), (n, n), (max(0, n - 3), n), (0, n), (64 + n - 1, n), (321, n)]
+    q, kc, vc, table, cu, lens, _ = paged4_problem(torch, reqs, heads[0], heads[1], 16,
+                                                   getattr(torch, dtype), 41)
+    o, L = run_paged4(torch, q, kc, vc, table, cu, lens)
+    check_paged4(torch, q, kc, vc, table, cu, lens, o, L)
+    o2, L2 = run_paged4(torch, q, kc, vc, table, cu, lens)
+    assert torch.equal(o, o2) and torch.equal(L, L2)
+
+
 @pytest.mark.parametrize("heads", [(8, 1), (12, 4), (5, 1)])
 def test_paged4_one_and_several_tokens_in_a_call(torch, heads):
     """Items of up to eight rows, and of up to sixteen, in one call."""
