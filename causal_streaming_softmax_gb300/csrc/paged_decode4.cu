@@ -655,6 +655,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         if (!ok) break;
         if (++slot == kRing) slot = 0, turn ^= 1;
         const uint32_t ks = sbase + C::kSmemStage + s * kStage;
+        // One column tile where the item fills no more: 64 one-token requests of a call that
+        // may have four tokens each take 72 us so, 77 with both.
         if (__builtin_expect(past_limit(t * kTileKeys, kTileKeys, first_lim), 0))
           walk(std::true_type{}, AllCols{}, ks, t * kTileKeys);
         else if (kCols > 1 && sg.r.n_new * a.G <= 8)
