@@ -27,8 +27,13 @@
 //    off V's codes (left in, it would be taken off a sum ten times the result);
 //  * weights times V's scales are binary16 too, a weight of 1 counting 2^kBias and the
 //    scales in a unit near the largest so far: spacing 2^-35 of that;
-//  * m and the unit are followed only when a lane's sum of a step's weights passes
-//    kMost or a scale v_most: one vote a step, no maximum over the keys' lanes;
+//  * m and the units are followed only when a lane's sum of a step's weights passes
+//    kMost or a scale leaves its unit's range: one vote a step, no maximum over the keys'
+//    lanes;
+//  * the two channel groups have units of their own, which the keys that every row of
+//    the item sees set.  In a tile whose scales lie further apart than binary16 weights hold,
+//    weights times scales go in as the sum of two bfloat16 numbers: 16 bits, and
+//    binary32's range (twice the products of V);
 //  * a lane converts the scales of two keys and passes them on through shared memory,
 //    each twice, as operands of the paired binary32 instructions.
 // Tiles of 64 keys go round four consumer warps a block, each with a ring of three;
@@ -61,11 +66,17 @@ namespace css {
 namespace {
 
 // A weight counts 2^kBias where the score is m, so that binary16 holds small ones
-// too.  What a lane's weights of a row in a step may add up to, and the binary orders
-// that a scale of V may pass its unit by, before m and the unit are followed: a weight
-// times a scale stays at or below 2^15.
-constexpr float kBias = 10.f, kMost = 0x1p13f;
-constexpr int kVSlack = 2;
+// too.  What a lane's weights of a row in a step may add up to, and what a scale of V
+// may reach in its unit, before m and the unit are followed: a weight times a scale
+// stays at or below 2^15.  A scale of kVLeast units is the least for the binary16
+// product: there a weight of 1 counts 1, so that what binary16 leaves out of a weight
+// times a scale is at most 2^-25 of the key's value, as where weights alone are held in it.
+constexpr float kBias = 10.f, kMost = 0x1p13f, kVMost = 4.f, kVLeast = 0x1p-10f;
+// The bfloat16 product: what a scale may reach in its unit, so that sums stay inside
+// binary32.  A tile for it sets a unit at its least scale, or kVFar of its largest: units
+// only go up, as sums that are carried to a higher one shrink and cannot overflow.
+constexpr float kVTop = 0x1p60f, kVFar = 0x1p-40f;
+constexpr float kVNone = 0x1p126f;  // the inverse before a group has a scale above zero
 constexpr int kTileKeys = 64;
 constexpr int kGroup = 4;  // tiles that the producer hands out at a time, eight lanes each
 // Pages of so many rows (their logarithm) are copied by tensor maps, whose boxes have
@@ -155,6 +166,7 @@ __device__ __forceinline__ void raw_codes(uint32_t w, uint32_t& lo0, uint32_t& h
   hi1 = v & 0x00f000f0u;
 }
 constexpr float kLoZero = 0x1p-21f, kHiZero = 0x1p-17f;  // what stands for code 0
+constexpr uint32_t kLoUnit = 0x33803380u, kHiUnit = 0x35803580u;  // pairs of bfloat16 2^-24, 2^-20
 
 // The same as code 2^-24 and code 2^-20.
 __device__ __forceinline__ void signed_codes(uint32_t w, uint32_t& lo0, uint32_t& hi0,
@@ -184,6 +196,22 @@ template <bool BF16>
 __device__ __forceinline__ bool odd_scale(uint32_t s) {
   constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
   return (s & e) == e || (s & (e << 16)) == (e << 16);
+}
+
+// The magnitudes of a row's two scales.
+template <bool BF16>
+__device__ __forceinline__ float2 magnitudes(uint32_t s) {
+  return make_float2(half_to_f32<BF16>((uint16_t)(s & 0x7fffu)),
+                     half_to_f32<BF16>((uint16_t)(s >> 16 & 0x7fffu)));
+}
+
+// The inverse of a power of two between 2^-126 and 2^126.
+__device__ __forceinline__ float inverse2(float x) {
+  return __uint_as_float((254u << 23) - __float_as_uint(x));
+}
+// That of the power of two at x, or the next below it (from 2^-125 on).
+__device__ __forceinline__ float inverse_unit(float x) {
+  return inverse2(fmaxf(__uint_as_float(__float_as_uint(x) & 0x7f800000u), 0x1p-125f));
 }
 
 template <bool BF16, class C>
@@ -429,10 +457,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
       pos += C::kWhole ? 1 : t1 - sg.t0;
       const int first_lim = row_limit(n_keys, sg.r.n_new, 0);  // keys that every row sees
       // neg_m: kBias - m in base 2; most: what a lane's weights of a row in a step may
-      // add up to.  V's scales count in a unit of their own: v_inv is its inverse,
-      // v_most what a scale may reach
+      // add up to.  V's scales count in units of their own, low and high channels, which
+      // only rise; v_inv are their inverses
       float2 neg_m[kCols], most[kCols], l[kCols];
-      float v_inv = 1.f, v_most = 0.f;
+      float2 v_inv = make_float2(kVNone, kVNone);
       float o[kCols][4][4];
 #pragma unroll
       for (int n = 0; n < kCols; ++n) {
@@ -442,35 +470,125 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         for (int j = 0; j < 4; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
       }
 
-      // the warp's keys of a tile for the first `cols` column tiles; EDGE: some row
-      // misses one of them
-      const auto walk = [&](auto edge_tag, auto cols_tag, uint32_t ks, int k0) {
+      // The warp's keys of a tile for the first `cols` column tiles.  EDGE: whatever they
+      // are; else every row sees all of them, and the answer is false, with nothing done,
+      // where a scale lies outside the units' range.
+      const auto walk = [&](auto edge_tag, auto cols_tag, uint32_t ks, int k0) -> bool {
         constexpr bool EDGE = decltype(edge_tag)::value;
         constexpr int cols = decltype(cols_tag)::value;
         const uint32_t vs = ks + kHalf;
         // scales, each twice, to where the lanes of a key find them: keys `lane` and 32 on
-        bool odd = false;  // a scale of the edge that some row must not meet
-        float2 v_s[2];     // low and high channels
+        const int in_unit = (lane >> 3) * kUnitBytes + kUnitScales + (lane & 7) * 4;
+        uint32_t vw[2];  // V's: low and high channels
+        float2 v[2];     // in their units
+        const auto in_units = [&] {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            v[x] = make_float2(half_to_f32<BF16>((uint16_t)vw[x]) * v_inv.x,
+                               half_to_f32<BF16>((uint16_t)(vw[x] >> 16)) * v_inv.y);
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          vw[x] = lds32(vs + in_unit + 4 * x * kUnitBytes);
+          // keys that no row sees count as zero whatever stands there
+          if (EDGE && k0 + lane + 32 * x >= n_keys) vw[x] = 0;
+        }
+        in_units();
+        const bool first = !EDGE && v_inv.x == kVNone && v_inv.y == kVNone;
+        if (first) {  // units at the tile's largest scales, if the others fit
+          float t[2] = {0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 m = magnitudes<BF16>(vw[x]);
+            t[0] = fmaxf(t[0], m.x), t[1] = fmaxf(t[1], m.y);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)  // as bits, which rise with them
+            t[h] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(t[h])));
+          if (t[0] > 0.f && t[0] < INFINITY) v_inv.x = inverse_unit(t[0]);
+          if (t[1] > 0.f && t[1] < INFINITY) v_inv.y = inverse_unit(t[1]);
+          in_units();
+        }
+        // a scale that the units do not hold, a zero among them (a NaN may stay: it gives
+        // NaN to the rows that see it, which in a full tile are all)
+        float2 size[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          size[x] = make_float2(fabsf(v[x].x), fabsf(v[x].y));
+          if (EDGE && k0 + lane + 32 * x >= n_keys) size[x] = make_float2(1.f, 1.f);
+        }
+        bool out =
+            !(fmaxf(fmax3(size[0].x, size[0].y, size[1].x), size[1].y) <= kVMost &&
+              fminf(fminf(size[0].x, size[0].y), fminf(size[1].x, size[1].y)) >= kVLeast);
+        if (EDGE) out |= odd_scale<BF16>(vw[0]) || odd_scale<BF16>(vw[1]);
+        bool odd = false;   // EDGE: a scale that some row must not meet
+        bool wide = false;  // EDGE: weights as two bfloat16 numbers
+        const auto apart = [&](uint32_t w) {  // of a key that some row misses: not a product
+          const float2 m = magnitudes<BF16>(w);
+          return odd_scale<BF16>(w) || m.x * v_inv.x > kVTop || m.y * v_inv.y > kVTop;
+        };
+        if (EDGE && __any_sync(0xffffffffu, out)) {
+          // the largest finite scale and the least above zero: of keys that every row
+          // sees, and of all where there is neither such a scale nor a unit
+          float t[2], u[2], inv[2] = {v_inv.x, v_inv.y};
+#pragma unroll 1
+          for (int lim = first_lim;; lim = n_keys) {
+            t[0] = t[1] = 0.f, u[0] = u[1] = INFINITY;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float2 m = magnitudes<BF16>(vw[x]);
+              const bool in = k0 + lane + 32 * x < lim;
+              if (in && m.x < INFINITY && m.x > 0.f)
+                t[0] = fmaxf(t[0], m.x), u[0] = fminf(u[0], m.x);
+              if (in && m.y < INFINITY && m.y > 0.f)
+                t[1] = fmaxf(t[1], m.y), u[1] = fminf(u[1], m.y);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // as bits, which rise with them
+              t[h] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(t[h])));
+              u[h] = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(u[h])));
+              // up to the largest where binary16 holds the others beside it; else, where
+              // it must be, low
+              const bool none = inv[h] == kVNone;
+              if (t[h] > 0.f && (none || (lim == first_lim && t[h] * inv[h] > kVMost))) {
+                const float to = inverse_unit(t[h]);
+                if (u[h] * to >= kVLeast)
+                  inv[h] = to;
+                else if (none || t[h] * inv[h] > kVTop)
+                  inv[h] = inverse_unit(fmaxf(u[h], t[h] * kVFar));
+              }
+            }
+            if (lim == n_keys || (inv[0] != kVNone && inv[1] != kVNone)) break;
+          }
+          const float2 f = make_float2(inv[0] * inverse2(v_inv.x), inv[1] * inverse2(v_inv.y));
+#pragma unroll
+          for (int n = 0; n < kCols; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[n][j][e] *= (j & 1) ? f.y : f.x;
+          v_inv = make_float2(inv[0], inv[1]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (k0 + lane + 32 * x >= first_lim && apart(vw[x])) vw[x] = 0, odd = true;
+          in_units();
+          out = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float lo = fabsf(v[x].x), hi = fabsf(v[x].y);
+            out |= lo > kVMost || (lo < kVLeast && lo > 0.f);
+            out |= hi > kVMost || (hi < kVLeast && hi > 0.f);
+          }
+          wide = __any_sync(0xffffffffu, out);
+        }
         __syncwarp();
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int key = lane + 32 * x;
-          const int at = (key >> 3) * kUnitBytes + kUnitScales + (key & 7) * 4;
-          const uint32_t kw = lds32(ks + at);
-          uint32_t vw = lds32(vs + at);
-          if (EDGE) {
-            // keys that no row sees count as zero whatever stands there, and so, for
-            // now, does one that some row misses and that is not finite
-            if (k0 + key >= n_keys) vw = 0;
-            if (k0 + key >= first_lim && odd_scale<BF16>(vw)) vw = 0, odd = true;
-          }
+          const uint32_t kw = lds32(ks + in_unit + 4 * x * kUnitBytes);
           const float lo = half_to_f32<BF16>((uint16_t)kw),
                       hi = half_to_f32<BF16>((uint16_t)(kw >> 16));
-          v_s[x] = make_float2(half_to_f32<BF16>((uint16_t)vw),
-                               half_to_f32<BF16>((uint16_t)(vw >> 16)));
-          const float2 v = make_float2(v_s[x].x * v_inv, v_s[x].y * v_inv);
-          s_scale[key] = make_float4(lo, lo, hi, hi);
-          s_scale[kTileKeys + key] = make_float4(v.x, v.x, v.y, v.y);
+          s_scale[lane + 32 * x] = make_float4(lo, lo, hi, hi);
+          s_scale[kTileKeys + lane + 32 * x] = make_float4(v[x].x, v[x].x, v[x].y, v[x].y);
         }
         __syncwarp();
         // scores: [.][step][key g, key g + 8 of the step], rows 2 tq and 2 tq + 1
@@ -533,29 +651,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
           }
           return big;
         };
-        const float v_top = fmaxf(fmaxf(fabsf(v_s[0].x), fabsf(v_s[0].y)),
-                                  fmaxf(fabsf(v_s[1].x), fabsf(v_s[1].y)));  // less NaN
         const bool big = weigh();
-        if (__any_sync(0xffffffffu, big || v_top > v_most)) {
-          // V's unit: a power of two at the largest scale that is finite
-          float v = 0.f, fv = 1.f;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (fabsf(v_s[x].x) < INFINITY) v = fmaxf(v, fabsf(v_s[x].x));
-            if (fabsf(v_s[x].y) < INFINITY) v = fmaxf(v, fabsf(v_s[x].y));
-          }
-          v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
-          if (v > v_most) {
-            const int ex = min(max((int)(__float_as_uint(v) >> 23) - 127, -110), 125);
-            const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-            fv = inv / v_inv;  // O is zero before the first
-            v_inv = inv;
-            v_most = __uint_as_float((uint32_t)(min(ex + kVSlack, 127) + 127) << 23);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float2 y = make_float2(v_s[x].x * v_inv, v_s[x].y * v_inv);
-              s_scale[kTileKeys + lane + 32 * x] = make_float4(y.x, y.x, y.y, y.y);
-            }
+        if (__any_sync(0xffffffffu, big || (!EDGE && out))) {
+          if (!EDGE && __any_sync(0xffffffffu, out)) {
+            if (first) v_inv = make_float2(kVNone, kVNone);
+            return false;
           }
 #pragma unroll
           for (int n = 0; n < cols; ++n) {
@@ -572,7 +672,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
             }
             follow(x.x, unit[n].x, &neg_m[n].x, &most[n].x, &l[n].x, &f.x);
             follow(x.y, unit[n].y, &neg_m[n].y, &most[n].y, &l[n].y, &f.y);
-            f.x *= fv, f.y *= fv;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               o[n][j][0] *= f.x, o[n][j][2] *= f.x;
@@ -584,36 +683,57 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         }
 #pragma unroll
         for (int n = 0; n < cols; ++n) l[n] = __fadd2_rn(l[n], sum[n]);
+        // O += V^T P^T.  WIDE: weights times scales in two terms
+        const auto product = [&](auto wide_tag) {
+          constexpr bool WIDE = decltype(wide_tag)::value;
+          constexpr int kTerms = WIDE ? 2 : 1;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          uint32_t pf[cols][2][2];  // [.][low, high channels][keys]
+          for (int i = 0; i < kSteps; ++i) {
+            uint32_t pf[kTerms][cols][2][2];  // [.][.][low, high channels][keys]
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float4 s4 = s_scale[kTileKeys + 16 * i + 8 * u + g];
+            for (int u = 0; u < 2; ++u) {
+              const float4 s4 = s_scale[kTileKeys + 16 * i + 8 * u + g];
 #pragma unroll
-            for (int n = 0; n < cols; ++n) {
-              const float2 lo = __fmul2_rn(p[n][i][u], make_float2(s4.x, s4.y)),
-                           hi = __fmul2_rn(p[n][i][u], make_float2(s4.z, s4.w));
-              pf[n][0][u] = transpose8(pack_f16x2(lo.x, lo.y));
-              pf[n][1][u] = transpose8(pack_f16x2(hi.x, hi.y));
+              for (int n = 0; n < cols; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float2 w = __fmul2_rn(p[n][i][u], h ? make_float2(s4.z, s4.w)
+                                                            : make_float2(s4.x, s4.y));
+                  const uint32_t term = pack2<WIDE>(w.x, w.y);
+                  pf[0][n][h][u] = transpose8(term);
+                  if (WIDE)
+                    pf[kTerms - 1][n][h][u] = transpose8(
+                        pack2<WIDE>(w.x - half_to_f32<WIDE>((uint16_t)term),
+                                    w.y - half_to_f32<WIDE>((uint16_t)(term >> 16))));
+                }
             }
+            uint32_t w[4];
+            ldmatrix_x4_trans(vs + (2 * i + (mi & 1)) * kUnitBytes + mr * 32 + (mi >> 1) * 16, w);
+            // channel tiles 2 g, 32 + 2 g, 2 g + 1, 33 + 2 g (rows g; + 16 in rows g + 8)
+            uint32_t x[4][4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t word = w[r == 1 ? 2 : (r == 2 ? 1 : r)];
+              if (WIDE)
+                scaled_codes<true>(word, kLoUnit, kHiUnit, x[0][r], x[1][r], x[2][r], x[3][r]);
+              else
+                signed_codes(word, x[0][r], x[1][r], x[2][r], x[3][r]);
+            }
+#pragma unroll
+            for (int n = 0; n < cols; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < kTerms; ++k)
+                  mma_16816<WIDE>(o[n][j], x[j], pf[k][n][j & 1][0], pf[k][n][j & 1][1]);
           }
-          uint32_t w[4];
-          ldmatrix_x4_trans(vs + (2 * i + (mi & 1)) * kUnitBytes + mr * 32 + (mi >> 1) * 16, w);
-          // channel tiles 2 g, 32 + 2 g, 2 g + 1, 33 + 2 g (rows g; + 16 in rows g + 8)
-          uint32_t x[4][4];
-          signed_codes(w[0], x[0][0], x[1][0], x[2][0], x[3][0]);
-          signed_codes(w[2], x[0][1], x[1][1], x[2][1], x[3][1]);
-          signed_codes(w[1], x[0][2], x[1][2], x[2][2], x[3][2]);
-          signed_codes(w[3], x[0][3], x[1][3], x[2][3], x[3][3]);
-#pragma unroll
-          for (int n = 0; n < cols; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma_f16(o[n][j], x[j], pf[n][j & 1], o[n][j]);
-        }
+        };
+        if (EDGE && wide)
+          product(std::true_type{});
+        else
+          product(std::false_type{});
         if (EDGE && __any_sync(0xffffffffu, odd)) {
-          // what those keys give the rows that see them: infinities and NaN, of
-          // whatever unit
+          // what those keys give the rows that see them, in binary32
           const int n_new = s_item[qbuf].r.n_new;
 #pragma unroll
           for (int i = 0; i < kSteps; ++i)
@@ -624,7 +744,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
                 const int key = k0 + 16 * i + 8 * u + k;
                 const uint32_t at = vs + (2 * i + u) * kUnitBytes;
                 const uint32_t sw = lds32(at + kUnitScales + 4 * k);
-                if (key < first_lim || key >= n_keys || !odd_scale<BF16>(sw)) continue;
+                if (key < first_lim || key >= n_keys || !apart(sw)) continue;
 #pragma unroll
                 for (int n = 0; n < cols; ++n)
 #pragma unroll
@@ -640,13 +760,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
                         const uint32_t b = smem[at - sbase + k * 32 + byte] >> (4 * (j & 1));
                         const float v = (float)((int)(b & 15) - 8) *
                                         half_to_f32<BF16>((uint16_t)(sw >> (16 * (j & 1))));
-                        // the row's other group, if finite, was dropped as well
-                        const float f = v * v_inv * ((j & 1) ? 0x1p-20f : 0x1p-24f);
+                        // both of the key's groups were dropped
+                        const float f =
+                            (j & 1) ? v * v_inv.y * 0x1p-20f : v * v_inv.x * 0x1p-24f;
                         if (key < lim) o[n][j][2 * h + e] = fmaf(wt, f, o[n][j][2 * h + e]);
                       }
                   }
               }
         }
+        return true;
       };
       for (int t = sg.t0 + (warp + kConsumers - it % kConsumers) % kConsumers; t < t1;
            t += kConsumers) {
@@ -657,12 +779,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         const uint32_t ks = sbase + C::kSmemStage + s * kStage;
         // One column tile where the item fills no more: 64 one-token requests of a call that
         // may have four tokens each take 72 us so, 77 with both.
-        if (__builtin_expect(past_limit(t * kTileKeys, kTileKeys, first_lim), 0))
-          walk(std::true_type{}, AllCols{}, ks, t * kTileKeys);
-        else if (kCols > 1 && sg.r.n_new * a.G <= 8)
-          walk(std::false_type{}, OneCol{}, ks, t * kTileKeys);
-        else
-          walk(std::false_type{}, AllCols{}, ks, t * kTileKeys);
+        bool edge = past_limit(t * kTileKeys, kTileKeys, first_lim);
+        if (!edge) {
+          if (kCols > 1 && sg.r.n_new * a.G <= 8)
+            edge = !walk(std::false_type{}, OneCol{}, ks, t * kTileKeys);
+          else
+            edge = !walk(std::false_type{}, AllCols{}, ks, t * kTileKeys);
+        }
+        if (__builtin_expect(edge, 0)) walk(std::true_type{}, AllCols{}, ks, t * kTileKeys);
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(BAR_EMPTY + s));
       }
@@ -691,7 +815,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {  // low and high channels, back to units of one
-          const float raw = (x ? 0x1p20f : 0x1p24f) * kOne, v_unit = 1.f / v_inv;
+          const float raw = (x ? 0x1p20f : 0x1p24f) * kOne,
+                      v_unit = inverse2(x ? v_inv.y : v_inv.x);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll

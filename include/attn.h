@@ -597,8 +597,11 @@ ATTN_API int attn_paged_fwd(const attn_paged_shape* shape, const void* q, const 
 
 /*
  * The same over a 4-bit cache: attn_paged_fwd on the values that the pools hold
- * (exact in 16 bits, so only the order of sums is another), with the workspace of
- * attn_paged_workspace_bytes.  A row of q that holds an infinity or a NaN (or, in
+ * (exact in 16 bits), with the workspace of attn_paged_workspace_bytes.  Beside the
+ * order of sums, weights are held otherwise: what a key's weight (the row's largest
+ * being 1) adds to an element may be off by 2^-25 of the key's value there, in bfloat16
+ * too.  V's magnitudes may differ by channel, by key and behind the mask, within a
+ * request by up to 2^100.  A row of q that holds an infinity or a NaN (or, in
  * bfloat16, an element of 2^110 or more) may give NaN; no other row does.
  */
 ATTN_API int attn_paged_fwd4(const attn_paged_shape* shape, const void* q, const uint8_t* k_cache,

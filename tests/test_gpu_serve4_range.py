@@ -1,0 +1,194 @@
+"""Attention over a 4-bit cache whose magnitudes differ: by channel group, by key, and
+behind the mask.  A row's bound knows the keys that the row sees and no others."""
+import random
+
+import pytest
+
+from serve4_range_util import own64, problem
+from serve_util import check
+
+pytestmark = pytest.mark.gpu
+
+SENTINEL = 7.0
+
+
+@pytest.fixture(scope="module")
+def torch(cuda_device):
+    import torch
+    from causal_streaming_softmax_gb300 import build
+    build.build()
+    return torch
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(cuda_device):
+    from causal_streaming_softmax_gb300 import api
+    yield
+    assert api.last_device_error() == 0
+
+
+def run(torch, p, max_new=None, scale=0.125):
+    from causal_streaming_softmax_gb300 import api
+    q, kc, vc, table, cu, lens = p
+    t, H, _ = q.shape
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    s = api.PagedShape(len(lens), t, H, kc.shape[1], kc.shape[2] * 8, kc.shape[0], len(table[0]),
+                       max_new=max_new or max(b - a for a, b in zip(cu, cu[1:])), dtype=q.dtype,
+                       scale=scale)
+    ws = api.alloc_paged_workspace(s)
+    ws.fill_(255)
+    o = torch.full_like(q, SENTINEL)
+    lse = torch.full((H, t), SENTINEL, device="cuda")
+    api.attn_paged_fwd4(s, q, kc, vc, i32(table), i32(cu), i32(lens), ws, o, lse)
+    return o, lse
+
+
+def run_and_check(torch, p, max_new=None, scale=0.125):
+    o, lse = run(torch, p, max_new, scale)
+    for rows, eo, el, to, tl in own64(*p, scale):
+        check(o[rows], eo, to, "O of rows %s" % rows)
+        check(lse[:, rows], el, tl, "L of rows %s" % rows)
+    return o, lse
+
+
+# The launches of the call: requests (keys, new tokens), heads, page, max_new.
+FORMS = {
+    "whole": ([(777, 1), (130, 1)], (8, 2), 16, None),
+    "whole_wide": ([(700, 2), (90, 1)], (8, 1), 16, None),
+    "split": ([(3000, 1), (1500, 1)], (8, 2), 64, None),
+    "split_wide": ([(2600, 4), (64, 1), (1029, 3)], (8, 2), 32, None),
+    "sub_items": ([(2600, 4), (900, 1), (300, 40)], (8, 2), 16, None),
+    "one_head": ([(5000, 1)], (2, 2), 128, None),
+    "tiles": ([(500, 70), (64, 64)], (8, 2), 16, None),
+}
+
+
+def shapes(kind, span):
+    """What V's magnitudes are: 2^-span/2 .. 2^span/2 by channel, key or block."""
+    import torch
+    half = span // 2
+
+    def scatter(n, seed, values):
+        r = random.Random(seed)
+        return torch.tensor([2.0 ** r.choice(values) for _ in range(n)], device="cuda",
+                            dtype=torch.float64)[:, None, None]
+
+    def by_key(f):
+        def shape(i, x):
+            n = x.shape[0]
+            x *= f(i, n)
+        return shape
+
+    pos = lambda n: torch.arange(n, device="cuda", dtype=torch.float64) / max(1, n - 1)
+    up = lambda i, n: (2.0 ** (span * pos(n) - half))[:, None, None]
+    down = lambda i, n: (2.0 ** (half - span * pos(n)))[:, None, None]
+
+    def low_channels(i, x):
+        x[..., :32] *= 2.0 ** -half
+        x[..., 32:] *= 2.0 ** half
+
+    def high_channels(i, x):
+        x[..., :32] *= 2.0 ** half
+        x[..., 32:] *= 2.0 ** -half
+
+    def one_channel(i, x):  # an outlier of one channel in every sixth key
+        x *= 2.0 ** -half
+        x[::6, :, 5] = 2.0 ** half
+
+    def zeros(i, x):
+        x[1::2] = 0
+        x[::5, :, 32:] = 0
+        x *= 2.0 ** -half
+
+    return {
+        "low_channels": low_channels, "high_channels": high_channels, "one_channel": one_channel,
+        "rising": by_key(up), "falling": by_key(down), "zeros": zeros,
+        "steps": by_key(lambda i, n: (2.0 ** ((torch.arange(n, device="cuda") // 70 % 5) *
+                                              (span / 4.0) - half))[:, None, None]),
+        "scatter": by_key(lambda i, n: scatter(n, i, range(-half, half + 1))),
+        "few_large": by_key(lambda i, n: scatter(n, i, [-half] * 40 + [half])),
+        "few_small": by_key(lambda i, n: scatter(n, i, [half] * 40 + [-half])),
+    }[kind]
+
+
+KINDS = ["low_channels", "high_channels", "one_channel", "rising", "falling", "zeros", "steps",
+         "scatter", "few_large", "few_small"]
+SPANS = {"float16": (6, 26), "bfloat16": (8, 40, 90)}
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype,span", [(d, s) for d in SPANS for s in SPANS[d]])
+def test_values_of_mixed_magnitudes(torch, form, kind, dtype, span):
+    reqs, heads, page, max_new = FORMS[form]
+    p = problem(reqs, *heads, page, getattr(torch, dtype), 7 + span, shape_v=shapes(kind, span))
+    o, _ = run_and_check(torch, p, max_new)
+    o2, _ = run(torch, p, max_new)
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,span", [("float16", 26), ("bfloat16", 40), ("bfloat16", 90)])
+def test_large_values_of_keys_that_hardly_count(torch, form, dtype, span):
+    """Keys with weights of some 2^-58 and V far above the others': neither do the others
+    disappear, nor does what such a key adds where it is comparable."""
+    reqs, heads, page, max_new = FORMS[form]
+
+    def away(i, x):
+        x[3::29] = 0
+        x[3::29, :, 0] = -40
+
+    def large(i, x):
+        x *= 2.0 ** -(span // 2)
+        x[3::29] *= 2.0 ** span
+
+    def ask(q):
+        q[..., 0] = 8
+
+    run_and_check(torch, problem(reqs, *heads, page, getattr(torch, dtype), 3, away, large, ask),
+                  max_new)
+
+
+@pytest.mark.parametrize("dtype,span", [("float16", 13), ("float16", 26), ("bfloat16", 14),
+                                        ("bfloat16", 40), ("bfloat16", 90), ("bfloat16", 160)])
+@pytest.mark.parametrize("heads,new,keys,other", [
+    ((8, 2), 4, 700, 1), ((8, 2), 2, 64 * 9 + 1, 1), ((8, 1), 2, 3000, 1), ((2, 2), 16, 400, 1),
+    ((8, 2), 4, 4, 1), ((2, 2), 16, 16, 1), ((8, 2), 4, 2000, 40), ((8, 2), 40, 300, 1)])
+def test_values_behind_the_mask(torch, dtype, span, heads, new, keys, other):
+    """The later tokens' V is far larger: earlier rows are what they are without it."""
+    dt, half = getattr(torch, dtype), span // 2
+    reqs = [(keys, new), (other + 50, other)]
+
+    def values(later):
+        def shape(i, x):
+            x *= 2.0 ** -half
+            if i == 0 and later:
+                x[keys - new // 2:] *= 2.0 ** span
+        return shape
+
+    p = problem(reqs, *heads, 16, dt, 11, shape_v=values(True))
+    o, L = run(torch, p)
+    before = new - new // 2
+    for rows, eo, el, to, tl in own64(*p):
+        a, b = rows.start, rows.start + before if rows.start == 0 else rows.stop
+        check(o[a:b], eo[:b - a], to[:b - a], "O")
+        if span < 100:
+            check(o[rows], eo, to, "O of all rows")
+        check(L[:, rows], el, tl, "L")
+    plain, L2 = run(torch, problem(reqs, *heads, 16, dt, 11, shape_v=values(False)))
+    off = (o[:before].double() - plain[:before].double()).abs()
+    assert bool((off <= 2 * own64(*p)[0][3][:before]).all())
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("at", [1, 64, 65, 255, 256, 600, 2000])
+def test_one_large_value_anywhere(torch, dtype, at):
+    """One key of one request, in either group, among ordinary ones; V's unit moves while
+    the sums of the keys before it are there, and not back."""
+    e = 12 if dtype == "float16" else 40
+
+    def shape(i, x):
+        x[max(0, x.shape[0] - at - i), 0, 32 * (i % 2) + 3] = 2.0 ** e * (-1) ** i
+
+    reqs = [(2100, 1), (2100, 2), (2164, 1), (2000 + at, 1)]
+    run_and_check(torch, problem(reqs, 8, 2, 16, getattr(torch, dtype), at, shape_v=shape))
