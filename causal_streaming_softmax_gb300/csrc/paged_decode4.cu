@@ -21,8 +21,9 @@
 //    codes of an element are the four channel tiles of O^T;
 //  * all products take binary16: the bits of code + 8 are the subnormal number
 //    (code + 8) 2^-24 (2^-20 in the high half of a byte), which costs an AND and no
-//    conversion.  q goes in with its row's largest element at 2^9.  K's scale is
-//    applied to the scores, the offset of 8 times the sum of q is where they start.
+//    conversion.  q goes in with its row's largest element at 2^9 (low channels 2^13).
+//    K's scale is applied to the scores, the offset of 8 times the sum of q is where they
+//    start.
 //    V's scale, which varies along the sum, goes into the weights, the offset comes
 //    off V's codes (left in, it would be taken off a sum ten times the result);
 //  * weights times V's scales are binary16 too, a weight of 1 counting 2^kBias and the
@@ -77,6 +78,14 @@ constexpr float kBias = 10.f, kMost = 0x1p13f, kVMost = 4.f, kVLeast = 0x1p-10f;
 // only go up, as sums that are carried to a higher one shrink and cannot overflow.
 constexpr float kVTop = 0x1p60f, kVFar = 0x1p-40f;
 constexpr float kVNone = 0x1p126f;  // the inverse before a group has a scale above zero
+// Scores: q goes in with one power of two for a row, which does not serve where a
+// channel group lies kQApart below the other, or where the row's largest element, or c
+// times it, is beyond kFar or its inverse.  Such items go through the edge's walk with a
+// power of two for each group; that scales the groups' products one by one, to scores
+// times 2^-kDrop, and takes c 2^kDrop from there, so that a score stays inside binary32
+// where sum q k does, whatever q, K and c are by themselves.
+constexpr float kQApart = 0x1p-12f, kFar = 0x1p100f;
+constexpr int kDrop = 12;
 constexpr int kTileKeys = 64;
 constexpr int kGroup = 4;  // tiles that the producer hands out at a time, eight lanes each
 // Pages of so many rows (their logarithm) are copied by tensor maps, whose boxes have
@@ -205,6 +214,9 @@ __device__ __forceinline__ float2 magnitudes(uint32_t s) {
                      half_to_f32<BF16>((uint16_t)(s >> 16 & 0x7fffu)));
 }
 
+// 2^e, -126 <= e <= 127; the binary order of x >= 0 (-127 below 2^-126).
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ int order(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 // The inverse of a power of two between 2^-126 and 2^126.
 __device__ __forceinline__ float inverse2(float x) {
   return __uint_as_float((254u << 23) - __float_as_uint(x));
@@ -234,6 +246,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (sbase - smem_u32(smem_raw));
   float* const s_join = reinterpret_cast<float*>(smem + C::kSmemJoin);
+  // [warp][row] an item's m and l; while its tiles are walked, what products of q's low
+  // and high channels count
   float2* const s_ml = reinterpret_cast<float2*>(smem + C::kSmemMl);
   long long* const s_pre = reinterpret_cast<long long*>(smem + C::kSmemPre);
   const uint32_t bar0 = sbase + C::kSmemBar;
@@ -400,47 +414,67 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
       uint32_t q[kCols][4][2];
       float z_lo[kCols][4], z_hi[kCols][4];  // where scores start
       float2 unit[kCols];                    // of the scores of rows 2 tq, 2 tq + 1
+      bool far = false;                      // they have none: the edge's walk
       Item sg{};
       bool ok = mbar_wait_warp(BAR(BAR_Q + qbuf), (nq >> 1) & 1, wc);
       if (ok) {
         sg = s_item[qbuf];
+        float x[kCols][2][8], top[kCols][2];  // a row's largest element of either group
 #pragma unroll
         for (int n = 0; n < kCols; ++n) {
-          float x[2][8], top = 0.f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // channels 32 h + 8 tq .. + 7 of row 8 n + g
             const uint4 w = *reinterpret_cast<const uint4*>(
                 smem + qbuf * kQ + sw128_offset(8 * n + g, 4 * h + tq));
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            float t = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              x[h][2 * i] = half_to_f32<BF16>((uint16_t)u[i]);
-              x[h][2 * i + 1] = half_to_f32<BF16>((uint16_t)(u[i] >> 16));
-              top = fmaxf(top, fmaxf(fabsf(x[h][2 * i]), fabsf(x[h][2 * i + 1])));
+              x[n][h][2 * i] = half_to_f32<BF16>((uint16_t)u[i]);
+              x[n][h][2 * i + 1] = half_to_f32<BF16>((uint16_t)(u[i] >> 16));
+              t = fmaxf(t, fmaxf(fabsf(x[n][h][2 * i]), fabsf(x[n][h][2 * i + 1])));
             }
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+            top[n][h] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
           }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int sh = min(9 - ((int)(__float_as_uint(top) >> 23) - 127), 120);
+          // a row that counts, is finite and not zero
+          const float most = fmaxf(top[n][0], top[n][1]), least = fminf(top[n][0], top[n][1]);
+          if (8 * n + g < sg.r.n_new * a.G && most < INFINITY && most > 0.f) {
+            const float at = a.c * fminf(most, kFar);
+            far |= !(fmaxf(most, at) <= kFar && fminf(most, at) >= 1.f / kFar);
+            far |= least > 0.f && least < most * kQApart;
+          }
+        }
+        far = __any_sync(0xffffffffu, far);
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) {
+          // q times 2^sh: the row's, or a group's, largest element counts 2^9 or 2^13
+          const float both = fmaxf(top[n][0], top[n][1]);
+          const int sh[2] = {
+              min(max(13 - order(far ? top[n][0] : both), -103 - a.drop), 127),
+              min(max(9 - order(far ? top[n][1] : both), -107 - a.drop), 123)};
           float sum[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float f = __uint_as_float((uint32_t)(sh + 127 + (h ? 0 : 4)) << 23);
+            const float f = exp2i(sh[h]);
             sum[h] = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const uint32_t w = pack_f16x2(x[h][4 * i + j] * f, x[h][4 * i + j + 2] * f);
+                const uint32_t w = pack_f16x2(x[n][h][4 * i + j] * f, x[n][h][4 * i + j + 2] * f);
                 q[n][2 * h + i][j] = w;
                 sum[h] += f16_bits_to_f32((uint16_t)w) + f16_bits_to_f32((uint16_t)(w >> 16));
               }
             sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
             sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
           }
-          // scores that may leave binary32 are NaN, not something else
-          float back = sh < -107 ? INFINITY : a.c * __uint_as_float((uint32_t)(147 - sh) << 23);
-          if (!(back < INFINITY)) back = __uint_as_float(0x7fc00000u);
+          // what a product counts: with c and for both groups together (far: not used),
+          // and a group at a time, 2^drop too little
+          const float back = a.c * exp2i(min(20 - sh[1], 127));
+          if (tq == 0)
+            s_ml[warp * kRows + 8 * n + g] =
+                make_float2(exp2i(24 - a.drop - sh[0]), exp2i(20 - a.drop - sh[1]));
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             z_lo[n][e] = z_lo[n][2 + e] =
@@ -451,6 +485,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
           unit[n].x = __shfl_sync(0xffffffffu, back, 8 * tq);
           unit[n].y = __shfl_sync(0xffffffffu, back, 8 * tq + 4);
         }
+        __syncwarp();
       }
       ++nq;
       const int t1 = sg.t1, n_keys = sg.r.n_keys;
@@ -591,6 +626,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
           s_scale[kTileKeys + lane + 32 * x] = make_float4(v[x].x, v[x].x, v[x].y, v[x].y);
         }
         __syncwarp();
+        // EDGE: what products of rows 2 tq and 2 tq + 1 count, low and high channels
+        float2 r_lo[cols], r_hi[cols];
+#pragma unroll
+        for (int n = 0; EDGE && n < cols; ++n) {
+          const float4 r = *reinterpret_cast<const float4*>(s_ml + warp * kRows + 8 * n + 2 * tq);
+          r_lo[n] = make_float2(r.x, r.z), r_hi[n] = make_float2(r.y, r.w);
+        }
         // scores: [.][step][key g, key g + 8 of the step], rows 2 tq and 2 tq + 1
         float2 sc[cols][kSteps][2];
 #pragma unroll
@@ -602,7 +644,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
             raw_codes(w.x, x[0][u], x[2][u], x[0][2 + u], x[2][2 + u]);
             raw_codes(w.y, x[1][u], x[3][u], x[1][2 + u], x[3][2 + u]);
           }
-          const float4 s4[2] = {s_scale[16 * i + g], s_scale[16 * i + 8 + g]};
+          const float4 s4[2] = {s_scale[16 * i + g], s_scale[16 * i + 8 + g]};  // K's
 #pragma unroll
           for (int n = 0; n < cols; ++n) {
             float lo[4], hi[4];
@@ -611,11 +653,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
             mma_f16(lo, x[1], q[n][1], lo);
             mma_f16(hi, x[3], q[n][3], hi);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-              sc[n][i][u] = __ffma2_rn(
-                  make_float2(lo[2 * u], lo[2 * u + 1]), make_float2(s4[u].x, s4[u].y),
-                  __fmul2_rn(make_float2(hi[2 * u], hi[2 * u + 1]),
-                             make_float2(s4[u].z, s4[u].w)));
+            for (int u = 0; u < 2; ++u) {
+              float2 a2 = make_float2(lo[2 * u], lo[2 * u + 1]),
+                     b2 = make_float2(hi[2 * u], hi[2 * u + 1]);
+              if (EDGE) a2 = __fmul2_rn(a2, r_lo[n]), b2 = __fmul2_rn(b2, r_hi[n]);
+              sc[n][i][u] = __ffma2_rn(a2, make_float2(s4[u].x, s4[u].y),
+                                       __fmul2_rn(b2, make_float2(s4[u].z, s4[u].w)));
+            }
           }
         }
         if (EDGE) {
@@ -634,6 +678,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
               }
           }
         }
+        const auto unit_of = [&](int n) {
+          return EDGE ? make_float2(a.c_drop, a.c_drop) : unit[n];
+        };
         float2 p[cols][kSteps][2], sum[cols];
         const auto weigh = [&] {
           bool big = false;
@@ -643,7 +690,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
             for (int i = 0; i < kSteps; ++i)
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const float2 x = __ffma2_rn(sc[n][i][u], unit[n], neg_m[n]);
+                const float2 x = __ffma2_rn(sc[n][i][u], unit_of(n), neg_m[n]);
                 p[n][i][u] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                 sum[n] = i + u ? __fadd2_rn(sum[n], p[n][i][u]) : p[n][i][u];
               }
@@ -670,8 +717,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
               x.x = fmaxf(x.x, __shfl_xor_sync(0xffffffffu, x.x, by));
               x.y = fmaxf(x.y, __shfl_xor_sync(0xffffffffu, x.y, by));
             }
-            follow(x.x, unit[n].x, &neg_m[n].x, &most[n].x, &l[n].x, &f.x);
-            follow(x.y, unit[n].y, &neg_m[n].y, &most[n].y, &l[n].y, &f.y);
+            follow(x.x, unit_of(n).x, &neg_m[n].x, &most[n].x, &l[n].x, &f.x);
+            follow(x.y, unit_of(n).y, &neg_m[n].y, &most[n].y, &l[n].y, &f.y);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               o[n][j][0] *= f.x, o[n][j][2] *= f.x;
@@ -779,7 +826,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         const uint32_t ks = sbase + C::kSmemStage + s * kStage;
         // One column tile where the item fills no more: 64 one-token requests of a call that
         // may have four tokens each take 72 us so, 77 with both.
-        bool edge = past_limit(t * kTileKeys, kTileKeys, first_lim);
+        bool edge = far || past_limit(t * kTileKeys, kTileKeys, first_lim);
         if (!edge) {
           if (kCols > 1 && sg.r.n_new * a.G <= 8)
             edge = !walk(std::false_type{}, OneCol{}, ks, t * kTileKeys);
@@ -927,7 +974,8 @@ int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q
   const int ntok = tokens4(d);
   const DecodeArgs args{d.batch, d.tokens, d.H, d.Hkv, d.G, ntok, d.max_new, d.pages, d.width,
                         d.shift, d.c, cu, lens, table, o, lse, part, ctx.err, ctx.wait_ns,
-                        splits(d) ? 8 / d.G : ntok};
+                        splits(d) ? 8 / d.G : ntok, d.c < kFar ? kDrop : 0,
+                        d.c < kFar ? ldexpf(d.c, kDrop) : d.c};
   if (splits(d))
     return launch<Config<1, false, true>>(d, ctx, q, kc, vc, args, blocks, kSmemDecode4SplitF16,
                                           stream);

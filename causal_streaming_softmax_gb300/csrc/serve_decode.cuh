@@ -17,7 +17,9 @@ struct DecodeArgs {
   PartArgs part;
   uint32_t* err;
   uint64_t wait_ns;
-  int split;  // C::kSplit: tokens of an item, at most; else all of a request
+  int split;  // 4 bits: tokens of an item, at most (all of a request unless C::kSplit)
+  int drop;   // 4 bits: binary orders that scores of the edge's walk are down by,
+  float c_drop;  // and c times as much
 };
 
 // A request's rows and keys; n_new 0 for one that this kernel does not take.

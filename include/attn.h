@@ -601,8 +601,10 @@ ATTN_API int attn_paged_fwd(const attn_paged_shape* shape, const void* q, const 
  * order of sums, weights are held otherwise: what a key's weight (the row's largest
  * being 1) adds to an element may be off by 2^-25 of the key's value there, in bfloat16
  * too.  V's magnitudes may differ by channel, by key and behind the mask, within a
- * request by up to 2^100.  A row of q that holds an infinity or a NaN (or, in
- * bfloat16, an element of 2^110 or more) may give NaN; no other row does.
+ * request by up to 2^100.  An element of q counts to 2^-21 of the largest of its 32
+ * channels where its own rounding is finer, and a score is a sum of q (code + 8) less
+ * 8 sum q in binary32, terms of up to 15 |q| scale: lse may be off accordingly.  A row
+ * of q that holds an infinity or a NaN may give NaN; no other row does.
  */
 ATTN_API int attn_paged_fwd4(const attn_paged_shape* shape, const void* q, const uint8_t* k_cache,
                              const uint8_t* v_cache, const int32_t* table, const int32_t* cu,

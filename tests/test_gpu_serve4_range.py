@@ -192,3 +192,93 @@ def test_one_large_value_anywhere(torch, dtype, at):
 
     reqs = [(2100, 1), (2100, 2), (2164, 1), (2000 + at, 1)]
     run_and_check(torch, problem(reqs, 8, 2, 16, getattr(torch, dtype), at, shape_v=shape))
+
+
+# dtype, binary orders between q's channel groups (K has them the other way round)
+APART = [("float16", 8), ("float16", 13), ("float16", 22), ("bfloat16", 12), ("bfloat16", 14),
+         ("bfloat16", 36), ("bfloat16", 80), ("bfloat16", 160)]
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,span", APART)
+def test_queries_whose_groups_lie_apart(torch, form, dtype, span):
+    """Either group of q is far below the other where K's is far above: both count.
+    Every third row is small as a whole."""
+    reqs, heads, page, max_new = FORMS[form]
+    low = span // 2 if heads[0] != 2 else -(span // 2)
+
+    def keys(i, x):
+        x[..., :32] *= 2.0 ** low
+        x[..., 32:] *= 2.0 ** -low
+
+    def ask(q):
+        q[..., :32] *= 2.0 ** -low
+        q[..., 32:] *= 2.0 ** low
+        q[::3] *= 2.0 ** -9
+
+    run_and_check(torch, problem(reqs, *heads, page, getattr(torch, dtype), span, keys, None, ask),
+                  max_new)
+
+
+# dtype, log2 of q, of K and of the scale: of scores of ordinary size
+FAR = [("float16", 12, -10, -5), ("float16", -12, 10, -1), ("bfloat16", 60, -117, 54),
+       ("bfloat16", 110, -110, -3), ("bfloat16", 120, -120, -3), ("bfloat16", 126, -124, -3),
+       ("bfloat16", -110, 110, -3), ("bfloat16", -125, 120, 2), ("bfloat16", 3, 100, -106),
+       ("bfloat16", 20, 100, -123), ("bfloat16", -60, -60, 117), ("bfloat16", 100, 20, -123),
+       ("bfloat16", -100, 20, 77), ("bfloat16", 0, -120, 117)]
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,qe,ke,se", FAR)
+def test_queries_and_scales_far_from_one(torch, form, dtype, qe, ke, se):
+    reqs, heads, page, max_new = FORMS[form]
+
+    def keys(i, x):
+        x *= 2.0 ** ke
+
+    def ask(q):
+        q *= 2.0 ** (qe - 1)
+        q[::2, 1::2] = 0  # beside rows of zeros
+
+    run_and_check(torch, problem(reqs, *heads, page, getattr(torch, dtype), 50 + se, keys, None,
+                                 ask), max_new, 2.0 ** se)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("scale", [1e-15, 1e-20, 1e-30, 1.2e-38, 1e-42])
+@pytest.mark.parametrize("form", ["whole", "whole_wide", "split_wide", "sub_items", "tiles"])
+def test_rows_of_zeros_under_small_scales(torch, dtype, scale, form):
+    """Such a row is the mean of the values that it sees, the masked ones left out."""
+    reqs, heads, page, max_new = FORMS[form]
+
+    def ask(q):
+        q[:, ::2] = 0
+
+    import struct
+    scale = struct.unpack("f", struct.pack("f", scale))[0]
+    run_and_check(torch, problem(reqs, *heads, page, getattr(torch, dtype), 9, shape_q=ask),
+                  max_new, scale)
+
+
+@pytest.mark.parametrize("form", ["whole_wide", "split_wide", "sub_items"])
+def test_rows_that_are_not_finite_beside_rows_far_apart(torch, form):
+    """An infinity or a NaN in q spoils its own row alone, whatever the others ask for."""
+    reqs, heads, page, max_new = FORMS[form]
+
+    def ask(q):
+        q[0, 1, :32] *= 2.0 ** -70
+
+    p = problem(reqs, *heads, page, torch.bfloat16, 4, shape_q=ask)
+    q = p[0]
+    good, _ = run(torch, p, max_new)
+    q[0, 0, 3], q[1, 2, 40], q[1, 3, 63] = float("inf"), float("nan"), -float("inf")
+    o, L = run(torch, p, max_new)
+    bad = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    bad[0, 0] = bad[1, 2] = bad[1, 3] = True
+    assert torch.isnan(o[bad]).all()
+    assert torch.equal(o[~bad].view(torch.int16), good[~bad].view(torch.int16))
+    q[bad] = 1.0
+    for rows, eo, el, to, tl in own64(*p):
+        fine = ~bad[rows]
+        check(o[rows][fine], eo[fine], to[fine], "O")
+        check(L[:, rows].T[fine], el.T[fine], tl.T[fine], "L")
