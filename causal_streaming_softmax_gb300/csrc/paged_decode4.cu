@@ -963,9 +963,15 @@ bool decode4_whole(const PagedDims& d, int sm_count) {
 }
 
 // One column tile serves a token step of up to eight heads a group.
-int decode4_blocks(const PagedDims& d) {
-  return splits(d) || tokens4(d) * d.G <= 8 ? Config<1, false>::kBlocks : Config<2, false>::kBlocks;
+int decode4_rows(const PagedDims& d) {
+  return splits(d) || tokens4(d) * d.G <= 8 ? Config<1, false>::kRows : Config<2, false>::kRows;
 }
+int decode4_blocks(const PagedDims& d) {
+  return decode4_rows(d) <= 8 ? Config<1, false>::kBlocks : Config<2, false>::kBlocks;
+}
+static_assert(Config<1, false>::kBlocks == 3 && Config<1, false>::kRows == 8 &&
+                  Config<2, false>::kBlocks == 2 && Config<2, false>::kRows == kDecodeRows,
+              "the workspace holds their parts");
 
 int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
                          const PoolArg& kc, const PoolArg& vc, const int32_t* table,

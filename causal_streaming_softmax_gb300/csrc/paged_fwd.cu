@@ -100,7 +100,7 @@ int launch_join(const PagedDims& d, const DevCtx& ctx, const PartArgs& p1, int n
 // The largest grid of the split kernels on any device this library runs on:
 // the workspace's size must not depend on the current device.
 constexpr int kMaxSm = 160;
-constexpr int kFewBlocks = 3;  // blocks a SM of the kernels for few rows, at most
+constexpr int kFewBlocks = 2;  // blocks a SM of the 16-bit kernel for few rows
 
 }  // namespace
 
@@ -145,9 +145,14 @@ constexpr int kLeastFew = 2, kLeastRows = 2;
 
 }  // namespace
 
+// The parts of few rows; the 4-bit kernel's three blocks a SM are of eight rows and find
+// room in the same.
+constexpr size_t kFewBytes = parts_bytes(kFewBlocks * kMaxSm, kDecodeRows);
+static_assert(parts_bytes(3 * kMaxSm, 8) <= kFewBytes, "parts of the 4-bit kernel");
+
 size_t paged_workspace_bytes(const PagedDims& d) {
   const int ntok = decode_tokens(d.G);
-  return (ntok > 0 ? parts_bytes(kFewBlocks * kMaxSm, kDecodeRows) : 0) +
+  return (ntok > 0 ? kFewBytes : 0) +
          (d.max_new > ntok ? parts_bytes(kMaxSm, kItemRows) : 0);
 }
 
@@ -161,9 +166,9 @@ int launch_paged_fwd(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, co
   PartArgs few{}, rows{};
   int n_few = 0, n_rows = 0, rc;
   if (ntok > 0) {
-    const int blocks = (four ? decode4_blocks(d) : 2) * sms;
-    few = parts_at(at, kFewBlocks * kMaxSm, kDecodeRows, kLeastFew);
-    at += parts_bytes(kFewBlocks * kMaxSm, kDecodeRows);
+    const int per_sm = four ? decode4_blocks(d) : kFewBlocks, blocks = per_sm * sms;
+    few = parts_at(at, per_sm * kMaxSm, four ? decode4_rows(d) : kDecodeRows, kLeastFew);
+    at += kFewBytes;
     rc = (four ? launch_paged_decode4 : launch_paged_decode)(d, ctx, q, kc, vc, table, cu, lens,
                                                              few, blocks, o, lse, stream);
     if (rc != ATTN_OK) return rc;

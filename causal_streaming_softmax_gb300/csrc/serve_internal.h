@@ -61,6 +61,7 @@ int launch_paged_rows(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, c
 // The same over a 4-bit cache (the pools' strides in bytes).
 bool decode4_whole(const PagedDims& d, int sm_count);
 int decode4_blocks(const PagedDims& d);  // a SM
+int decode4_rows(const PagedDims& d);    // of an item, at most
 int launch_paged_decode4(const PagedDims& d, const DevCtx& ctx, const RowsArg& q,
                          const PoolArg& kc, const PoolArg& vc, const int32_t* table,
                          const int32_t* cu, const int32_t* lens, const PartArgs& part, int blocks,

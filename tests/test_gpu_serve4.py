@@ -973,3 +973,26 @@ def test_arrays_that_something_else_writes(torch):
     o.fill_(SENTINEL)
     api.attn_paged_fwd4(s, q, kc, vc, *arrays, ws, o)
     check_paged4(torch, q, kc, vc, table, cu, lens, o, None)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("heads,reqs,bound", [
+    ((8, 8), [(30000, 1)] * 9, 1), ((8, 2), [(9000, 1)] * 70, 1), ((8, 2), [(5000, 4)] * 40, 4),
+    ((16, 1), [(20000, 1)] * 20, 1), ((8, 2), [(4000, 3)] * 50 + [(3000, 200)], 200)])
+def test_paged_stays_inside_its_workspace(torch, bits, heads, reqs, bound):
+    """Every block leaves parts, in a workspace of just the size asked for."""
+    from causal_streaming_softmax_gb300 import api
+    q, kc, vc, table, cu, lens, width = paged4_problem(torch, reqs, *heads, 64, torch.float16, 17)
+    if bits == 16:
+        kc, vc = (values(x, q.dtype)[0].half() for x in (kc, vc))
+    s = api.PagedShape(len(lens), q.shape[0], *heads, 64, kc.shape[0], width, max_new=bound)
+    need = api.paged_workspace_bytes(s)
+    room = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+    o = torch.full_like(q, SENTINEL)
+    call = api.attn_paged_fwd4 if bits == 4 else api.attn_paged_fwd
+    call(s, q, kc, vc, i32(torch, table), i32(torch, cu), i32(torch, lens), room[:need], o)
+    assert (room[need:] == 171).all()
+    if bits == 4:
+        check_paged4(torch, q, kc, vc, table, cu, lens, o, None)
+    else:
+        assert torch.isfinite(o).all()

@@ -133,6 +133,19 @@ def test_fwd4_pointers_refused(lib):
     assert fwd4(lib, paged(True, tokens=0), *[None] * 7, 0, None) == api.ATTN_OK
 
 
+@pytest.mark.parametrize("kw,size", [(dict(), 2708480), (dict(max_new=1), 2708480),
+                                     (dict(max_new=9), 2708480 + 32442880),
+                                     (dict(heads=32, kv_heads=1), 32442880)])
+def test_the_workspace_is_that_of_the_16_bit_call(lib, kw, size):
+    """A workspace of the size that attn_paged_fwd had before the 4-bit cache came serves
+    both calls: two parts of 16 rows (264 bytes and a description of 16 a block) for 320
+    blocks, and of 384 rows for 160 where requests may be chunks."""
+    assert 320 * (16 + 2 * 16 * 264) == 2708480 and 160 * (16 + 2 * 384 * 264) == 32442880
+    for four in (False, True):
+        s = paged(four, q_token=2048, o_token=2048, **kw)
+        assert lib.attn_paged_workspace_bytes(ctypes.byref(s)) == size
+
+
 def test_python_binding_refuses_host_tensors():
     s = api.PagedShape(1, 2, 2, 1, 16, 3, 1)
     q, k = torch.zeros((2, 2, 64), dtype=torch.float16), torch.zeros((2, 1, 64),
