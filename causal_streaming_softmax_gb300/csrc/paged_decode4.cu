@@ -2,8 +2,9 @@
 // a group <= 16) over the pages of a 4-bit cache: the token step of a server.
 //
 // The arithmetic is that of the 16-bit kernel (S = Q K^T, P = 2^(S c - m), running
-// maximum m and sum l in binary32, O += P V with P rounded to the operands' type)
-// over values code * scale, which are exact in 16 bits (pool4.cuh).
+// maximum m and sum l in binary32, O += P V) over values code * scale, which are exact
+// in 16 bits (pool4.cuh); what is rounded to 16 bits is q, once an item, and P times V's
+// scales, both to binary16 whatever the cache's type.
 //
 // 72 bytes a key and K/V head come from memory where the 16-bit cache has 256, so
 // the same arithmetic has less than a third of the time: for 16 keys of a K/V head
@@ -23,24 +24,23 @@
 //    (code + 8) 2^-24 (2^-20 in the high half of a byte), which costs an AND and no
 //    conversion.  q goes in with its row's largest element at 2^9 (low channels 2^13).
 //    K's scale is applied to the scores, the offset of 8 times the sum of q is where they
-//    start.
-//    V's scale, which varies along the sum, goes into the weights, the offset comes
-//    off V's codes (left in, it would be taken off a sum ten times the result);
+//    start.  V's scale, which varies along the sum, goes into the weights, the offset
+//    comes off V's codes (left in, it would be taken off a sum ten times the result);
 //  * weights times V's scales are binary16 too, a weight of 1 counting 2^kBias and the
-//    scales in a unit near the largest so far: spacing 2^-35 of that;
+//    scales in a unit near the largest so far: spacing 2^-34 of that;
 //  * m and the units are followed only when a lane's sum of a step's weights passes
 //    kMost or a scale leaves its unit's range: one vote a step, no maximum over the keys'
 //    lanes;
 //  * the two channel groups have units of their own, which the keys that every row of
-//    the item sees set.  In a tile whose scales lie further apart than binary16 weights hold,
-//    weights times scales go in as the sum of two bfloat16 numbers: 16 bits, and
+//    the item sees set.  In a tile whose scales lie further apart than binary16 weights
+//    hold, weights times scales go in as the sum of two bfloat16 numbers: 16 bits, and
 //    binary32's range (twice the products of V);
 //  * a lane converts the scales of two keys and passes them on through shared memory,
 //    each twice, as operands of the paired binary32 instructions.
-// Tiles of 64 keys go round four consumer warps a block, each with a ring of three;
-// the producer hands out four at a time, eight lanes each.  Items, places and the
-// joining of parts are those of the 16-bit kernel (serve_decode.cuh,
-// serve_parts.cuh).
+// Tiles of 64 keys go round four consumer warps a block, each with a ring of three (with
+// two column tiles four); the producer hands out four at a time, eight lanes each.
+// Items, places and the joining of parts are those of the 16-bit kernel
+// (serve_decode.cuh, serve_parts.cuh).
 //
 // Measured (GB300, join included): 256 requests over 1024..16384 keys, 32 / 4 heads,
 // 130 us = 4.75 TB/s, 70% of the measured copy rate; 2 over 50000..65536, 16 / 16 heads,
@@ -913,9 +913,12 @@ int launch(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const PoolAr
   const uint32_t units = (1u << d.shift) / 8;
   const uint32_t box = units < kTileKeys / 8 ? units : kTileKeys / 8;
   if (!encode_tmap_4d(&tq, d.bf16, q.p, d.G, d.Hkv, d.tokens, q.h, q.h * d.G, q.t, d.G, 1,
-                      args.split) ||
-      !encode_tmap_units(&tk, kc.p, units, d.Hkv, d.pages, kc.h, kc.pg, box) ||
-      !encode_tmap_units(&tv, vc.p, units, d.Hkv, d.pages, vc.h, vc.pg, box))
+                      args.split))
+    return ATTN_ERR_CUDA;
+  tk = tv = tq;  // small pages: not used
+  if (d.shift >= kTiledShift &&
+      (!encode_tmap_units(&tk, kc.p, units, d.Hkv, d.pages, kc.h, kc.pg, box) ||
+       !encode_tmap_units(&tv, vc.p, units, d.Hkv, d.pages, vc.h, vc.pg, box)))
     return ATTN_ERR_CUDA;
   const size_t smem = C::kSmemPre + 8 * (size_t)(d.batch + 1) + 1024;
   auto* kernel = d.bf16 ? paged_decode4_kernel<true, C> : paged_decode4_kernel<false, C>;

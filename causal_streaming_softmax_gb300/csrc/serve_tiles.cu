@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = kt > kLand ? kt - kLand : 0; k < kt; ++k)
           drain_wait(BAR(BAR_FULL + k % kLand), (k / kLand) & 1);
       }
-    } else if (warp < 12 + kNT) {
+    } else {
       // ---------------- products of row tile t ----------------
       const int t = warp - 12;
       const uint32_t d_s = tmem + kColS + 64 * t, d_p = tmem + kColP + 32 * t,
