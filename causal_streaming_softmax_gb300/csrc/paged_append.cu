@@ -265,9 +265,11 @@ constexpr int kManySets = 2, kManyMoves = 4;
 // A thread takes several pieces where there is more than so many blocks a SM of work.
 // Of 16 bits (32 / 8 heads; one set, two): 800 tokens 3.1, 3.3 us; 1200 4.5, 3.9; 1600
 // 5.0, 4.1; 6400 17.5, 15.8: once not all warps of one set are resident.  Into 4 bits
-// (with the rows read back): 3200 tokens 19.3, 22.2; 12800 44.2, 46.2; 25600 79.0, 76.8.
+// a set's arithmetic is longer.  With rotation (32 / 8 heads): 1600 5.6, 6.1; 3200 8.7,
+// 8.7; 6400 15.5, 14.1; 12800 33.2, 30.7; 50000 120, 104.  Without (16 heads): 800 3.3,
+// 3.7; 1600 4.4, 4.1 (but 9.1, 9.4 with 2070 rows read back behind it); 12800 20.9, 19.7.
 // Rows read back (4 heads, random slots; one, four): 80,000 22.2, 23.0; 150,000 44, 39.
-constexpr int kMany = 4, kMany4 = 80, kManyLoad = 48;
+constexpr int kMany = 4, kMany4 = 16, kManyLoad = 48;
 constexpr int kBlocks = 8;  // a full SM
 
 }  // namespace
