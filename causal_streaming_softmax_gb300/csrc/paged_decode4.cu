@@ -505,9 +505,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         for (int j = 0; j < 4; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
       }
 
-      // The warp's keys of a tile for the first `cols` column tiles.  EDGE: whatever they
-      // are; else every row sees all of them, and the answer is false, with nothing done,
-      // where a scale lies outside the units' range.
+      // The warp's keys of a tile for the first `cols` column tiles.  The answer is false
+      // where a scale of V lies outside the units' range.  EDGE: whatever the keys are; else
+      // every row sees all of them, and a tile that gives false has not been done.
       const auto walk = [&](auto edge_tag, auto cols_tag, uint32_t ks, int k0) -> bool {
         constexpr bool EDGE = decltype(edge_tag)::value;
         constexpr int cols = decltype(cols_tag)::value;
@@ -558,11 +558,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         if (EDGE) out |= odd_scale<BF16>(vw[0]) || odd_scale<BF16>(vw[1]);
         bool odd = false;   // EDGE: a scale that some row must not meet
         bool wide = false;  // EDGE: weights as two bfloat16 numbers
+        const bool even = !EDGE || !__any_sync(0xffffffffu, out);
         const auto apart = [&](uint32_t w) {  // of a key that some row misses: not a product
           const float2 m = magnitudes<BF16>(w);
           return odd_scale<BF16>(w) || m.x * v_inv.x > kVTop || m.y * v_inv.y > kVTop;
         };
-        if (EDGE && __any_sync(0xffffffffu, out)) {
+        if (!even) {
           // the largest finite scale and the least above zero: of keys that every row
           // sees, and of all where there is neither such a scale nor a unit
           float t[2], u[2], inv[2] = {v_inv.x, v_inv.y};
@@ -815,8 +816,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
                   }
               }
         }
-        return true;
+        return even;
       };
+      // A tile behind one with scales out of range goes to the edge's walk at once: 64
+      // requests of 2048..8192 keys, 32 / 8 heads, 48 us, with V times 2^0..2^20 by key 83
+      // (93 where each tile tries the other walk first), with an eighth of V zero 64 (75).
+      bool uneven = far;
       for (int t = sg.t0 + (warp + kConsumers - it % kConsumers) % kConsumers; t < t1;
            t += kConsumers) {
         const int s = warp * kRing + slot;
@@ -826,14 +831,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         const uint32_t ks = sbase + C::kSmemStage + s * kStage;
         // One column tile where the item fills no more: 64 one-token requests of a call that
         // may have four tokens each take 72 us so, 77 with both.
-        bool edge = far || past_limit(t * kTileKeys, kTileKeys, first_lim);
+        bool edge = uneven || past_limit(t * kTileKeys, kTileKeys, first_lim);
         if (!edge) {
           if (kCols > 1 && sg.r.n_new * a.G <= 8)
             edge = !walk(std::false_type{}, OneCol{}, ks, t * kTileKeys);
           else
             edge = !walk(std::false_type{}, AllCols{}, ks, t * kTileKeys);
         }
-        if (__builtin_expect(edge, 0)) walk(std::true_type{}, AllCols{}, ks, t * kTileKeys);
+        if (__builtin_expect(edge, 0))
+          uneven = !walk(std::true_type{}, AllCols{}, ks, t * kTileKeys) || far;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(BAR_EMPTY + s));
       }
