@@ -5,6 +5,7 @@ import random
 import pytest
 
 from serve4_range_util import own64, problem
+from serve4_util import put
 from serve_util import check
 
 pytestmark = pytest.mark.gpu
@@ -282,3 +283,44 @@ def test_rows_that_are_not_finite_beside_rows_far_apart(torch, form):
         fine = ~bad[rows]
         check(o[rows][fine], eo[fine], to[fine], "O")
         check(L[:, rows].T[fine], el.T[fine], tl.T[fine], "L")
+
+
+@pytest.mark.parametrize("heads,max_new", [((8, 2), None), ((2, 2), None), ((8, 1), None),
+                                           ((8, 2), 40)])
+@pytest.mark.parametrize("scale", [0.125, 1e-30])
+def test_rows_that_see_nothing_beside_extremes(torch, heads, max_new, scale):
+    """Fewer keys than new tokens: the first rows are zero and -infinity whatever the
+    others' q, K and V ask for."""
+    reqs = [(0, 1), (1, 2), (1, 1), (2, 2), (700, 2), (0, 2), (65, 2)]
+    dt = torch.bfloat16
+
+    def ask(q):
+        q[::2, :, :32] *= 2.0 ** -60
+        q[1::2, ::2] = 0
+
+    p = problem(reqs, *heads, 8, dt, 23, None, shapes("scatter", 80), ask)
+    o, L = run_and_check(torch, p, max_new, scale)
+    assert (o[0] == 0).all() and torch.isneginf(L[:, 0]).all()
+    assert (o[1] == 0).all() and torch.isneginf(L[:, 1]).all()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("form,new", [("whole_wide", 2), ("split_wide", 4), ("tiles", 70)])
+def test_any_bytes_behind_the_mask(torch, dtype, form, new):
+    """The last new token's rows of K and V hold any bytes: infinite, NaN, largest and
+    smallest scales among them.  The rows before it are what they were."""
+    reqs, heads, page, max_new = FORMS[form]
+    q, kc, vc, table, cu, lens = problem(reqs, *heads, page, getattr(torch, dtype), 6)
+    want = own64(q, kc, vc, table, cu, lens)[0]
+    at = lens[0] - 1
+    where = [torch.tensor([x]) for x in (table[0][at // page], at % page)]
+    g = torch.Generator().manual_seed(2)
+    for rep in range(12):
+        for pool in (kc, vc):
+            rows = torch.randint(0, 256, (1, heads[1], 36), generator=g, dtype=torch.uint8)
+            if rep < 6:  # scales of every exponent: infinities, NaN, the largest, the smallest
+                rows[..., 33::2] = [0x7c, 0xfc, 0x7f, 0x7b, 0x00, 0x80][rep]
+            put(pool, *where, rows.cuda())
+        o, L = run(torch, (q, kc, vc, table, cu, lens), max_new)
+        check(o[:new - 1], want[1][:-1], want[3][:-1], "O, %d" % rep)
+        check(L[:, :new - 1], want[2][:, :-1], want[4][:, :-1], "L, %d" % rep)
