@@ -21,7 +21,7 @@
 // measured copy rate (one set of eight rows a warp 90 us, three 71, six 74; blocks for
 // all the work instead of a full SM's 75).  22,900 tokens into 4 bits 53 us, 69% of it:
 // the arithmetic of a K or V row, some 200 instructions a thread, takes as long as its
-// bytes (1700 instructions a token, issue slots 69% busy; three blocks a SM 52.8 us,
+// bytes (1700 instructions a token, issue slots 67% busy; three blocks a SM 52.8 us,
 // four 53.3, two 62).  64 tokens 2.4 us, one 1.9: launch and the chain offsets ->
 // length -> angles.  Rows read back: 150,000 random slots, 4 heads, 39 us = 4.6 TB/s (a
 // row's 36 bytes lie in two sectors, so that 64 come from memory for each); a whole

@@ -43,8 +43,11 @@
 // (serve_decode.cuh, serve_parts.cuh).
 //
 // Measured (GB300, join included): 256 requests over 1024..16384 keys, 32 / 4 heads,
-// 130 us = 4.75 TB/s, 70% of the measured copy rate; 2 over 50000..65536, 16 / 16 heads,
-// 37 us = 3.8 TB/s; one over 777 keys 8.4 us.  The copies alone take 105 us of the 130
+// 132 us = 4.7 TB/s, 69% of the measured copy rate; 2 over 50000..65536, 16 / 16 heads,
+// 38 us = 3.75 TB/s; one over 777 keys 8.7 us.  (The ranges of V and q cost 1 to 2% of
+// that, or nothing, from one arrangement of the same instructions to the next; edge tiles
+// always with two terms of weights 141, zeros told apart in the full walk 132 to 141.)
+// Before them the copies alone took 105 us of 130
 // with two blocks a SM and rings of five (copies of 2304 bytes, 26 clocks each beside
 // their bytes: pages of 16 rows 1.3 times the time of pages of 64), the arithmetic alone
 // about 100: neither hides all of the other.  What was slower: 8 warps of 32 keys in
@@ -830,7 +833,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks)
         if (++slot == kRing) slot = 0, turn ^= 1;
         const uint32_t ks = sbase + C::kSmemStage + s * kStage;
         // One column tile where the item fills no more: 64 one-token requests of a call that
-        // may have four tokens each take 72 us so, 77 with both.
+        // may have four tokens each take 60 us so, 70 with both.
         bool edge = uneven || past_limit(t * kTileKeys, kTileKeys, first_lim);
         if (!edge) {
           if (kCols > 1 && sg.r.n_new * a.G <= 8)
@@ -948,7 +951,7 @@ int tokens4(const PagedDims& d) {
 // Beside chunks, requests of nine to sixteen rows are rare and go as items of up to
 // eight, which read K and V again (from L2 for the most part): 32 requests over
 // 2048..8192 keys, 32 / 8 heads, and a chunk of 300 tokens, us with two column tiles for
-// all / with items of eight: one token each 84 / 76, four 90 / 99.
+// all / with items of eight: one token each 91 / 82, four 95 / 106.
 bool splits(const PagedDims& d) { return d.G <= 8 && d.max_new > decode_tokens(d.G); }
 
 template <int COLS>
@@ -963,9 +966,10 @@ int launch_cols(const PagedDims& d, const DevCtx& ctx, const RowsArg& q, const P
 
 // Whole items where each finds a block at once and the table leaves room for no more
 // than kWholeKeys keys a request: the parts and the second launch fall away.  Split /
-// whole, us (8 K/V heads): one request of 100 keys 6.4 / 4.8, of 777 9.5 / 8.4, of 1500
-// 9.0 / 12.3; eight of 250 9.2 / 5.9, of 777 10.9 / 8.9, of 1500 10.1 / 12.9; fifty of
-// 500 17.4 / 9.1.  The width stands for the lengths, which the host does not see.
+// whole, us (8 K/V heads): one request of 100 keys 7.3 / 5.9, of 777 10.8 / 9.2, of 1500
+// 10.2 / 13.0; eight of 250 10.4 / 6.9, of 777 12.2 / 9.8, of 1500 11.0 / 13.7; fifty of
+// 500 17.9 / 9.6.  The width stands for the lengths, which the host does not see: a wide
+// table over short caches (the default of a server's is every page) takes the split form.
 bool decode4_whole(const PagedDims& d, int sm_count) {
   return !splits(d) && (long long)d.batch * d.Hkv <= decode4_blocks(d) * sm_count &&
          ((long long)d.width << d.shift) <= kWholeKeys;

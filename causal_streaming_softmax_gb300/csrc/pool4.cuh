@@ -1,5 +1,12 @@
 // pool4.cuh - the rows of a 4-bit cache.
 //
+// The block rule, a group's signed extremum over -8 as its scale and codes -8..7, is that
+// of the published 4-bit block format Q4_0 of open model files; the scale's bits, cut so
+// that products are exact, and the unit's layout are this cache's own.  Small whole numbers
+// through the bits of 1024 + x (binary16) or 16 + x (bfloat16) are the old device of adding
+// 2^23 to read a number off a significand, as Kim et al. (2022, on serving mixtures of
+// experts) use it for weights of few bits.
+//
 // A row of 64 channels is 32 bytes of codes and two 16-bit scales.  Byte c holds
 // channel c in its low half and channel c + 32 in its high half, each as code + 8
 // with code in -8..7; the value is code * scale of the channel's group (0..31,

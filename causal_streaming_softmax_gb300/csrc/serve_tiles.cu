@@ -59,7 +59,8 @@
 // tile n mod 3 turns those of key tile n into the 16-bit rows of a K/V stage, exactly,
 // two steps before their use.  Four chunks of 301..1024 tokens over 2048..8192 keys, 32 / 8
 // heads, take 128 us where the 16-bit cache takes 108, a prompt of 16384 tokens 1.40 ms
-// against 1.07: some 180 instructions a thread on the chain of every third step.
+// against 1.07: the counters have 300 instructions more a thread and key tile, waits
+// included, on the chain of every third step (82 million for the 16 bits, 108 for the 4).
 // Slower were: two row tiles and four warps that unpack beside them (134 us, 1.56 ms),
 // warp 15 for all tiles (163, 1.98) or every fourth (154, 1.69), warps 12 to 15 for a
 // quarter of each (159, 1.73: products come late).  Four warps more beside three row
